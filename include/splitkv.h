@@ -402,7 +402,8 @@ splitkv_status splitkv_read_stats(const splitkv_plan_t* plan, const void* worksp
 
 enum {
   SPLITKV_DEVERR_TIMEOUT = 1,    /* a bounded wait on a shared-memory barrier gave up */
-  SPLITKV_DEVERR_SEQLEN = 2,     /* device seq_lens differs from the plan's           */
+  SPLITKV_DEVERR_SEQLEN = 2,     /* device seq_lens differs from the plan's, or is not
+                                    one the cache can hold                            */
   SPLITKV_DEVERR_PAGE = 4        /* a block-table entry was outside [0, num_pages)    */
 };
 
@@ -423,6 +424,157 @@ splitkv_status splitkv_debug_gather(const splitkv_desc_t* desc, const void* page
                                     int32_t row_elems, const int32_t* block_table,
                                     int32_t b, int32_t h_kv, int32_t n_keys, void* dst,
                                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * Cache operators: what fills, weighs and prunes the paged cache around the
+ * decode step.  They take the decode's descriptor, pools and block table, run
+ * without a plan, and read every length on the device, so that a captured
+ * CUDA graph of them serves changing lengths.
+ *
+ * State of the cached keys, optional for a caller that never evicts: for
+ * every sequence, KV head and key slot an accumulated attention weight (fp32)
+ * and a position (int32), arrays [B][Hkv][max_pages_per_seq * P].  Entries at
+ * or behind a sequence's length mean nothing.
+ *
+ * Pages that a call writes (append: those of the new keys; evict: those of
+ * the first min(L, budget) keys) belong to one sequence: two sequences that
+ * share such a page overwrite one another's keys.
+ *
+ * `status` (int32 on the device, or NULL) collects SPLITKV_DEVERR_* bits; the
+ * calls only set bits, the caller clears them.  max_pages_per_seq * P is at
+ * most 2^31 - 4096.
+ */
+
+/* How the components of a rotated head row form pairs. */
+typedef enum splitkv_rope_pairing {
+  SPLITKV_ROPE_HALVES = 0,      /* (i, i + rot_dim / 2)                         */
+  SPLITKV_ROPE_NEIGHBOURS = 1   /* (2 i, 2 i + 1)                               */
+} splitkv_rope_pairing;
+
+/* Opaque host object: the frequencies of rotary positions with 1..4 axes. */
+typedef struct splitkv_rope_s splitkv_rope_t;
+
+/*
+ * splitkv_rope_create -- rotary positions over columns [rot_offset,
+ * rot_offset + rot_dim) of every query and key head row (host only).  Pair i
+ * of the rot_dim / 2 pairs turns by positions[axis(i)] * freq_i, where the
+ * first sections[0] pairs go by axis 0, the next sections[1] by axis 1 (time,
+ * height, width for images and video), and so on.
+ *   rot_offset     non-negative multiple of 16 (512 for the MLA latent rows)
+ *   rot_dim        multiple of 16 in [16, 128]
+ *   n_axes         1..4
+ *   sections_host  [n_axes], summing to rot_dim / 2; NULL allowed for one axis
+ *   pairing        splitkv_rope_pairing
+ *   base           freq_i = base^(-2 i / rot_dim), unless
+ *   freqs_host     [rot_dim / 2] radians per position, or NULL (|f| < 1e6)
+ * Angles are exact to 2^-31 half turns for every int32 position.  Free with
+ * splitkv_rope_destroy (NULL is ignored); a call holds its own copy.
+ */
+splitkv_status splitkv_rope_create(int32_t rot_offset, int32_t rot_dim, int32_t n_axes,
+                                   const int32_t* sections_host, int32_t pairing, double base,
+                                   const double* freqs_host, splitkv_rope_t** rope_out);
+void splitkv_rope_destroy(splitkv_rope_t* rope);
+
+/*
+ * splitkv_append -- rotates the queries and keys of new tokens and writes the
+ * keys and values into the cache's pages, from the projections' output, for
+ * one decode step or for whole prompts.  Token n of sequence b, one of the
+ * tokens [cu_tokens[b], cu_tokens[b + 1]), becomes key
+ * j = seq_lens[b] - (cu_tokens[b + 1] - n): the lengths count the new tokens,
+ * as for splitkv_decode.  Tokens outside [cu_tokens[0], cu_tokens[B]) are
+ * padding: nothing of theirs is read or written.
+ *   desc           the cache (q_tokens counts only without cu_tokens; there is
+ *                  no limit on query rows per KV head here): qk_dim = v_dim =
+ *                  128, or one KV head with qk_dim 576 and v_dim 512
+ *   rope           NULL: nothing is rotated (encoder states)
+ *   cu_tokens      int32 [B + 1], not decreasing, or NULL: q_tokens tokens for
+ *                  every sequence, n_tokens = B * q_tokens
+ *   positions      int32 [n_axes][n_tokens]; may be NULL without rope and
+ *                  key_positions (one axis without rope)
+ *   q              bf16, token n's heads [Hq][Dk] at q + n * q_stride (strides
+ *                  in elements, multiples of 8: the three may be columns of
+ *                  one buffer); NULL with q_out: keys alone
+ *   k, v           bf16 [Hkv][Dk] and [Hkv][Dv] per token; v NULL with
+ *                  v_shares_k
+ *   kv_scale, k_scale, v_scale  e4m3 caches store round(x / scale) with
+ *                  saturation at +-448: kv_scale, or per KV head where k_scale
+ *                  and v_scale (fp32 [Hkv], device) are given
+ *   q_out          bf16, strided like q; may be q itself
+ *   k_pages, v_pages  the pools, in desc->kv_layout
+ *   key_weights, key_positions  state arrays or NULL: the new slots get weight
+ *                  0 and position positions[0][n]
+ * A key whose slot lies outside the cache sets SPLITKV_DEVERR_SEQLEN, one
+ * whose page id is out of range SPLITKV_DEVERR_PAGE; neither is stored.
+ * EINVAL for bad arguments, EUNSUPPORTED for other row widths.
+ */
+splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* rope,
+                              int32_t n_tokens, const int32_t* cu_tokens, const int32_t* positions,
+                              const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const int32_t* block_table,
+                              const int32_t* seq_lens, float kv_scale, const float* k_scale,
+                              const float* v_scale, void* q_out, int64_t q_out_stride,
+                              void* k_pages, void* v_pages, float* key_weights,
+                              int32_t* key_positions, int32_t* status, void* stream);
+
+/*
+ * splitkv_key_weights -- how much attention every cached key got from the
+ * query tokens of a decode call, added to what it had:
+ *
+ *     out[b][h][j] = decay * in[b][h][j] + sum over t and the query heads of
+ *                    KV head h, j <= L-T+t, of exp(s_j - lse[b][t][head])
+ *
+ * for j < L = seq_lens[b]; other entries of `out` are not written.  q,
+ * k_pages, block_table, seq_lens, scale, kv_scale are those of the decode call
+ * and lse its output; a row with lse = -inf (no visible key) adds nothing.
+ *   desc         as for splitkv_decode, GQA shapes (T * Hq / Hkv <= 32)
+ *   k_scale      fp32 [Hkv] (e4m3, replaces kv_scale) or NULL
+ *   decay        1 accumulates; 0 starts anew (weights_in is then not read and
+ *                may be NULL)
+ *   weights_in, weights_out  state arrays; may be the same
+ * A length outside [0, max_pages_per_seq * P] or in (0, q_tokens) sets
+ * SPLITKV_DEVERR_SEQLEN and its sequence is left out; a page id out of range
+ * sets SPLITKV_DEVERR_PAGE (page 0 is read in its place).  Results do not
+ * depend on the order of execution.
+ * EUNSUPPORTED for the MLA shape and for more query rows.
+ */
+splitkv_status splitkv_key_weights(const splitkv_desc_t* desc, const void* q, const void* k_pages,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   const float* lse, float scale, float kv_scale,
+                                   const float* k_scale, float decay, const float* weights_in,
+                                   float* weights_out, int32_t* status, void* stream);
+
+/*
+ * splitkv_evict -- cuts every sequence to at most `budget` keys, for each KV
+ * head the ones that rank best: protected keys first (position < sink, or
+ * among the last `recent` positions: above the head's largest position minus
+ * recent), then by accumulated weight (negative and NaN weights count as 0),
+ * ties to the lowest slot.  With n = min(L, budget), kept keys in slots below
+ * n stay where they are; the i-th kept key at or behind slot n moves to the
+ * i-th freed slot below n.  The slots of a head are therefore no longer in the
+ * order of the positions (attention does not depend on it, and tokens appended
+ * later are the last slots again, as the causal limits among them need).
+ *   budget           keys per sequence, >= 1
+ *   k_pages, v_pages changed in place: rows of slots below n only
+ *   weights_in, positions_in    state arrays; positions may be NULL with sink =
+ *                    recent = 0
+ *   weights_out, positions_out  the state of slots below n (other entries are
+ *                    not written); each may be its input
+ *   seq_lens_out     int32 [B]: n; may be seq_lens
+ *   workspace        splitkv_evict_workspace_size bytes, 16-byte aligned, used
+ *                    by this call alone until it has finished on the device
+ * A length outside [0, max_pages_per_seq * P] sets SPLITKV_DEVERR_SEQLEN and
+ * its sequence is left as it is; a page id out of range sets
+ * SPLITKV_DEVERR_PAGE and the rows that it would hold are not moved.
+ * Two kernels; results do not depend on the order of execution.
+ */
+size_t splitkv_evict_workspace_size(const splitkv_desc_t* desc, int32_t budget);
+splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t sink,
+                             int32_t recent, void* k_pages, void* v_pages,
+                             const int32_t* block_table, const int32_t* seq_lens,
+                             const float* weights_in, const int32_t* positions_in,
+                             float* weights_out, int32_t* positions_out, int32_t* seq_lens_out,
+                             void* workspace, size_t workspace_bytes, int32_t* status,
+                             void* stream);
 
 /* Thread-local description of the last error returned on this thread. */
 const char* splitkv_last_error(void);

@@ -29,6 +29,7 @@ SPLITKV_LAYOUT_HND, SPLITKV_LAYOUT_NHD = 0, 1
 SPLITKV_ITEM_FIELDS = 8
 SPLITKV_RANGE_FIELDS = 5
 SPLITKV_DEVERR_TIMEOUT, SPLITKV_DEVERR_SEQLEN, SPLITKV_DEVERR_PAGE = 1, 2, 4
+SPLITKV_ROPE_HALVES, SPLITKV_ROPE_NEIGHBOURS = 0, 1
 ITEM_FIELD_NAMES = ("b", "h_kv", "split", "num_splits", "page_begin", "page_end", "slot", "group")
 
 
@@ -46,6 +47,7 @@ class SplitKVError(RuntimeError):
 
 
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_i64, _f64 = ctypes.c_int64, ctypes.c_double
 _SIGNATURES = {
     "splitkv_plan": (_i32, [ctypes.POINTER(splitkv_desc_t), _vp, _i32, _i32, ctypes.POINTER(_vp)]),
     "splitkv_plan_fixed": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, ctypes.POINTER(_vp)]),
@@ -72,6 +74,16 @@ _SIGNATURES = {
     "splitkv_read_stats": (_i32, [_vp, _vp, _vp, _i32, _vp, _vp]),
     "splitkv_debug_gather": (_i32, [ctypes.POINTER(splitkv_desc_t), _vp, _i32, _vp, _i32, _i32,
                                     _i32, _vp, _vp]),
+    "splitkv_rope_create": (_i32, [_i32, _i32, _i32, _vp, _i32, _f64, _vp, ctypes.POINTER(_vp)]),
+    "splitkv_rope_destroy": (None, [_vp]),
+    "splitkv_append": (_i32, [ctypes.POINTER(splitkv_desc_t), _vp, _i32, _vp, _vp, _vp, _i64, _vp, _i64,
+                              _vp, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                              _vp]),
+    "splitkv_key_weights": (_i32, [ctypes.POINTER(splitkv_desc_t), _vp, _vp, _vp, _vp, _vp, _f32, _f32,
+                                   _vp, _f32, _vp, _vp, _vp, _vp]),
+    "splitkv_evict_workspace_size": (_sz, [ctypes.POINTER(splitkv_desc_t), _i32]),
+    "splitkv_evict": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                             _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "splitkv_last_error": (ctypes.c_char_p, []),
 }
 
@@ -291,6 +303,160 @@ def splitkv_debug_gather(desc: splitkv_desc_t, pages, row_elems: int, block_tabl
                          h_kv: int, n_keys: int, dst, stream=None):
     _check(_lib.splitkv_debug_gather(ctypes.byref(desc), _ptr(pages), row_elems, _ptr(block_table),
                                      b, h_kv, n_keys, _ptr(dst), _stream(stream)))
+
+
+# ------------------------------------------------------------ cache operators
+
+def _tensor(name, x, dtype, numel, what=""):
+    """Checks a tensor argument (addresses pass unchecked): its type, that its
+    elements are adjacent, that there are enough of them, and that it is on
+    torch's current device, where the call's kernels run."""
+    if x is None or isinstance(x, int):
+        return
+    import torch
+    if x.dtype is not getattr(torch, dtype) or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor, got {x.dtype}")
+    if x.numel() < numel:
+        raise ValueError(f"{name} has {x.numel()} elements, the call needs {numel}{what}")
+    _on_current_device(name, x)
+
+
+def _on_current_device(name, x):
+    import torch
+    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
+
+
+def _token_rows(name, x, tokens, heads, dim):
+    """(address, token stride) of a bf16 tensor [tokens][heads][dim] whose tokens may be strided."""
+    if x is None or isinstance(x, int):
+        return x, heads * dim
+    import torch
+    if x.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 tensor, got {x.dtype}")
+    if x.dim() == 4:
+        x = x.flatten(0, 1) if x.is_contiguous() else x
+    if tuple(x.shape) != (tokens, heads, dim):
+        raise ValueError(f"{name} must be [{tokens}][{heads}][{dim}], got {tuple(x.shape)}")
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
+        raise ValueError(f"the heads of a token of {name} must be adjacent")
+    _on_current_device(name, x)
+    return x.data_ptr(), x.stride(0) if tokens > 1 else heads * dim
+
+
+def _pools(desc, k_pages, v_pages):
+    dtype = "uint8" if desc.kv_dtype == SPLITKV_FP8_E4M3 else "bfloat16"
+    rows = desc.num_pages_total * desc.num_kv_heads * desc.page_size
+    _tensor("k_pages", k_pages, dtype, rows * desc.qk_dim)
+    _tensor("v_pages", v_pages, dtype, rows * desc.v_dim)
+
+
+def _cache_index(desc, block_table, seq_lens):
+    _tensor("block_table", block_table, "int32", desc.batch * desc.max_pages_per_seq)
+    _tensor("seq_lens", seq_lens, "int32", desc.batch)
+
+
+def _state_numel(desc) -> int:
+    return desc.batch * desc.num_kv_heads * desc.max_pages_per_seq * desc.page_size
+
+
+class Rope:
+    """Owns a ``splitkv_rope_t*``; frees it when collected."""
+
+    def __init__(self, handle: int, n_axes: int):
+        self.handle = handle
+        self.n_axes = n_axes
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            _lib.splitkv_rope_destroy(self.handle)
+            self.handle = None
+
+
+def splitkv_rope_create(rot_dim: int, sections=None, base: float = 10000.0, freqs=None,
+                        rot_offset: int = 0, pairing: int = SPLITKV_ROPE_HALVES) -> Rope:
+    """Rotary positions with one axis per entry of ``sections`` (None: one axis)."""
+    sec = None if sections is None else np.ascontiguousarray(np.asarray(sections, dtype=np.int32))
+    frq = None if freqs is None else np.ascontiguousarray(np.asarray(freqs, dtype=np.float64))
+    if frq is not None and frq.shape != (rot_dim // 2,):
+        raise ValueError(f"freqs must have rot_dim / 2 = {rot_dim // 2} entries, got {frq.shape}")
+    n_axes = 1 if sec is None else int(sec.size)
+    h = _vp()
+    _check(_lib.splitkv_rope_create(rot_offset, rot_dim, n_axes, _ptr(sec), pairing, base, _ptr(frq),
+                                    ctypes.byref(h)))
+    return Rope(h.value, n_axes)
+
+
+def splitkv_append(desc: splitkv_desc_t, rope, positions, q, k, v, block_table, seq_lens, q_out,
+                   k_pages, v_pages, cu_tokens=None, kv_scale: float = 1.0, k_scale=None, v_scale=None,
+                   key_weights=None, key_positions=None, status=None, n_tokens=None, stream=None):
+    """Rotates queries and keys of new tokens (``rope`` None: rotates nothing)
+    and writes the keys and values into the pages.  ``n_tokens`` is needed only
+    where ``k`` is an address."""
+    n = n_tokens if n_tokens is not None else (k.numel() // (desc.num_kv_heads * desc.qk_dim))
+    qp, qs = _token_rows("q", q, n, desc.num_q_heads, desc.qk_dim)
+    op, os_ = _token_rows("q_out", q_out, n, desc.num_q_heads, desc.qk_dim)
+    kp, ks = _token_rows("k", k, n, desc.num_kv_heads, desc.qk_dim)
+    vp, vs = _token_rows("v", v, n, desc.num_kv_heads, desc.v_dim)
+    _pools(desc, k_pages, v_pages)
+    _cache_index(desc, block_table, seq_lens)
+    _tensor("positions", positions, "int32", n * (rope.n_axes if rope is not None else 1))
+    _tensor("cu_tokens", cu_tokens, "int32", desc.batch + 1)
+    _tensor("key_weights", key_weights, "float32", _state_numel(desc))
+    _tensor("key_positions", key_positions, "int32", _state_numel(desc))
+    _tensor("k_scale", k_scale, "float32", desc.num_kv_heads)
+    _tensor("v_scale", v_scale, "float32", desc.num_kv_heads)
+    _tensor("status", status, "int32", 1)
+    _check(_lib.splitkv_append(ctypes.byref(desc), None if rope is None else rope.handle, n,
+                               _ptr(cu_tokens), _ptr(positions), qp, qs, kp, ks, vp, vs,
+                               _ptr(block_table), _ptr(seq_lens), kv_scale, _ptr(k_scale),
+                               _ptr(v_scale), op, os_, _ptr(k_pages), _ptr(v_pages),
+                               _ptr(key_weights), _ptr(key_positions), _ptr(status), _stream(stream)))
+
+
+def splitkv_key_weights(desc: splitkv_desc_t, q, k_pages, block_table, seq_lens, lse, scale: float,
+                        kv_scale: float, decay: float, weights_in, weights_out, k_scale=None,
+                        status=None, stream=None):
+    """Adds the attention every cached key got from ``q`` (``lse`` from the decode call)."""
+    rows = desc.batch * desc.q_tokens * desc.num_q_heads
+    _tensor("q", q, "bfloat16", rows * desc.qk_dim)
+    _pools(desc, k_pages, None)
+    _cache_index(desc, block_table, seq_lens)
+    _tensor("lse", lse, "float32", rows)
+    _tensor("weights_in", weights_in, "float32", _state_numel(desc))
+    _tensor("weights_out", weights_out, "float32", _state_numel(desc))
+    _tensor("k_scale", k_scale, "float32", desc.num_kv_heads)
+    _tensor("status", status, "int32", 1)
+    _check(_lib.splitkv_key_weights(ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(block_table),
+                                    _ptr(seq_lens), _ptr(lse), scale, kv_scale, _ptr(k_scale), decay,
+                                    _ptr(weights_in), _ptr(weights_out), _ptr(status),
+                                    _stream(stream)))
+
+
+def splitkv_evict_workspace_size(desc: splitkv_desc_t, budget: int) -> int:
+    return int(_lib.splitkv_evict_workspace_size(ctypes.byref(desc), budget))
+
+
+def splitkv_evict(desc: splitkv_desc_t, budget: int, sink: int, recent: int, k_pages, v_pages,
+                  block_table, seq_lens, weights_in, positions_in, weights_out, positions_out,
+                  seq_lens_out, workspace, workspace_bytes=None, status=None, stream=None):
+    """Cuts every sequence to at most ``budget`` keys per KV head, the best by weight."""
+    _pools(desc, k_pages, v_pages)
+    _cache_index(desc, block_table, seq_lens)
+    n = _state_numel(desc)
+    _tensor("weights_in", weights_in, "float32", n)
+    _tensor("weights_out", weights_out, "float32", n)
+    _tensor("positions_in", positions_in, "int32", n)
+    _tensor("positions_out", positions_out, "int32", n)
+    _tensor("seq_lens_out", seq_lens_out, "int32", desc.batch)
+    _tensor("workspace", workspace, "uint8", 0)
+    _tensor("status", status, "int32", 1)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel()
+    _check(_lib.splitkv_evict(ctypes.byref(desc), budget, sink, recent, _ptr(k_pages), _ptr(v_pages),
+                              _ptr(block_table), _ptr(seq_lens), _ptr(weights_in), _ptr(positions_in),
+                              _ptr(weights_out), _ptr(positions_out), _ptr(seq_lens_out),
+                              _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)))
 
 
 def splitkv_last_error() -> str:

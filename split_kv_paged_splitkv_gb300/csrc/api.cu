@@ -18,6 +18,8 @@ thread_local char g_err[512] = "";
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -31,6 +33,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+namespace {
 
 // Tensor map over a GQA K or V page pool (rows of 128 elements) in either
 // layout, with coordinates that do not depend on the layout -- (dims, key in
@@ -110,11 +114,13 @@ splitkv_status make_u8_map(TmaDesc* out, const void* base, int dim, int64_t rows
   return SPLITKV_OK;
 }
 
+}  // namespace
+
 splitkv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(SPLITKV_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-splitkv_status validate_desc(const splitkv_desc_t* d) {
+splitkv_status validate_shape(const splitkv_desc_t* d) {
   if (!d) return fail(SPLITKV_EINVAL, "desc is NULL");
   if (d->batch < 1 || d->q_tokens < 1 || d->num_q_heads < 1 || d->num_kv_heads < 1)
     return fail(SPLITKV_EINVAL, "batch, q_tokens and head counts must be >= 1");
@@ -137,6 +143,14 @@ splitkv_status validate_desc(const splitkv_desc_t* d) {
     return fail(SPLITKV_EINVAL, "unknown kv_layout %d", d->kv_layout);
   if (int64_t(d->num_pages_total) * d->num_kv_heads * d->page_size >= (int64_t(1) << 31))
     return fail(SPLITKV_EINVAL, "num_pages_total * num_kv_heads * page_size must be < 2^31");
+  return SPLITKV_OK;
+}
+
+namespace {
+
+splitkv_status validate_desc(const splitkv_desc_t* d) {
+  splitkv_status st = validate_shape(d);
+  if (st != SPLITKV_OK) return st;
   if (family_of(*d) == Family::kNone)
     return fail(SPLITKV_EUNSUPPORTED,
                 "no kernel for qk_dim=%d v_dim=%d T=%d G=%d kv_dtype=%d v_shares_k=%d "

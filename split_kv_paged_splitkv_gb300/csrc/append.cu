@@ -1,0 +1,305 @@
+// Rotary positions and the paged append, sm_103a.
+//
+// For every new token n of sequence b (the tokens [cu[b], cu[b + 1]) of the
+// call, the last ones of the sequence's seq_lens[b] keys), with angle
+//     a_i = positions[axis(i)][n] * freq_i,
+// pair i = (u, v) of each query and key head row becomes
+//     (u cos a_i - v sin a_i, u sin a_i + v cos a_i);
+// the query goes to q_out, the key and the value into row j % P of page
+// block_table[b][j / P], j = seq_lens[b] - (cu[b + 1] - n).
+//
+// Angles.  A position times a frequency needs more digits than 32-bit
+// arithmetic has (2^20 * 1.0 rad leaves 2^-4 rad of it).  freq_i is held as a
+// fraction of a full turn in 64-bit fixed point, so position * freq modulo a
+// turn is one wrapping 64-bit product, off by at most |position| * 2^-65
+// turns; its top 32 bits, as a signed number of half turns in [-1, 1), go to
+// sincospif.  Rotation is in fp32, rounded once: to bf16, or to e4m3 after
+// the division by the cache's scale.
+//
+// Bound: the bytes of q (read and written), k and v (read, and written in the
+// cache's type); a decode step of a few tokens is bound by one chain of
+// loads, so nothing but the token's own loads precedes its stores.
+//
+// One thread handles 32-byte units (two 16-byte chunks of a head row, the
+// two halves of the same eight pairs where pairs are half a row apart), so
+// every load and store is 16 bytes wide; a CTA computes the sines and cosines
+// of its tokens once, for all heads.
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace splitkv {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;                    // units of a thread in flight
+constexpr int kUnits = kThreads * kUnroll;    // units a CTA covers
+constexpr int kMaxTok = 32;                   // tokens of a CTA, at most
+
+struct Token {
+  int32_t b, slot, page, in_page;  // b < 0: padding; page < 0: no key is stored
+};
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(const float* x) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
+  return uint32_t(lo) | (uint32_t(hi) << 16);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                    pack_bf16(f[6], f[7]));
+}
+
+// The sequence whose tokens [cu[b], cu[b + 1]) hold n, or -1.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int n) {
+  if (n < cu[0] || n >= cu[batch]) return -1;
+  int lo = 0, hi = batch;  // cu[lo] <= n < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= n) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <int DK, int DV, bool FP8>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a,
+                                                          int tok_per_cta) {
+  constexpr int UK = DK / 16, UV = DV / 16;  // units of a q or k row, of a v row
+  __shared__ Token tok[kMaxTok];
+  __shared__ float2 cs[kMaxTok * kMaxRotPairs];  // (cos, sin) of each pair
+
+  launch_dependents();
+  wait_prerequisites();
+
+  const int n0 = blockIdx.x * tok_per_cta;
+  const int ntok = min(tok_per_cta, a.n_tokens - n0);
+  const int half = a.rope.rot_dim / 2;
+  const int per_tok = (a.q ? a.Hq * UK : 0) + a.Hkv * (UK + (a.v ? UV : 0));
+  const int total = ntok * per_tok;
+  const int64_t cap = int64_t(a.max_pages) * a.P;
+
+  // where the tokens' keys go, and their sines and cosines
+  for (int i = threadIdx.x; i < ntok; i += kThreads) {
+    const int n = n0 + i;
+    Token t;
+    t.b = a.cu ? find_seq(a.cu, a.batch, n) : n / a.T;
+    t.page = -1;
+    t.slot = t.in_page = 0;
+    if (t.b >= 0) {
+      const int64_t end = a.cu ? a.cu[t.b + 1] : int64_t(t.b + 1) * a.T;
+      const int64_t slot = int64_t(a.seq_lens[t.b]) - (end - n);
+      int err = 0;
+      if (slot < 0 || slot >= cap) {
+        err = SPLITKV_DEVERR_SEQLEN;
+      } else {
+        const int lp = int(slot) / a.P;
+        const int ph = a.block_table[size_t(t.b) * a.max_pages + lp];
+        if (ph < 0 || ph >= a.num_pages) {
+          err = SPLITKV_DEVERR_PAGE;
+        } else {
+          t.page = ph;
+          t.slot = int(slot);
+          t.in_page = int(slot) - lp * a.P;
+        }
+      }
+      if (err && a.status && blockIdx.y == 0) atomicOr(a.status, err);
+    }
+    tok[i] = t;
+  }
+  for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
+    const int t = i / half, p = i - t * half;
+    const int64_t pos = a.positions[size_t(a.rope.axis[p]) * a.n_tokens + n0 + t];
+    const uint64_t phase = uint64_t(pos) * a.rope.turns[p];
+    float s, c;
+    sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s, &c);
+    cs[t * kMaxRotPairs + p] = make_float2(c, s);
+  }
+  __syncthreads();
+
+  // the state of the new keys
+  if (blockIdx.y == 0 && (a.key_weights || a.key_positions)) {
+    for (int i = threadIdx.x; i < ntok * a.Hkv; i += kThreads) {
+      const int t = i / a.Hkv, h = i - t * a.Hkv;
+      if (tok[t].page < 0) continue;
+      const size_t at = (size_t(tok[t].b) * a.Hkv + h) * cap + tok[t].slot;
+      if (a.key_weights) a.key_weights[at] = 0.f;
+      if (a.key_positions) a.key_positions[at] = a.positions[n0 + t];
+    }
+  }
+
+  const int qu = a.q ? a.Hq * UK : 0, ku = a.Hkv * UK;
+  const int rot0 = a.rope.rot_offset / 8, rotc = a.rope.rot_dim / 8;  // rotated chunks
+  const bool halves = a.rope.pairing == SPLITKV_ROPE_HALVES;
+
+  // Chunks of unit u of a row: the two halves of eight pairs while u counts
+  // rotated pairs half a row apart, then the other chunks in order.
+  auto chunks = [&](int u, int& c0, int& c1) {
+    if (!halves || rotc == 0) {
+      c0 = 2 * u;
+      c1 = c0 + 1;
+    } else if (u < rotc / 2) {
+      c0 = rot0 + u;
+      c1 = c0 + rotc / 2;
+    } else {
+      c0 = 2 * u - rotc;
+      c1 = c0 + 1;
+      c0 += c0 >= rot0 ? rotc : 0;
+      c1 += c1 >= rot0 ? rotc : 0;
+    }
+  };
+
+  struct Unit {
+    uint4 x0, x1;
+    int t, row, c0, c1, kind;  // kind 0 q, 1 k, 2 v, -1 none
+  };
+
+  // A CTA of slice y covers units y * kUnits + ... of its tokens' units.
+  for (int base = blockIdx.y * kUnits; base < total; base += gridDim.y * kUnits) {
+    Unit un[kUnroll];
+#pragma unroll
+    for (int r = 0; r < kUnroll; ++r) {
+      const int i = base + r * kThreads + threadIdx.x;
+      un[r].kind = -1;
+      if (i >= total) continue;
+      const int t = i / per_tok;
+      int u = i - t * per_tok;
+      if (tok[t].b < 0) continue;
+      const __nv_bfloat16* src;
+      if (u < qu) {
+        un[r].kind = 0;
+        un[r].row = u / UK;
+        u -= un[r].row * UK;
+        chunks(u, un[r].c0, un[r].c1);
+        src = static_cast<const __nv_bfloat16*>(a.q) + int64_t(n0 + t) * a.q_stride + un[r].row * DK;
+      } else if (tok[t].page < 0) {
+        continue;
+      } else if (u < qu + ku) {
+        u -= qu;
+        un[r].kind = 1;
+        un[r].row = u / UK;
+        u -= un[r].row * UK;
+        chunks(u, un[r].c0, un[r].c1);
+        src = static_cast<const __nv_bfloat16*>(a.k) + int64_t(n0 + t) * a.k_stride + un[r].row * DK;
+      } else {
+        u -= qu + ku;
+        un[r].kind = 2;
+        un[r].row = u / UV;
+        u -= un[r].row * UV;
+        un[r].c0 = 2 * u;
+        un[r].c1 = 2 * u + 1;
+        src = static_cast<const __nv_bfloat16*>(a.v) + int64_t(n0 + t) * a.v_stride + un[r].row * DV;
+      }
+      un[r].t = t;
+      un[r].x0 = reinterpret_cast<const uint4*>(src)[un[r].c0];
+      un[r].x1 = reinterpret_cast<const uint4*>(src)[un[r].c1];
+    }
+#pragma unroll
+    for (int r = 0; r < kUnroll; ++r) {
+      if (un[r].kind < 0) continue;
+      const int c0 = un[r].c0, c1 = un[r].c1, t = un[r].t;
+      float f0[8], f1[8];
+      unpack8(un[r].x0, f0);
+      unpack8(un[r].x1, f1);
+      if (un[r].kind < 2 && rotc) {
+        const float2* w = cs + t * kMaxRotPairs;
+        if (halves) {
+          if (c0 >= rot0 && c0 < rot0 + rotc) {  // then c1 is the other half of the pairs
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 z = w[(c0 - rot0) * 8 + e];
+              const float u = f0[e], v = f1[e];
+              f0[e] = u * z.x - v * z.y;
+              f1[e] = u * z.y + v * z.x;
+            }
+          }
+        } else {
+          auto turn = [&](float (&f)[8], int c) {
+            if (c < rot0 || c >= rot0 + rotc) return;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 z = w[(c - rot0) * 4 + e];
+              const float u = f[2 * e], v = f[2 * e + 1];
+              f[2 * e] = u * z.x - v * z.y;
+              f[2 * e + 1] = u * z.y + v * z.x;
+            }
+          };
+          turn(f0, c0);
+          turn(f1, c1);
+        }
+      }
+      if (un[r].kind == 0) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) +
+                                              int64_t(n0 + t) * a.q_out_stride + un[r].row * DK);
+        dst[c0] = pack8(f0);
+        dst[c1] = pack8(f1);
+        continue;
+      }
+      const Token tk = tok[t];
+      const int h = un[r].row;
+      const size_t line = a.nhd ? (size_t(tk.page) * a.P + tk.in_page) * a.Hkv + h
+                                : (size_t(tk.page) * a.Hkv + h) * a.P + tk.in_page;
+      const bool is_k = un[r].kind == 1;
+      const int D = is_k ? DK : DV;
+      void* pool = is_k ? a.k_pages : a.v_pages;
+      if (FP8) {
+        const float* per_head = is_k ? a.k_scale : a.v_scale;
+        const float sc = per_head ? per_head[h] : a.kv_scale;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f0[e] = __fdiv_rn(f0[e], sc);
+          f1[e] = __fdiv_rn(f1[e], sc);
+        }
+        uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + line * D);
+        dst[c0] = make_uint2(pack_e4m3x4(f0), pack_e4m3x4(f0 + 4));
+        dst[c1] = make_uint2(pack_e4m3x4(f1), pack_e4m3x4(f1 + 4));
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + line * D);
+        dst[c0] = is_k ? pack8(f0) : un[r].x0;
+        dst[c1] = is_k ? pack8(f1) : un[r].x1;
+      }
+    }
+  }
+}
+
+template <int DK, int DV, bool FP8>
+cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t s) {
+  const int per_tok = (a.q ? a.Hq * DK / 16 : 0) + a.Hkv * (DK / 16 + (a.v ? DV / 16 : 0));
+  const int tpc = per_tok >= kUnits ? 1 : min(kMaxTok, kUnits / per_tok);
+  const int64_t slices = (int64_t(per_tok) * tpc + kUnits - 1) / kUnits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.n_tokens + tpc - 1) / tpc, unsigned(slices > 65535 ? 65535 : slices), 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = la;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, append_kernel<DK, DV, FP8>, a, tpc);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a.n_tokens == 0) return cudaSuccess;
+  if (qk_dim == 128 && v_dim == 128)
+    return fp8 ? launch_append_t<128, 128, true>(a, s) : launch_append_t<128, 128, false>(a, s);
+  return fp8 ? launch_append_t<576, 512, true>(a, s) : launch_append_t<576, 512, false>(a, s);
+}
+
+}  // namespace splitkv

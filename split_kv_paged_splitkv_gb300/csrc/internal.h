@@ -72,6 +72,11 @@ void build_fixed_plan(splitkv_plan_s* p);
 
 // Thread-local error text (api.cu).
 splitkv_status fail(splitkv_status s, const char* fmt, ...);
+splitkv_status cuda_fail(cudaError_t e, const char* what);
+
+// The checks of a descriptor that do not depend on a decode kernel (api.cu):
+// positive sizes, known enums, page size, index ranges.
+splitkv_status validate_shape(const splitkv_desc_t* d);
 
 // ----------------------------------------------------------------- kernels
 
@@ -143,5 +148,80 @@ cudaError_t launch_debug_gather(const TmaDesc& t, bool fp8, const int32_t* table
 cudaError_t launch_mla_debug_gather(const TmaDesc& t, bool fp8, const int32_t* table_row, int32_t P,
                                     int32_t num_pages, int32_t row_elems, int32_t n_keys, void* dst,
                                     void* stream);
+
+// ---------------------------------------------------- cache operators
+
+constexpr int kMaxRotPairs = 64;  // rotated pairs of a head row
+constexpr int kMaxAxes = 4;       // position axes
+
+}  // namespace splitkv
+
+// Rotary table (host): pair i turns by positions[axis[i]] * turns[i], in units
+// of 2^-64 of a full turn.
+struct splitkv_rope_s {
+  int32_t rot_offset = 0, rot_dim = 0, n_axes = 1, pairing = 0;
+  uint64_t turns[splitkv::kMaxRotPairs] = {};
+  unsigned char axis[splitkv::kMaxRotPairs] = {};
+};
+
+namespace splitkv {
+
+struct AppendArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements per token
+  const int32_t* cu;         // [batch + 1] or null: T tokens per sequence
+  const int32_t* positions;  // [n_axes][n_tokens] or null
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* k_scale;      // e4m3 per-KV-head scales or null: kv_scale
+  const float* v_scale;
+  float* key_weights;        // [batch][Hkv][max_pages * P] or null
+  int32_t* key_positions;    // likewise
+  int32_t* status;           // or null
+  float kv_scale;
+  int32_t n_tokens, batch, T, Hq, Hkv, P, max_pages, num_pages, nhd;
+  splitkv_rope_s rope;       // rot_dim 0: nothing is rotated
+};
+
+struct WeightArgs {
+  const void* q;
+  const void* k_pages;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* lse;
+  const float* k_scale;  // e4m3 per-KV-head scales or null
+  const float* w_in;     // [batch][Hkv][max_pages * P]
+  float* w_out;
+  int32_t* status;       // or null
+  float qk_scale_log2, decay;
+  int32_t batch, T, Hq, Hkv, G, P, max_pages, num_pages, nhd;
+};
+
+struct EvictArgs {
+  void* k_pages;
+  void* v_pages;  // or null
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* w_in;      // [batch][Hkv][max_pages * P]
+  const int32_t* pos_in;  // likewise, or null (no protected keys)
+  float* w_out;
+  int32_t* pos_out;       // or null
+  int32_t* lens_out;
+  int32_t* meta;          // workspace: [groups][2] {moves, new length}
+  int32_t* moves;         // workspace: [groups][2][max_moves] sources, destinations
+  int32_t* status;        // or null
+  int32_t batch, Hkv, P, max_pages, num_pages, nhd;
+  int32_t budget, sink, recent, max_moves;
+  int32_t k_row, v_row;   // bytes of one key's row
+};
+
+cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream);
+cudaError_t launch_key_weights(const WeightArgs& a, bool fp8, void* stream);
+cudaError_t launch_evict(const EvictArgs& a, void* stream);
 
 }  // namespace splitkv
