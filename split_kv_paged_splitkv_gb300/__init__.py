@@ -13,8 +13,10 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
+import types
 
 import numpy as np
 
@@ -124,7 +126,8 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # (the handle alone: making a Stream object costs ten times as much)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -307,57 +310,55 @@ def splitkv_debug_gather(desc: splitkv_desc_t, pages, row_elems: int, block_tabl
 
 # ------------------------------------------------------------ cache operators
 
-def _tensor(name, x, dtype, numel, what=""):
-    """Checks a tensor argument (addresses pass unchecked): its type, that its
-    elements are adjacent, that there are enough of them, and that it is on
-    torch's current device, where the call's kernels run."""
-    if x is None or isinstance(x, int):
-        return
+@functools.lru_cache(maxsize=256)
+def _sizes(desc_bytes: bytes):
+    """Element counts of a call's arrays, by the descriptor's content."""
     import torch
-    if x.dtype is not getattr(torch, dtype) or not x.is_contiguous():
+    d = splitkv_desc_t.from_buffer_copy(desc_bytes)
+    rows = d.num_pages_total * d.num_kv_heads * d.page_size
+    return types.SimpleNamespace(
+        torch=torch, pool_dtype=torch.uint8 if d.kv_dtype == SPLITKV_FP8_E4M3 else torch.bfloat16,
+        k_pool=rows * d.qk_dim, v_pool=rows * d.v_dim, table=d.batch * d.max_pages_per_seq, batch=d.batch,
+        state=d.batch * d.num_kv_heads * d.max_pages_per_seq * d.page_size, heads=d.num_q_heads,
+        kv_heads=d.num_kv_heads, k_dim=d.qk_dim, v_dim=d.v_dim, k_token=d.num_kv_heads * d.qk_dim,
+        q_rows=d.batch * d.q_tokens * d.num_q_heads)
+
+
+def _addr(name, x, dtype, numel, device):
+    """The address of a tensor argument (addresses and None pass unchecked),
+    after checking its type, that its elements are adjacent, that there are
+    enough of them, and that it is on torch's current device, where the call's
+    kernels run."""
+    if x is None or type(x) is int:
+        return x
+    if x.dtype is dtype and x.numel() >= numel and x.get_device() == device and x.is_contiguous():
+        return x.data_ptr()
+    if x.dtype is not dtype or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor, got {x.dtype}")
     if x.numel() < numel:
-        raise ValueError(f"{name} has {x.numel()} elements, the call needs {numel}{what}")
-    _on_current_device(name, x)
+        raise ValueError(f"{name} has {x.numel()} elements, the call needs {numel}")
+    raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
 
 
-def _on_current_device(name, x):
-    import torch
-    if not x.is_cuda or x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
-
-
-def _token_rows(name, x, tokens, heads, dim):
+def _token_rows(name, x, tokens, heads, dim, z, device):
     """(address, token stride) of a bf16 tensor [tokens][heads][dim] whose tokens may be strided."""
-    if x is None or isinstance(x, int):
+    if x is None or type(x) is int:
         return x, heads * dim
-    import torch
-    if x.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be a bfloat16 tensor, got {x.dtype}")
-    if x.dim() == 4:
-        x = x.flatten(0, 1) if x.is_contiguous() else x
-    if tuple(x.shape) != (tokens, heads, dim):
-        raise ValueError(f"{name} must be [{tokens}][{heads}][{dim}], got {tuple(x.shape)}")
-    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
+    if x.dim() == 4 and x.is_contiguous():
+        x = x.flatten(0, 1)
+    if x.dtype is not z.torch.bfloat16 or x.shape != (tokens, heads, dim):
+        raise ValueError(f"{name} must be a bfloat16 tensor [{tokens}][{heads}][{dim}], got {x.dtype} {tuple(x.shape)}")
+    stride = x.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
         raise ValueError(f"the heads of a token of {name} must be adjacent")
-    _on_current_device(name, x)
-    return x.data_ptr(), x.stride(0) if tokens > 1 else heads * dim
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
+    return x.data_ptr(), stride[0] if tokens > 1 else heads * dim
 
 
-def _pools(desc, k_pages, v_pages):
-    dtype = "uint8" if desc.kv_dtype == SPLITKV_FP8_E4M3 else "bfloat16"
-    rows = desc.num_pages_total * desc.num_kv_heads * desc.page_size
-    _tensor("k_pages", k_pages, dtype, rows * desc.qk_dim)
-    _tensor("v_pages", v_pages, dtype, rows * desc.v_dim)
-
-
-def _cache_index(desc, block_table, seq_lens):
-    _tensor("block_table", block_table, "int32", desc.batch * desc.max_pages_per_seq)
-    _tensor("seq_lens", seq_lens, "int32", desc.batch)
-
-
-def _state_numel(desc) -> int:
-    return desc.batch * desc.num_kv_heads * desc.max_pages_per_seq * desc.page_size
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
 
 
 class Rope:
@@ -393,44 +394,42 @@ def splitkv_append(desc: splitkv_desc_t, rope, positions, q, k, v, block_table, 
     """Rotates queries and keys of new tokens (``rope`` None: rotates nothing)
     and writes the keys and values into the pages.  ``n_tokens`` is needed only
     where ``k`` is an address."""
-    n = n_tokens if n_tokens is not None else (k.numel() // (desc.num_kv_heads * desc.qk_dim))
-    qp, qs = _token_rows("q", q, n, desc.num_q_heads, desc.qk_dim)
-    op, os_ = _token_rows("q_out", q_out, n, desc.num_q_heads, desc.qk_dim)
-    kp, ks = _token_rows("k", k, n, desc.num_kv_heads, desc.qk_dim)
-    vp, vs = _token_rows("v", v, n, desc.num_kv_heads, desc.v_dim)
-    _pools(desc, k_pages, v_pages)
-    _cache_index(desc, block_table, seq_lens)
-    _tensor("positions", positions, "int32", n * (rope.n_axes if rope is not None else 1))
-    _tensor("cu_tokens", cu_tokens, "int32", desc.batch + 1)
-    _tensor("key_weights", key_weights, "float32", _state_numel(desc))
-    _tensor("key_positions", key_positions, "int32", _state_numel(desc))
-    _tensor("k_scale", k_scale, "float32", desc.num_kv_heads)
-    _tensor("v_scale", v_scale, "float32", desc.num_kv_heads)
-    _tensor("status", status, "int32", 1)
-    _check(_lib.splitkv_append(ctypes.byref(desc), None if rope is None else rope.handle, n,
-                               _ptr(cu_tokens), _ptr(positions), qp, qs, kp, ks, vp, vs,
-                               _ptr(block_table), _ptr(seq_lens), kv_scale, _ptr(k_scale),
-                               _ptr(v_scale), op, os_, _ptr(k_pages), _ptr(v_pages),
-                               _ptr(key_weights), _ptr(key_positions), _ptr(status), _stream(stream)))
+    z, dev = _sizes(bytes(desc)), _current_device()
+    i32, f32 = z.torch.int32, z.torch.float32
+    n = n_tokens if n_tokens is not None else k.numel() // z.k_token if k is not None else 0
+    qp, qs = _token_rows("q", q, n, z.heads, z.k_dim, z, dev)
+    op, os_ = _token_rows("q_out", q_out, n, z.heads, z.k_dim, z, dev)
+    kp, ks = _token_rows("k", k, n, z.kv_heads, z.k_dim, z, dev)
+    vp, vs = _token_rows("v", v, n, z.kv_heads, z.v_dim, z, dev)
+    _check(_lib.splitkv_append(
+        ctypes.byref(desc), None if rope is None else rope.handle, n,
+        _addr("cu_tokens", cu_tokens, i32, z.batch + 1, dev),
+        _addr("positions", positions, i32, n * (rope.n_axes if rope is not None else 1), dev),
+        qp, qs, kp, ks, vp, vs, _addr("block_table", block_table, i32, z.table, dev),
+        _addr("seq_lens", seq_lens, i32, z.batch, dev), kv_scale,
+        _addr("k_scale", k_scale, f32, z.kv_heads, dev), _addr("v_scale", v_scale, f32, z.kv_heads, dev),
+        op, os_, _addr("k_pages", k_pages, z.pool_dtype, z.k_pool, dev),
+        _addr("v_pages", v_pages, z.pool_dtype, z.v_pool, dev),
+        _addr("key_weights", key_weights, f32, z.state, dev),
+        _addr("key_positions", key_positions, i32, z.state, dev), _addr("status", status, i32, 1, dev),
+        _stream(stream)))
 
 
 def splitkv_key_weights(desc: splitkv_desc_t, q, k_pages, block_table, seq_lens, lse, scale: float,
                         kv_scale: float, decay: float, weights_in, weights_out, k_scale=None,
                         status=None, stream=None):
     """Adds the attention every cached key got from ``q`` (``lse`` from the decode call)."""
-    rows = desc.batch * desc.q_tokens * desc.num_q_heads
-    _tensor("q", q, "bfloat16", rows * desc.qk_dim)
-    _pools(desc, k_pages, None)
-    _cache_index(desc, block_table, seq_lens)
-    _tensor("lse", lse, "float32", rows)
-    _tensor("weights_in", weights_in, "float32", _state_numel(desc))
-    _tensor("weights_out", weights_out, "float32", _state_numel(desc))
-    _tensor("k_scale", k_scale, "float32", desc.num_kv_heads)
-    _tensor("status", status, "int32", 1)
-    _check(_lib.splitkv_key_weights(ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(block_table),
-                                    _ptr(seq_lens), _ptr(lse), scale, kv_scale, _ptr(k_scale), decay,
-                                    _ptr(weights_in), _ptr(weights_out), _ptr(status),
-                                    _stream(stream)))
+    z, dev = _sizes(bytes(desc)), _current_device()
+    i32, f32 = z.torch.int32, z.torch.float32
+    _check(_lib.splitkv_key_weights(
+        ctypes.byref(desc), _addr("q", q, z.torch.bfloat16, z.q_rows * z.k_dim, dev),
+        _addr("k_pages", k_pages, z.pool_dtype, z.k_pool, dev),
+        _addr("block_table", block_table, i32, z.table, dev), _addr("seq_lens", seq_lens, i32, z.batch, dev),
+        _addr("lse", lse, f32, z.q_rows, dev), scale, kv_scale,
+        _addr("k_scale", k_scale, f32, z.kv_heads, dev), decay,
+        _addr("weights_in", weights_in, f32, z.state, dev),
+        _addr("weights_out", weights_out, f32, z.state, dev), _addr("status", status, i32, 1, dev),
+        _stream(stream)))
 
 
 def splitkv_evict_workspace_size(desc: splitkv_desc_t, budget: int) -> int:
@@ -441,22 +440,21 @@ def splitkv_evict(desc: splitkv_desc_t, budget: int, sink: int, recent: int, k_p
                   block_table, seq_lens, weights_in, positions_in, weights_out, positions_out,
                   seq_lens_out, workspace, workspace_bytes=None, status=None, stream=None):
     """Cuts every sequence to at most ``budget`` keys per KV head, the best by weight."""
-    _pools(desc, k_pages, v_pages)
-    _cache_index(desc, block_table, seq_lens)
-    n = _state_numel(desc)
-    _tensor("weights_in", weights_in, "float32", n)
-    _tensor("weights_out", weights_out, "float32", n)
-    _tensor("positions_in", positions_in, "int32", n)
-    _tensor("positions_out", positions_out, "int32", n)
-    _tensor("seq_lens_out", seq_lens_out, "int32", desc.batch)
-    _tensor("workspace", workspace, "uint8", 0)
-    _tensor("status", status, "int32", 1)
+    z, dev = _sizes(bytes(desc)), _current_device()
+    i32, f32 = z.torch.int32, z.torch.float32
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel()
-    _check(_lib.splitkv_evict(ctypes.byref(desc), budget, sink, recent, _ptr(k_pages), _ptr(v_pages),
-                              _ptr(block_table), _ptr(seq_lens), _ptr(weights_in), _ptr(positions_in),
-                              _ptr(weights_out), _ptr(positions_out), _ptr(seq_lens_out),
-                              _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)))
+    _check(_lib.splitkv_evict(
+        ctypes.byref(desc), budget, sink, recent, _addr("k_pages", k_pages, z.pool_dtype, z.k_pool, dev),
+        _addr("v_pages", v_pages, z.pool_dtype, z.v_pool, dev),
+        _addr("block_table", block_table, i32, z.table, dev), _addr("seq_lens", seq_lens, i32, z.batch, dev),
+        _addr("weights_in", weights_in, f32, z.state, dev),
+        _addr("positions_in", positions_in, i32, z.state, dev),
+        _addr("weights_out", weights_out, f32, z.state, dev),
+        _addr("positions_out", positions_out, i32, z.state, dev),
+        _addr("seq_lens_out", seq_lens_out, i32, z.batch, dev),
+        _addr("workspace", workspace, z.torch.uint8, 0, dev), workspace_bytes,
+        _addr("status", status, i32, 1, dev), _stream(stream)))
 
 
 def splitkv_last_error() -> str:

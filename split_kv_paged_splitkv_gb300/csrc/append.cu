@@ -35,9 +35,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                    // units of a thread in flight
-constexpr int kUnits = kThreads * kUnroll;    // units a CTA covers
-constexpr int kMaxTok = 32;                   // tokens of a CTA, at most
+constexpr int kMaxTok = 32;  // tokens of a CTA, at most
 
 struct Token {
   int32_t b, slot, page, in_page;  // b < 0: padding; page < 0: no key is stored
@@ -64,23 +62,24 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16(f[6], f[7]));
 }
 
-// The sequence whose tokens [cu[b], cu[b + 1]) hold n, or -1.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int n) {
-  if (n < cu[0] || n >= cu[batch]) return -1;
-  int lo = 0, hi = batch;  // cu[lo] <= n < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= n) lo = mid; else hi = mid;
+// The sequence whose tokens [cu[b], cu[b + 1]) hold n, or -1 (by a warp).
+__device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int n, int lane) {
+  int ended = 0;  // sequences whose tokens end at or before n
+  for (int b0 = 0; b0 < batch; b0 += 32) {
+    const int b = b0 + lane;
+    ended += __popc(__ballot_sync(kFull, b < batch && cu[b + 1] <= n));
   }
-  return lo;
+  return ended < batch && cu[0] <= n ? ended : -1;
 }
 
-template <int DK, int DV, bool FP8>
+// U: units of a thread in flight.
+template <int DK, int DV, bool FP8, int U>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a,
                                                           int tok_per_cta) {
   constexpr int UK = DK / 16, UV = DV / 16;  // units of a q or k row, of a v row
   __shared__ Token tok[kMaxTok];
   __shared__ float2 cs[kMaxTok * kMaxRotPairs];  // (cos, sin) of each pair
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   launch_dependents();
   wait_prerequisites();
@@ -88,60 +87,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int n0 = blockIdx.x * tok_per_cta;
   const int ntok = min(tok_per_cta, a.n_tokens - n0);
   const int half = a.rope.rot_dim / 2;
-  const int per_tok = (a.q ? a.Hq * UK : 0) + a.Hkv * (UK + (a.v ? UV : 0));
-  const int total = ntok * per_tok;
-  const int64_t cap = int64_t(a.max_pages) * a.P;
-
-  // where the tokens' keys go, and their sines and cosines
-  for (int i = threadIdx.x; i < ntok; i += kThreads) {
-    const int n = n0 + i;
-    Token t;
-    t.b = a.cu ? find_seq(a.cu, a.batch, n) : n / a.T;
-    t.page = -1;
-    t.slot = t.in_page = 0;
-    if (t.b >= 0) {
-      const int64_t end = a.cu ? a.cu[t.b + 1] : int64_t(t.b + 1) * a.T;
-      const int64_t slot = int64_t(a.seq_lens[t.b]) - (end - n);
-      int err = 0;
-      if (slot < 0 || slot >= cap) {
-        err = SPLITKV_DEVERR_SEQLEN;
-      } else {
-        const int lp = int(slot) / a.P;
-        const int ph = a.block_table[size_t(t.b) * a.max_pages + lp];
-        if (ph < 0 || ph >= a.num_pages) {
-          err = SPLITKV_DEVERR_PAGE;
-        } else {
-          t.page = ph;
-          t.slot = int(slot);
-          t.in_page = int(slot) - lp * a.P;
-        }
-      }
-      if (err && a.status && blockIdx.y == 0) atomicOr(a.status, err);
-    }
-    tok[i] = t;
-  }
-  for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
-    const int t = i / half, p = i - t * half;
-    const int64_t pos = a.positions[size_t(a.rope.axis[p]) * a.n_tokens + n0 + t];
-    const uint64_t phase = uint64_t(pos) * a.rope.turns[p];
-    float s, c;
-    sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s, &c);
-    cs[t * kMaxRotPairs + p] = make_float2(c, s);
-  }
-  __syncthreads();
-
-  // the state of the new keys
-  if (blockIdx.y == 0 && (a.key_weights || a.key_positions)) {
-    for (int i = threadIdx.x; i < ntok * a.Hkv; i += kThreads) {
-      const int t = i / a.Hkv, h = i - t * a.Hkv;
-      if (tok[t].page < 0) continue;
-      const size_t at = (size_t(tok[t].b) * a.Hkv + h) * cap + tok[t].slot;
-      if (a.key_weights) a.key_weights[at] = 0.f;
-      if (a.key_positions) a.key_positions[at] = a.positions[n0 + t];
-    }
-  }
-
   const int qu = a.q ? a.Hq * UK : 0, ku = a.Hkv * UK;
+  const int per_tok = qu + ku + (a.v ? a.Hkv * UV : 0);
+  const int total = ntok * per_tok;
   const int rot0 = a.rope.rot_offset / 8, rotc = a.rope.rot_dim / 8;  // rotated chunks
   const bool halves = a.rope.pairing == SPLITKV_ROPE_HALVES;
 
@@ -161,60 +109,104 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       c1 += c1 >= rot0 ? rotc : 0;
     }
   };
-
-  struct Unit {
-    uint4 x0, x1;
-    int t, row, c0, c1, kind;  // kind 0 q, 1 k, 2 v, -1 none
+  // Unit i of the CTA: kind 0 q, 1 k, 2 v; token, head row, chunks.
+  auto unit = [&](int i, int& kind, int& t, int& row, int& c0, int& c1) {
+    t = i / per_tok;
+    int u = i - t * per_tok;
+    kind = u < qu ? 0 : u < qu + ku ? 1 : 2;
+    if (kind < 2) {
+      u -= kind ? qu : 0;
+      row = u / UK;
+      chunks(u - row * UK, c0, c1);
+    } else {
+      u -= qu + ku;
+      row = u / UV;
+      c0 = 2 * (u - row * UV);
+      c1 = c0 + 1;
+    }
   };
 
-  // A CTA of slice y covers units y * kUnits + ... of its tokens' units.
-  for (int base = blockIdx.y * kUnits; base < total; base += gridDim.y * kUnits) {
-    Unit un[kUnroll];
+  bool ready = false;
+  for (int base = blockIdx.y * (U * kThreads); base < total || !ready; base += gridDim.y * (U * kThreads)) {
+    // The tokens' own rows first (those of padding are within the inputs
+    // too): they are in flight while the tokens' places are looked up.
+    uint4 x0[U], x1[U];
 #pragma unroll
-    for (int r = 0; r < kUnroll; ++r) {
+    for (int r = 0; r < U; ++r) {
       const int i = base + r * kThreads + threadIdx.x;
-      un[r].kind = -1;
       if (i >= total) continue;
-      const int t = i / per_tok;
-      int u = i - t * per_tok;
-      if (tok[t].b < 0) continue;
-      const __nv_bfloat16* src;
-      if (u < qu) {
-        un[r].kind = 0;
-        un[r].row = u / UK;
-        u -= un[r].row * UK;
-        chunks(u, un[r].c0, un[r].c1);
-        src = static_cast<const __nv_bfloat16*>(a.q) + int64_t(n0 + t) * a.q_stride + un[r].row * DK;
-      } else if (tok[t].page < 0) {
-        continue;
-      } else if (u < qu + ku) {
-        u -= qu;
-        un[r].kind = 1;
-        un[r].row = u / UK;
-        u -= un[r].row * UK;
-        chunks(u, un[r].c0, un[r].c1);
-        src = static_cast<const __nv_bfloat16*>(a.k) + int64_t(n0 + t) * a.k_stride + un[r].row * DK;
-      } else {
-        u -= qu + ku;
-        un[r].kind = 2;
-        un[r].row = u / UV;
-        u -= un[r].row * UV;
-        un[r].c0 = 2 * u;
-        un[r].c1 = 2 * u + 1;
-        src = static_cast<const __nv_bfloat16*>(a.v) + int64_t(n0 + t) * a.v_stride + un[r].row * DV;
+      int kind, t, row, c0, c1;
+      unit(i, kind, t, row, c0, c1);
+      const void* from = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+      const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(from) +
+                                                        int64_t(n0 + t) * stride + row * (kind < 2 ? DK : DV));
+      x0[r] = src[c0];
+      x1[r] = src[c1];
+    }
+    if (!ready) {
+      ready = true;
+      // where the tokens' keys go, and their sines and cosines
+      for (int i = warp; i < ntok; i += kThreads / 32) {
+        const int n = n0 + i;
+        Token t;
+        t.b = a.cu ? find_seq(a.cu, a.batch, n, lane) : n / a.T;
+        t.page = -1;
+        t.slot = t.in_page = 0;
+        if (t.b >= 0) {
+          const int64_t cap = int64_t(a.max_pages) * a.P;
+          const int64_t end = a.cu ? a.cu[t.b + 1] : int64_t(t.b + 1) * a.T;
+          const int64_t slot = int64_t(a.seq_lens[t.b]) - (end - n);
+          int err = 0;
+          if (slot < 0 || slot >= cap) {
+            err = SPLITKV_DEVERR_SEQLEN;
+          } else {
+            const int lp = int(slot) / a.P;
+            const int ph = a.block_table[size_t(t.b) * a.max_pages + lp];
+            if (ph < 0 || ph >= a.num_pages) {
+              err = SPLITKV_DEVERR_PAGE;
+            } else {
+              t.page = ph;
+              t.slot = int(slot);
+              t.in_page = int(slot) - lp * a.P;
+            }
+          }
+          if (err && lane == 0 && a.status && blockIdx.y == 0) atomicOr(a.status, err);
+        }
+        if (lane == 0) tok[i] = t;
       }
-      un[r].t = t;
-      un[r].x0 = reinterpret_cast<const uint4*>(src)[un[r].c0];
-      un[r].x1 = reinterpret_cast<const uint4*>(src)[un[r].c1];
+      for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
+        const int t = i / half, p = i - t * half;
+        const int64_t pos = a.positions[size_t(a.rope.axis[p]) * a.n_tokens + n0 + t];
+        const uint64_t phase = uint64_t(pos) * a.rope.turns[p];
+        float s, c;
+        sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s, &c);
+        cs[t * kMaxRotPairs + p] = make_float2(c, s);
+      }
+      __syncthreads();
+      // the state of the new keys
+      if (blockIdx.y == 0 && (a.key_weights || a.key_positions)) {
+        for (int i = threadIdx.x; i < ntok * a.Hkv; i += kThreads) {
+          const int t = i / a.Hkv, h = i - t * a.Hkv;
+          if (tok[t].page < 0) continue;
+          const size_t at = (size_t(tok[t].b) * a.Hkv + h) * (size_t(a.max_pages) * a.P) + tok[t].slot;
+          if (a.key_weights) a.key_weights[at] = 0.f;
+          if (a.key_positions) a.key_positions[at] = a.positions[n0 + t];
+        }
+      }
     }
 #pragma unroll
-    for (int r = 0; r < kUnroll; ++r) {
-      if (un[r].kind < 0) continue;
-      const int c0 = un[r].c0, c1 = un[r].c1, t = un[r].t;
+    for (int r = 0; r < U; ++r) {
+      const int i = base + r * kThreads + threadIdx.x;
+      if (i >= total) continue;
+      int kind, t, row, c0, c1;
+      unit(i, kind, t, row, c0, c1);
+      const Token tk = tok[t];
+      if (tk.b < 0 || (kind > 0 && tk.page < 0)) continue;
       float f0[8], f1[8];
-      unpack8(un[r].x0, f0);
-      unpack8(un[r].x1, f1);
-      if (un[r].kind < 2 && rotc) {
+      unpack8(x0[r], f0);
+      unpack8(x1[r], f1);
+      if (kind < 2 && rotc) {
         const float2* w = cs + t * kMaxRotPairs;
         if (halves) {
           if (c0 >= rot0 && c0 < rot0 + rotc) {  // then c1 is the other half of the pairs
@@ -241,23 +233,21 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
           turn(f1, c1);
         }
       }
-      if (un[r].kind == 0) {
+      if (kind == 0) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) +
-                                              int64_t(n0 + t) * a.q_out_stride + un[r].row * DK);
+                                              int64_t(n0 + t) * a.q_out_stride + row * DK);
         dst[c0] = pack8(f0);
         dst[c1] = pack8(f1);
         continue;
       }
-      const Token tk = tok[t];
-      const int h = un[r].row;
-      const size_t line = a.nhd ? (size_t(tk.page) * a.P + tk.in_page) * a.Hkv + h
-                                : (size_t(tk.page) * a.Hkv + h) * a.P + tk.in_page;
-      const bool is_k = un[r].kind == 1;
+      const size_t line = a.nhd ? (size_t(tk.page) * a.P + tk.in_page) * a.Hkv + row
+                                : (size_t(tk.page) * a.Hkv + row) * a.P + tk.in_page;
+      const bool is_k = kind == 1;
       const int D = is_k ? DK : DV;
       void* pool = is_k ? a.k_pages : a.v_pages;
       if (FP8) {
         const float* per_head = is_k ? a.k_scale : a.v_scale;
-        const float sc = per_head ? per_head[h] : a.kv_scale;
+        const float sc = per_head ? per_head[row] : a.kv_scale;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           f0[e] = __fdiv_rn(f0[e], sc);
@@ -268,18 +258,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         dst[c1] = make_uint2(pack_e4m3x4(f1), pack_e4m3x4(f1 + 4));
       } else {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + line * D);
-        dst[c0] = is_k ? pack8(f0) : un[r].x0;
-        dst[c1] = is_k ? pack8(f1) : un[r].x1;
+        dst[c0] = is_k ? pack8(f0) : x0[r];
+        dst[c1] = is_k ? pack8(f1) : x1[r];
       }
     }
   }
 }
 
-template <int DK, int DV, bool FP8>
-cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t s) {
-  const int per_tok = (a.q ? a.Hq * DK / 16 : 0) + a.Hkv * (DK / 16 + (a.v ? DV / 16 : 0));
-  const int tpc = per_tok >= kUnits ? 1 : min(kMaxTok, kUnits / per_tok);
-  const int64_t slices = (int64_t(per_tok) * tpc + kUnits - 1) / kUnits;
+template <int DK, int DV, bool FP8, int U>
+cudaError_t launch_append_u(const AppendArgs& a, int per_tok, cudaStream_t s) {
+  constexpr int units = U * kThreads;  // a CTA's
+  const int tpc = per_tok >= units ? 1 : min(kMaxTok, units / per_tok);
+  const int64_t slices = (int64_t(per_tok) * tpc + units - 1) / units;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.n_tokens + tpc - 1) / tpc, unsigned(slices > 65535 ? 65535 : slices), 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -289,7 +279,18 @@ cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t s) {
   la[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = la;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<DK, DV, FP8>, a, tpc);
+  return cudaLaunchKernelEx(&cfg, append_kernel<DK, DV, FP8, U>, a, tpc);
+}
+
+// A call of few tokens takes one unit per thread, to use more of the GPU's
+// SMs; a long one four, for bytes in flight.
+constexpr int64_t kFewUnits = 1 << 17;
+
+template <int DK, int DV, bool FP8>
+cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t s) {
+  const int per_tok = (a.q ? a.Hq * (DK / 16) : 0) + a.Hkv * (DK / 16 + (a.v ? DV / 16 : 0));
+  return int64_t(per_tok) * a.n_tokens <= kFewUnits ? launch_append_u<DK, DV, FP8, 1>(a, per_tok, s)
+                                                    : launch_append_u<DK, DV, FP8, 4>(a, per_tok, s);
 }
 
 }  // namespace

@@ -290,12 +290,12 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
     return fail(SPLITKV_EINVAL, "positions_in and positions_out must both be given or both be NULL");
   if ((sink > 0 || recent > 0) && !positions_in)
     return fail(SPLITKV_EINVAL, "sink and recent need positions");
-  if (misaligned(k_pages, 16) || misaligned(v_pages, 16))
-    return fail(SPLITKV_EINVAL, "the pages must be 16-byte aligned");
-  const void* words[] = {block_table, seq_lens, weights_in, positions_in, weights_out, positions_out,
-                         seq_lens_out, status};
+  const void* wide[] = {k_pages, v_pages, weights_in, positions_in, weights_out, positions_out};
+  for (const void* p : wide)
+    if (misaligned(p, 16)) return fail(SPLITKV_EINVAL, "the pages and state arrays must be 16-byte aligned");
+  const void* words[] = {block_table, seq_lens, seq_lens_out, status};
   for (const void* p : words)
-    if (misaligned(p, 4)) return fail(SPLITKV_EINVAL, "index and state arrays must be 4-byte aligned");
+    if (misaligned(p, 4)) return fail(SPLITKV_EINVAL, "index arrays must be 4-byte aligned");
   const size_t sb = state_bytes(d), lb = size_t(d.batch) * 4;
   if (half_shared(weights_in, weights_out, sb) || half_shared(positions_in, positions_out, sb) ||
       half_shared(seq_lens, seq_lens_out, lb))

@@ -17,11 +17,10 @@
 // a key is a 32-bit number (protected in the top bit, then the bits of the
 // weight, whose order is that of non-negative floats), its n-th largest value
 // is found by radix selection in three digits over histograms that the
-// cluster's CTAs read from one another's shared memory; then ballots and
-// prefix sums give every freed slot and every moving key its place in the
+// cluster's CTAs add up in the shared memory of the first; then prefix sums give every freed slot and every moving key its place in the
 // list.  move_kernel copies the rows, persistent over the groups' lists.
-// Bound: 8 bytes of state per key read once (the ranks stay in shared
-// memory), 8 written per kept key, each moved row read and written once.
+// Bound: 8 bytes of state per key read once (the ranks stay in
+// shared memory), 8 written per kept key, each moved row read and written once.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -34,42 +33,61 @@ namespace {
 using namespace ptx;
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBatch = 4;              // 16-byte vectors a lane loads at a time
 constexpr int kBins = 2048;            // 11-bit digits: bits 31-21, 20-10, and 9-0
 constexpr int kMaxCluster = 8;
-constexpr int kRankCap = 40960;        // ranks a CTA keeps in shared memory (160 KB)
+constexpr int kRankCap = 49152;        // ranks a CTA can keep in shared memory (192 KB)
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBatch = 32;         // moves a CTA takes at a time
+constexpr int kMoveBatch = 64;         // moves a CTA takes at a time
+constexpr int kMoveUnroll = 8;         // 16-byte pieces a thread has in flight
+constexpr int kMoveGroups = 1024;      // groups whose prefix a CTA holds at a time
 
 struct SelShared {
-  uint32_t hist[2][kBins];  // by turns, so that one cluster barrier per digit suffices
+  uint32_t hist[kBins];      // this CTA's
+  uint32_t total[3][kBins];  // the cluster's, a digit each, in its first CTA
   int32_t warp_sum[kSelWarps];
-  int32_t pub[4];   // read by the cluster: largest position, equals, holes, movers
-  int32_t found[2]; // digit, keys above it
+  int32_t pub[4];    // read by the cluster: largest position, equals, holes, movers
+  int32_t found[3];  // digit, keys above it, keys of it
 };
 
-// Exclusive prefix sum of one int per warp; returns the block total.
-__device__ __forceinline__ int warp_prefix(int mine, int warp, int lane, int32_t* sums, int* before) {
-  __syncthreads();
+// Exclusive prefix over the CTA's warps of one value per warp; `total`
+// receives the sum.
+__device__ __forceinline__ int warps_prefix(int mine, int warp, int lane, int32_t* sums, int* total) {
+  __syncthreads();  // (sums may still be read from the call before)
   if (lane == 0) sums[warp] = mine;
   __syncthreads();
-  const int v = sums[lane];
+  const int v = lane < kSelWarps ? sums[lane] : 0;
   int x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x += y;
   }
-  *before = __shfl_sync(kFull, x - v, warp);
-  return __shfl_sync(kFull, x, 31);
+  *total = __shfl_sync(kFull, x, 31);
+  return __shfl_sync(kFull, x - v, warp);
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_constant__ EvictArgs a,
+// Sum over the lanes before this one of popcounts of 4-bit masks, in slot
+// order (lane, then bit); `total` receives the warp's.
+__device__ __forceinline__ int lanes_before(uint32_t bits, int lane, int* total) {
+  const unsigned under = (1u << lane) - 1;
+  int before = 0, all = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const unsigned m = __ballot_sync(kFull, bits >> e & 1);
+    before += __popc(m & under);
+    all += __popc(m);
+  }
+  *total = all;
+  return before;
+}
+
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ EvictArgs a,
                                                                 int rank_cap) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  SelShared& sh = *reinterpret_cast<SelShared*>(smem);
-  uint32_t* ranks = reinterpret_cast<uint32_t*>(smem + sizeof(SelShared));
+  extern __shared__ __align__(16) uint32_t ranks[];  // of this CTA's slots, if they fit
+  __shared__ SelShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = cluster.num_blocks(), cr = cluster.block_rank();
   const int group = blockIdx.x / nc;
@@ -88,186 +106,277 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
   const int32_t* pos = a.pos_in ? a.pos_in + size_t(group) * cap : nullptr;
   float* wo = a.w_out + size_t(group) * cap;
   int32_t* po = a.pos_out ? a.pos_out + size_t(group) * cap : nullptr;
-  const bool copy_w = wo != w, copy_p = po && po != pos;
+  const bool rank_pos = a.sink > 0 || a.recent > 0;
 
-  // this CTA's slots [lo, hi), this warp's [wlo, whi); multiples of 32
-  const int per = int(((int64_t(L) + nc - 1) / nc + 31) & ~int64_t(31));
+  // This CTA's slots [lo, hi) and this warp's [wlo, whi): multiples of 4, so
+  // that a lane takes four at a time (a row of the state is padded to 16).
+  const int per = int(((int64_t(L) + nc - 1) / nc + 3) & ~int64_t(3));
   const int lo = int(min(int64_t(L), int64_t(cr) * per)), hi = int(min(int64_t(L), int64_t(lo) + per));
-  const int seg = ((per + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int seg = ((per + kSelWarps - 1) / kSelWarps + 127) & ~127;
   const int wlo = int(min(int64_t(hi), int64_t(lo) + int64_t(warp) * seg));
   const int whi = int(min(int64_t(hi), int64_t(wlo) + seg));
+  const bool in_smem = per <= rank_cap;
+  const bool stay_all = L <= n;  // (the same for the whole cluster)
 
-  if (L <= n) {  // everything stays (the same for the whole cluster)
-    for (int j = lo + threadIdx.x; j < hi; j += kSelThreads) {
-      if (copy_w) wo[j] = w[j];
-      if (copy_p) po[j] = pos[j];
+  // ---- the state: the largest position, and what stays in its slot handed
+  // on (the move kernel fills the slots that are freed)
+  int newest = INT32_MIN;
+  if (!stay_all || wo != w || po != pos) {
+    for (int64_t j0 = wlo; j0 < whi; j0 += 128 * kBatch) {
+      uint4 x[kBatch];
+      int4 y[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t j = j0 + u * 128 + lane * 4;
+        if (j >= whi) continue;
+        x[u] = *reinterpret_cast<const uint4*>(w + j);
+        if (pos) y[u] = *reinterpret_cast<const int4*>(pos + j);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t j = j0 + u * 128 + lane * 4;
+        if (j >= whi) continue;
+        if (in_smem && !stay_all) *reinterpret_cast<uint4*>(ranks + (j - lo)) = x[u];
+        const int32_t ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+        if (pos) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < whi) newest = max(newest, ys[e]);
+        }
+        if (j + 4 <= n) {
+          if (wo != w) *reinterpret_cast<uint4*>(wo + j) = x[u];
+          if (po != pos) *reinterpret_cast<int4*>(po + j) = y[u];
+        } else if (j < n) {
+          const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < n) {
+              if (wo != w) wo[j + e] = __uint_as_float(xs[e]);
+              if (po != pos) po[j + e] = ys[e];
+            }
+        }
+      }
     }
+  }
+  if (stay_all) {
     if (cr == 0 && threadIdx.x == 0) {
       a.meta[2 * group] = 0;
       a.meta[2 * group + 1] = bad ? raw : n;
     }
     return;
   }
-
-  // ---- the largest position
-  int64_t newest = INT64_MIN;
-  if (pos) {
-    int m = INT32_MIN;
-    for (int j = lo + threadIdx.x; j < hi; j += kSelThreads) m = max(m, pos[j]);
-    m = __reduce_max_sync(kFull, m);
-    if (lane == 0) sh.warp_sum[warp] = m;
-    __syncthreads();
-    if (warp == 0) {
-      m = __reduce_max_sync(kFull, sh.warp_sum[lane]);
-      if (lane == 0) sh.pub[0] = m;
-    }
-    cluster.sync();
-    m = INT32_MIN;
-    for (int c = 0; c < nc; ++c) m = max(m, cluster.map_shared_rank(sh.pub, c)[0]);
-    newest = m;
+  if (cr == 0)
+    for (int i = threadIdx.x; i < 3 * kBins / 4; i += kSelThreads)
+      reinterpret_cast<uint4*>(sh.total)[i] = make_uint4(0, 0, 0, 0);
+  newest = __reduce_max_sync(kFull, newest);
+  if (lane == 0) sh.warp_sum[warp] = newest;
+  __syncthreads();
+  if (warp == 0) {
+    newest = __reduce_max_sync(kFull, sh.warp_sum[lane % kSelWarps]);
+    if (lane == 0) sh.pub[0] = newest;
   }
-  auto rank_at = [&](int j) -> uint32_t {
-    const float x = w[j];
-    uint32_t r = x > 0.f ? __float_as_uint(x) : 0u;  // negative and NaN count as 0
-    if (pos) {
-      const int32_t p = pos[j];
-      if (p < a.sink || int64_t(p) > newest - a.recent) r |= 0x80000000u;
-    }
-    return r;
+  cluster.sync();  // (the cleared totals, too)
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c)
+    if (c < nc) newest = max(newest, cluster.map_shared_rank(sh.pub, c)[0]);
+  const int64_t after = int64_t(newest) - a.recent;  // protected: positions beyond it
+
+  // The rank of a weight and its position; negative weights and NaN count as 0.
+  auto rank = [&](uint32_t bits, int32_t p) -> uint32_t {
+    uint32_t v = __uint_as_float(bits) > 0.f ? bits : 0u;
+    if (rank_pos && (p < a.sink || int64_t(p) > after)) v |= 0x80000000u;
+    return v;
   };
-  const bool kept_in_smem = per <= rank_cap;
-  auto rank_of = [&](int j) { return kept_in_smem ? ranks[j - lo] : rank_at(j); };
+  auto ranks_at = [&](int64_t j, uint4 x) -> uint4 {  // x: the weights of slots j .. j + 3
+    int4 y = make_int4(0, 0, 0, 0);
+    if (rank_pos) y = *reinterpret_cast<const int4*>(pos + j);
+    return make_uint4(rank(x.x, y.x), rank(x.y, y.y), rank(x.z, y.z), rank(x.w, y.w));
+  };
+  if (in_smem) {  // (a lane's own slots: no barrier)
+    for (int64_t j0 = wlo; j0 < whi; j0 += 128 * kBatch) {
+      uint4 x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t j = j0 + u * 128 + lane * 4;
+        if (j < whi) x[u] = ranks_at(j, *reinterpret_cast<const uint4*>(ranks + (j - lo)));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t j = j0 + u * 128 + lane * 4;
+        if (j < whi) *reinterpret_cast<uint4*>(ranks + (j - lo)) = x[u];
+      }
+    }
+  }
+  // Visits this warp's slots in order, four to a lane: body(first slot of the
+  // lane, ranks, mask of its slots that exist).
+  auto visit = [&](auto&& body) {
+    for (int64_t j0 = wlo; j0 < whi; j0 += 128) {
+      const int64_t j = j0 + lane * 4;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      uint32_t live = 0;
+      if (j < whi) {
+        x = in_smem ? *reinterpret_cast<const uint4*>(ranks + (j - lo))
+                    : ranks_at(j, *reinterpret_cast<const uint4*>(w + j));
+        live = whi - j >= 4 ? 15u : (1u << (whi - j)) - 1;
+      }
+      const uint32_t r[4] = {x.x, x.y, x.z, x.w};
+      body(j, r, live);
+    }
+  };
 
   // ---- radix selection: the n-th largest rank T, `above` keys beyond it
-  uint32_t prefix = 0;  // digits found so far
+  uint32_t T = 0;  // the digits found so far
   int above = 0;
   for (int d = 0; d < 3; ++d) {
-    uint32_t* hist = sh.hist[d & 1];
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
     const int bits = d == 2 ? 10 : 11, nbins = 1 << bits;
     const uint32_t mask = d == 0 ? 0u : ~0u << (shift + bits);
-    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    // Thread i has the kPer bins from nbins - kPer * (i + 1) on.
+    constexpr int kPer = kBins / kSelThreads;
+    const int low = nbins - kPer * (int(threadIdx.x) + 1);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 4)
+      if (low >= 0) *reinterpret_cast<uint4*>(sh.hist + low + e) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    for (int j0 = lo; j0 < hi; j0 += kSelThreads) {
-      const int j = j0 + threadIdx.x;
-      bool in = j < hi;
-      uint32_t r = 0;
-      if (in) {
-        if (d == 0) {
-          r = rank_at(j);
-          if (kept_in_smem) ranks[j - lo] = r;
-        } else {
-          r = rank_of(j);
-        }
-        in = (r & mask) == prefix;
+    visit([&](int64_t, const uint32_t (&r)[4], uint32_t live) {
+      // equal ranks throughout the warp's 128 slots: one addition
+      const uint32_t r0 = __shfl_sync(kFull, r[0], 0);
+      const bool same = live == 15u && r[0] == r0 && r[1] == r0 && r[2] == r0 && r[3] == r0;
+      if (__all_sync(kFull, same)) {
+        if (lane == 0 && (r0 & mask) == T) atomicAdd(sh.hist + ((r0 >> shift) & (nbins - 1)), 128u);
+        return;
       }
-      const int bin = in ? int((r >> shift) & (nbins - 1)) : -1;
-      // one bin for the whole warp (equal weights): one addition
-      const int lead = __shfl_sync(kFull, bin, 0);
-      if (__all_sync(kFull, bin == lead)) {
-        if (lane == 0 && lead >= 0) atomicAdd(hist + lead, 32u);
-      } else if (bin >= 0) {
-        atomicAdd(hist + bin, 1u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((live >> e & 1) && (r[e] & mask) == T) atomicAdd(sh.hist + ((r[e] >> shift) & (nbins - 1)), 1u);
+    });
+    __syncthreads();
+    // This CTA's counts (of few bins) into the first CTA's sums, which all read.
+    uint32_t* total = cluster.map_shared_rank(sh.total[d], 0);
+    if (low >= 0) {
+#pragma unroll
+      for (int e = 0; e < kPer; e += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(sh.hist + low + e);
+        if (v.x) atomicAdd(total + low + e, v.x);
+        if (v.y) atomicAdd(total + low + e + 1, v.y);
+        if (v.z) atomicAdd(total + low + e + 2, v.z);
+        if (v.w) atomicAdd(total + low + e + 3, v.w);
       }
     }
     cluster.sync();
-    // Every CTA sums the cluster's histograms from the top: thread i holds
-    // bins nbins - 1 - 2 i and the one below it.
-    const int top = nbins - 1 - 2 * int(threadIdx.x);
-    int c0 = 0, c1 = 0;
-    if (top >= 1) {
-      for (int c = 0; c < nc; ++c) {
-        const uint32_t* g = cluster.map_shared_rank(hist, c);
-        c0 += int(g[top]);
-        c1 += int(g[top - 1]);
-      }
+    int c[kPer], sum = 0;  // from the highest bin down
+#pragma unroll
+    for (int e = 0; e < kPer; e += 4) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (low >= 0) v = *reinterpret_cast<const uint4*>(total + low + e);
+      c[kPer - 1 - e] = int(v.x);
+      c[kPer - 2 - e] = int(v.y);
+      c[kPer - 3 - e] = int(v.z);
+      c[kPer - 4 - e] = int(v.w);
     }
-    const int sum = c0 + c1;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) sum += c[e];
     int x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kFull, x, o);
       if (lane >= o) x += y;
     }
-    int before;
-    warp_prefix(__shfl_sync(kFull, x, 31), warp, lane, sh.warp_sum, &before);
-    const int start = above + before + x - sum;  // keys above this thread's bins
-    if (top >= 1) {
-      if (start < n && start + c0 >= n) {
-        sh.found[0] = top;
+    int all;
+    int start = above + x - sum + warps_prefix(__shfl_sync(kFull, x, 31), warp, lane, sh.warp_sum, &all);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {  // `start`: keys above this bin
+      if (start < n && start + c[e] >= n) {
+        sh.found[0] = low + kPer - 1 - e;
         sh.found[1] = start;
-      } else if (start + c0 < n && start + sum >= n) {
-        sh.found[0] = top - 1;
-        sh.found[1] = start + c0;
+        sh.found[2] = c[e];
       }
+      start += c[e];
     }
     __syncthreads();
-    prefix |= uint32_t(sh.found[0]) << shift;
+    T |= uint32_t(sh.found[0]) << shift;
     above = sh.found[1];
-    __syncthreads();
   }
-  const uint32_t T = prefix;
   const int need = n - above;  // keys of rank T that stay: the lowest slots
+  const bool ties = need < sh.found[2];
 
-  // ---- equals before this warp's slots
-  int eq = 0;
-  for (int j0 = wlo; j0 < whi; j0 += 32) {
-    const int j = j0 + lane;
-    eq += __popc(__ballot_sync(kFull, j < whi && rank_of(j) == T));
+  // ---- keys of rank T before this warp's slots, if not all of them stay
+  int eq_at = 0;
+  if (ties) {
+    int eq = 0, eq_cta;
+    visit([&](int64_t, const uint32_t (&r)[4], uint32_t live) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) eq += (live >> e & 1) && r[e] == T;
+    });
+    eq_at = warps_prefix(__reduce_add_sync(kFull, eq), warp, lane, sh.warp_sum, &eq_cta);
+    if (threadIdx.x == 0) sh.pub[1] = eq_cta;
+    cluster.sync();
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (c < cr) eq_at += cluster.map_shared_rank(sh.pub, c)[1];
   }
-  int eq_before;
-  const int eq_cta = warp_prefix(eq, warp, lane, sh.warp_sum, &eq_before);
-  if (threadIdx.x == 0) sh.pub[1] = eq_cta;
-  cluster.sync();
-  for (int c = 0; c < cr; ++c) eq_before += cluster.map_shared_rank(sh.pub, c)[1];
 
-  // ---- what stays, 32 slots at a time
-  auto walk = [&](auto&& visit) {
-    int seen = eq_before;
-    for (int j0 = wlo; j0 < whi; j0 += 32) {
-      const int j = j0 + lane;
-      const uint32_t r = j < whi ? rank_of(j) : 0u;
-      const unsigned same = __ballot_sync(kFull, j < whi && r == T);
-      const bool stays = j < whi && (r > T || (r == T && seen + __popc(same & ((1u << lane) - 1)) < need));
-      seen += __popc(same);
-      visit(j, stays);
-    }
+  // ---- what is freed below slot n and what moves from behind it
+  auto changes = [&](auto&& body) {
+    int seen = eq_at;
+    visit([&](int64_t j, const uint32_t (&r)[4], uint32_t live) {
+      uint32_t stay = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) stay |= uint32_t(ties ? r[e] > T : r[e] >= T) << e;
+      if (ties) {
+        uint32_t same = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) same |= uint32_t(r[e] == T) << e;
+        same &= live;
+        int all, at = seen + lanes_before(same, lane, &all);
+        seen += all;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (same >> e & 1) stay |= uint32_t(at++ < need) << e;
+      }
+      const uint32_t below = j >= n ? 0u : n - j >= 4 ? 15u : (1u << (n - j)) - 1;
+      body(j, ~stay & below & live, stay & ~below & live);
+    });
   };
   int holes = 0, movers = 0;
-  walk([&](int j, bool stays) {
-    holes += __popc(__ballot_sync(kFull, j < min(whi, n) && !stays));
-    movers += __popc(__ballot_sync(kFull, j >= n && stays));
+  changes([&](int64_t, uint32_t hole, uint32_t mover) {
+    holes += __popc(hole);
+    movers += __popc(mover);
   });
-  int hole_at, mover_at;
-  const int holes_cta = warp_prefix(holes, warp, lane, sh.warp_sum, &hole_at);
-  const int movers_cta = warp_prefix(movers, warp, lane, sh.warp_sum, &mover_at);
+  int hole_at, mover_at, holes_cta, movers_cta;
+  hole_at = warps_prefix(__reduce_add_sync(kFull, holes), warp, lane, sh.warp_sum, &holes_cta);
+  mover_at = warps_prefix(__reduce_add_sync(kFull, movers), warp, lane, sh.warp_sum, &movers_cta);
   if (threadIdx.x == 0) {
     sh.pub[2] = holes_cta;
     sh.pub[3] = movers_cta;
   }
   cluster.sync();
   int moves = 0;
-  for (int c = 0; c < nc; ++c) {
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) {
+    if (c >= nc) break;
     const int32_t* p = cluster.map_shared_rank(sh.pub, c);
-    if (c < cr) {
-      hole_at += p[2];
-      mover_at += p[3];
-    }
-    moves += p[3];
+    const int ho = p[2], mo = p[3];
+    hole_at += c < cr ? ho : 0;
+    mover_at += c < cr ? mo : 0;
+    moves += mo;
   }
   int32_t* src = a.moves + size_t(group) * 2 * a.max_moves;
   int32_t* dst = src + a.max_moves;
-  walk([&](int j, bool stays) {
-    const bool hole = j < min(whi, n) && !stays, mover = j >= n && stays;
-    const unsigned hb = __ballot_sync(kFull, hole), mb = __ballot_sync(kFull, mover);
-    const unsigned under = (1u << lane) - 1;
-    if (hole) dst[hole_at + __popc(hb & under)] = j;
-    if (mover) src[mover_at + __popc(mb & under)] = j;
-    hole_at += __popc(hb);
-    mover_at += __popc(mb);
-    if (stays && j < n) {
-      if (copy_w) wo[j] = w[j];
-      if (copy_p) po[j] = pos[j];
+  changes([&](int64_t j, uint32_t hole, uint32_t mover) {
+    if (__any_sync(kFull, hole)) {
+      int all, at = hole_at + lanes_before(hole, lane, &all);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (hole >> e & 1) dst[at++] = int(j) + e;
+      hole_at += all;
+    }
+    if (__any_sync(kFull, mover)) {
+      int all, at = mover_at + lanes_before(mover, lane, &all);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (mover >> e & 1) src[at++] = int(j) + e;
+      mover_at += all;
     }
   });
   if (cr == 0 && threadIdx.x == 0) {
@@ -277,9 +386,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ int64_t from[kMoveBatch], to[kMoveBatch];  // rows of the pools; from < 0: not moved
+// The moves of all groups, in batches of kMoveBatch moves of one group; the
+// batches form one line of which a CTA takes every gridDim.x-th.  While the
+// rows of a batch are in flight, the first threads look up the next one's.
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ int32_t upto[kMoveGroups];  // batches of the groups up to and with this one
   __shared__ int32_t part[kMoveThreads / 32];
+  __shared__ int64_t from[2][kMoveBatch], to[2][kMoveBatch];  // rows of the pools; from < 0: not moved
+  __shared__ int32_t count[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
   wait_prerequisites();
@@ -287,13 +401,20 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   const size_t cap = size_t(a.max_pages) * a.P;
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.batch; b += kMoveThreads) a.lens_out[b] = a.meta[2 * (b * a.Hkv) + 1];
+  const int nk = a.k_row >> 4, np = nk + (a.v_row >> 4);  // 16-byte pieces of a key
 
-  // The batches of all groups form one line; this CTA takes every gridDim.x-th.
-  int64_t want = blockIdx.x, passed = 0;
-  for (int g0 = 0; g0 < groups; g0 += kMoveThreads) {
-    const int g = g0 + threadIdx.x;
-    const int mine = g < groups ? (a.meta[2 * g] + kMoveBatch - 1) / kMoveBatch : 0;
-    int x = mine;
+  int64_t passed = 0;  // batches of the groups before g0
+  for (int g0 = 0; g0 < groups; g0 += kMoveGroups) {
+    const int ng = min(kMoveGroups, groups - g0);
+    constexpr int PT = kMoveGroups / kMoveThreads;
+    int mine[PT], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int g = int(threadIdx.x) * PT + i;
+      mine[i] = g < ng ? (a.meta[2 * (g0 + g)] + kMoveBatch - 1) / kMoveBatch : 0;
+      sum += mine[i];
+    }
+    int x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kFull, x, o);
@@ -302,65 +423,97 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
     __syncthreads();
     if (lane == 31) part[warp] = x;
     __syncthreads();
-    int64_t upto = passed + x, all = passed;
+    int at = x - sum, all = 0;
+#pragma unroll
     for (int i = 0; i < kMoveThreads / 32; ++i) {
-      if (i < warp) upto += part[i];
+      if (i < warp) at += part[i];
       all += part[i];
     }
-    // the thread whose group holds batch `want` announces it
-    __shared__ int32_t cur[2];
-    while (want < all) {
-      if (want < upto && want >= upto - mine) {
-        cur[0] = g;
-        cur[1] = int(want - (upto - mine));
-      }
-      __syncthreads();
-      const int grp = cur[0], first = cur[1] * kMoveBatch;
-      const int b = grp / a.Hkv, h = grp - b * a.Hkv;
-      const int count = min(kMoveBatch, a.meta[2 * grp] - first);
-      if (threadIdx.x < count) {
-        const int32_t* src = a.moves + size_t(grp) * 2 * a.max_moves + first;
-        const int s = src[threadIdx.x], d = src[a.max_moves + threadIdx.x];
-        const int32_t* trow = a.block_table + size_t(b) * a.max_pages;
-        auto line = [&](int j) -> int64_t {
-          const int lp = j / a.P, ph = trow[lp], in = j - lp * a.P;
-          if (ph < 0 || ph >= a.num_pages) return -1;
-          return a.nhd ? (int64_t(ph) * a.P + in) * a.Hkv + h : (int64_t(ph) * a.Hkv + h) * a.P + in;
-        };
-        const int64_t ls = line(s), ld = line(d);
-        if ((ls < 0 || ld < 0) && a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
-        from[threadIdx.x] = ld < 0 ? -1 : ls;
-        to[threadIdx.x] = ld;
-        const size_t st = size_t(grp) * cap;
-        a.w_out[st + d] = a.w_in[st + s];
-        if (a.pos_out) a.pos_out[st + d] = a.pos_in[st + s];
-      }
-      __syncthreads();
-      const int nk = a.k_row >> 4, np = nk + (a.v_row >> 4);  // 16-byte pieces of a key
-      for (int p0 = threadIdx.x; p0 < count * np; p0 += 4 * kMoveThreads) {
-        uint4 x4[4];
-        uint4* out[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int p = p0 + r * kMoveThreads;
-          out[r] = nullptr;
-          if (p >= count * np) continue;
-          const int m = p / np, c = p - m * np;
-          if (from[m] < 0) continue;
-          const bool is_k = c < nk;
-          uint8_t* pool = static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages);
-          const int row = is_k ? a.k_row : a.v_row, off = (is_k ? c : c - nk) << 4;
-          x4[r] = *reinterpret_cast<const uint4*>(pool + from[m] * row + off);
-          out[r] = reinterpret_cast<uint4*>(pool + to[m] * row + off);
+    for (int i = 0; i < PT; ++i) {
+      at += mine[i];
+      upto[threadIdx.x * PT + i] = at;
+    }
+    __syncthreads();
+
+    // looks up batch `i` of this stretch of groups: kMoveBatch threads
+    auto look_up = [&](int i, int buf) {
+      if (threadIdx.x >= kMoveBatch || i >= all) return;
+      int l = 0, r = ng - 1;  // the first group whose batches reach past i
+      while (l < r) {
+        const int m = (l + r) >> 1;
+        if (upto[m] > i) r = m; else l = m + 1;
+      }
+      const int grp = g0 + l, begin = (i - (l ? upto[l - 1] : 0)) * kMoveBatch;
+      const int c = min(kMoveBatch, a.meta[2 * grp] - begin);
+      if (threadIdx.x == 0) count[buf] = c;
+      if (threadIdx.x >= c) return;
+      const int b = grp / a.Hkv, h = grp - b * a.Hkv;
+      const int32_t* src = a.moves + size_t(grp) * 2 * a.max_moves + begin;
+      const int s = src[threadIdx.x], d = src[a.max_moves + threadIdx.x];
+      const int32_t* trow = a.block_table + size_t(b) * a.max_pages;
+      const int sp = s / a.P, dp = d / a.P;
+      const int sph = trow[sp], dph = trow[dp];
+      const size_t st = size_t(grp) * cap;
+      a.w_out[st + d] = a.w_in[st + s];
+      if (a.pos_out) a.pos_out[st + d] = a.pos_in[st + s];
+      auto line = [&](int ph, int in) -> int64_t {
+        return a.nhd ? (int64_t(ph) * a.P + in) * a.Hkv + h : (int64_t(ph) * a.Hkv + h) * a.P + in;
+      };
+      const bool ok = sph >= 0 && sph < a.num_pages && dph >= 0 && dph < a.num_pages;
+      if (!ok && a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
+      from[buf][threadIdx.x] = ok ? line(sph, s - sp * a.P) : -1;
+      to[buf][threadIdx.x] = ok ? line(dph, d - dp * a.P) : 0;
+    };
+
+    int64_t skip = (int64_t(blockIdx.x) - passed) % int64_t(gridDim.x);
+    int i = int(skip < 0 ? skip + gridDim.x : skip);
+    int buf = 0;
+    look_up(i, buf);
+    __syncthreads();
+    for (; i < all; i += gridDim.x, buf ^= 1) {
+      const int total = count[buf] * np;
+      bool looked = false;
+      for (int p0 = threadIdx.x; p0 < total || !looked; p0 += kMoveUnroll * kMoveThreads) {
+        uint4 x4[kMoveUnroll];
+        // piece u of this pass: its move, which pool, its byte offset in the row
+        auto piece = [&](int u, int& m, bool& is_k) -> size_t {
+          const int p = p0 + u * kMoveThreads;
+          m = p / np;
+          const int c = p - m * np;
+          is_k = c < nk;
+          return size_t(is_k ? c : c - nk) << 4;
+        };
+#pragma unroll
+        for (int u = 0; u < kMoveUnroll; ++u) {
+          if (p0 + u * kMoveThreads >= total) break;
+          bool is_k;
+          int m;
+          const size_t off = piece(u, m, is_k);
+          const int64_t line = from[buf][m];
+          if (line < 0) continue;
+          x4[u] = *reinterpret_cast<const uint4*>(static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages) +
+                                                  line * (is_k ? a.k_row : a.v_row) + off);
+        }
+        if (!looked) {
+          look_up(i + int(gridDim.x), buf ^ 1);
+          looked = true;
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (out[r]) *out[r] = x4[r];
+        for (int u = 0; u < kMoveUnroll; ++u) {
+          if (p0 + u * kMoveThreads >= total) break;
+          bool is_k;
+          int m;
+          const size_t off = piece(u, m, is_k);
+          if (from[buf][m] < 0) continue;
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages) +
+                                    to[buf][m] * (is_k ? a.k_row : a.v_row) + off) = x4[u];
+        }
       }
       __syncthreads();
-      want += gridDim.x;
     }
-    passed = all;
+    passed += all;
+    __syncthreads();
   }
 }
 
@@ -370,14 +523,21 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t cap = int64_t(a.max_pages) * a.P;
   const int groups = a.batch * a.Hkv;
-  // CTAs per (sequence, head): one for each 8192 slots of capacity, up to 8.
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // CTAs per (sequence, head): one for each 512 slots of capacity while the
+  // groups do not fill the GPU (four CTAs per SM), and one for each 16,384
+  // slots in any case (64 KB of ranks, so that CTAs share an SM).
   int nc = 1;
-  while (nc < kMaxCluster && cap > int64_t(nc) * 8192) nc *= 2;
-  const int64_t per = ((cap + nc - 1) / nc + 31) & ~int64_t(31);
-  const int rank_cap = per <= kRankCap ? int(per) : kRankCap;
-  const int smem = int(sizeof(SelShared)) + rank_cap * 4;
-  static cudaError_t attr = cudaFuncSetAttribute(
-      select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(SelShared)) + kRankCap * 4);
+  while (nc < kMaxCluster && ((cap > int64_t(nc) * 512 && int64_t(groups) * nc * 2 <= int64_t(sms) * 4) ||
+                              cap > int64_t(nc) * 16384))
+    nc *= 2;
+  const int64_t per = ((cap + nc - 1) / nc + 3) & ~int64_t(3);
+  const int rank_cap = int(per <= kRankCap ? per : kRankCap);
+  static cudaError_t attr =
+      cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRankCap * 4);
   if (attr != cudaSuccess) return attr;
 
   cudaLaunchAttribute la[2];
@@ -389,19 +549,15 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(groups) * nc, 1, 1);
   cfg.blockDim = dim3(kSelThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = size_t(rank_cap) * 4;
   cfg.stream = s;
   cfg.attrs = la;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, a, rank_cap);
+  e = cudaLaunchKernelEx(&cfg, select_kernel, a, rank_cap);
   if (e != cudaSuccess) return e;
 
-  int dev = 0, sms = 0;
-  e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const int64_t most = int64_t(groups) * ((a.max_moves + kMoveBatch - 1) / kMoveBatch);
-  const int64_t grid = most < int64_t(sms) * 8 ? (most > 0 ? most : 1) : int64_t(sms) * 8;
+  const int64_t grid = most < int64_t(sms) * 4 ? (most > 0 ? most : 1) : int64_t(sms) * 4;
   cudaLaunchConfig_t mv = {};
   mv.gridDim = dim3(unsigned(grid), 1, 1);
   mv.blockDim = dim3(kMoveThreads, 1, 1);
