@@ -38,11 +38,85 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBatch = 4;              // 16-byte vectors a lane loads at a time
 constexpr int kBins = 2048;            // 11-bit digits: bits 31-21, 20-10, and 9-0
 constexpr int kMaxCluster = 8;
-constexpr int kRankCap = 49152;        // ranks a CTA can keep in shared memory (192 KB)
+constexpr int kRankCap = 46080;        // ranks a CTA can keep in shared memory (180 KB)
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 64;         // moves a CTA takes at a time
 constexpr int kMoveUnroll = 8;         // 16-byte pieces a thread has in flight
 constexpr int kMoveGroups = 1024;      // groups whose prefix a CTA holds at a time
+
+// Rows of the pools that a batch of moves reads and writes.
+template <int N>
+struct Rows {
+  int64_t from[N], to[N];  // from < 0: not moved
+};
+
+// Thread m < count looks up move `begin + m` of a group and moves its state.
+template <int N>
+__device__ __forceinline__ void look_up(const EvictArgs& a, int grp, int begin, int count, Rows<N>& rows) {
+  if (int(threadIdx.x) >= count) return;
+  const int b = grp / a.Hkv, h = grp - b * a.Hkv;
+  const int32_t* src = a.moves + size_t(grp) * 2 * a.max_moves + begin;
+  const int s = src[threadIdx.x], d = src[a.max_moves + threadIdx.x];
+  const int32_t* trow = a.block_table + size_t(b) * a.max_pages;
+  const int sp = s / a.P, dp = d / a.P;
+  const int sph = trow[sp], dph = trow[dp];
+  const size_t st = size_t(grp) * (size_t(a.max_pages) * a.P);
+  a.w_out[st + d] = a.w_in[st + s];
+  if (a.pos_out) a.pos_out[st + d] = a.pos_in[st + s];
+  auto line = [&](int ph, int in) -> int64_t {
+    return a.nhd ? (int64_t(ph) * a.P + in) * a.Hkv + h : (int64_t(ph) * a.Hkv + h) * a.P + in;
+  };
+  const bool ok = sph >= 0 && sph < a.num_pages && dph >= 0 && dph < a.num_pages;
+  if (!ok && a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
+  rows.from[threadIdx.x] = ok ? line(sph, s - sp * a.P) : -1;
+  rows.to[threadIdx.x] = ok ? line(dph, d - dp * a.P) : 0;
+}
+
+// NT threads copy the rows of a batch; `meanwhile` runs once with the first
+// rows in flight.
+template <int NT, int N, class F>
+__device__ __forceinline__ void copy_rows(const EvictArgs& a, const Rows<N>& rows, int count, F&& meanwhile) {
+  const int nk = a.k_row >> 4, np = nk + (a.v_row >> 4);  // 16-byte pieces of a key
+  const int total = count * np;
+  bool met = false;
+#pragma unroll 1
+  for (int p0 = threadIdx.x; p0 < total || !met; p0 += kMoveUnroll * NT) {
+    uint4 x[kMoveUnroll];
+    // piece u of this pass: its move, which pool, its byte offset in the row
+    auto piece = [&](int u, int& m, bool& is_k) -> size_t {
+      const int p = p0 + u * NT;
+      m = p / np;
+      const int c = p - m * np;
+      is_k = c < nk;
+      return size_t(is_k ? c : c - nk) << 4;
+    };
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      if (p0 + u * NT >= total) break;
+      bool is_k;
+      int m;
+      const size_t off = piece(u, m, is_k);
+      const int64_t line = rows.from[m];
+      if (line < 0) continue;
+      x[u] = *reinterpret_cast<const uint4*>(static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages) +
+                                             line * (is_k ? a.k_row : a.v_row) + off);
+    }
+    if (!met) {
+      meanwhile();
+      met = true;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      if (p0 + u * NT >= total) break;
+      bool is_k;
+      int m;
+      const size_t off = piece(u, m, is_k);
+      if (rows.from[m] < 0) continue;
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages) +
+                                rows.to[m] * (is_k ? a.k_row : a.v_row) + off) = x[u];
+    }
+  }
+}
 
 struct SelShared {
   uint32_t hist[kBins];      // this CTA's
@@ -122,19 +196,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   // on (the move kernel fills the slots that are freed)
   int newest = INT32_MIN;
   if (!stay_all || wo != w || po != pos) {
-    for (int64_t j0 = wlo; j0 < whi; j0 += 128 * kBatch) {
+    #pragma unroll 1
+    for (int j0 = wlo; j0 < whi; j0 += 128 * kBatch) {
       uint4 x[kBatch];
       int4 y[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t j = j0 + u * 128 + lane * 4;
+        const int j = j0 + u * 128 + lane * 4;
         if (j >= whi) continue;
         x[u] = *reinterpret_cast<const uint4*>(w + j);
         if (pos) y[u] = *reinterpret_cast<const int4*>(pos + j);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t j = j0 + u * 128 + lane * 4;
+        const int j = j0 + u * 128 + lane * 4;
         if (j >= whi) continue;
         if (in_smem && !stay_all) *reinterpret_cast<uint4*>(ranks + (j - lo)) = x[u];
         const int32_t ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
@@ -187,22 +262,23 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     if (rank_pos && (p < a.sink || int64_t(p) > after)) v |= 0x80000000u;
     return v;
   };
-  auto ranks_at = [&](int64_t j, uint4 x) -> uint4 {  // x: the weights of slots j .. j + 3
+  auto ranks_at = [&](int j, uint4 x) -> uint4 {  // x: the weights of slots j .. j + 3
     int4 y = make_int4(0, 0, 0, 0);
     if (rank_pos) y = *reinterpret_cast<const int4*>(pos + j);
     return make_uint4(rank(x.x, y.x), rank(x.y, y.y), rank(x.z, y.z), rank(x.w, y.w));
   };
   if (in_smem) {  // (a lane's own slots: no barrier)
-    for (int64_t j0 = wlo; j0 < whi; j0 += 128 * kBatch) {
+    #pragma unroll 1
+    for (int j0 = wlo; j0 < whi; j0 += 128 * kBatch) {
       uint4 x[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t j = j0 + u * 128 + lane * 4;
+        const int j = j0 + u * 128 + lane * 4;
         if (j < whi) x[u] = ranks_at(j, *reinterpret_cast<const uint4*>(ranks + (j - lo)));
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t j = j0 + u * 128 + lane * 4;
+        const int j = j0 + u * 128 + lane * 4;
         if (j < whi) *reinterpret_cast<uint4*>(ranks + (j - lo)) = x[u];
       }
     }
@@ -210,8 +286,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   // Visits this warp's slots in order, four to a lane: body(first slot of the
   // lane, ranks, mask of its slots that exist).
   auto visit = [&](auto&& body) {
-    for (int64_t j0 = wlo; j0 < whi; j0 += 128) {
-      const int64_t j = j0 + lane * 4;
+#pragma unroll 1
+    for (int j0 = wlo; j0 < whi; j0 += 128) {
+      const int j = j0 + lane * 4;
       uint4 x = make_uint4(0, 0, 0, 0);
       uint32_t live = 0;
       if (j < whi) {
@@ -227,6 +304,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   // ---- radix selection: the n-th largest rank T, `above` keys beyond it
   uint32_t T = 0;  // the digits found so far
   int above = 0;
+#pragma unroll 1  // (code that runs once waits for its instructions)
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
     const int bits = d == 2 ? 10 : 11, nbins = 1 << bits;
@@ -238,7 +316,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     for (int e = 0; e < kPer; e += 4)
       if (low >= 0) *reinterpret_cast<uint4*>(sh.hist + low + e) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    visit([&](int64_t, const uint32_t (&r)[4], uint32_t live) {
+    visit([&](int, const uint32_t (&r)[4], uint32_t live) {
       // equal ranks throughout the warp's 128 slots: one addition
       const uint32_t r0 = __shfl_sync(kFull, r[0], 0);
       const bool same = live == 15u && r[0] == r0 && r[1] == r0 && r[2] == r0 && r[3] == r0;
@@ -304,7 +382,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   int eq_at = 0;
   if (ties) {
     int eq = 0, eq_cta;
-    visit([&](int64_t, const uint32_t (&r)[4], uint32_t live) {
+    visit([&](int, const uint32_t (&r)[4], uint32_t live) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) eq += (live >> e & 1) && r[e] == T;
     });
@@ -319,7 +397,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   // ---- what is freed below slot n and what moves from behind it
   auto changes = [&](auto&& body) {
     int seen = eq_at;
-    visit([&](int64_t j, const uint32_t (&r)[4], uint32_t live) {
+    visit([&](int j, const uint32_t (&r)[4], uint32_t live) {
       uint32_t stay = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) stay |= uint32_t(ties ? r[e] > T : r[e] >= T) << e;
@@ -339,7 +417,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     });
   };
   int holes = 0, movers = 0;
-  changes([&](int64_t, uint32_t hole, uint32_t mover) {
+  changes([&](int, uint32_t hole, uint32_t mover) {
     holes += __popc(hole);
     movers += __popc(mover);
   });
@@ -363,19 +441,19 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   }
   int32_t* src = a.moves + size_t(group) * 2 * a.max_moves;
   int32_t* dst = src + a.max_moves;
-  changes([&](int64_t j, uint32_t hole, uint32_t mover) {
+  changes([&](int j, uint32_t hole, uint32_t mover) {
     if (__any_sync(kFull, hole)) {
       int all, at = hole_at + lanes_before(hole, lane, &all);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (hole >> e & 1) dst[at++] = int(j) + e;
+        if (hole >> e & 1) dst[at++] = j + e;
       hole_at += all;
     }
     if (__any_sync(kFull, mover)) {
       int all, at = mover_at + lanes_before(mover, lane, &all);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (mover >> e & 1) src[at++] = int(j) + e;
+        if (mover >> e & 1) src[at++] = j + e;
       mover_at += all;
     }
   });
@@ -392,16 +470,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
 __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ int32_t upto[kMoveGroups];  // batches of the groups up to and with this one
   __shared__ int32_t part[kMoveThreads / 32];
-  __shared__ int64_t from[2][kMoveBatch], to[2][kMoveBatch];  // rows of the pools; from < 0: not moved
+  __shared__ Rows<kMoveBatch> rows[2];
   __shared__ int32_t count[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
   wait_prerequisites();
   const int groups = a.batch * a.Hkv;
-  const size_t cap = size_t(a.max_pages) * a.P;
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.batch; b += kMoveThreads) a.lens_out[b] = a.meta[2 * (b * a.Hkv) + 1];
-  const int nk = a.k_row >> 4, np = nk + (a.v_row >> 4);  // 16-byte pieces of a key
 
   int64_t passed = 0;  // batches of the groups before g0
   for (int g0 = 0; g0 < groups; g0 += kMoveGroups) {
@@ -436,8 +512,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
     }
     __syncthreads();
 
-    // looks up batch `i` of this stretch of groups: kMoveBatch threads
-    auto look_up = [&](int i, int buf) {
+    // looks up batch `i` of this stretch of groups
+    auto find = [&](int i, int buf) {
       if (threadIdx.x >= kMoveBatch || i >= all) return;
       int l = 0, r = ng - 1;  // the first group whose batches reach past i
       while (l < r) {
@@ -447,69 +523,16 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
       const int grp = g0 + l, begin = (i - (l ? upto[l - 1] : 0)) * kMoveBatch;
       const int c = min(kMoveBatch, a.meta[2 * grp] - begin);
       if (threadIdx.x == 0) count[buf] = c;
-      if (threadIdx.x >= c) return;
-      const int b = grp / a.Hkv, h = grp - b * a.Hkv;
-      const int32_t* src = a.moves + size_t(grp) * 2 * a.max_moves + begin;
-      const int s = src[threadIdx.x], d = src[a.max_moves + threadIdx.x];
-      const int32_t* trow = a.block_table + size_t(b) * a.max_pages;
-      const int sp = s / a.P, dp = d / a.P;
-      const int sph = trow[sp], dph = trow[dp];
-      const size_t st = size_t(grp) * cap;
-      a.w_out[st + d] = a.w_in[st + s];
-      if (a.pos_out) a.pos_out[st + d] = a.pos_in[st + s];
-      auto line = [&](int ph, int in) -> int64_t {
-        return a.nhd ? (int64_t(ph) * a.P + in) * a.Hkv + h : (int64_t(ph) * a.Hkv + h) * a.P + in;
-      };
-      const bool ok = sph >= 0 && sph < a.num_pages && dph >= 0 && dph < a.num_pages;
-      if (!ok && a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
-      from[buf][threadIdx.x] = ok ? line(sph, s - sp * a.P) : -1;
-      to[buf][threadIdx.x] = ok ? line(dph, d - dp * a.P) : 0;
+      look_up(a, grp, begin, c, rows[buf]);
     };
 
     int64_t skip = (int64_t(blockIdx.x) - passed) % int64_t(gridDim.x);
     int i = int(skip < 0 ? skip + gridDim.x : skip);
     int buf = 0;
-    look_up(i, buf);
+    find(i, buf);
     __syncthreads();
     for (; i < all; i += gridDim.x, buf ^= 1) {
-      const int total = count[buf] * np;
-      bool looked = false;
-      for (int p0 = threadIdx.x; p0 < total || !looked; p0 += kMoveUnroll * kMoveThreads) {
-        uint4 x4[kMoveUnroll];
-        // piece u of this pass: its move, which pool, its byte offset in the row
-        auto piece = [&](int u, int& m, bool& is_k) -> size_t {
-          const int p = p0 + u * kMoveThreads;
-          m = p / np;
-          const int c = p - m * np;
-          is_k = c < nk;
-          return size_t(is_k ? c : c - nk) << 4;
-        };
-#pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-          if (p0 + u * kMoveThreads >= total) break;
-          bool is_k;
-          int m;
-          const size_t off = piece(u, m, is_k);
-          const int64_t line = from[buf][m];
-          if (line < 0) continue;
-          x4[u] = *reinterpret_cast<const uint4*>(static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages) +
-                                                  line * (is_k ? a.k_row : a.v_row) + off);
-        }
-        if (!looked) {
-          look_up(i + int(gridDim.x), buf ^ 1);
-          looked = true;
-        }
-#pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-          if (p0 + u * kMoveThreads >= total) break;
-          bool is_k;
-          int m;
-          const size_t off = piece(u, m, is_k);
-          if (from[buf][m] < 0) continue;
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(is_k ? a.k_pages : a.v_pages) +
-                                    to[buf][m] * (is_k ? a.k_row : a.v_row) + off) = x4[u];
-        }
-      }
+      copy_rows<kMoveThreads>(a, rows[buf], count[buf], [&]() { find(i + int(gridDim.x), buf ^ 1); });
       __syncthreads();
     }
     passed += all;
@@ -556,14 +579,14 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   e = cudaLaunchKernelEx(&cfg, select_kernel, a, rank_cap);
   if (e != cudaSuccess) return e;
 
-  const int64_t most = int64_t(groups) * ((a.max_moves + kMoveBatch - 1) / kMoveBatch);
-  const int64_t grid = most < int64_t(sms) * 4 ? (most > 0 ? most : 1) : int64_t(sms) * 4;
   cudaLaunchConfig_t mv = {};
-  mv.gridDim = dim3(unsigned(grid), 1, 1);
-  mv.blockDim = dim3(kMoveThreads, 1, 1);
   mv.stream = s;
   mv.attrs = la;
   mv.numAttrs = 1;
+  mv.blockDim = dim3(kMoveThreads, 1, 1);
+  const int64_t most = int64_t(groups) * ((a.max_moves + kMoveBatch - 1) / kMoveBatch);
+  const int64_t grid = most < int64_t(sms) * 4 ? (most > 0 ? most : 1) : int64_t(sms) * 4;
+  mv.gridDim = dim3(unsigned(grid), 1, 1);
   return cudaLaunchKernelEx(&mv, move_kernel, a);
 }
 

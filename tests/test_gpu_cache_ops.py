@@ -402,7 +402,7 @@ def test_evict_long_sequences(cap_pages, lens):
 
 
 def test_evict_more_keys_than_shared_memory_holds():
-    c = Cache([340001], kv_heads=1, heads=1, page=64, device="cuda", seed=28)  # 42,501 a CTA
+    c = Cache([380001], kv_heads=1, heads=1, page=64, device="cuda", seed=28)  # 47,504 a CTA
     few = np.random.default_rng(1).integers(0, 50, (1, 1, c.cap)).astype(np.float32)
     run_evict(c, 100003, sink=4, recent=1000, weights=few)
 
