@@ -576,6 +576,39 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
                              void* workspace, size_t workspace_bytes, int32_t* status,
                              void* stream);
 
+/*
+ * splitkv_cross_attend -- attention of query tokens over a paged cache of
+ * another length, without a causal mask: every token of sequence b attends to
+ * all seq_lens[b] keys (an encoder's states, written once with
+ * splitkv_append).  Any number of tokens per sequence, one (a decode step) to
+ * whole prompts.
+ *   desc         the cache, bf16, qk_dim = v_dim = 128 (q_tokens counts only
+ *                without cu_tokens; any number of query rows per KV head)
+ *   cu_tokens    int32 [B + 1], not decreasing, within [0, n_tokens], or NULL:
+ *                q_tokens tokens for every sequence.  Tokens outside
+ *                [cu_tokens[0], cu_tokens[B]) are left as they are
+ *   q            bf16, token n's heads [Hq][128] at q + n * q_stride (elements,
+ *                a multiple of 8)
+ *   scale        softmax scale, positive
+ *   out          bf16 [n_tokens][Hq][128]; must not overlap q
+ *   lse          fp32 [n_tokens][Hq] natural-log LSE of the scaled scores, or
+ *                NULL.  A token of a sequence without keys gets out = 0 and
+ *                lse = -inf
+ *   workspace    splitkv_cross_workspace_size bytes (0: may be NULL), 16-byte
+ *                aligned, used by this call alone until it has finished
+ * A length outside [0, max_pages_per_seq * P] sets SPLITKV_DEVERR_SEQLEN and
+ * counts as 0; a page id out of range sets SPLITKV_DEVERR_PAGE (page 0 is read
+ * in its place).  One kernel, or two where the keys are split (few tokens).
+ * EUNSUPPORTED for e4m3 caches and other row widths.
+ */
+size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens);
+splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens,
+                                    const int32_t* cu_tokens, const void* q, int64_t q_stride,
+                                    const void* k_pages, const void* v_pages,
+                                    const int32_t* block_table, const int32_t* seq_lens,
+                                    float scale, void* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, int32_t* status, void* stream);
+
 /* Thread-local description of the last error returned on this thread. */
 const char* splitkv_last_error(void);
 

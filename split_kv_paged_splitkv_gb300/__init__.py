@@ -86,6 +86,9 @@ _SIGNATURES = {
     "splitkv_evict_workspace_size": (_sz, [ctypes.POINTER(splitkv_desc_t), _i32]),
     "splitkv_evict": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                              _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "splitkv_cross_workspace_size": (_sz, [ctypes.POINTER(splitkv_desc_t), _i32]),
+    "splitkv_cross_attend": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, _vp, _vp, _i64, _vp, _vp, _vp,
+                                    _vp, _f32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "splitkv_last_error": (ctypes.c_char_p, []),
 }
 
@@ -453,6 +456,32 @@ def splitkv_evict(desc: splitkv_desc_t, budget: int, sink: int, recent: int, k_p
         _addr("weights_out", weights_out, f32, z.state, dev),
         _addr("positions_out", positions_out, i32, z.state, dev),
         _addr("seq_lens_out", seq_lens_out, i32, z.batch, dev),
+        _addr("workspace", workspace, z.torch.uint8, 0, dev), workspace_bytes,
+        _addr("status", status, i32, 1, dev), _stream(stream)))
+
+
+def splitkv_cross_workspace_size(desc: splitkv_desc_t, n_tokens: int) -> int:
+    return int(_lib.splitkv_cross_workspace_size(ctypes.byref(desc), n_tokens))
+
+
+def splitkv_cross_attend(desc: splitkv_desc_t, cu_tokens, q, k_pages, v_pages, block_table, seq_lens,
+                         scale: float, out, lse, workspace, workspace_bytes=None, status=None,
+                         n_tokens=None, stream=None):
+    """Attention of ragged query tokens over all keys of each sequence's cache.
+    ``n_tokens`` is needed only where ``q`` is an address."""
+    z, dev = _sizes(bytes(desc)), _current_device()
+    i32 = z.torch.int32
+    n = n_tokens if n_tokens is not None else q.numel() // (z.heads * z.k_dim) if q is not None else 0
+    qp, qs = _token_rows("q", q, n, z.heads, z.k_dim, z, dev)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel()
+    _check(_lib.splitkv_cross_attend(
+        ctypes.byref(desc), n, _addr("cu_tokens", cu_tokens, i32, z.batch + 1, dev), qp, qs,
+        _addr("k_pages", k_pages, z.pool_dtype, z.k_pool, dev),
+        _addr("v_pages", v_pages, z.pool_dtype, z.v_pool, dev),
+        _addr("block_table", block_table, i32, z.table, dev), _addr("seq_lens", seq_lens, i32, z.batch, dev),
+        scale, _addr("out", out, z.torch.bfloat16, n * z.heads * z.v_dim, dev),
+        _addr("lse", lse, z.torch.float32, n * z.heads, dev),
         _addr("workspace", workspace, z.torch.uint8, 0, dev), workspace_bytes,
         _addr("status", status, i32, 1, dev), _stream(stream)))
 

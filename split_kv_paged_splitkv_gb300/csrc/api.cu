@@ -18,8 +18,6 @@ thread_local char g_err[512] = "";
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-}  // namespace
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -33,8 +31,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
-
-namespace {
 
 // Tensor map over a GQA K or V page pool (rows of 128 elements) in either
 // layout, with coordinates that do not depend on the layout -- (dims, key in
@@ -115,6 +111,24 @@ splitkv_status make_u8_map(TmaDesc* out, const void* base, int dim, int64_t rows
 }
 
 }  // namespace
+
+splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys) {
+  auto fn = encode_fn();
+  if (!fn) return fail(SPLITKV_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t row = 256u, P = cuuint64_t(d.page_size), H = cuuint64_t(d.num_kv_heads);
+  const bool nhd = d.kv_layout == SPLITKV_LAYOUT_NHD;
+  CUtensorMap m;
+  cuuint64_t gdim[5] = {64u, P, 2u, H, cuuint64_t(d.num_pages_total)};
+  cuuint64_t gstride[4] = {nhd ? row * H : row, 128u, nhd ? row : row * P, row * P * H};
+  cuuint32_t box[5] = {64u, cuuint32_t(keys), 1u, 1u, 1u};
+  cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  CUresult r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), gdim, gstride, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SPLITKV_ECUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  std::memcpy(out, &m, sizeof(m));
+  return SPLITKV_OK;
+}
 
 splitkv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(SPLITKV_ECUDA, "%s: %s", what, cudaGetErrorString(e));

@@ -1,5 +1,5 @@
 // C-ABI layer of the cache operators: append with rotary positions, key
-// weights, eviction.  Argument validation, workspace layout, launches.
+// weights, eviction, cross attention.  Argument validation, workspace layout, launches.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -68,6 +68,16 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 int64_t max_moves(const splitkv_desc_t& d, int32_t budget) {
   const int64_t cap = int64_t(d.max_pages_per_seq) * d.page_size;
   return budget >= cap ? 0 : (budget < cap - budget ? budget : cap - budget);
+}
+
+splitkv_status validate_cross(const splitkv_desc_t* d, int32_t n_tokens) {
+  splitkv_status st = validate_cache(d);
+  if (st != SPLITKV_OK) return st;
+  if (d->qk_dim != 128 || d->kv_dtype != SPLITKV_BF16)
+    return fail(SPLITKV_EUNSUPPORTED, "cross attention needs qk_dim = v_dim = 128 and a bf16 cache");
+  if (n_tokens < 0 || int64_t(n_tokens) * d->num_q_heads >= (int64_t(1) << 31) || d->num_kv_heads > 65535)
+    return fail(SPLITKV_EINVAL, "n_tokens must be >= 0 with n_tokens * num_q_heads < 2^31, and num_kv_heads at most 65535");
+  return SPLITKV_OK;
 }
 
 }  // namespace
@@ -334,6 +344,77 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
   a.v_row = d.v_shares_k ? 0 : d.v_dim * elem;
   cudaError_t e = launch_evict(a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launching the eviction kernels");
+  return SPLITKV_OK;
+}
+
+size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
+  if (validate_cross(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
+  const int splits = cross_splits(*desc, n_tokens);
+  return splits == 1 ? 0 : align256(size_t(splits) * n_tokens * desc->num_q_heads * 129 * sizeof(float));
+}
+
+splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens,
+                                    const int32_t* cu_tokens, const void* q, int64_t q_stride,
+                                    const void* k_pages, const void* v_pages,
+                                    const int32_t* block_table, const int32_t* seq_lens,
+                                    float scale, void* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, int32_t* status, void* stream) {
+  splitkv_status st = validate_cross(desc, n_tokens);
+  if (st != SPLITKV_OK) return st;
+  const splitkv_desc_t& d = *desc;
+  if (!cu_tokens && int64_t(d.batch) * d.q_tokens != n_tokens)
+    return fail(SPLITKV_EINVAL, "without cu_tokens, n_tokens (%d) must be batch * q_tokens", n_tokens);
+  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !out)
+    return fail(SPLITKV_EINVAL, "q, k_pages, v_pages, block_table, seq_lens and out must not be NULL");
+  const void* wide[] = {q, k_pages, v_pages, out};
+  for (const void* p : wide)
+    if (misaligned(p, 16)) return fail(SPLITKV_EINVAL, "q, out and the pages must be 16-byte aligned");
+  const void* words[] = {cu_tokens, block_table, seq_lens, lse, status};
+  for (const void* p : words)
+    if (misaligned(p, 4)) return fail(SPLITKV_EINVAL, "index arrays and lse must be 4-byte aligned");
+  const int64_t row = int64_t(d.num_q_heads) * 128;
+  if (q_stride < row || q_stride % 8)
+    return fail(SPLITKV_EINVAL, "q_stride must be a multiple of 8 elements and hold a token's heads");
+  if (n_tokens > 0 && overlap(q, size_t((n_tokens - 1) * q_stride + row) * 2, out, size_t(n_tokens) * row * 2))
+    return fail(SPLITKV_EINVAL, "out overlaps q");
+  if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPLITKV_EINVAL, "scale must be positive and finite");
+  if (n_tokens == 0) return SPLITKV_OK;
+  CrossArgs a{};
+  a.splits = cross_splits(d, n_tokens);
+  if (a.splits > 1) {
+    if (!workspace) return fail(SPLITKV_EWORKSPACE, "workspace is NULL");
+    if (misaligned(workspace, 16)) return fail(SPLITKV_EINVAL, "workspace must be 16-byte aligned");
+    const size_t need = splitkv_cross_workspace_size(desc, n_tokens);
+    if (workspace_bytes < need)
+      return fail(SPLITKV_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
+    a.o_part = static_cast<float*>(workspace);
+    a.lse_part = a.o_part + size_t(a.splits) * n_tokens * row;
+  }
+  a.q = q;
+  a.cu = cu_tokens;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.lse = lse;
+  a.status = status;
+  a.q_stride = q_stride;
+  a.qk_scale_log2 = scale * kLog2e;
+  a.n_tokens = n_tokens;
+  a.batch = d.batch;
+  a.T = d.q_tokens;
+  a.Hq = d.num_q_heads;
+  a.Hkv = d.num_kv_heads;
+  a.G = d.num_q_heads / d.num_kv_heads;
+  a.P = d.page_size;
+  a.max_pages = d.max_pages_per_seq;
+  a.num_pages = d.num_pages_total;
+  a.box_rows = cross_box_rows(d);
+  TmaDesc tk, tv;
+  st = make_half_map(&tk, k_pages, d, a.box_rows);
+  if (st == SPLITKV_OK) st = make_half_map(&tv, v_pages, d, a.box_rows);
+  if (st != SPLITKV_OK) return st;
+  cudaError_t e = launch_cross(a, cross_row_tiles(d, n_tokens), tk, tv, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the cross attention kernels");
   return SPLITKV_OK;
 }
 

@@ -220,8 +220,35 @@ struct EvictArgs {
   int32_t k_row, v_row;   // bytes of one key's row
 };
 
+constexpr int kMaxCrossSplits = 16;  // key splits of cross attention
+constexpr int kSmCount = 152;        // SMs that cross attention plans for
+
+struct CrossArgs {
+  const void* q;
+  const int32_t* cu;  // [batch + 1] or null: T tokens per sequence
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  void* out;
+  float* lse;         // or null
+  float* o_part;      // [splits][n_tokens * Hq][128], with more than one split
+  float* lse_part;    // [splits][n_tokens * Hq]
+  int32_t* status;    // or null
+  int64_t q_stride;   // elements per token
+  float qk_scale_log2;
+  int32_t n_tokens, batch, T, Hq, Hkv, G, P, max_pages, num_pages, splits, box_rows;
+};
+
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream);
 cudaError_t launch_key_weights(const WeightArgs& a, bool fp8, void* stream);
 cudaError_t launch_evict(const EvictArgs& a, void* stream);
+int64_t cross_row_tiles(const splitkv_desc_t& d, int64_t n_tokens);
+int cross_splits(const splitkv_desc_t& d, int64_t n_tokens);
+int cross_box_rows(const splitkv_desc_t& d);  // keys of one TMA box
+cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv,
+                         void* stream);
+// Tensor map over a bf16 pool of 128-wide rows, coordinates (64 columns, key
+// in page, column half, KV head, page) in either layout, boxes of `keys` keys
+// and one column half, 128-byte swizzle (api.cu).
+splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys);
 
 }  // namespace splitkv

@@ -164,6 +164,39 @@ def test_evict_workspace():
     refused(EINVAL, call_evict, desc(Hq=128, Hkv=1, Dk=576, Dv=512, shares=1))
 
 
+# ------------------------------------------------------------------ cross attention
+
+def call_cross(d, **kw):
+    a = dict(desc=d, cu_tokens=None, q=A, k_pages=A, v_pages=A, block_table=A, seq_lens=A, scale=0.1, out=1 << 40, lse=A,
+             workspace=A, workspace_bytes=1 << 40, n_tokens=d.batch * d.q_tokens, stream=0)
+    a.update(kw)
+    return skv.splitkv_cross_attend(**a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(k_pages=None), dict(v_pages=None), dict(block_table=None), dict(seq_lens=None), dict(out=None),
+    dict(q=A + 8), dict(out=A), dict(out=A + 256), dict(lse=A + 2), dict(cu_tokens=A + 2), dict(scale=0.0), dict(scale=math.nan),
+    dict(n_tokens=-1), dict(n_tokens=5), dict(n_tokens=1 << 28, cu_tokens=A)])
+def test_cross_refusals(kw):
+    refused(EINVAL, call_cross, desc(), **kw)
+
+
+def test_cross_refuses_other_caches_and_small_workspaces():
+    refused(EUNSUPPORTED, call_cross, desc(fp8=True))
+    refused(EUNSUPPORTED, call_cross, desc(Hq=128, Hkv=1, Dk=576, Dv=512, shares=1))
+    d = desc(B=1, Hkv=1, maxp=512)  # one row tile over 8192 slots: split
+    need = skv.splitkv_cross_workspace_size(d, 1)
+    assert need >= 2 * 8 * 129 * 4
+    refused(EWORKSPACE, call_cross, d, workspace=None, workspace_bytes=0)
+    refused(EWORKSPACE, call_cross, d, workspace_bytes=need - 1)
+    refused(EINVAL, call_cross, d, workspace=A + 8)
+    assert skv.splitkv_cross_workspace_size(desc(Hkv=2, maxp=512), 1 << 20) == 0  # many rows: not split
+    assert skv.splitkv_cross_workspace_size(d, 0) == 0 and skv.splitkv_cross_workspace_size(d, -1) == 0
+    call_cross(d, cu_tokens=A, n_tokens=0)  # nothing to do, nothing launched
+    lib = skv._lib.splitkv_cross_attend
+    assert lib(ctypes.byref(d), 1, None, A, 1016, A, A, A, A, 0.1, 1 << 40, None, A, 1 << 40, None, 0) == EINVAL
+
+
 def test_tensor_arguments_are_checked():
     import torch
     d = desc()
