@@ -349,8 +349,7 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
 
 size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
   if (validate_cross(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
-  const int splits = cross_splits(*desc, n_tokens);
-  return splits == 1 ? 0 : align256(size_t(splits) * n_tokens * desc->num_q_heads * 129 * sizeof(float));
+  return align256(size_t(2) * cross_parts(*desc, n_tokens) * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float));
 }
 
 splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens,
@@ -380,15 +379,16 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPLITKV_EINVAL, "scale must be positive and finite");
   if (n_tokens == 0) return SPLITKV_OK;
   CrossArgs a{};
-  a.splits = cross_splits(d, n_tokens);
-  if (a.splits > 1) {
+  a.parts = cross_parts(d, n_tokens);
+  a.part_rows = cross_part_rows(d, n_tokens);
+  if (a.parts > 0) {
     if (!workspace) return fail(SPLITKV_EWORKSPACE, "workspace is NULL");
     if (misaligned(workspace, 16)) return fail(SPLITKV_EINVAL, "workspace must be 16-byte aligned");
     const size_t need = splitkv_cross_workspace_size(desc, n_tokens);
     if (workspace_bytes < need)
       return fail(SPLITKV_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
     a.o_part = static_cast<float*>(workspace);
-    a.lse_part = a.o_part + size_t(a.splits) * n_tokens * row;
+    a.lse_part = a.o_part + size_t(2) * a.parts * a.part_rows * 128;
   }
   a.q = q;
   a.cu = cu_tokens;

@@ -8,8 +8,8 @@
 // the rows of 128 and the shared KV heads of the GQA decode.
 //
 // Work.  The T_b * G query rows that share a KV head form tiles of 256 rows,
-// two MMA row blocks A and B of 128.  One CTA per (row tile, KV head, split of
-// the keys); keys stream in blocks of 128.  Per key block and row block:
+// two MMA row blocks A and B of 128; an item is one (sequence, KV head, row
+// tile) over all key blocks of 128.  Per key block and row block:
 //   S = Q . K^T      (M=128 N=128 K=128, operands in shared memory)
 //   softmax warps: one thread per query row; online softmax with a lazy
 //     reference maximum (O is rescaled only when a row's maximum grows by more
@@ -27,10 +27,14 @@
 // 128-byte swizzled; K is read K-major, V with its dims on N.
 // TMEM columns: S_A [0, 128), S_B [128, 256), O_A [256, 384), O_B [384, 512).
 //
-// Few rows (a decoder token over the encoder's states): the bound is the bytes
-// of K and V, the keys are split so that every SM has a part, a row block
-// without rows is left out, and merge_kernel joins the parts by their
-// log-sum-exps.  Many rows: the bound is 4 * 128 * rows * L operations.
+// Many items (prompts): a CTA per item; the bound is 4 * 128 * rows * L
+// operations.  Few items (a decoder token over the encoder's states, short
+// prompts; the bound is the bytes of K and V, or the longest item): the key
+// blocks of all items form one line, cut by the device lengths into equal
+// parts, one per SM.  A CTA then walks the pieces of items in its part (the
+// ring and the barriers run on across them); an item that lies in more than
+// one part leaves partial results, at most two of a CTA, and merge_kernel
+// joins them by their log-sum-exps.  A row block without rows is left out.
 //
 // P is rounded to bf16 for the second product (half a step, 2^-8 of a weight,
 // as in the decode kernels); sums, maxima and O are fp32.
@@ -54,16 +58,17 @@ struct Cross {
   static constexpr int OFF_RING = 2 * TILE;      // after Q's two row blocks
   static constexpr int OFF_BAR = OFF_RING + NST * TILE;
   static constexpr int SMEM = 1024 + OFF_BAR + 256;
-  static constexpr int SOFTMAX_THREADS = 256;
-  static constexpr int THREADS = SOFTMAX_THREADS + 64;
+  static constexpr int SOFTMAX_WARPS = 8;
+  static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 1;  // warps
+  static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
   static constexpr uint32_t TMEM_COLS = 512, S_COL = 0, O_COL = 256;  // + 128 per row block
   static constexpr float RESCALE_LOG2 = 8.f;
 };
 static_assert(Cross::SMEM <= 227 * 1024, "shared memory budget");
 
 enum {
-  B_Q = 0,                       // Q in shared memory (256 threads)
-  B_FULL = 1,                    // [NST]
+  B_Q = 0,                       // [2] Q of a row block in shared memory (128 threads)
+  B_FULL = 2,                    // [NST]
   B_EMPTY = B_FULL + Cross::NST, // [NST]
   B_S = B_EMPTY + Cross::NST,    // [2] S of a row block complete
   B_P = B_S + 2,                 // [2] P of a row block in TMEM (128 threads)
@@ -92,6 +97,93 @@ __device__ __forceinline__ int tokens_of(const CrossArgs& a, int b, int* first) 
   return max(t1 - t0, 0);
 }
 
+// Key blocks of an item over n_keys keys; an item without keys counts as one
+// (it writes its zeros).
+__device__ __forceinline__ int blocks_of(int n_keys) { return max(1, (n_keys + Cross::BK - 1) / Cross::BK); }
+
+// Where a CTA stands in the line of items (b, h, tile), the row tile innermost.
+struct Place {
+  int64_t w, w1;        // of the line: here, and the end of this CTA's part
+  int32_t b, h, tile, block;
+};
+
+// One piece of an item: `nblk` key blocks from j0 on.
+struct Piece {
+  int b, h, first, row0, n_rows, L, j0, nblk;  // n_rows: rows from row0 on (may exceed a tile)
+  bool starts, ends;                           // holds the item's first, last key block
+};
+
+// Behind the barriers.
+struct Tail {
+  uint32_t tmem;  // written by the allocation
+  Place start;
+};
+static_assert(B_COUNT * 8 + sizeof(Tail) <= 256, "barriers, then the tail");
+
+// Row tiles of sequence b.
+__device__ __forceinline__ int tiles_of(const CrossArgs& a, int b) {
+  int first;
+  return (tokens_of(a, b, &first) * a.G + Cross::ROWS - 1) / Cross::ROWS;
+}
+
+// Takes the next piece of this CTA's part; false at its end.
+__device__ __forceinline__ bool next_piece(const CrossArgs& a, Place& p, Piece& q) {
+  if (p.w >= p.w1) return false;
+  q.b = p.b;
+  q.h = p.h;
+  const int rows = tokens_of(a, p.b, &q.first) * a.G;
+  q.row0 = p.tile * Cross::ROWS;
+  q.n_rows = rows - q.row0;
+  q.L = keys_of(a, p.b);
+  const int nb = blocks_of(q.L), take = int(min(int64_t(nb - p.block), p.w1 - p.w));
+  q.j0 = p.block;
+  q.nblk = q.L > 0 ? take : 0;
+  q.starts = p.block == 0;
+  q.ends = p.block + take == nb;
+  p.w += take;
+  p.block = 0;
+  if (p.w < p.w1) {  // (then this item is done)
+    if (++p.tile * Cross::ROWS >= rows) {
+      p.tile = 0;
+      if (++p.h == a.Hkv) {
+        p.h = 0;
+        do ++p.b; while (tiles_of(a, p.b) == 0);
+      }
+    }
+  }
+  return true;
+}
+
+// By a warp: the length of the line, and the first place of sequence `want`
+// or of the sequence that place `at` lies in (b = that sequence; -1: none).
+__device__ __forceinline__ int64_t survey(const CrossArgs& a, int lane, int64_t at, int want, int64_t* origin, int* b) {
+  int64_t total = 0;
+  *b = -1;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int bl = b0 + lane;
+    const int64_t n = bl < a.batch ? int64_t(tiles_of(a, bl)) * a.Hkv * blocks_of(keys_of(a, bl)) : 0;
+    int64_t x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    const unsigned hit = __ballot_sync(kFull, want >= 0 ? bl == want : total + x > at);
+    if (hit && *b < 0) {
+      const int f = __ffs(hit) - 1;
+      *b = b0 + f;
+      *origin = total + __shfl_sync(kFull, x - n, f);
+    }
+    total += __shfl_sync(kFull, x, 31);
+  }
+  return total;
+}
+
+// CTAs that share a line of W key blocks: two blocks each at least.
+__device__ __forceinline__ int64_t parts_of(const CrossArgs& a, int64_t W) {
+  return max(int64_t(1), min(int64_t(a.parts), W / 2));
+}
+
 // 64 consecutive fp32 columns of this warp's 32 TMEM lanes (one lane per thread).
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
   uint32_t r[64];
@@ -116,12 +208,131 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+
+// 8 columns, without a wait.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
+
+// Two sums at once.
+__device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v));
+}
+
 // (a * s + b) for two numbers at once.
 __device__ __forceinline__ void fma2(float& x, float& y, float s, float b) {
   asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmov.b64 w, {%3, %3};\n\t"
       "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
       : "+f"(x), "+f"(y)
       : "f"(s), "f"(b));
+}
+
+// Eight MMAs of one K = 128 product, issued by a converged warp: one lane,
+// elected once, issues all of them (between two MMAs nothing but the next
+// descriptors' additions, in units of 16 bytes).
+// S = Q . K^T: both operands are two 64-column halves, 32 bytes per step.
+__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t"
+      ".reg .pred e, q, y;\n\t"
+      ".reg .b64 a, b;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.eq.b32 y, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
+      "add.s64 a, %1, 2;\n\t"
+      "add.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+      "add.s64 a, %1, 4;\n\t"
+      "add.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+      "add.s64 a, %1, 6;\n\t"
+      "add.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+      "add.s64 a, %1, 1024;\n\t"
+      "add.s64 b, %2, 1024;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+      "add.s64 a, %1, 1026;\n\t"
+      "add.s64 b, %2, 1026;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+      "add.s64 a, %1, 1028;\n\t"
+      "add.s64 b, %2, 1028;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+      "add.s64 a, %1, 1030;\n\t"
+      "add.s64 b, %2, 1030;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+      "}" ::"r"(d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(0)
+      : "memory");
+}
+// O (+)= P . V: P in TMEM, 8 columns per step; V 16 keys of 128 bytes per step.
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t more) {
+  asm volatile(
+      "{\n\t"
+      ".reg .pred e, q, y;\n\t"
+      ".reg .b64 b;\n\t"
+      ".reg .b32 a;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.eq.b32 y, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+      "add.s32 a, %1, 8;\n\t"
+      "add.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "add.s32 a, %1, 16;\n\t"
+      "add.s64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "add.s32 a, %1, 24;\n\t"
+      "add.s64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "add.s32 a, %1, 32;\n\t"
+      "add.s64 b, %2, 512;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "add.s32 a, %1, 40;\n\t"
+      "add.s64 b, %2, 640;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "add.s32 a, %1, 48;\n\t"
+      "add.s64 b, %2, 768;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "add.s32 a, %1, 56;\n\t"
+      "add.s64 b, %2, 896;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "}" ::"r"(d),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(more)
+      : "memory");
 }
 
 __global__ void __launch_bounds__(Cross::THREADS, 1)
@@ -131,19 +342,17 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_COUNT);
-  int32_t* where = reinterpret_cast<int32_t*>(tmem_slot + 1);  // sequence, row tile
+  Tail& tail = *reinterpret_cast<Tail*>(bars + B_COUNT);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, split = blockIdx.z;
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(B_Q), C::SOFTMAX_THREADS);
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(bar(B_FULL + s), 1);
       mbar_init(bar(B_EMPTY + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(B_Q + t), 128);
       mbar_init(bar(B_S + t), 1);
       mbar_init(bar(B_P + t), 128);
       mbar_init(bar(B_O + t), 1);
@@ -151,8 +360,8 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     mbar_init(bar(B_DONE), 1);
     fence_mbar_init();
   }
-  if (warp == 8) {
-    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+  if (warp == C::PRODUCER) {
+    tmem_alloc(smem_u32(&tail.tmem), C::TMEM_COLS);
     if (lane == 0) {
       prefetch_tmap(&tk);
       prefetch_tmap(&tv);
@@ -160,67 +369,75 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   }
   launch_dependents();
   wait_prerequisites();
-  if (warp == 9) {
-    // the sequence and row tile of this CTA: tiles of all sequences in a line
-    int before = 0, b = -1, tile = 0;
-    for (int b0 = 0; b0 < a.batch && b < 0; b0 += 32) {
-      int first;
-      const int bl = b0 + lane;
-      const int rows = bl < a.batch ? tokens_of(a, bl, &first) * a.G : 0;
-      const int n = (rows + C::ROWS - 1) / C::ROWS;
-      int x = n;
+  if (warp == C::ISSUER) {
+    Place p;
+    p.w = p.w1 = 0;
+    p.b = p.h = p.tile = p.block = 0;
+    int64_t origin = 0;
+    if (a.parts > 0) {
+      int b;
+      const int64_t W = survey(a, lane, INT64_MAX, -1, &origin, &b), n = parts_of(a, W);
+      if (blockIdx.x < n && W > 0) {
+        p.w = W * blockIdx.x / n;
+        p.w1 = W * (blockIdx.x + 1) / n;
+        survey(a, lane, p.w, -1, &origin, &p.b);
+        const int nb = blocks_of(keys_of(a, p.b)), tiles = tiles_of(a, p.b);
+        const int64_t item = (p.w - origin) / nb;
+        p.block = int(p.w - origin - item * nb);
+        p.h = int(item / tiles);
+        p.tile = int(item - int64_t(p.h) * tiles);
+      }
+    } else {
+      // a CTA per item: row tile blockIdx.x of all sequences' (the grid counts
+      // tiles for any split of the tokens among the sequences), head blockIdx.y
+      int before = 0;
+      for (int b0 = 0; b0 < a.batch && p.w1 == 0; b0 += 32) {
+        const int bl = b0 + lane, n = bl < a.batch ? tiles_of(a, bl) : 0;
+        int x = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kFull, x, o);
-        if (lane >= o) x += y;
-      }
-      const unsigned past = __ballot_sync(kFull, before + x > int(blockIdx.x));
-      if (past) {
-        const int f = __ffs(past) - 1;
-        b = b0 + f;
-        tile = int(blockIdx.x) - before - (__shfl_sync(kFull, x, f) - __shfl_sync(kFull, n, f));
-      } else {
-        before += __shfl_sync(kFull, x, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFull, x, o);
+          if (lane >= o) x += y;
+        }
+        const unsigned past = __ballot_sync(kFull, before + x > int(blockIdx.x));
+        if (past) {
+          const int f = __ffs(past) - 1;
+          p.b = b0 + f;
+          p.h = blockIdx.y;
+          p.tile = int(blockIdx.x) - before - __shfl_sync(kFull, x - n, f);
+          p.w1 = blocks_of(keys_of(a, p.b));
+        } else {
+          before += __shfl_sync(kFull, x, 31);
+        }
       }
     }
-    if (lane == 0) {
-      where[0] = b;
-      where[1] = tile;
-    }
+    if (lane == 0) tail.start = p;
     // one CTA reports lengths that the cache cannot hold
-    if (a.status && blockIdx.x == 0 && h == 0 && split == 0)
+    if (a.status && blockIdx.x == 0 && blockIdx.y == 0)
       for (int i = lane; i < a.batch; i += 32)
         if (a.seq_lens[i] != keys_of(a, i)) atomicOr(a.status, SPLITKV_DEVERR_SEQLEN);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int b = where[0];
-  // (the grid counts tiles for any split of the tokens among the sequences)
-  if (b >= 0) {
-    int first;
-    const int n_rows = tokens_of(a, b, &first) * a.G - where[1] * C::ROWS;  // from this tile on
-    const int row0 = where[1] * C::ROWS;
-    const int blocks = n_rows > 128 ? 2 : 1;  // row blocks with rows
-    const int L = keys_of(a, b);
-    // this split's key blocks
-    const int all = (L + C::BK - 1) / C::BK;
-    const int j0 = int(int64_t(all) * split / a.splits), j1 = int(int64_t(all) * (split + 1) / a.splits);
-    const int nblk = j1 - j0, k_begin = j0 * C::BK, k_end = min(L, j1 * C::BK);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
+  Place place = tail.start;
+  Piece pc;
 
-    if (warp == 8) {
-      // ------------------------------------------------------------ producer
-      // Item 2 j is K block j, item 2 j + 1 V block j; item i lies in slot
-      // i % NST.  A block is BK / br pieces of br keys of one page each; lane
-      // g holds the page of piece g.  Pieces behind the last key are not read.
-      const int32_t* trow = a.block_table + size_t(b) * a.max_pages;
-      const int br = a.box_rows;
-      bool ok = true;
-      int issued = 0;
-      for (int j = 0; j < nblk && ok; ++j) {
-        const int key0 = k_begin + j * C::BK;
-        const int np = (min(C::BK, k_end - key0) + br - 1) / br;
+  if (warp == C::PRODUCER) {
+    // -------------------------------------------------------------- producer
+    // K block, V block, K block, ... of all pieces; item i of this sequence
+    // lies in slot i % NST.  A block is BK / br groups of br keys of one page
+    // each; lane g holds the page of group g.  Groups behind the last key are
+    // not read.
+    const int br = a.box_rows;
+    bool ok = true;
+    int issued = 0;
+    while (ok && next_piece(a, place, pc)) {
+      const int32_t* trow = a.block_table + size_t(pc.b) * a.max_pages;
+      for (int j = 0; j < pc.nblk && ok; ++j) {
+        const int key0 = (pc.j0 + j) * C::BK;
+        const int np = (min(C::BK, pc.L - key0) + br - 1) / br;
         int ph = 0, in = 0;
         if (lane < np) {
           const int key = key0 + lane * br, lp = key / a.P;
@@ -232,69 +449,74 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
           }
         }
         for (int v = 0; v < 2 && ok; ++v) {
-          const int i = 2 * j + v, st = i % C::NST;
-          if (i >= C::NST) ok = __all_sync(kFull, mbar_wait(bar(B_EMPTY + st), (i / C::NST - 1) & 1));
+          const int st = issued % C::NST;
+          if (issued >= C::NST) ok = __all_sync(kFull, mbar_wait(bar(B_EMPTY + st), (issued / C::NST - 1) & 1));
           if (!ok) break;
           mbar_arrive_expect_tx_warp(bar(B_FULL + st), uint32_t(np * br * 256));
           const uint32_t dst = smem_u32(sm + C::OFF_RING + st * C::TILE);
           const CUtensorMap* tm = v ? &tv : &tk;
           for (int g = 0; g < np; ++g) {
             const int pg = __shfl_sync(kFull, ph, g), kp = __shfl_sync(kFull, in, g);
-            tma_load_5d_warp(dst + g * br * 128, tm, bar(B_FULL + st), 0, kp, 0, h, pg);
-            tma_load_5d_warp(dst + C::HALF + g * br * 128, tm, bar(B_FULL + st), 0, kp, 1, h, pg);
+            tma_load_5d_warp(dst + g * br * 128, tm, bar(B_FULL + st), 0, kp, 0, pc.h, pg);
+            tma_load_5d_warp(dst + C::HALF + g * br * 128, tm, bar(B_FULL + st), 0, kp, 1, pc.h, pg);
           }
-          issued = i + 1;
+          ++issued;
         }
       }
-      if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
-      // stay until every issued copy has landed
-      if (lane == 0) {
-        for (int st = 0; st < C::NST && st < issued; ++st) {
-          const int last = st + C::NST * ((issued - 1 - st) / C::NST);
-          if (!mbar_wait(bar(B_FULL + st), (last / C::NST) & 1)) break;
-        }
+    }
+    if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
+    // stay until every issued copy has landed
+    if (lane == 0) {
+      for (int st = 0; st < C::NST && st < issued; ++st) {
+        const int last = st + C::NST * ((issued - 1 - st) / C::NST);
+        if (!mbar_wait(bar(B_FULL + st), (last / C::NST) & 1)) break;
       }
-    } else if (warp == 9) {
-      // ---------------------------------------------------------- MMA issuer
-      constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, 0, 0), idesc_pv = umma_idesc_bf16(128, 128, 0, 1);
-      bool ok = true;
-      auto wait = [&](int i, int phase) {
-        ok = ok && __all_sync(kFull, mbar_wait(bar(i), phase & 1));
-        return ok;
-      };
-      auto slot = [&](int i) { return smem_u32(sm + C::OFF_RING + (i % C::NST) * C::TILE); };
-      auto qk = [&](int t, int j) {  // S_t = Q_t . K_j^T
-        const uint32_t q = smem_u32(sm + t * C::TILE), k = slot(2 * j);
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int kin = 0; kin < 4; ++kin)
-            umma_bf16_warp(tmem + C::S_COL + 128 * t, umma_desc(q + half * C::HALF + kin * 32, 16, 1024, 2),
-                           umma_desc(k + half * C::HALF + kin * 32, 16, 1024, 2), idesc_qk, (half | kin) != 0);
-        umma_commit_warp(bar(B_S + t));
-        __syncwarp();
-      };
-      auto pv = [&](int t, int j) {  // O_t += P_t . V_j
-        const uint32_t v = slot(2 * j + 1);
-#pragma unroll
-        for (int kin = 0; kin < 8; ++kin)
-          umma_bf16_ta_warp(tmem + C::O_COL + 128 * t, tmem + C::S_COL + 128 * t + kin * 8,
-                            umma_desc(v + kin * 16 * 128, C::HALF, 1024, 2), idesc_pv, (j | kin) != 0);
-        if (j == nblk - 1) umma_commit_warp(bar(B_O + t));
-        __syncwarp();
-      };
-      if (nblk > 0 && wait(B_Q, 0) && wait(B_FULL, 0)) {
+    }
+  } else if (warp == C::ISSUER) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, 0, 0), idesc_pv = umma_idesc_bf16(128, 128, 0, 1);
+    bool ok = true;
+    int item = 0;                      // ring items consumed
+    uint32_t n_q = 0, n_p = 0;  // phases of B_Q and B_P so far, a bit per row block
+    auto wait = [&](int i, int phase) {
+      ok = ok && __all_sync(kFull, mbar_wait(bar(i), phase & 1));
+      return ok;
+    };
+    auto slot = [&](int i) { return smem_u32(sm + C::OFF_RING + (i % C::NST) * C::TILE); };
+    static_assert(C::HALF >> 4 == 1024, "descriptor steps of mma_qk");
+    auto qk = [&](int t, int i) {  // S_t = Q_t . K^T, K in ring item i
+      mma_qk(tmem + C::S_COL + 128 * t, umma_desc(smem_u32(sm + t * C::TILE), 16, 1024, 2), umma_desc(slot(i), 16, 1024, 2),
+             idesc_qk);
+      umma_commit_warp(bar(B_S + t));
+    };
+    auto pv = [&](int t, int i, bool more, bool last) {  // O_t (+)= P_t . V, V in ring item i
+      mma_pv(tmem + C::O_COL + 128 * t, tmem + C::S_COL + 128 * t, umma_desc(slot(i), C::HALF, 1024, 2), idesc_pv, more);
+      if (last) umma_commit_warp(bar(B_O + t));
+    };
+    auto release = [&](int i) {
+      umma_commit_warp(bar(B_EMPTY + i % C::NST));
+    };
+    while (ok && next_piece(a, place, pc)) {
+      if (pc.nblk == 0) continue;
+      const int blocks = pc.n_rows > 128 ? 2 : 1;  // row blocks with rows
+      for (int t = 0; t < blocks && ok; ++t) {
+        const bool q_in = wait(B_Q + t, n_q >> t);
+        n_q ^= 1u << t;
+        if (!q_in || (t == 0 && !wait(B_FULL + item % C::NST, item / C::NST))) break;
         tc_fence_after();
-        for (int t = 0; t < blocks; ++t) qk(t, 0);
-        umma_commit_warp(bar(B_EMPTY));
-        __syncwarp();
+        qk(t, item);
+        if (t == blocks - 1) release(item);
       }
-      for (int j = 0; j < nblk && ok; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;  // V block j, K block j + 1
+      for (int j = 0; j < pc.nblk && ok; ++j) {
+        const int iv = item + 2 * j + 1, ik = iv + 1;  // V of this block, K of the next
+        bool k_in = true;
         for (int t = 0; t < blocks && ok; ++t) {
           if (t == 0) {
+            // (off the way from P to the next product, if K has landed by now)
+            if (j + 1 < pc.nblk)
+              k_in = __all_sync(kFull, mbar_test(bar(B_FULL + ik % C::NST), (ik / C::NST) & 1));
             if (!wait(B_FULL + iv % C::NST, iv / C::NST)) break;
-            const int valid = k_end - (k_begin + j * C::BK);
+            const int valid = pc.L - (pc.j0 + j) * C::BK;
             if (valid < C::BK) {
               // key slots past the last key may hold anything (even NaN): zero
               // their V rows, so that 0 * V stays 0
@@ -306,81 +528,81 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
               __syncwarp();
             }
           }
-          if (!wait(B_P + t, j)) break;
+          if (!wait(B_P + t, n_p >> t)) break;
+          n_p ^= 1u << t;
           tc_fence_after();
-          pv(t, j);
-          if (t == blocks - 1) {
-            umma_commit_warp(bar(B_EMPTY + iv % C::NST));
-            __syncwarp();
-          }
-          if (j + 1 < nblk) {
-            if (t == 0 && !wait(B_FULL + ik % C::NST, ik / C::NST)) break;
+          pv(t, iv, j > 0, j == pc.nblk - 1);
+          if (t == blocks - 1) release(iv);
+          if (j + 1 < pc.nblk) {
+            if (!k_in && !wait(B_FULL + ik % C::NST, ik / C::NST)) break;
+            k_in = true;
             tc_fence_after();
-            qk(t, j + 1);
-            if (t == blocks - 1) {
-              umma_commit_warp(bar(B_EMPTY + ik % C::NST));
-              __syncwarp();
-            }
+            qk(t, ik);
+            if (t == blocks - 1) release(ik);
           }
         }
       }
-      if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
-      // every MMA issued above completes before TMEM is released
-      umma_commit_warp(bar(B_DONE));
-      __syncwarp();
-      mbar_wait(bar(B_DONE), 0);
-    } else {
-      // ------------------------------------------------------- softmax warps
-      const int t = warp >> 2;                         // row block
-      const int r = (warp & 3) * 32 + lane;            // TMEM lane
-      const int row = t * 128 + r;                     // of the tile
-      const bool live = row < n_rows;
-      const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
-      const int tok = (row0 + row) / a.G, g = (row0 + row) - tok * a.G;
-      const size_t out_row = (size_t(first) + tok) * a.Hq + size_t(h) * a.G + g;
-      {
-        // this row of Q, swizzled; rows behind the last are zero
+      item += 2 * pc.nblk;
+    }
+    if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
+    // every MMA issued above completes before TMEM is released
+    umma_commit_warp(bar(B_DONE));
+    __syncwarp();
+    mbar_wait(bar(B_DONE), 0);
+  } else {
+    // --------------------------------------------------------- softmax warps
+    const int t = warp >> 2;                       // row block
+    const int r = (warp & 3) * 32 + lane;          // TMEM lane
+    const int row = t * 128 + r;                   // of the tile
+    // this warp's lanes and the columns of S and, + 256 - 128 t, of O
+    const uint32_t scol = tmem + (uint32_t((warp & 3) * 32) << 16) + C::S_COL + 128 * t;
+    const uint32_t ocol = scol + (C::O_COL - C::S_COL);
+    const float sl2 = a.qk_scale_log2;
+    uint32_t n_s = 0, n_o = 0;  // phases of B_S and B_O so far
+    bool ok = true;
+    while (ok && next_piece(a, place, pc)) {
+      if (t == 1 && pc.n_rows <= 128) continue;
+      const bool live = row < pc.n_rows;
+      const bool any = __any_sync(kFull, live);  // a warp without rows only keeps step
+      const int tok = (pc.row0 + row) / a.G, g = (pc.row0 + row) - tok * a.G;
+      if (pc.nblk > 0) {
+        // this row of Q, swizzled; rows behind the last are zero (the products
+        // that read the Q before are done: B_O)
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                          (int64_t(first) + tok) * a.q_stride + (h * a.G + g) * 128);
+                                                          (int64_t(pc.first) + tok) * a.q_stride +
+                                                          (pc.h * a.G + g) * 128);
         uint8_t* dst = sm + t * C::TILE + r * 128;
-        if (t < blocks) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint4 x = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * C::HALF + (((c & 7) ^ (r & 7)) << 4)) = x;
-          }
+        for (int i = 0; i < 16; ++i) {
+          const uint4 x = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * C::HALF + (((i & 7) ^ (r & 7)) << 4)) = x;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(bar(B_Q));
+        mbar_arrive(bar(B_Q + t));
       }
-      const bool any = __any_sync(kFull, live);  // a warp without rows only keeps step
-      const uint32_t scol = C::S_COL + 128 * t, ocol = C::O_COL + 128 * t;
-      const float sl2 = a.qk_scale_log2;
       float m_ref = -INFINITY, l = 0.f;
-      bool ok = true;
-      for (int j = 0; j < nblk && t < blocks; ++j) {
-        ok = __all_sync(kFull, mbar_wait(bar(B_S + t), j & 1));
+      int valid = pc.L - pc.j0 * C::BK;  // keys from the block's first on
+      for (int j = 0; j < pc.nblk; ++j, valid -= C::BK) {
+        ok = __all_sync(kFull, mbar_wait(bar(B_S + t), n_s++ & 1));
         if (!ok) break;
         tc_fence_after();
         if (any) {
           float s[128];
-          tmem_ld64(lanes + scol, s);
-          tmem_ld64(lanes + scol + 64, s + 64);
-          const int valid = k_end - (k_begin + j * C::BK);
+          tmem_ld64(scol, s);
+          tmem_ld64(scol + 64, s + 64);
           if (valid < C::BK) {
 #pragma unroll
             for (int k = 0; k < 128; ++k) s[k] = k < valid ? s[k] : -INFINITY;
           }
           // row maximum on the raw scores (the scale is positive)
-          float m8[8];
+          float m4[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) m8[i] = fmaxf(s[i], s[8 + i]);
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(s[i], s[4 + i]);
 #pragma unroll
-          for (int k = 16; k < 128; k += 8)
+          for (int k = 8; k < 128; k += 8)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[k + i]);
-          const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                 fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * sl2;
+            for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[k + i], s[k + 4 + i]);
+          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * sl2;
           float alpha = 1.f;
           bool rescale = false;
           if (mx > m_ref + C::RESCALE_LOG2 || (m_ref == -INFINITY && mx != -INFINITY)) {
@@ -389,34 +611,32 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
             m_ref = mx;
             l *= alpha;
           }
-          // (PV(j - 1) was issued before the product this S came from: O rests)
+          // (the PV before was issued before the product this S came from: O rests)
           if (__any_sync(kFull, rescale)) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < 128; c0 += 32) {
-              float o[32];
-              tmem_ld32(lanes + ocol + c0, o);
+            for (int c0 = 0; c0 < 128; c0 += 16) {
+              float o[16];
+              tmem_ld16(ocol + c0, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tmem_st32(lanes + ocol + c0, o);
+              for (int i = 0; i < 16; ++i) o[i] *= alpha;
+              tmem_st16(ocol + c0, o);
             }
           }
           const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[32];
+          for (int q = 0; q < 8; ++q) {
+            uint32_t pk[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float& x = s[64 * c + 2 * i];
-              float& y = s[64 * c + 2 * i + 1];
+            for (int i = 0; i < 8; ++i) {
+              float x = s[16 * q + 2 * i], y = s[16 * q + 2 * i + 1];
               fma2(x, y, sl2, nm);
               x = ex2(x);
               y = ex2(y);
-              l4[(2 * i) & 3] += x;
-              l4[(2 * i + 1) & 3] += y;
+              add2(l4[(2 * i) & 3], l4[(2 * i + 1) & 3], x, y);
               pk[i] = pack_bf16(x, y);
             }
-            tmem_st32u(lanes + scol + 32 * c, pk);
+            tmem_st8(scol + 8 * q, pk);
           }
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
           tmem_wait_st();
@@ -424,89 +644,108 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
         tc_fence_before();
         mbar_arrive(bar(B_P + t));
       }
-      if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
 
-      // ---- epilogue
-      if (t < blocks) {
-        bool have = ok && nblk > 0;
-        if (have && !__all_sync(kFull, mbar_wait(bar(B_O + t), 0))) {
-          have = false;
-          if (lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
-        }
-        if (have) tc_fence_after();
+      // ---- the piece's result
+      if (ok && pc.nblk > 0) ok = __all_sync(kFull, mbar_wait(bar(B_O + t), n_o++ & 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (any) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse = l > 0.f ? (m_ref + lg2(l)) * kLn2 : -INFINITY;
-        const size_t part = size_t(split) * a.n_tokens * a.Hq + out_row;
-        if (any) {
+        const bool whole = pc.starts && pc.ends;
+        const size_t part = (size_t(blockIdx.x) * 2 + (pc.starts ? 1 : 0)) * a.part_rows + row;
+        const size_t out_row = (size_t(pc.first) + tok) * a.Hq + size_t(pc.h) * a.G + g;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            float o[32];
-            if (have) {
-              tmem_ld32(lanes + ocol + c0, o);
-            } else {
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          float o[32];
+          if (pc.nblk > 0) {
+            tmem_ld32(ocol + c0, o);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
-            if (!live) continue;
-            if (a.splits == 1) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128 + c0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                    pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                    pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                    pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(a.o_part + part * 128 + c0);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-            }
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
           }
-          if (live) {
-            if (a.splits > 1) a.lse_part[part] = lse;
-            else if (a.lse) a.lse[out_row] = lse;
+          if (!live) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128 + c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                  pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                  pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.o_part + part * 128 + c0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
           }
+        }
+        if (live) {
+          if (!whole) a.lse_part[part] = lse;
+          else if (a.lse) a.lse[out_row] = lse;
         }
       }
     }
+    if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
   }
 
   // ---- teardown: TMEM is freed by the warp that allocated it
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == C::PRODUCER) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
-// Joins the splits: a warp per (token, query head), four dims per lane.
-// Tokens of no sequence are left as they are.
+// Joins the parts of the items that lie in more than one CTA's part of the
+// line: a warp per (token, query head), four dims per lane.  Tokens of no
+// sequence are left as they are.
 __global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
   launch_dependents();
   wait_prerequisites();
   const int64_t rows = int64_t(a.n_tokens) * a.Hq, r = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
-  if (a.cu && (r < int64_t(a.cu[0]) * a.Hq || r >= int64_t(a.cu[a.batch]) * a.Hq)) return;
-  const float ls = lane < a.splits ? a.lse_part[int64_t(lane) * rows + r] : -INFINITY;
-  float M = ls;
+  const int n = int(r / a.Hq), head = int(r - int64_t(n) * a.Hq);
+  int b = -1;
+  if (a.cu) {
+    int ended = 0;  // sequences whose tokens end at or before n
+    for (int b0 = 0; b0 < a.batch; b0 += 32)
+      ended += __popc(__ballot_sync(kFull, b0 + lane < a.batch && a.cu[b0 + lane + 1] <= n));
+    if (ended < a.batch && a.cu[0] <= n) b = ended;
+  } else {
+    b = n / a.T;
+  }
+  if (b < 0) return;
+  int64_t origin;
+  int found, first;
+  const int64_t W = survey(a, lane, 0, b, &origin, &found), parts = parts_of(a, W);
+  tokens_of(a, b, &first);
+  const int h = head / a.G, row = (n - first) * a.G + head - h * a.G;
+  const int nb = blocks_of(keys_of(a, b)), tile = row / Cross::ROWS, in = row - tile * Cross::ROWS;
+  const int64_t o = origin + (int64_t(h) * tiles_of(a, b) + tile) * nb;
+  // the CTA of place o is the last whose part begins at or before it
+  const int c0 = int(((o + 1) * parts - 1) / W), c1 = int(((o + nb) * parts - 1) / W);
+  if (c0 == c1) return;  // written by that CTA
+  auto slot = [&](int c) { return (size_t(c) * 2 + (c == c0 ? 1 : 0)) * a.part_rows + in; };
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.lse_part[slot(c)]);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-  const float w = M == -INFINITY ? 0.f : ex2((ls - M) * 1.4426950408889634f);
-  float sum = w;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+  float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < a.splits; ++s) {
-    const float ws = __shfl_sync(kFull, w, s);
-    if (ws == 0.f) continue;  // (a part without keys may hold anything)
-    const float4 x = *reinterpret_cast<const float4*>(a.o_part + (s * rows + r) * 128 + lane * 4);
-    acc.x += ws * x.x;
-    acc.y += ws * x.y;
-    acc.z += ws * x.z;
-    acc.w += ws * x.w;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const size_t s = slot(c);
+    const float ls = a.lse_part[s];
+    const float4 x = *reinterpret_cast<const float4*>(a.o_part + s * 128 + lane * 4);
+    const float w = M == -INFINITY ? 0.f : ex2((ls - M) * 1.4426950408889634f);
+    sum += w;
+    acc.x += w * x.x;
+    acc.y += w * x.y;
+    acc.z += w * x.z;
+    acc.w += w * x.w;
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   uint2 v;
@@ -525,23 +764,16 @@ int64_t cross_row_tiles(const splitkv_desc_t& d, int64_t n_tokens) {
   return full + some;
 }
 
-// Key splits.  A CTA has an SM to itself; the call lasts as long as the SM
-// with most work, in key blocks, plus about four blocks' time for a CTA's
-// start and end and, with more than one split, two for the merge.
-int cross_splits(const splitkv_desc_t& d, int64_t n_tokens) {
-  const int64_t ctas = cross_row_tiles(d, n_tokens) * d.num_kv_heads;
-  const int64_t blocks = (int64_t(d.max_pages_per_seq) * d.page_size + Cross::BK - 1) / Cross::BK;
-  int best = 1;
-  int64_t least = INT64_MAX;
-  for (int s = 1; s <= kMaxCrossSplits && s <= blocks; ++s) {
-    const int64_t waves = (ctas * s + kSmCount - 1) / kSmCount;
-    const int64_t cost = waves * ((blocks + s - 1) / s + 4) + (s > 1 ? 2 : 0);
-    if (cost < least) {
-      least = cost;
-      best = s;
-    }
-  }
-  return best;
+// CTAs that share the line of key blocks, or 0: a CTA per item.  With four
+// items per SM the unequal ends of a grid of items cost less than an eighth,
+// and the items of a head run side by side, so that its K and V come from L2.
+int cross_parts(const splitkv_desc_t& d, int64_t n_tokens) {
+  return cross_row_tiles(d, n_tokens) * d.num_kv_heads >= 4 * kSmCount ? 0 : kSmCount;
+}
+
+int cross_part_rows(const splitkv_desc_t& d, int64_t n_tokens) {
+  const int64_t rows = n_tokens * (d.num_q_heads / d.num_kv_heads);
+  return int(rows < Cross::ROWS ? rows : Cross::ROWS);
 }
 
 int cross_box_rows(const splitkv_desc_t& d) {
@@ -559,7 +791,7 @@ cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& t
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(row_tiles), unsigned(a.Hkv), unsigned(a.splits));
+  cfg.gridDim = a.parts ? dim3(unsigned(a.parts), 1, 1) : dim3(unsigned(row_tiles), unsigned(a.Hkv), 1);
   cfg.blockDim = dim3(Cross::THREADS, 1, 1);
   cfg.dynamicSmemBytes = Cross::SMEM;
   cfg.stream = s;
@@ -567,7 +799,7 @@ cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& t
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, cross_attend_kernel, a, *reinterpret_cast<const CUtensorMap*>(&tk),
                                      *reinterpret_cast<const CUtensorMap*>(&tv));
-  if (e != cudaSuccess || a.splits == 1) return e;
+  if (e != cudaSuccess || a.parts == 0) return e;
   cfg.gridDim = dim3(unsigned((int64_t(a.n_tokens) * a.Hq + 3) / 4), 1, 1);
   cfg.blockDim = dim3(128, 1, 1);
   cfg.dynamicSmemBytes = 0;

@@ -220,8 +220,7 @@ struct EvictArgs {
   int32_t k_row, v_row;   // bytes of one key's row
 };
 
-constexpr int kMaxCrossSplits = 16;  // key splits of cross attention
-constexpr int kSmCount = 152;        // SMs that cross attention plans for
+constexpr int kSmCount = 152;  // SMs that cross attention plans for
 
 struct CrossArgs {
   const void* q;
@@ -230,19 +229,22 @@ struct CrossArgs {
   const int32_t* seq_lens;
   void* out;
   float* lse;         // or null
-  float* o_part;      // [splits][n_tokens * Hq][128], with more than one split
-  float* lse_part;    // [splits][n_tokens * Hq]
+  float* o_part;      // [2 parts][part_rows][128]: two partial results of a CTA
+  float* lse_part;    // [2 parts][part_rows]
   int32_t* status;    // or null
   int64_t q_stride;   // elements per token
   float qk_scale_log2;
-  int32_t n_tokens, batch, T, Hq, Hkv, G, P, max_pages, num_pages, splits, box_rows;
+  int32_t n_tokens, batch, T, Hq, Hkv, G, P, max_pages, num_pages, box_rows;
+  int32_t parts;      // CTAs that share all items' key blocks; 0: a CTA per item
+  int32_t part_rows;  // rows of an item, at most
 };
 
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream);
 cudaError_t launch_key_weights(const WeightArgs& a, bool fp8, void* stream);
 cudaError_t launch_evict(const EvictArgs& a, void* stream);
 int64_t cross_row_tiles(const splitkv_desc_t& d, int64_t n_tokens);
-int cross_splits(const splitkv_desc_t& d, int64_t n_tokens);
+int cross_parts(const splitkv_desc_t& d, int64_t n_tokens);
+int cross_part_rows(const splitkv_desc_t& d, int64_t n_tokens);
 int cross_box_rows(const splitkv_desc_t& d);  // keys of one TMA box
 cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv,
                          void* stream);

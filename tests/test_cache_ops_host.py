@@ -186,7 +186,7 @@ def test_cross_refuses_other_caches_and_small_workspaces():
     refused(EUNSUPPORTED, call_cross, desc(Hq=128, Hkv=1, Dk=576, Dv=512, shares=1))
     d = desc(B=1, Hkv=1, maxp=512)  # one row tile over 8192 slots: split
     need = skv.splitkv_cross_workspace_size(d, 1)
-    assert need >= 2 * 8 * 129 * 4
+    assert need >= 2 * 8 * 129 * 4  # two partial results at least
     refused(EWORKSPACE, call_cross, d, workspace=None, workspace_bytes=0)
     refused(EWORKSPACE, call_cross, d, workspace_bytes=need - 1)
     refused(EINVAL, call_cross, d, workspace=A + 8)
