@@ -349,7 +349,8 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
 
 size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
   if (validate_cross(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
-  return align256(size_t(2) * cross_parts(*desc, n_tokens) * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float));
+  const size_t parts = size_t(cross_parts(*desc, n_tokens));
+  return align256(2 * parts * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float)) + align256(parts * sizeof(CrossSplit));
 }
 
 splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens,
@@ -389,6 +390,8 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
       return fail(SPLITKV_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
     a.o_part = static_cast<float*>(workspace);
     a.lse_part = a.o_part + size_t(2) * a.parts * a.part_rows * 128;
+    a.split = reinterpret_cast<CrossSplit*>(static_cast<unsigned char*>(workspace) + need -
+                                            align256(size_t(a.parts) * sizeof(CrossSplit)));
   }
   a.q = q;
   a.cu = cu_tokens;

@@ -154,34 +154,58 @@ __device__ __forceinline__ bool next_piece(const CrossArgs& a, Place& p, Piece& 
   return true;
 }
 
-// By a warp: the length of the line, and the first place of sequence `want`
-// or of the sequence that place `at` lies in (b = that sequence; -1: none).
-__device__ __forceinline__ int64_t survey(const CrossArgs& a, int lane, int64_t at, int want, int64_t* origin, int* b) {
-  int64_t total = 0;
-  *b = -1;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+// CTAs that share a line of W key blocks: two blocks each at least.
+__device__ __forceinline__ int64_t parts_of(const CrossArgs& a, int64_t W) {
+  return max(int64_t(1), min(int64_t(a.parts), W / 2));
+}
+
+// By a warp: the part of CTA `c` of the line (w == w1: none).
+__device__ __forceinline__ Place find_part(const CrossArgs& a, int c, int lane) {
+  Place p;
+  p.w = p.w1 = 0;
+  p.b = p.h = p.tile = p.block = 0;
+  // blocks of 32 sequences at a time: their total first, then the sequence
+  // that holds the part's first block (a batch of up to 32 is read once)
+  int tiles = 0, nb = 1;
+  int64_t n = 0, W = 0, x = 0;
+  auto read = [&](int b0) {
     const int bl = b0 + lane;
-    const int64_t n = bl < a.batch ? int64_t(tiles_of(a, bl)) * a.Hkv * blocks_of(keys_of(a, bl)) : 0;
-    int64_t x = n;
+    tiles = bl < a.batch ? tiles_of(a, bl) : 0;
+    nb = bl < a.batch ? blocks_of(keys_of(a, bl)) : 1;
+    n = int64_t(tiles) * a.Hkv * nb;
+    x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(kFull, x, o);
       if (lane >= o) x += y;
     }
-    const unsigned hit = __ballot_sync(kFull, want >= 0 ? bl == want : total + x > at);
-    if (hit && *b < 0) {
-      const int f = __ffs(hit) - 1;
-      *b = b0 + f;
-      *origin = total + __shfl_sync(kFull, x - n, f);
-    }
-    total += __shfl_sync(kFull, x, 31);
+  };
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    read(b0);
+    W += __shfl_sync(kFull, x, 31);
   }
-  return total;
-}
-
-// CTAs that share a line of W key blocks: two blocks each at least.
-__device__ __forceinline__ int64_t parts_of(const CrossArgs& a, int64_t W) {
-  return max(int64_t(1), min(int64_t(a.parts), W / 2));
+  const int64_t parts = parts_of(a, W);
+  if (c >= parts || W == 0) return p;
+  p.w = W * c / parts;
+  p.w1 = W * (c + 1) / parts;
+  int64_t before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    if (a.batch > 32) read(b0);
+    const unsigned past = __ballot_sync(kFull, before + x > p.w);
+    if (past) {
+      const int f = __ffs(past) - 1;
+      const int in = int(p.w - before - __shfl_sync(kFull, x - n, f));  // of the sequence's blocks
+      tiles = __shfl_sync(kFull, tiles, f);
+      nb = __shfl_sync(kFull, nb, f);
+      const int item = in / nb;
+      p.b = b0 + f;
+      p.block = in - item * nb;
+      p.h = item / tiles;
+      p.tile = item - p.h * tiles;
+      return p;
+    }
+    before += __shfl_sync(kFull, x, 31);
+  }
 }
 
 // 64 consecutive fp32 columns of this warp's 32 TMEM lanes (one lane per thread).
@@ -371,23 +395,11 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   wait_prerequisites();
   if (warp == C::ISSUER) {
     Place p;
-    p.w = p.w1 = 0;
-    p.b = p.h = p.tile = p.block = 0;
-    int64_t origin = 0;
     if (a.parts > 0) {
-      int b;
-      const int64_t W = survey(a, lane, INT64_MAX, -1, &origin, &b), n = parts_of(a, W);
-      if (blockIdx.x < n && W > 0) {
-        p.w = W * blockIdx.x / n;
-        p.w1 = W * (blockIdx.x + 1) / n;
-        survey(a, lane, p.w, -1, &origin, &p.b);
-        const int nb = blocks_of(keys_of(a, p.b)), tiles = tiles_of(a, p.b);
-        const int64_t item = (p.w - origin) / nb;
-        p.block = int(p.w - origin - item * nb);
-        p.h = int(item / tiles);
-        p.tile = int(item - int64_t(p.h) * tiles);
-      }
+      p = find_part(a, blockIdx.x, lane);
     } else {
+      p.w = p.w1 = 0;
+      p.b = p.h = p.tile = p.block = 0;
       // a CTA per item: row tile blockIdx.x of all sequences' (the grid counts
       // tiles for any split of the tokens among the sequences), head blockIdx.y
       int before = 0;
@@ -478,6 +490,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     bool ok = true;
     int item = 0;                      // ring items consumed
     uint32_t n_q = 0, n_p = 0;  // phases of B_Q and B_P so far, a bit per row block
+    CrossSplit split = {0, 0, 0, 0, 0, 0};
     auto wait = [&](int i, int phase) {
       ok = ok && __all_sync(kFull, mbar_wait(bar(i), phase & 1));
       return ok;
@@ -489,14 +502,22 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
              idesc_qk);
       umma_commit_warp(bar(B_S + t));
     };
-    auto pv = [&](int t, int i, bool more, bool last) {  // O_t (+)= P_t . V, V in ring item i
+    auto pv = [&](int t, int i, bool more) {  // O_t (+)= P_t . V, V in ring item i
       mma_pv(tmem + C::O_COL + 128 * t, tmem + C::S_COL + 128 * t, umma_desc(slot(i), C::HALF, 1024, 2), idesc_pv, more);
-      if (last) umma_commit_warp(bar(B_O + t));
     };
     auto release = [&](int i) {
       umma_commit_warp(bar(B_EMPTY + i % C::NST));
     };
     while (ok && next_piece(a, place, pc)) {
+      if (pc.starts && !pc.ends) {
+        split.begins = 1;
+        split.first = pc.first;
+        split.head = pc.h;
+        split.row0 = pc.row0;
+        split.rows = min(pc.n_rows, C::ROWS);
+      } else if (!pc.starts && pc.ends) {
+        split.ends = 1;
+      }
       if (pc.nblk == 0) continue;
       const int blocks = pc.n_rows > 128 ? 2 : 1;  // row blocks with rows
       for (int t = 0; t < blocks && ok; ++t) {
@@ -531,20 +552,28 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
           if (!wait(B_P + t, n_p >> t)) break;
           n_p ^= 1u << t;
           tc_fence_after();
-          pv(t, iv, j > 0, j == pc.nblk - 1);
-          if (t == blocks - 1) release(iv);
+          pv(t, iv, j > 0);
           if (j + 1 < pc.nblk) {
-            if (!k_in && !wait(B_FULL + ik % C::NST, ik / C::NST)) break;
-            k_in = true;
-            tc_fence_after();
+            if (!k_in) {
+              if (!wait(B_FULL + ik % C::NST, ik / C::NST)) break;
+              tc_fence_after();
+              k_in = true;
+            }
             qk(t, ik);
-            if (t == blocks - 1) release(ik);
+          } else {
+            umma_commit_warp(bar(B_O + t));
+          }
+          // (behind the products, which are not to wait for it)
+          if (t == blocks - 1) {
+            release(iv);
+            if (j + 1 < pc.nblk) release(ik);
           }
         }
       }
       item += 2 * pc.nblk;
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
+    if (a.parts > 0 && lane == 0) a.split[blockIdx.x] = split;
     // every MMA issued above completes before TMEM is released
     umma_commit_warp(bar(B_DONE));
     __syncwarp();
@@ -560,26 +589,57 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     const float sl2 = a.qk_scale_log2;
     uint32_t n_s = 0, n_o = 0;  // phases of B_S and B_O so far
     bool ok = true;
-    while (ok && next_piece(a, place, pc)) {
-      if (t == 1 && pc.n_rows <= 128) continue;
-      const bool live = row < pc.n_rows;
-      const bool any = __any_sync(kFull, live);  // a warp without rows only keeps step
-      const int tok = (pc.row0 + row) / a.G, g = (pc.row0 + row) - tok * a.G;
-      if (pc.nblk > 0) {
-        // this row of Q, swizzled; rows behind the last are zero (the products
-        // that read the Q before are done: B_O)
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                          (int64_t(pc.first) + tok) * a.q_stride +
-                                                          (pc.h * a.G + g) * 128);
-        uint8_t* dst = sm + t * C::TILE + r * 128;
+    // 16-byte chunk `ch` of row `rr` of the row block's Q in shared memory.
+    auto chunk_at = [&](int rr, int ch) -> uint8_t* {
+      return sm + t * C::TILE + (ch >> 3) * C::HALF + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
+    };
+    // Visits this warp's 32 rows of a piece, 16 lanes to a row: body(i, row of
+    // the row block, whether it exists, its token and head).
+    auto each_row = [&](const Piece& q, auto&& body) {
+      int rr = (warp & 3) * 32 + (lane >> 4);
+      const int first = q.row0 + t * 128 + rr;
+      int tok = first / a.G, g = first - tok * a.G;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint4 x = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * C::HALF + (((i & 7) ^ (r & 7)) << 4)) = x;
+      for (int i = 0; i < 16; ++i, rr += 2) {
+        body(i, rr, t * 128 + rr < q.n_rows, int64_t(q.first) + tok, q.h * a.G + g);
+        g += 2;
+        while (g >= a.G) {
+          g -= a.G;
+          ++tok;
         }
+      }
+    };
+    // The query rows of this warp, 16 lanes to a row, swizzled; rows behind
+    // the last are zero.  Called when the products that read the Q before are
+    // done (S of the last block has arrived); false: no piece, or none of
+    // this row block's.
+    auto take_piece = [&](Piece& q) {
+      do {
+        if (!next_piece(a, place, q)) return false;
+      } while (t == 1 && q.n_rows <= 128);
+      if (q.nblk > 0) {
+        uint4 x[16];
+        each_row(q, [&](int i, int rr, bool in, int64_t token, int head) {
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (in)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + token * a.q_stride +
+                                                        head * 128) + (lane & 15));
+        });
+#pragma unroll
+        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(chunk_at((warp & 3) * 32 + 2 * i + (lane >> 4), lane & 15)) = x[i];
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
         mbar_arrive(bar(B_Q + t));
       }
+      return true;
+    };
+    Piece nx;
+    bool more = take_piece(nx);
+    while (ok && more) {
+      pc = nx;
+      const bool live = row < pc.n_rows;
+      const bool any = __any_sync(kFull, live);  // a warp without rows only keeps step
+      const bool whole = pc.starts && pc.ends;
       float m_ref = -INFINITY, l = 0.f;
       int valid = pc.L - pc.j0 * C::BK;  // keys from the block's first on
       for (int j = 0; j < pc.nblk; ++j, valid -= C::BK) {
@@ -645,16 +705,19 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
         mbar_arrive(bar(B_P + t));
       }
 
-      // ---- the piece's result
-      if (ok && pc.nblk > 0) ok = __all_sync(kFull, mbar_wait(bar(B_O + t), n_o++ & 1));
+      // ---- the piece's result.  A partial one goes straight from registers
+      // (its layout puts a column's rows side by side), with the next piece's
+      // Q already under way; a whole one through this warp's rows of Q's
+      // shared memory, so that whole rows are written.
+      if (!ok) break;
+      if (!whole) more = take_piece(nx);
+      if (pc.nblk > 0) ok = __all_sync(kFull, mbar_wait(bar(B_O + t), n_o++ & 1));
       if (!ok) break;
       tc_fence_after();
       if (any) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse = l > 0.f ? (m_ref + lg2(l)) * kLn2 : -INFINITY;
-        const bool whole = pc.starts && pc.ends;
-        const size_t part = (size_t(blockIdx.x) * 2 + (pc.starts ? 1 : 0)) * a.part_rows + row;
-        const size_t out_row = (size_t(pc.first) + tok) * a.Hq + size_t(pc.h) * a.G + g;
+        const size_t slot = size_t(blockIdx.x) * 2 + (pc.starts ? 1 : 0);
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
           float o[32];
@@ -664,27 +727,39 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0.f;
           }
-          if (!live) continue;
           if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128 + c0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                  pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                  pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.o_part + part * 128 + c0);
+            for (int i = 0; i < 4; ++i) {
+              *reinterpret_cast<uint4*>(chunk_at(r, c0 / 8 + i)) =
+                  make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                             pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                             pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                             pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            }
+          } else if (live) {
+            float4* dst = reinterpret_cast<float4*>(a.o_part) + (slot * 32 + c0 / 4) * a.part_rows + row;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+              dst[size_t(i) * a.part_rows] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
           }
         }
-        if (live) {
-          if (!whole) a.lse_part[part] = lse;
-          else if (a.lse) a.lse[out_row] = lse;
+        if (whole) {
+          __syncwarp();
+          each_row(pc, [&](int, int rr, bool in, int64_t token, int head) {
+            if (in)
+              reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (token * a.Hq + head) * 128)[lane & 15] =
+                  *reinterpret_cast<const uint4*>(chunk_at(rr, lane & 15));
+          });
+          __syncwarp();
+          if (live && a.lse) {
+            const int tok = (pc.row0 + row) / a.G, g = (pc.row0 + row) - tok * a.G;
+            a.lse[(size_t(pc.first) + tok) * a.Hq + size_t(pc.h) * a.G + g] = lse;
+          }
+        } else if (live) {
+          a.lse_part[slot * a.part_rows + row] = lse;
         }
       }
+      if (whole) more = take_piece(nx);
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
   }
@@ -698,61 +773,68 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   }
 }
 
-// Joins the parts of the items that lie in more than one CTA's part of the
-// line: a warp per (token, query head), four dims per lane.  Tokens of no
-// sequence are left as they are.
-__global__ void __launch_bounds__(128) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
+// Joins the partial results of an item that CTA blockIdx.x began and did not
+// finish: those of that CTA (its slot 1) and of the following ones (their slot
+// 0) up to the one that ended it.  32 rows of the item, a lane each; a warp
+// takes every eighth group of four dims, read side by side for the rows.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
+  __shared__ uint2 rows_out[32][33];  // bf16 rows (of 32 pieces of 8 bytes, and one to spread the banks)
   launch_dependents();
   wait_prerequisites();
-  const int64_t rows = int64_t(a.n_tokens) * a.Hq, r = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (r >= rows) return;
-  const int n = int(r / a.Hq), head = int(r - int64_t(n) * a.Hq);
-  int b = -1;
-  if (a.cu) {
-    int ended = 0;  // sequences whose tokens end at or before n
-    for (int b0 = 0; b0 < a.batch; b0 += 32)
-      ended += __popc(__ballot_sync(kFull, b0 + lane < a.batch && a.cu[b0 + lane + 1] <= n));
-    if (ended < a.batch && a.cu[0] <= n) b = ended;
-  } else {
-    b = n / a.T;
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CrossSplit sp = a.split[c];
+  const int r0 = blockIdx.y * 32, row = r0 + lane;
+  if (!sp.begins || r0 >= sp.rows) return;
+  int last = c;  // the CTA that ended the item
+  for (int k = c + 1; last == c && k < a.parts; k += 32) {
+    const unsigned m = __ballot_sync(kFull, k + lane < a.parts && a.split[k + lane].ends);
+    if (m) last = k + __ffs(m) - 1;
   }
-  if (b < 0) return;
-  int64_t origin;
-  int found, first;
-  const int64_t W = survey(a, lane, 0, b, &origin, &found), parts = parts_of(a, W);
-  tokens_of(a, b, &first);
-  const int h = head / a.G, row = (n - first) * a.G + head - h * a.G;
-  const int nb = blocks_of(keys_of(a, b)), tile = row / Cross::ROWS, in = row - tile * Cross::ROWS;
-  const int64_t o = origin + (int64_t(h) * tiles_of(a, b) + tile) * nb;
-  // the CTA of place o is the last whose part begins at or before it
-  const int c0 = int(((o + 1) * parts - 1) / W), c1 = int(((o + nb) * parts - 1) / W);
-  if (c0 == c1) return;  // written by that CTA
-  auto slot = [&](int c) { return (size_t(c) * 2 + (c == c0 ? 1 : 0)) * a.part_rows + in; };
+  const bool live = row < sp.rows;
+  auto slot = [&](int k) { return size_t(k) * 2 + (k == c ? 1 : 0); };
   float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.lse_part[slot(c)]);
-#pragma unroll
-  for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const size_t s = slot(c);
-    const float ls = a.lse_part[s];
-    const float4 x = *reinterpret_cast<const float4*>(a.o_part + s * 128 + lane * 4);
+  for (int k = c; k <= last; ++k)
+    if (live) M = fmaxf(M, a.lse_part[slot(k) * a.part_rows + row]);
+  float sum = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = c; k <= last; ++k) {
+    if (!live) continue;
+    const float ls = a.lse_part[slot(k) * a.part_rows + row];
+    const float4* src = reinterpret_cast<const float4*>(a.o_part) + (slot(k) * 32 + warp) * a.part_rows + row;
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = src[size_t(i) * kMergeWarps * a.part_rows];
     const float w = M == -INFINITY ? 0.f : ex2((ls - M) * 1.4426950408889634f);
     sum += w;
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[i].x += w * x[i].x;
+      acc[i].y += w * x[i].y;
+      acc[i].z += w * x[i].z;
+      acc[i].w += w * x[i].w;
+    }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint2 v;
-  v.x = pack_bf16(acc.x * inv, acc.y * inv);
-  v.y = pack_bf16(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + r * 128 + lane * 4) = v;
-  if (lane == 0 && a.lse) a.lse[r] = sum > 0.f ? M + lg2(sum) * kLn2 : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    rows_out[lane][warp + i * kMergeWarps] =
+        make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+  __syncthreads();
+  // whole rows out, a warp to a row
+  for (int i = warp; i < 32 && r0 + i < sp.rows; i += kMergeWarps) {
+    const int tok = (sp.row0 + r0 + i) / a.G, g = (sp.row0 + r0 + i) - tok * a.G;
+    const size_t out_row = (size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g;
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128)[lane] = rows_out[i][lane];
+  }
+  if (warp == 0 && live && a.lse) {
+    const int tok = (sp.row0 + row) / a.G, g = (sp.row0 + row) - tok * a.G;
+    a.lse[(size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g] = sum > 0.f ? M + lg2(sum) * kLn2 : -INFINITY;
+  }
 }
 
 }  // namespace
@@ -800,8 +882,8 @@ cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& t
   cudaError_t e = cudaLaunchKernelEx(&cfg, cross_attend_kernel, a, *reinterpret_cast<const CUtensorMap*>(&tk),
                                      *reinterpret_cast<const CUtensorMap*>(&tv));
   if (e != cudaSuccess || a.parts == 0) return e;
-  cfg.gridDim = dim3(unsigned((int64_t(a.n_tokens) * a.Hq + 3) / 4), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3(unsigned(a.parts), unsigned((a.part_rows + 31) / 32), 1);
+  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, cross_merge_kernel, a);
 }

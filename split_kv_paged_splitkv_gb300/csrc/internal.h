@@ -222,6 +222,13 @@ struct EvictArgs {
 
 constexpr int kSmCount = 152;  // SMs that cross attention plans for
 
+// The item that a CTA of cross attention begins and does not finish, and
+// whether it ends an item that an earlier CTA began.
+struct CrossSplit {
+  int32_t begins, first, head, row0, rows;  // first: token of the sequence
+  int32_t ends;
+};
+
 struct CrossArgs {
   const void* q;
   const int32_t* cu;  // [batch + 1] or null: T tokens per sequence
@@ -229,8 +236,10 @@ struct CrossArgs {
   const int32_t* seq_lens;
   void* out;
   float* lse;         // or null
-  float* o_part;      // [2 parts][part_rows][128]: two partial results of a CTA
+  float* o_part;      // [2 parts][32][part_rows][4]: two partial results of a CTA, in
+                      //   groups of four dims
   float* lse_part;    // [2 parts][part_rows]
+  CrossSplit* split;  // [parts]
   int32_t* status;    // or null
   int64_t q_stride;   // elements per token
   float qk_scale_log2;
