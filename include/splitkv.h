@@ -492,8 +492,8 @@ void splitkv_rope_destroy(splitkv_rope_t* rope);
  *   positions      int32 [n_axes][n_tokens]; may be NULL without rope and
  *                  key_positions (one axis without rope)
  *   q              bf16, token n's heads [Hq][Dk] at q + n * q_stride (strides
- *                  in elements, multiples of 8: the three may be columns of
- *                  one buffer); NULL with q_out: keys alone
+ *                  in elements, multiples of 8 below 2^31: the three may be
+ *                  columns of one buffer); NULL with q_out: keys alone
  *   k, v           bf16 [Hkv][Dk] and [Hkv][Dv] per token; v NULL with
  *                  v_shares_k
  *   kv_scale, k_scale, v_scale  e4m3 caches store round(x / scale) with

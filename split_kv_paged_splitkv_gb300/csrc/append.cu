@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                                                           int tok_per_cta) {
   constexpr int UK = DK / 16, UV = DV / 16;  // units of a q or k row, of a v row
   __shared__ Token tok[kMaxTok];
-  __shared__ float2 cs[kMaxTok * kMaxRotPairs];  // (cos, sin) of each pair
+  // Cosines and sines of two pairs of a chunk to a float4 (c, c, s, s), the
+  // chunks of a row side by side: its lanes read consecutive 16 bytes.
+  __shared__ float4 cs[kMaxTok * kMaxRotPairs / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   launch_dependents();
@@ -92,6 +94,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int total = ntok * per_tok;
   const int rot0 = a.rope.rot_offset / 8, rotc = a.rope.rot_dim / 8;  // rotated chunks
   const bool halves = a.rope.pairing == SPLITKV_ROPE_HALVES;
+  const int chunk_pairs = halves ? 8 : 4, turned = half / chunk_pairs;  // pairs of a chunk, chunks with own pairs
 
   // Chunks of unit u of a row: the two halves of eight pairs while u counts
   // rotated pairs half a row apart, then the other chunks in order.
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   };
   // Unit i of the CTA: kind 0 q, 1 k, 2 v; token, head row, chunks.
   auto unit = [&](int i, int& kind, int& t, int& row, int& c0, int& c1) {
-    t = i / per_tok;
+    t = int(__umulhi(unsigned(i), a.per_tok_magic));  // i / per_tok
     int u = i - t * per_tok;
     kind = u < qu ? 0 : u < qu + ku ? 1 : 2;
     if (kind < 2) {
@@ -125,22 +128,29 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       c1 = c0 + 1;
     }
   };
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + int64_t(n0) * a.q_stride;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + int64_t(n0) * a.k_stride;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + int64_t(n0) * a.v_stride;
+  __nv_bfloat16* q_out = static_cast<__nv_bfloat16*>(a.q_out) + int64_t(n0) * a.q_out_stride;
 
   bool ready = false;
   for (int base = blockIdx.y * (U * kThreads); base < total || !ready; base += gridDim.y * (U * kThreads)) {
     // The tokens' own rows first (those of padding are within the inputs
     // too): they are in flight while the tokens' places are looked up.
     uint4 x0[U], x1[U];
+    uint32_t tag[U];  // token, kind, first chunk, second chunk (5, 2, 7, 7 bits)
+    int rows[U];
 #pragma unroll
     for (int r = 0; r < U; ++r) {
       const int i = base + r * kThreads + threadIdx.x;
+      tag[r] = ~0u;
       if (i >= total) continue;
-      int kind, t, row, c0, c1;
-      unit(i, kind, t, row, c0, c1);
-      const void* from = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-      const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(from) +
-                                                        int64_t(n0 + t) * stride + row * (kind < 2 ? DK : DV));
+      int kind, t, c0, c1;
+      unit(i, kind, t, rows[r], c0, c1);
+      tag[r] = t | kind << 5 | c0 << 7 | c1 << 14;
+      const __nv_bfloat16* from = kind == 0 ? q : kind == 1 ? k : v;
+      const int stride = int(kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride);  // (below 2^31)
+      const uint4* src = reinterpret_cast<const uint4*>(from + int64_t(t) * stride + rows[r] * (kind < 2 ? DK : DV));
       x0[r] = src[c0];
       x1[r] = src[c1];
     }
@@ -181,7 +191,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         const uint64_t phase = uint64_t(pos) * a.rope.turns[p];
         float s, c;
         sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s, &c);
-        cs[t * kMaxRotPairs + p] = make_float2(c, s);
+        const int ch = p / chunk_pairs, e = p - ch * chunk_pairs;
+        float* z = reinterpret_cast<float*>(cs + t * (kMaxRotPairs / 2) + (e >> 1) * turned + ch) + (e & 1);
+        z[0] = c;
+        z[2] = s;
       }
       __syncthreads();
       // the state of the new keys
@@ -197,45 +210,45 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     }
 #pragma unroll
     for (int r = 0; r < U; ++r) {
-      const int i = base + r * kThreads + threadIdx.x;
-      if (i >= total) continue;
-      int kind, t, row, c0, c1;
-      unit(i, kind, t, row, c0, c1);
+      if (tag[r] == ~0u) continue;
+      const int t = tag[r] & 31, kind = tag[r] >> 5 & 3, c0 = tag[r] >> 7 & 127, c1 = tag[r] >> 14 & 127, row = rows[r];
       const Token tk = tok[t];
       if (tk.b < 0 || (kind > 0 && tk.page < 0)) continue;
       float f0[8], f1[8];
       unpack8(x0[r], f0);
       unpack8(x1[r], f1);
       if (kind < 2 && rotc) {
-        const float2* w = cs + t * kMaxRotPairs;
+        const float4* w = cs + t * (kMaxRotPairs / 2);
+        auto turn = [](float& u, float& v, float c, float s) {
+          const float x = u * c - v * s;
+          v = u * s + v * c;
+          u = x;
+        };
         if (halves) {
           if (c0 >= rot0 && c0 < rot0 + rotc) {  // then c1 is the other half of the pairs
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 z = w[(c0 - rot0) * 8 + e];
-              const float u = f0[e], v = f1[e];
-              f0[e] = u * z.x - v * z.y;
-              f1[e] = u * z.y + v * z.x;
+            for (int e = 0; e < 4; ++e) {
+              const float4 z = w[e * turned + c0 - rot0];
+              turn(f0[2 * e], f1[2 * e], z.x, z.z);
+              turn(f0[2 * e + 1], f1[2 * e + 1], z.y, z.w);
             }
           }
         } else {
-          auto turn = [&](float (&f)[8], int c) {
+          auto both = [&](float (&f)[8], int c) {
             if (c < rot0 || c >= rot0 + rotc) return;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 z = w[(c - rot0) * 4 + e];
-              const float u = f[2 * e], v = f[2 * e + 1];
-              f[2 * e] = u * z.x - v * z.y;
-              f[2 * e + 1] = u * z.y + v * z.x;
+            for (int e = 0; e < 2; ++e) {
+              const float4 z = w[e * turned + c - rot0];
+              turn(f[4 * e], f[4 * e + 1], z.x, z.z);
+              turn(f[4 * e + 2], f[4 * e + 3], z.y, z.w);
             }
           };
-          turn(f0, c0);
-          turn(f1, c1);
+          both(f0, c0);
+          both(f1, c1);
         }
       }
       if (kind == 0) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) +
-                                              int64_t(n0 + t) * a.q_out_stride + row * DK);
+        uint4* dst = reinterpret_cast<uint4*>(q_out + int64_t(t) * int(a.q_out_stride) + row * DK);
         dst[c0] = pack8(f0);
         dst[c1] = pack8(f1);
         continue;
@@ -266,8 +279,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 }
 
 template <int DK, int DV, bool FP8, int U>
-cudaError_t launch_append_u(const AppendArgs& a, int per_tok, cudaStream_t s) {
-  constexpr int units = U * kThreads;  // a CTA's
+cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s) {
+  AppendArgs a = args;
+  // i * magic >> 32 is i / per_tok for every unit i of a CTA, as i * per_tok is
+  // below 2^32 or the CTA has one token (0: that token's, however many units)
+  a.per_tok_magic = per_tok > 65536 ? 0 : unsigned(((uint64_t(1) << 32) + per_tok - 1) / per_tok);
+  // A CTA's units.  In a long call two passes share the lookup of the places
+  // and the sines (26k tokens of 40 rows: 99 us, with one pass 106).
+  constexpr int units = (U == 1 ? 1 : 2) * U * kThreads;
   const int tpc = per_tok >= units ? 1 : min(kMaxTok, units / per_tok);
   const int64_t slices = (int64_t(per_tok) * tpc + units - 1) / units;
   cudaLaunchConfig_t cfg = {};

@@ -176,9 +176,12 @@ splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* 
     if (misaligned(p, 4)) return fail(SPLITKV_EINVAL, "index and state arrays must be 4-byte aligned");
   const int64_t q_row = int64_t(d.num_q_heads) * d.qk_dim, k_row = int64_t(d.num_kv_heads) * d.qk_dim,
                 v_row = int64_t(d.num_kv_heads) * d.v_dim;
-  if ((q && (q_stride < q_row || q_stride % 8 || q_out_stride < q_row || q_out_stride % 8)) ||
-      k_stride < k_row || k_stride % 8 || (v && (v_stride < v_row || v_stride % 8)))
-    return fail(SPLITKV_EINVAL, "token strides must be multiples of 8 elements and hold a token's heads");
+  const int64_t big = (int64_t(1) << 31) - 8;
+  if ((q && (q_stride < q_row || q_stride % 8 || q_stride > big || q_out_stride < q_row || q_out_stride % 8 ||
+             q_out_stride > big)) ||
+      k_stride < k_row || k_stride % 8 || k_stride > big || (v && (v_stride < v_row || v_stride % 8 || v_stride > big)))
+    return fail(SPLITKV_EINVAL,
+                "token strides must be multiples of 8 elements, hold a token's heads and be below 2^31");
   if (q && n_tokens > 0 && !(q == q_out && q_stride == q_out_stride) &&
       overlap(q, size_t((n_tokens - 1) * q_stride + q_row) * 2, q_out,
               size_t((n_tokens - 1) * q_out_stride + q_row) * 2))

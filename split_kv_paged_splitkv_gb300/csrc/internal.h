@@ -185,6 +185,7 @@ struct AppendArgs {
   int32_t* status;           // or null
   float kv_scale;
   int32_t n_tokens, batch, T, Hq, Hkv, P, max_pages, num_pages, nhd;
+  uint32_t per_tok_magic;    // set by the launch: 2^32 / units of a token, rounded up
   splitkv_rope_s rope;       // rot_dim 0: nothing is rotated
 };
 
