@@ -9,10 +9,12 @@
 // state), so the kernel lives on bytes in flight.  A warp takes 16 keys of a
 // KV head at a time as the M side of m16n8k16 products with 8 query rows on
 // N.  The order of the 128 dims inside the products is free as long as both
-// operands use the same one, so each lane loads 16-byte pieces of two key
-// rows straight into the registers of its A operand (four lanes read 64
-// consecutive bytes) and query pieces the same way into B: no shared memory,
-// no barrier, and every warp of the SM has its own 4 KB in flight.
+// operands use the same one, so each lane owns 16-byte pieces of two key rows
+// that are its A operand as they lie (four lanes read 64 consecutive bytes),
+// and query pieces chosen the same way are its B operand.  A lane copies its
+// pieces of the next tiles into shared memory asynchronously and reads back
+// only what it copied itself: a ring per warp with no barrier at all, and up
+// to ten tiles of a warp in flight.
 //
 // Work is split by the device lengths: the 16-key tiles of all (sequence, KV
 // head) pairs form one line, cut into equal contiguous parts, one per warp.
@@ -28,6 +30,21 @@ namespace {
 using namespace ptx;
 
 constexpr int kWarps = 4;
+
+// 16 bytes global -> shared, asynchronously, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The length of sequence b, or 0 where the device value is not one the cache
@@ -39,10 +56,14 @@ __device__ __forceinline__ int seq_len(const WeightArgs& a, int b, bool report) 
   return 0;
 }
 
-template <bool FP8, int NRG>
+template <bool FP8, int NRG, int STAGES>
 __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_constant__ WeightArgs a) {
   const int lane = threadIdx.x & 31;
   const int gi = lane >> 2, ci = lane & 3;
+  // this lane's pieces of a tile: piece i of stage s at ring + (s * 2 NC + i) * 512
+  constexpr int NC = FP8 ? 2 : 4;  // 16-byte pieces of a row per lane
+  extern __shared__ __align__(16) uint8_t smem[];
+  const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * (STAGES * 2 * NC * 512) + lane * 16;
   launch_dependents();
   wait_prerequisites();
 
@@ -88,7 +109,6 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
   const int rph = a.T * a.G;
   const size_t cap = size_t(a.max_pages) * a.P;
   constexpr int RB = FP8 ? 128 : 256;      // bytes of a key row
-  constexpr int NC = FP8 ? 2 : 4;          // 16-byte pieces of a row per lane
   const size_t key_step = a.nhd ? size_t(a.Hkv) * RB : RB;
 
   while (i0 < i1) {
@@ -159,11 +179,11 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
         const int r = rg * 8 + 2 * ci + e;
         sl[rg][e] = qk * __shfl_sync(kFull, down, (2 * ci + e) * 4);
         lim[rg][e] = -1;
-        ls[rg][e] = 0.f;
+        ls[rg][e] = INFINITY;  // (a row that is none, or has no keys, weighs nothing)
         if (r < rph) {
           const int rt = r / a.G, rgq = r - rt * a.G;
           const float v = __ldg(a.lse + (size_t(b) * a.T + rt) * a.Hq + size_t(h) * a.G + rgq);
-          if (v != -INFINITY) {  // a row without keys weighs nothing
+          if (v != -INFINITY) {
             ls[rg][e] = v * kLog2e;
             lim[rg][e] = L - a.T + rt;
           }
@@ -174,30 +194,60 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
     // ---- its tiles
     const int32_t* trow = a.block_table + size_t(b) * a.max_pages;
     const size_t state = (size_t(b) * a.Hkv + h) * cap;
-    auto page_of = [&](int tl) { return __ldg(trow + (tl * 16) / a.P); };
-    int ph = page_of(tile);
+    // The places of 32 tiles at a time, a lane each.  Copies run STAGES - 1 tiles
+    // ahead, a group per tile (empty ones behind the last, so that the count of
+    // groups says which have landed); the state one tile ahead.
+    int tiles0 = -32;     // first tile of the lanes' rows
+    int64_t rows_at = 0;  // where the rows of tile tiles0 + lane begin
+    const uint8_t* mine = static_cast<const uint8_t*>(a.k_pages) + gi * key_step + ci * 16;
+    auto fetch = [&](int tl) {
+      if (tl < end) {
+        if (tl >= tiles0 + 32) {
+          tiles0 = tl;
+          if (tl + lane < end) {
+            const int lp = (tl + lane) * 16 / a.P, kp = (tl + lane) * 16 - lp * a.P;
+            int ph = __ldg(trow + lp);
+            if (ph < 0 || ph >= a.num_pages) {
+              if (a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
+              ph = 0;
+            }
+            rows_at = (a.nhd ? (int64_t(ph) * a.P + kp) * a.Hkv + h : (int64_t(ph) * a.Hkv + h) * a.P + kp) * RB;
+          }
+        }
+        const uint8_t* kr = mine + __shfl_sync(kFull, rows_at, tl - tiles0);
+        const uint32_t dst = ring + (tl % STAGES) * (2 * NC * 512);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          copy16(dst + 2 * i * 512, kr + i * 64);
+          copy16(dst + (2 * i + 1) * 512, kr + 8 * key_step + i * 64);
+        }
+      }
+      copy_commit();
+    };
+    // lanes ci = 0 and 1 hold the state of keys gi and gi + 8
+    auto state_of = [&](int tl) {
+      const int key = tl * 16 + gi + 8 * ci;
+      return tl < end && ci < 2 && key < L && a.w_in ? a.w_in[state + key] : 0.f;
+    };
+    for (int i = 0; i < STAGES - 1; ++i) fetch(tile + i);
+    float old = state_of(tile);
     for (; tile < end; ++tile) {
       const int key0 = tile * 16;
-      if (ph < 0 || ph >= a.num_pages) {
-        if (lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
-        ph = 0;
-      }
-      const int kp = key0 - (key0 / a.P) * a.P;
-      const size_t line = a.nhd ? (size_t(ph) * a.P + kp) * a.Hkv + h : (size_t(ph) * a.Hkv + h) * a.P + kp;
-      const uint8_t* kr = static_cast<const uint8_t*>(a.k_pages) + line * RB + gi * key_step + ci * 16;
+      copy_wait<STAGES - 2>();  // this tile's copies
       uint4 x0[NC], x1[NC];
+      {
+        const uint32_t at = ring + (tile % STAGES) * (2 * NC * 512);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        x0[i] = __ldg(reinterpret_cast<const uint4*>(kr + i * 64));
-        x1[i] = __ldg(reinterpret_cast<const uint4*>(kr + 8 * key_step + i * 64));
+        for (int i = 0; i < NC; ++i) {
+          x0[i] = lds16(at + 2 * i * 512);
+          x1[i] = lds16(at + (2 * i + 1) * 512);
+        }
       }
-      // lanes ci = 0 and 1 store keys gi and gi + 8
-      const int mine = key0 + gi + 8 * ci;
-      const bool owner = ci < 2 && mine < L;
-      float old = 0.f;
-      if (owner && a.w_in) old = a.w_in[state + mine];
-      const int next_ph = tile + 1 < end ? page_of(tile + 1) : 0;
+      // (into the stage read one tile ago)
+      fetch(tile + STAGES - 1);
+      const float next_old = state_of(tile + 1);
 
+      const bool all_seen = key0 + 15 <= L - a.T;  // by every query token
       float wa = 0.f, wb = 0.f;
 #pragma unroll
       for (int rg = 0; rg < NRG; ++rg) {
@@ -222,16 +272,18 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
         for (int e = 0; e < 2; ++e) {
           const float ea = ex2(fmaf(sc[e] + sd[e], sl[rg][e], -ls[rg][e]));
           const float eb = ex2(fmaf(sc[2 + e] + sd[2 + e], sl[rg][e], -ls[rg][e]));
-          wa += key0 + gi <= lim[rg][e] ? ea : 0.f;
-          wb += key0 + gi + 8 <= lim[rg][e] ? eb : 0.f;
+          // (NaN may lie behind the last key, and only there: a choice, no product)
+          wa += all_seen || key0 + gi <= lim[rg][e] ? ea : 0.f;
+          wb += all_seen || key0 + gi + 8 <= lim[rg][e] ? eb : 0.f;
         }
       }
       wa += __shfl_xor_sync(kFull, wa, 1);
       wb += __shfl_xor_sync(kFull, wb, 1);
       wa += __shfl_xor_sync(kFull, wa, 2);
       wb += __shfl_xor_sync(kFull, wb, 2);
-      if (owner) a.w_out[state + mine] = fmaf(a.decay, old, ci ? wb : wa);
-      ph = next_ph;
+      const int key = key0 + gi + 8 * ci;
+      if (ci < 2 && key < L) a.w_out[state + key] = fmaf(a.decay, old, ci ? wb : wa);
+      old = next_old;
       ++i0;
     }
     // ---- the next (sequence, head) with tiles
@@ -247,12 +299,17 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
 
 template <bool FP8, int NRG>
 cudaError_t launch_weights_t(const WeightArgs& a, cudaStream_t s) {
+  constexpr int STAGES = 2;
+  constexpr int SMEM = kWarps * STAGES * (FP8 ? 2048 : 4096);
+  static cudaError_t attr = cudaFuncSetAttribute(key_weights_kernel<FP8, NRG, STAGES>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (attr != cudaSuccess) return attr;
   // as many CTAs as the GPU holds at once
   int dev = 0, sms = 0, per_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, key_weights_kernel<FP8, NRG>, kWarps * 32, 0);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, key_weights_kernel<FP8, NRG, STAGES>, kWarps * 32, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   // (tiles at most, so that a short cache is not spread over idle CTAs)
@@ -260,13 +317,14 @@ cudaError_t launch_weights_t(const WeightArgs& a, cudaStream_t s) {
   const int64_t grid = int64_t(sms) * (per_sm > 0 ? per_sm : 1);
   cfg.gridDim = dim3(unsigned(grid < most ? grid : most), 1, 1);
   cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = la;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, key_weights_kernel<FP8, NRG>, a);
+  return cudaLaunchKernelEx(&cfg, key_weights_kernel<FP8, NRG, STAGES>, a);
 }
 
 template <bool FP8>
