@@ -40,8 +40,7 @@ constexpr int kBins = 2048;            // 11-bit digits: bits 31-21, 20-10, and 
 constexpr int kMaxCluster = 8;
 constexpr int kRankCap = 46080;        // ranks a CTA can keep in shared memory (180 KB)
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBatch = 64;         // moves a CTA takes at a time
-constexpr int kMoveUnroll = 8;         // 16-byte pieces a thread has in flight
+constexpr int kFewBatch = 32, kManyBatch = 64;  // moves a CTA takes at a time
 constexpr int kMoveGroups = 1024;      // groups whose prefix a CTA holds at a time
 
 // Rows of the pools that a batch of moves reads and writes.
@@ -74,14 +73,14 @@ __device__ __forceinline__ void look_up(const EvictArgs& a, int grp, int begin, 
 
 // NT threads copy the rows of a batch; `meanwhile` runs once with the first
 // rows in flight.
-template <int NT, int N, class F>
+template <int NT, int UNROLL, int N, class F>
 __device__ __forceinline__ void copy_rows(const EvictArgs& a, const Rows<N>& rows, int count, F&& meanwhile) {
   const int nk = a.k_row >> 4, np = nk + (a.v_row >> 4);  // 16-byte pieces of a key
   const int total = count * np;
   bool met = false;
 #pragma unroll 1
-  for (int p0 = threadIdx.x; p0 < total || !met; p0 += kMoveUnroll * NT) {
-    uint4 x[kMoveUnroll];
+  for (int p0 = threadIdx.x; p0 < total || !met; p0 += UNROLL * NT) {
+    uint4 x[UNROLL];
     // piece u of this pass: its move, which pool, its byte offset in the row
     auto piece = [&](int u, int& m, bool& is_k) -> size_t {
       const int p = p0 + u * NT;
@@ -91,7 +90,7 @@ __device__ __forceinline__ void copy_rows(const EvictArgs& a, const Rows<N>& row
       return size_t(is_k ? c : c - nk) << 4;
     };
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
+    for (int u = 0; u < UNROLL; ++u) {
       if (p0 + u * NT >= total) break;
       bool is_k;
       int m;
@@ -106,7 +105,7 @@ __device__ __forceinline__ void copy_rows(const EvictArgs& a, const Rows<N>& row
       met = true;
     }
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
+    for (int u = 0; u < UNROLL; ++u) {
       if (p0 + u * NT >= total) break;
       bool is_k;
       int m;
@@ -464,13 +463,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-// The moves of all groups, in batches of kMoveBatch moves of one group; the
+// The moves of all groups, in batches of BATCH moves of one group; the
 // batches form one line of which a CTA takes every gridDim.x-th.  While the
 // rows of a batch are in flight, the first threads look up the next one's.
+template <int BATCH, int UNROLL>
 __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ int32_t upto[kMoveGroups];  // batches of the groups up to and with this one
   __shared__ int32_t part[kMoveThreads / 32];
-  __shared__ Rows<kMoveBatch> rows[2];
+  __shared__ Rows<BATCH> rows[2];
   __shared__ int32_t count[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   launch_dependents();
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
       const int g = int(threadIdx.x) * PT + i;
-      mine[i] = g < ng ? (a.meta[2 * (g0 + g)] + kMoveBatch - 1) / kMoveBatch : 0;
+      mine[i] = g < ng ? (a.meta[2 * (g0 + g)] + BATCH - 1) / BATCH : 0;
       sum += mine[i];
     }
     int x = sum;
@@ -514,14 +514,14 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
 
     // looks up batch `i` of this stretch of groups
     auto find = [&](int i, int buf) {
-      if (threadIdx.x >= kMoveBatch || i >= all) return;
+      if (threadIdx.x >= BATCH || i >= all) return;
       int l = 0, r = ng - 1;  // the first group whose batches reach past i
       while (l < r) {
         const int m = (l + r) >> 1;
         if (upto[m] > i) r = m; else l = m + 1;
       }
-      const int grp = g0 + l, begin = (i - (l ? upto[l - 1] : 0)) * kMoveBatch;
-      const int c = min(kMoveBatch, a.meta[2 * grp] - begin);
+      const int grp = g0 + l, begin = (i - (l ? upto[l - 1] : 0)) * BATCH;
+      const int c = min(BATCH, a.meta[2 * grp] - begin);
       if (threadIdx.x == 0) count[buf] = c;
       look_up(a, grp, begin, c, rows[buf]);
     };
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_cons
     find(i, buf);
     __syncthreads();
     for (; i < all; i += gridDim.x, buf ^= 1) {
-      copy_rows<kMoveThreads>(a, rows[buf], count[buf], [&]() { find(i + int(gridDim.x), buf ^ 1); });
+      copy_rows<kMoveThreads, UNROLL>(a, rows[buf], count[buf], [&]() { find(i + int(gridDim.x), buf ^ 1); });
       __syncthreads();
     }
     passed += all;
@@ -550,12 +550,14 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // CTAs per (sequence, head): one for each 512 slots of capacity while the
-  // groups do not fill the GPU (four CTAs per SM), and one for each 16,384
-  // slots in any case (64 KB of ranks, so that CTAs share an SM).
+  // CTAs per (sequence, head): one for each 2048 slots of capacity while the
+  // groups do not fill the GPU, and one for each 32,768 slots in any case (128
+  // KB of ranks).  5.9k slots of 2 heads: 14.8 us with four, 17.0 with eight,
+  // 16.5 with one; 64k slots of one: 32 with four, 26 with eight; 256 heads of
+  // 131k: 227 with four, 233 with eight, 281 with two.
   int nc = 1;
-  while (nc < kMaxCluster && ((cap > int64_t(nc) * 512 && int64_t(groups) * nc * 2 <= int64_t(sms) * 4) ||
-                              cap > int64_t(nc) * 16384))
+  while (nc < kMaxCluster && ((cap > int64_t(nc) * 2048 && int64_t(groups) * nc * 2 <= int64_t(sms) * 4) ||
+                              cap > int64_t(nc) * 32768))
     nc *= 2;
   const int64_t per = ((cap + nc - 1) / nc + 3) & ~int64_t(3);
   const int rank_cap = int(per <= kRankCap ? per : kRankCap);
@@ -584,10 +586,16 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   mv.attrs = la;
   mv.numAttrs = 1;
   mv.blockDim = dim3(kMoveThreads, 1, 1);
-  const int64_t most = int64_t(groups) * ((a.max_moves + kMoveBatch - 1) / kMoveBatch);
+  // Few moves go in small batches, so that more SMs take part (12k rows of 576
+  // bytes: 24.5 us in batches of 32, 26.4 of 64), many in large ones, for bytes
+  // in flight (840k pairs of 256-byte rows: 266 us and 233).
+  const bool few = int64_t(groups) * a.max_moves <= int64_t(sms) * 256;
+  const int batch = few ? kFewBatch : kManyBatch;
+  const int64_t most = int64_t(groups) * ((a.max_moves + batch - 1) / batch);
   const int64_t grid = most < int64_t(sms) * 4 ? (most > 0 ? most : 1) : int64_t(sms) * 4;
   mv.gridDim = dim3(unsigned(grid), 1, 1);
-  return cudaLaunchKernelEx(&mv, move_kernel, a);
+  return few ? cudaLaunchKernelEx(&mv, move_kernel<kFewBatch, kFewBatch / 8>, a)
+             : cudaLaunchKernelEx(&mv, move_kernel<kManyBatch, kManyBatch / 8>, a);
 }
 
 }  // namespace splitkv
