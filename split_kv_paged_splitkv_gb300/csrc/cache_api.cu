@@ -353,7 +353,7 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
 size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
   if (validate_cross(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
   const size_t parts = size_t(cross_parts(*desc, n_tokens));
-  return align256(2 * parts * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float)) + align256(parts * sizeof(CrossSplit));
+  return align256(2 * parts * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float)) + align256(2 * parts * sizeof(CrossSplit));
 }
 
 splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens,
@@ -385,6 +385,7 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   CrossArgs a{};
   a.parts = cross_parts(d, n_tokens);
   a.part_rows = cross_part_rows(d, n_tokens);
+  a.merge_cost = a.part_rows > 64 ? 5 : 3;
   if (a.parts > 0) {
     if (!workspace) return fail(SPLITKV_EWORKSPACE, "workspace is NULL");
     if (misaligned(workspace, 16)) return fail(SPLITKV_EINVAL, "workspace must be 16-byte aligned");
@@ -394,7 +395,7 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
     a.o_part = static_cast<float*>(workspace);
     a.lse_part = a.o_part + size_t(2) * a.parts * a.part_rows * 128;
     a.split = reinterpret_cast<CrossSplit*>(static_cast<unsigned char*>(workspace) + need -
-                                            align256(size_t(a.parts) * sizeof(CrossSplit)));
+                                            align256(size_t(2) * a.parts * sizeof(CrossSplit)));
   }
   a.q = q;
   a.cu = cu_tokens;

@@ -29,17 +29,18 @@
 //
 // Many items (prompts): a CTA per item; the bound is 4 * 128 * rows * L
 // operations.  Few items (a decoder token over the encoder's states, short
-// prompts; the bound is the bytes of K and V, or the longest item): the key
-// blocks of all items form one line, cut by the device lengths into equal
-// parts, one per SM.  A CTA then walks the pieces of items in its part (the
-// ring and the barriers run on across them); an item that lies in more than
-// one part leaves partial results, at most two of a CTA, and merge_kernel
-// joins them by their log-sum-exps.  A row block without rows is left out.
+// prompts; the bound is the bytes of K and V, or the longest item): one CTA
+// per SM, which finds by the device lengths how finely to cut the items' keys
+// and walks its pieces (the ring and the barriers run on across them); cut
+// items leave partial results that merge_kernel joins by their log-sum-exps.
+// A row block without rows is left out.
 //
 // P is rounded to bf16 for the second product (half a step, 2^-8 of a weight,
 // as in the decode kernels); sums, maxima and O are fp32.
 #include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <climits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -57,7 +58,7 @@ struct Cross {
   static constexpr int NST = 5;
   static constexpr int OFF_RING = 2 * TILE;      // after Q's two row blocks
   static constexpr int OFF_BAR = OFF_RING + NST * TILE;
-  static constexpr int SMEM = 1024 + OFF_BAR + 256;
+  static constexpr int SMEM = 1024 + OFF_BAR + 512;
   static constexpr int SOFTMAX_WARPS = 8;
   static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 1;  // warps
   static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
@@ -101,24 +102,20 @@ __device__ __forceinline__ int tokens_of(const CrossArgs& a, int b, int* first) 
 // (it writes its zeros).
 __device__ __forceinline__ int blocks_of(int n_keys) { return max(1, (n_keys + Cross::BK - 1) / Cross::BK); }
 
-// Where a CTA stands in the line of items (b, h, tile), the row tile innermost.
-struct Place {
-  int64_t w, w1;        // of the line: here, and the end of this CTA's part
-  int32_t b, h, tile, block;
-};
-
-// One piece of an item: `nblk` key blocks from j0 on.
+// One piece of an item: `nblk` key blocks from j0 on (0: an item without keys).
 struct Piece {
   int b, h, first, row0, n_rows, L, j0, nblk;  // n_rows: rows from row0 on (may exceed a tile)
-  bool starts, ends;                           // holds the item's first, last key block
+  int slot;                                    // of its partial result; -1: the whole item
 };
+constexpr int kMaxPieces = 4;  // of a CTA
 
 // Behind the barriers.
 struct Tail {
   uint32_t tmem;  // written by the allocation
-  Place start;
+  int32_t pieces;
+  Piece piece[kMaxPieces];
 };
-static_assert(B_COUNT * 8 + sizeof(Tail) <= 256, "barriers, then the tail");
+static_assert(B_COUNT * 8 + sizeof(Tail) <= 512, "barriers, then the tail");
 
 // Row tiles of sequence b.
 __device__ __forceinline__ int tiles_of(const CrossArgs& a, int b) {
@@ -126,85 +123,97 @@ __device__ __forceinline__ int tiles_of(const CrossArgs& a, int b) {
   return (tokens_of(a, b, &first) * a.G + Cross::ROWS - 1) / Cross::ROWS;
 }
 
-// Takes the next piece of this CTA's part; false at its end.
-__device__ __forceinline__ bool next_piece(const CrossArgs& a, Place& p, Piece& q) {
-  if (p.w >= p.w1) return false;
-  q.b = p.b;
-  q.h = p.h;
-  const int rows = tokens_of(a, p.b, &q.first) * a.G;
-  q.row0 = p.tile * Cross::ROWS;
-  q.n_rows = rows - q.row0;
-  q.L = keys_of(a, p.b);
-  const int nb = blocks_of(q.L), take = int(min(int64_t(nb - p.block), p.w1 - p.w));
-  q.j0 = p.block;
-  q.nblk = q.L > 0 ? take : 0;
-  q.starts = p.block == 0;
-  q.ends = p.block + take == nb;
-  p.w += take;
-  p.block = 0;
-  if (p.w < p.w1) {  // (then this item is done)
-    if (++p.tile * Cross::ROWS >= rows) {
-      p.tile = 0;
-      if (++p.h == a.Hkv) {
-        p.h = 0;
-        do ++p.b; while (tiles_of(a, p.b) == 0);
-      }
-    }
-  }
-  return true;
-}
-
-// CTAs that share a line of W key blocks: two blocks each at least.
-__device__ __forceinline__ int64_t parts_of(const CrossArgs& a, int64_t W) {
-  return max(int64_t(1), min(int64_t(a.parts), W / 2));
-}
-
-// By a warp: the part of CTA `c` of the line (w == w1: none).
-__device__ __forceinline__ Place find_part(const CrossArgs& a, int c, int lane) {
-  Place p;
-  p.w = p.w1 = 0;
-  p.b = p.h = p.tile = p.block = 0;
-  // blocks of 32 sequences at a time: their total first, then the sequence
-  // that holds the part's first block (a batch of up to 32 is read once)
+// By a warp: which pieces this CTA computes.
+//
+// A CTA per item (a.parts = 0): row tile blockIdx.x of all sequences' (the grid
+// counts tiles for any split of the tokens among the sequences), head
+// blockIdx.y.
+//
+// Few items: every item of nb key blocks is cut into ceil(nb / t) equal pieces,
+// and CTA c takes pieces c, c + parts, ... of the line of all items' pieces.
+// Lane i weighs t = ceil(longest nb / (i + 1)): the blocks of the CTA with most,
+// two more for each of its pieces, and a.merge_cost if anything is cut.
+__device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& tail) {
   int tiles = 0, nb = 1;
-  int64_t n = 0, W = 0, x = 0;
-  auto read = [&](int b0) {
-    const int bl = b0 + lane;
-    tiles = bl < a.batch ? tiles_of(a, bl) : 0;
-    nb = bl < a.batch ? blocks_of(keys_of(a, bl)) : 1;
-    n = int64_t(tiles) * a.Hkv * nb;
-    x = n;
+  auto read = [&](int b0) {  // lane: sequence b0 + lane
+    const int b = b0 + lane;
+    tiles = b < a.batch ? tiles_of(a, b) : 0;
+    nb = b < a.batch ? blocks_of(keys_of(a, b)) : 1;
+  };
+  auto before = [&](int n, int* total) {  // sum over the lanes before this one
+    int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(kFull, x, o);
+      const int y = __shfl_up_sync(kFull, x, o);
       if (lane >= o) x += y;
     }
+    *total = __shfl_sync(kFull, x, 31);
+    return x - n;
   };
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    read(b0);
-    W += __shfl_sync(kFull, x, 31);
-  }
-  const int64_t parts = parts_of(a, W);
-  if (c >= parts || W == 0) return p;
-  p.w = W * c / parts;
-  p.w1 = W * (c + 1) / parts;
-  int64_t before = 0;
-  for (int b0 = 0;; b0 += 32) {
-    if (a.batch > 32) read(b0);
-    const unsigned past = __ballot_sync(kFull, before + x > p.w);
-    if (past) {
-      const int f = __ffs(past) - 1;
-      const int in = int(p.w - before - __shfl_sync(kFull, x - n, f));  // of the sequence's blocks
-      tiles = __shfl_sync(kFull, tiles, f);
-      nb = __shfl_sync(kFull, nb, f);
-      const int item = in / nb;
-      p.b = b0 + f;
-      p.block = in - item * nb;
-      p.h = item / tiles;
-      p.tile = item - p.h * tiles;
-      return p;
+  int T = INT_MAX, P = 0, items = 0;
+  if (a.parts > 0) {
+    int longest = 1;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      read(b0);
+      items += __reduce_add_sync(kFull, tiles);
+      longest = max(longest, __reduce_max_sync(kFull, tiles > 0 ? nb : 1));
     }
-    before += __shfl_sync(kFull, x, 31);
+    items *= a.Hkv;
+    const int t = (longest + lane) / (lane + 1);
+    int n = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      if (a.batch > 32) read(b0);
+      for (int i = 0; i < min(32, a.batch - b0); ++i)
+        n += __shfl_sync(kFull, tiles, i) * ((__shfl_sync(kFull, nb, i) + t - 1) / t);
+    }
+    n *= a.Hkv;
+    // (cut pieces have a slot each; uncut items need none)
+    const bool fits = lane == 0 || n <= 2 * a.parts;
+    const uint32_t cost = (n + a.parts - 1) / a.parts * (t + 2) + (n > items ? a.merge_cost : 0);
+    const int best = __reduce_min_sync(kFull, fits ? cost * 32 + lane : ~0u) & 31;
+    T = __shfl_sync(kFull, t, best);
+    P = __shfl_sync(kFull, n, best);
+  }
+  int k = 0;
+  for (int p = blockIdx.x; a.parts == 0 ? k == 0 : p < P && k < kMaxPieces; p += a.parts, ++k) {
+    Piece q;
+    int cuts = 0, passed = 0, total;
+    bool found = false;
+    for (int b0 = 0; b0 < a.batch && !found; b0 += 32) {
+      if (a.batch > 32 || a.parts == 0) read(b0);
+      const int s = a.parts > 0 ? (nb + T - 1) / T : 1;
+      const int n = a.parts > 0 ? tiles * a.Hkv * s : tiles;
+      const int at = passed + before(n, &total);
+      const unsigned m = __ballot_sync(kFull, p >= at && p < at + n);
+      passed += total;
+      if (m) {
+        const int f = __ffs(m) - 1;
+        found = true;
+        q.b = b0 + f;
+        cuts = __shfl_sync(kFull, s, f);
+        const int in = p - __shfl_sync(kFull, at, f), item = in / cuts, cut = in - item * cuts;
+        const int ts = __shfl_sync(kFull, tiles, f), blocks = __shfl_sync(kFull, nb, f);
+        const int tile = a.parts > 0 ? item % ts : item;
+        q.h = a.parts > 0 ? item / ts : int(blockIdx.y);
+        q.n_rows = tokens_of(a, q.b, &q.first) * a.G - tile * Cross::ROWS;
+        q.row0 = tile * Cross::ROWS;
+        q.L = keys_of(a, q.b);
+        q.j0 = blocks * cut / cuts;
+        q.nblk = q.L > 0 ? blocks * (cut + 1) / cuts - q.j0 : 0;
+        q.slot = cuts > 1 ? p : -1;
+        // the merge's record, with the first piece of a cut item
+        if (lane == 0 && k < 2 && a.parts > 0) {
+          const CrossSplit r = {cuts > 1 && cut == 0 ? cuts : 0, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
+          a.split[p] = r;
+        }
+      }
+    }
+    if (!found) break;
+    if (lane == 0) tail.piece[k] = q;
+  }
+  if (lane == 0) {
+    tail.pieces = k;
+    for (int i = k; i < 2 && a.parts > 0; ++i) a.split[blockIdx.x + i * a.parts].cuts = 0;
   }
 }
 
@@ -394,36 +403,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   launch_dependents();
   wait_prerequisites();
   if (warp == C::ISSUER) {
-    Place p;
-    if (a.parts > 0) {
-      p = find_part(a, blockIdx.x, lane);
-    } else {
-      p.w = p.w1 = 0;
-      p.b = p.h = p.tile = p.block = 0;
-      // a CTA per item: row tile blockIdx.x of all sequences' (the grid counts
-      // tiles for any split of the tokens among the sequences), head blockIdx.y
-      int before = 0;
-      for (int b0 = 0; b0 < a.batch && p.w1 == 0; b0 += 32) {
-        const int bl = b0 + lane, n = bl < a.batch ? tiles_of(a, bl) : 0;
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(kFull, x, o);
-          if (lane >= o) x += y;
-        }
-        const unsigned past = __ballot_sync(kFull, before + x > int(blockIdx.x));
-        if (past) {
-          const int f = __ffs(past) - 1;
-          p.b = b0 + f;
-          p.h = blockIdx.y;
-          p.tile = int(blockIdx.x) - before - __shfl_sync(kFull, x - n, f);
-          p.w1 = blocks_of(keys_of(a, p.b));
-        } else {
-          before += __shfl_sync(kFull, x, 31);
-        }
-      }
-    }
-    if (lane == 0) tail.start = p;
+    plan_pieces(a, lane, tail);
     // one CTA reports lengths that the cache cannot hold
     if (a.status && blockIdx.x == 0 && blockIdx.y == 0)
       for (int i = lane; i < a.batch; i += 32)
@@ -433,8 +413,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
-  Place place = tail.start;
-  Piece pc;
+  const int pieces = *reinterpret_cast<volatile int32_t*>(&tail.pieces);
 
   if (warp == C::PRODUCER) {
     // -------------------------------------------------------------- producer
@@ -445,7 +424,8 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     const int br = a.box_rows;
     bool ok = true;
     int issued = 0;
-    while (ok && next_piece(a, place, pc)) {
+    for (int k = 0; k < pieces && ok; ++k) {
+      const Piece pc = tail.piece[k];
       const int32_t* trow = a.block_table + size_t(pc.b) * a.max_pages;
       for (int j = 0; j < pc.nblk && ok; ++j) {
         const int key0 = (pc.j0 + j) * C::BK;
@@ -490,7 +470,6 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     bool ok = true;
     int item = 0;                      // ring items consumed
     uint32_t n_q = 0, n_p = 0;  // phases of B_Q and B_P so far, a bit per row block
-    CrossSplit split = {0, 0, 0, 0, 0, 0};
     auto wait = [&](int i, int phase) {
       ok = ok && __all_sync(kFull, mbar_wait(bar(i), phase & 1));
       return ok;
@@ -508,16 +487,8 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     auto release = [&](int i) {
       umma_commit_warp(bar(B_EMPTY + i % C::NST));
     };
-    while (ok && next_piece(a, place, pc)) {
-      if (pc.starts && !pc.ends) {
-        split.begins = 1;
-        split.first = pc.first;
-        split.head = pc.h;
-        split.row0 = pc.row0;
-        split.rows = min(pc.n_rows, C::ROWS);
-      } else if (!pc.starts && pc.ends) {
-        split.ends = 1;
-      }
+    for (int k = 0; k < pieces && ok; ++k) {
+      const Piece pc = tail.piece[k];
       if (pc.nblk == 0) continue;
       const int blocks = pc.n_rows > 128 ? 2 : 1;  // row blocks with rows
       for (int t = 0; t < blocks && ok; ++t) {
@@ -573,7 +544,6 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
       item += 2 * pc.nblk;
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
-    if (a.parts > 0 && lane == 0) a.split[blockIdx.x] = split;
     // every MMA issued above completes before TMEM is released
     umma_commit_warp(bar(B_DONE));
     __syncwarp();
@@ -593,53 +563,51 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     auto chunk_at = [&](int rr, int ch) -> uint8_t* {
       return sm + t * C::TILE + (ch >> 3) * C::HALF + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
     };
-    // Visits this warp's 32 rows of a piece, 16 lanes to a row: body(i, row of
-    // the row block, whether it exists, its token and head).
+    // Visits this warp's 32 rows of a piece, 16 lanes to a row: body(row of the
+    // row block, whether it exists, its token and head).  Rolled, as is all
+    // that runs once for a piece: such code waits for its own instructions.
     auto each_row = [&](const Piece& q, auto&& body) {
       int rr = (warp & 3) * 32 + (lane >> 4);
       const int first = q.row0 + t * 128 + rr;
       int tok = first / a.G, g = first - tok * a.G;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 16; ++i, rr += 2) {
-        body(i, rr, t * 128 + rr < q.n_rows, int64_t(q.first) + tok, q.h * a.G + g);
-        g += 2;
-        while (g >= a.G) {
-          g -= a.G;
-          ++tok;
-        }
+        body(rr, t * 128 + rr < q.n_rows, int64_t(q.first) + tok, q.h * a.G + g);
+        for (g += 2; g >= a.G; g -= a.G) ++tok;
       }
     };
-    // The query rows of this warp, 16 lanes to a row, swizzled; rows behind
-    // the last are zero.  Called when the products that read the Q before are
-    // done (S of the last block has arrived); false: no piece, or none of
-    // this row block's.
-    auto take_piece = [&](Piece& q) {
-      do {
-        if (!next_piece(a, place, q)) return false;
-      } while (t == 1 && q.n_rows <= 128);
-      if (q.nblk > 0) {
-        uint4 x[16];
-        each_row(q, [&](int i, int rr, bool in, int64_t token, int head) {
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (in)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + token * a.q_stride +
-                                                        head * 128) + (lane & 15));
+    // The next piece with rows of this row block: its query rows, swizzled, on
+    // their way into shared memory (rows behind the last are zero).  Not before
+    // the products that read the Q before are done.
+    int k = 0;
+    auto take_piece = [&]() {
+      while (t == 1 && k < pieces && tail.piece[k].n_rows <= 128) ++k;
+      if (k == pieces) return false;
+      if (tail.piece[k].nblk > 0)
+        each_row(tail.piece[k], [&](int rr, bool in, int64_t token, int head) {
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (in ? token * a.q_stride + head * 128 : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(chunk_at(rr, lane & 15))),
+                       "l"(src + 8 * (lane & 15)), "r"(in ? 16 : 0)
+                       : "memory");
         });
-#pragma unroll
-        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(chunk_at((warp & 3) * 32 + 2 * i + (lane >> 4), lane & 15)) = x[i];
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        mbar_arrive(bar(B_Q + t));
-      }
       return true;
     };
-    Piece nx;
-    bool more = take_piece(nx);
+    bool more = take_piece();
     while (ok && more) {
-      pc = nx;
+      const Piece pc = tail.piece[k++];
       const bool live = row < pc.n_rows;
       const bool any = __any_sync(kFull, live);  // a warp without rows only keeps step
-      const bool whole = pc.starts && pc.ends;
+      const bool whole = pc.slot < 0;
+      // A whole result goes through this warp's rows of Q's shared memory, so
+      // that whole rows are written; a partial one (whose layout puts a
+      // column's rows side by side), and one of a few rows, straight from
+      // registers, with the next piece's Q already on its way.
+      const bool staged = whole && (a.parts == 0 || pc.n_rows > 128);
+      if (pc.nblk > 0) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(bar(B_Q + t));
+      }
       float m_ref = -INFINITY, l = 0.f;
       int valid = pc.L - pc.j0 * C::BK;  // keys from the block's first on
       for (int j = 0; j < pc.nblk; ++j, valid -= C::BK) {
@@ -705,19 +673,17 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
         mbar_arrive(bar(B_P + t));
       }
 
-      // ---- the piece's result.  A partial one goes straight from registers
-      // (its layout puts a column's rows side by side), with the next piece's
-      // Q already under way; a whole one through this warp's rows of Q's
-      // shared memory, so that whole rows are written.
-      if (!ok) break;
-      if (!whole) more = take_piece(nx);
-      if (pc.nblk > 0) ok = __all_sync(kFull, mbar_wait(bar(B_O + t), n_o++ & 1));
+      // ---- the piece's result (S of its last block has come: Q is read)
+      if (ok && !staged) more = take_piece();
+      if (ok && pc.nblk > 0) ok = __all_sync(kFull, mbar_wait(bar(B_O + t), n_o++ & 1));
       if (!ok) break;
       tc_fence_after();
       if (any) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse = l > 0.f ? (m_ref + lg2(l)) * kLn2 : -INFINITY;
-        const size_t slot = size_t(blockIdx.x) * 2 + (pc.starts ? 1 : 0);
+        const size_t slot = pc.slot;
+        const int tok = (pc.row0 + row) / a.G, g = (pc.row0 + row) - tok * a.G;
+        const size_t out_row = (size_t(pc.first) + tok) * a.Hq + size_t(pc.h) * a.G + g;
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
           float o[32];
@@ -730,11 +696,14 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
           if (whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              *reinterpret_cast<uint4*>(chunk_at(r, c0 / 8 + i)) =
-                  make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                             pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                             pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                             pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              const uint4 x = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                         pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                         pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                         pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              if (staged)
+                *reinterpret_cast<uint4*>(chunk_at(r, c0 / 8 + i)) = x;
+              else if (live)
+                reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128 + c0)[i] = x;
             }
           } else if (live) {
             float4* dst = reinterpret_cast<float4*>(a.o_part) + (slot * 32 + c0 / 4) * a.part_rows + row;
@@ -743,23 +712,21 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
               dst[size_t(i) * a.part_rows] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
           }
         }
-        if (whole) {
+        if (staged) {
           __syncwarp();
-          each_row(pc, [&](int, int rr, bool in, int64_t token, int head) {
+          each_row(pc, [&](int rr, bool in, int64_t token, int head) {
             if (in)
               reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (token * a.Hq + head) * 128)[lane & 15] =
                   *reinterpret_cast<const uint4*>(chunk_at(rr, lane & 15));
           });
           __syncwarp();
-          if (live && a.lse) {
-            const int tok = (pc.row0 + row) / a.G, g = (pc.row0 + row) - tok * a.G;
-            a.lse[(size_t(pc.first) + tok) * a.Hq + size_t(pc.h) * a.G + g] = lse;
-          }
-        } else if (live) {
-          a.lse_part[slot * a.part_rows + row] = lse;
+        }
+        if (live) {
+          if (!whole) a.lse_part[slot * a.part_rows + row] = lse;
+          else if (a.lse) a.lse[out_row] = lse;
         }
       }
-      if (whole) more = take_piece(nx);
+      if (staged) more = take_piece();
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
   }
@@ -773,9 +740,8 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   }
 }
 
-// Joins the partial results of an item that CTA blockIdx.x began and did not
-// finish: those of that CTA (its slot 1) and of the following ones (their slot
-// 0) up to the one that ended it.  32 rows of the item, a lane each; a warp
+// Joins the partial results of the item whose first piece is blockIdx.x: its
+// pieces have consecutive slots.  32 rows of the item, a lane each; a warp
 // takes every eighth group of four dims, read side by side for the rows.
 constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
@@ -785,23 +751,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __g
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CrossSplit sp = a.split[c];
   const int r0 = blockIdx.y * 32, row = r0 + lane;
-  if (!sp.begins || r0 >= sp.rows) return;
-  int last = c;  // the CTA that ended the item
-  for (int k = c + 1; last == c && k < a.parts; k += 32) {
-    const unsigned m = __ballot_sync(kFull, k + lane < a.parts && a.split[k + lane].ends);
-    if (m) last = k + __ffs(m) - 1;
-  }
+  if (sp.cuts == 0 || r0 >= sp.rows) return;
+  const int last = c + sp.cuts - 1;
   const bool live = row < sp.rows;
-  auto slot = [&](int k) { return size_t(k) * 2 + (k == c ? 1 : 0); };
+  auto slot = [&](int k) { return size_t(k); };
   float M = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = c; k <= last; ++k)
     if (live) M = fmaxf(M, a.lse_part[slot(k) * a.part_rows + row]);
   float sum = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
   for (int k = c; k <= last; ++k) {
     if (!live) continue;
     const float ls = a.lse_part[slot(k) * a.part_rows + row];
@@ -850,7 +812,7 @@ int64_t cross_row_tiles(const splitkv_desc_t& d, int64_t n_tokens) {
 // items per SM the unequal ends of a grid of items cost less than an eighth,
 // and the items of a head run side by side, so that its K and V come from L2.
 int cross_parts(const splitkv_desc_t& d, int64_t n_tokens) {
-  return cross_row_tiles(d, n_tokens) * d.num_kv_heads >= 4 * kSmCount ? 0 : kSmCount;
+  return cross_row_tiles(d, n_tokens) * d.num_kv_heads >= kMaxPieces * kSmCount ? 0 : kSmCount;
 }
 
 int cross_part_rows(const splitkv_desc_t& d, int64_t n_tokens) {
@@ -882,7 +844,7 @@ cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& t
   cudaError_t e = cudaLaunchKernelEx(&cfg, cross_attend_kernel, a, *reinterpret_cast<const CUtensorMap*>(&tk),
                                      *reinterpret_cast<const CUtensorMap*>(&tv));
   if (e != cudaSuccess || a.parts == 0) return e;
-  cfg.gridDim = dim3(unsigned(a.parts), unsigned((a.part_rows + 31) / 32), 1);
+  cfg.gridDim = dim3(unsigned(2 * a.parts), unsigned((a.part_rows + 31) / 32), 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, cross_merge_kernel, a);

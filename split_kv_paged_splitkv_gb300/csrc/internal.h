@@ -223,11 +223,10 @@ struct EvictArgs {
 
 constexpr int kSmCount = 152;  // SMs that cross attention plans for
 
-// The item that a CTA of cross attention begins and does not finish, and
-// whether it ends an item that an earlier CTA began.
+// A piece of cross attention's items, for the merge: the number of pieces that
+// its item is cut into if it is the first of them, else 0.
 struct CrossSplit {
-  int32_t begins, first, head, row0, rows;  // first: token of the sequence
-  int32_t ends;
+  int32_t cuts, first, head, row0, rows;  // first: token of the sequence
 };
 
 struct CrossArgs {
@@ -237,16 +236,17 @@ struct CrossArgs {
   const int32_t* seq_lens;
   void* out;
   float* lse;         // or null
-  float* o_part;      // [2 parts][32][part_rows][4]: two partial results of a CTA, in
-                      //   groups of four dims
+  float* o_part;      // [2 parts][32][part_rows][4]: partial results, in groups of four
+                      //   dims
   float* lse_part;    // [2 parts][part_rows]
-  CrossSplit* split;  // [parts]
+  CrossSplit* split;  // [2 parts]
   int32_t* status;    // or null
   int64_t q_stride;   // elements per token
   float qk_scale_log2;
   int32_t n_tokens, batch, T, Hq, Hkv, G, P, max_pages, num_pages, box_rows;
   int32_t parts;      // CTAs that share all items' key blocks; 0: a CTA per item
   int32_t part_rows;  // rows of an item, at most
+  int32_t merge_cost;  // of cutting items, in key blocks
 };
 
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream);
