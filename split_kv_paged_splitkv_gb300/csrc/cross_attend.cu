@@ -33,14 +33,13 @@
 // per SM, which finds by the device lengths how finely to cut the items' keys
 // and walks its pieces (the ring and the barriers run on across them); cut
 // items leave partial results that merge_kernel joins by their log-sum-exps.
-// A row block without rows is left out.
+// An item of up to 128 rows uses the second row block for every other key
+// block of the same rows.
 //
 // P is rounded to bf16 for the second product (half a step, 2^-8 of a weight,
 // as in the decode kernels); sums, maxima and O are fp32.
 #include <cuda.h>
 #include <cuda_runtime.h>
-
-#include <climits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -58,10 +57,12 @@ struct Cross {
   static constexpr int NST = 5;
   static constexpr int OFF_RING = 2 * TILE;      // after Q's two row blocks
   static constexpr int OFF_BAR = OFF_RING + NST * TILE;
-  static constexpr int SMEM = 1024 + OFF_BAR + 512;
+  static constexpr int OFF_ML = OFF_BAR + 512;   // [128] (maximum, sum) of row block B
+  static constexpr int SMEM = 1024 + OFF_ML + 1024;
   static constexpr int SOFTMAX_WARPS = 8;
-  static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 1;  // warps
-  static constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
+  // warps: the producers of K and of V, the issuer of the MMAs
+  static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 2;
+  static constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
   static constexpr uint32_t TMEM_COLS = 512, S_COL = 0, O_COL = 256;  // + 128 per row block
   static constexpr float RESCALE_LOG2 = 8.f;
 };
@@ -74,7 +75,9 @@ enum {
   B_S = B_EMPTY + Cross::NST,    // [2] S of a row block complete
   B_P = B_S + 2,                 // [2] P of a row block in TMEM (128 threads)
   B_O = B_P + 2,                 // [2] the last PV of a row block complete
-  B_DONE = B_O + 2,
+  B_ML = B_O + 2,                // narrow pieces: B's maxima and sums written (128 threads)
+  B_JOINED,                      //   A has read them and B's O (128 threads)
+  B_DONE,
   B_COUNT
 };
 
@@ -123,6 +126,12 @@ __device__ __forceinline__ int tiles_of(const CrossArgs& a, int b) {
   return (tokens_of(a, b, &first) * a.G + Cross::ROWS - 1) / Cross::ROWS;
 }
 
+// Pieces of about t key blocks that an item of nb is cut into.  (In floating
+// point, for speed: any count in 1 .. nb is right, as long as all agree on it.)
+__device__ __forceinline__ int cuts_of(int nb, float t) {
+  return max(1, min(nb, int(ceilf(__fdividef(float(nb), t) - 1e-3f))));
+}
+
 // By a warp: which pieces this CTA computes.
 //
 // A CTA per item (a.parts = 0): row tile blockIdx.x of all sequences' (the grid
@@ -150,7 +159,8 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
     *total = __shfl_sync(kFull, x, 31);
     return x - n;
   };
-  int T = INT_MAX, P = 0, items = 0;
+  float T = 0.f;
+  int P = 0, items = 0;
   if (a.parts > 0) {
     int longest = 1;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
@@ -159,17 +169,17 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
       longest = max(longest, __reduce_max_sync(kFull, tiles > 0 ? nb : 1));
     }
     items *= a.Hkv;
-    const int t = (longest + lane) / (lane + 1);
+    const float t = ceilf(__fdividef(longest, lane + 1));
     int n = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
       if (a.batch > 32) read(b0);
       for (int i = 0; i < min(32, a.batch - b0); ++i)
-        n += __shfl_sync(kFull, tiles, i) * ((__shfl_sync(kFull, nb, i) + t - 1) / t);
+        n += __shfl_sync(kFull, tiles, i) * cuts_of(__shfl_sync(kFull, nb, i), t);
     }
     n *= a.Hkv;
     // (cut pieces have a slot each; uncut items need none)
     const bool fits = lane == 0 || n <= 2 * a.parts;
-    const uint32_t cost = (n + a.parts - 1) / a.parts * (t + 2) + (n > items ? a.merge_cost : 0);
+    const uint32_t cost = (n + a.parts - 1) / a.parts * (uint32_t(t) + 2) + (n > items ? a.merge_cost : 0);
     const int best = __reduce_min_sync(kFull, fits ? cost * 32 + lane : ~0u) & 31;
     T = __shfl_sync(kFull, t, best);
     P = __shfl_sync(kFull, n, best);
@@ -181,7 +191,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
     bool found = false;
     for (int b0 = 0; b0 < a.batch && !found; b0 += 32) {
       if (a.batch > 32 || a.parts == 0) read(b0);
-      const int s = a.parts > 0 ? (nb + T - 1) / T : 1;
+      const int s = a.parts > 0 ? cuts_of(nb, T) : 1;
       const int n = a.parts > 0 ? tiles * a.Hkv * s : tiles;
       const int at = passed + before(n, &total);
       const unsigned m = __ballot_sync(kFull, p >= at && p < at + n);
@@ -390,6 +400,8 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
       mbar_init(bar(B_P + t), 128);
       mbar_init(bar(B_O + t), 1);
     }
+    mbar_init(bar(B_ML), 128);
+    mbar_init(bar(B_JOINED), 128);
     mbar_init(bar(B_DONE), 1);
     fence_mbar_init();
   }
@@ -415,19 +427,22 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
   const int pieces = *reinterpret_cast<volatile int32_t*>(&tail.pieces);
 
-  if (warp == C::PRODUCER) {
-    // -------------------------------------------------------------- producer
-    // K block, V block, K block, ... of all pieces; item i of this sequence
-    // lies in slot i % NST.  A block is BK / br groups of br keys of one page
-    // each; lane g holds the page of group g.  Groups behind the last key are
-    // not read.
+  if (warp == C::PRODUCER || warp == C::PRODUCER + 1) {
+    // ------------------------------------------------------------- producers
+    // Of all pieces, key block j's K is ring item 2 j, its V item 2 j + 1; item
+    // i lies in slot i % NST.  One warp copies the K, one the V (a warp issues
+    // a box in some 100 cycles: one alone would bring 64 KB in 3,200).  A block
+    // is BK / br groups of br keys of one page each; lane g holds the page of
+    // group g.  Groups behind the last key are not read.
+    const int v = warp - C::PRODUCER;
+    const CUtensorMap* tm = v ? &tv : &tk;
     const int br = a.box_rows;
     bool ok = true;
-    int issued = 0;
+    int item = v;
     for (int k = 0; k < pieces && ok; ++k) {
       const Piece pc = tail.piece[k];
       const int32_t* trow = a.block_table + size_t(pc.b) * a.max_pages;
-      for (int j = 0; j < pc.nblk && ok; ++j) {
+      for (int j = 0; j < pc.nblk; ++j, item += 2) {
         const int key0 = (pc.j0 + j) * C::BK;
         const int np = (min(C::BK, pc.L - key0) + br - 1) / br;
         int ph = 0, in = 0;
@@ -440,29 +455,27 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
             ph = 0;
           }
         }
-        for (int v = 0; v < 2 && ok; ++v) {
-          const int st = issued % C::NST;
-          if (issued >= C::NST) ok = __all_sync(kFull, mbar_wait(bar(B_EMPTY + st), (issued / C::NST - 1) & 1));
-          if (!ok) break;
-          mbar_arrive_expect_tx_warp(bar(B_FULL + st), uint32_t(np * br * 256));
-          const uint32_t dst = smem_u32(sm + C::OFF_RING + st * C::TILE);
-          const CUtensorMap* tm = v ? &tv : &tk;
-          for (int g = 0; g < np; ++g) {
-            const int pg = __shfl_sync(kFull, ph, g), kp = __shfl_sync(kFull, in, g);
-            tma_load_5d_warp(dst + g * br * 128, tm, bar(B_FULL + st), 0, kp, 0, pc.h, pg);
-            tma_load_5d_warp(dst + C::HALF + g * br * 128, tm, bar(B_FULL + st), 0, kp, 1, pc.h, pg);
-          }
-          ++issued;
+        const int st = item % C::NST;
+        if (item >= C::NST) ok = __all_sync(kFull, mbar_wait(bar(B_EMPTY + st), (item / C::NST - 1) & 1));
+        if (!ok) break;
+        mbar_arrive_expect_tx_warp(bar(B_FULL + st), uint32_t(np * br * 256));
+        const uint32_t dst = smem_u32(sm + C::OFF_RING + st * C::TILE);
+        for (int g = 0; g < np; ++g) {
+          const int pg = __shfl_sync(kFull, ph, g), kp = __shfl_sync(kFull, in, g);
+          tma_load_5d_warp(dst + g * br * 128, tm, bar(B_FULL + st), 0, kp, 0, pc.h, pg);
+          tma_load_5d_warp(dst + C::HALF + g * br * 128, tm, bar(B_FULL + st), 0, kp, 1, pc.h, pg);
         }
       }
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
-    // stay until every issued copy has landed
+    // Stay until every copy has landed: the last item of each slot, or after a
+    // wait that ran out this warp's own last ones.
     if (lane == 0) {
-      for (int st = 0; st < C::NST && st < issued; ++st) {
-        const int last = st + C::NST * ((issued - 1 - st) / C::NST);
-        if (!mbar_wait(bar(B_FULL + st), (last / C::NST) & 1)) break;
-      }
+      int items = 0;
+      for (int k = 0; k < pieces; ++k) items += 2 * tail.piece[k].nblk;
+      const int end = ok ? items : item;  // (item: the one that was not issued)
+      for (int i = ok ? end - 1 : end - 2; i >= 0 && i >= end - C::NST; i -= ok ? 1 : 2)
+        if (!mbar_wait(bar(B_FULL + i % C::NST), (i / C::NST) & 1)) break;
     }
   } else if (warp == C::ISSUER) {
     // ------------------------------------------------------------ MMA issuer
@@ -476,8 +489,8 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     };
     auto slot = [&](int i) { return smem_u32(sm + C::OFF_RING + (i % C::NST) * C::TILE); };
     static_assert(C::HALF >> 4 == 1024, "descriptor steps of mma_qk");
-    auto qk = [&](int t, int i) {  // S_t = Q_t . K^T, K in ring item i
-      mma_qk(tmem + C::S_COL + 128 * t, umma_desc(smem_u32(sm + t * C::TILE), 16, 1024, 2), umma_desc(slot(i), 16, 1024, 2),
+    auto qk = [&](int t, int q, int i) {  // S_t = Q_q . K^T, K in ring item i
+      mma_qk(tmem + C::S_COL + 128 * t, umma_desc(smem_u32(sm + q * C::TILE), 16, 1024, 2), umma_desc(slot(i), 16, 1024, 2),
              idesc_qk);
       umma_commit_warp(bar(B_S + t));
     };
@@ -487,38 +500,71 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     auto release = [&](int i) {
       umma_commit_warp(bar(B_EMPTY + i % C::NST));
     };
+    // V of key block j of a piece has landed; key slots past the last key may
+    // hold anything (even NaN): their V rows are zeroed, so that 0 * V stays 0.
+    auto v_ready = [&](const Piece& pc, int j, int iv) {
+      if (!wait(B_FULL + iv % C::NST, iv / C::NST)) return false;
+      const int valid = pc.L - (pc.j0 + j) * C::BK;
+      if (valid < C::BK) {
+        uint8_t* v = sm + C::OFF_RING + (iv % C::NST) * C::TILE;
+        for (int x = lane; x < (C::BK - valid) * 16; x += 32)
+          *reinterpret_cast<uint4*>(v + (x & 1) * C::HALF + (valid + (x >> 4)) * 128 + ((x >> 1) & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
+      return true;
+    };
     for (int k = 0; k < pieces && ok; ++k) {
       const Piece pc = tail.piece[k];
       if (pc.nblk == 0) continue;
-      const int blocks = pc.n_rows > 128 ? 2 : 1;  // row blocks with rows
-      for (int t = 0; t < blocks && ok; ++t) {
+      if (pc.n_rows <= 128) {
+        // narrow: A takes the even key blocks, B the odd ones, of the same rows
+        const bool q_in = wait(B_Q, n_q);
+        n_q ^= 1u;
+        for (int j = 0; j < min(2, pc.nblk) && q_in; ++j) {
+          if (!wait(B_FULL + (item + 2 * j) % C::NST, (item + 2 * j) / C::NST)) break;
+          tc_fence_after();
+          qk(j, 0, item + 2 * j);
+          release(item + 2 * j);
+        }
+        for (int j = 0; j < pc.nblk && ok; ++j) {
+          const int t = j & 1, iv = item + 2 * j + 1, ik = item + 2 * j + 4;  // V of this block, K of the next but one
+          if (!v_ready(pc, j, iv) || !wait(B_P + t, n_p >> t)) break;
+          n_p ^= 1u << t;
+          tc_fence_after();
+          pv(t, iv, j > 1);
+          if (j + 2 < pc.nblk) {
+            if (!wait(B_FULL + ik % C::NST, ik / C::NST)) break;
+            tc_fence_after();
+            qk(t, 0, ik);
+            release(iv);
+            release(ik);
+          } else {
+            umma_commit_warp(bar(B_O + t));
+            release(iv);
+          }
+        }
+        item += 2 * pc.nblk;
+        continue;
+      }
+      for (int t = 0; t < 2 && ok; ++t) {
         const bool q_in = wait(B_Q + t, n_q >> t);
         n_q ^= 1u << t;
         if (!q_in || (t == 0 && !wait(B_FULL + item % C::NST, item / C::NST))) break;
         tc_fence_after();
-        qk(t, item);
-        if (t == blocks - 1) release(item);
+        qk(t, t, item);
+        if (t == 1) release(item);
       }
       for (int j = 0; j < pc.nblk && ok; ++j) {
         const int iv = item + 2 * j + 1, ik = iv + 1;  // V of this block, K of the next
         bool k_in = true;
-        for (int t = 0; t < blocks && ok; ++t) {
+        for (int t = 0; t < 2 && ok; ++t) {
           if (t == 0) {
             // (off the way from P to the next product, if K has landed by now)
             if (j + 1 < pc.nblk)
               k_in = __all_sync(kFull, mbar_test(bar(B_FULL + ik % C::NST), (ik / C::NST) & 1));
-            if (!wait(B_FULL + iv % C::NST, iv / C::NST)) break;
-            const int valid = pc.L - (pc.j0 + j) * C::BK;
-            if (valid < C::BK) {
-              // key slots past the last key may hold anything (even NaN): zero
-              // their V rows, so that 0 * V stays 0
-              uint8_t* v = sm + C::OFF_RING + (iv % C::NST) * C::TILE;
-              for (int x = lane; x < (C::BK - valid) * 16; x += 32)
-                *reinterpret_cast<uint4*>(v + (x & 1) * C::HALF + (valid + (x >> 4)) * 128 + ((x >> 1) & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-            }
+            if (!v_ready(pc, j, iv)) break;
           }
           if (!wait(B_P + t, n_p >> t)) break;
           n_p ^= 1u << t;
@@ -530,12 +576,12 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
               tc_fence_after();
               k_in = true;
             }
-            qk(t, ik);
+            qk(t, t, ik);
           } else {
             umma_commit_warp(bar(B_O + t));
           }
           // (behind the products, which are not to wait for it)
-          if (t == blocks - 1) {
+          if (t == 1) {
             release(iv);
             if (j + 1 < pc.nblk) release(ik);
           }
@@ -552,7 +598,6 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     // --------------------------------------------------------- softmax warps
     const int t = warp >> 2;                       // row block
     const int r = (warp & 3) * 32 + lane;          // TMEM lane
-    const int row = t * 128 + r;                   // of the tile
     // this warp's lanes and the columns of S and, + 256 - 128 t, of O
     const uint32_t scol = tmem + (uint32_t((warp & 3) * 32) << 16) + C::S_COL + 128 * t;
     const uint32_t ocol = scol + (C::O_COL - C::S_COL);
@@ -568,7 +613,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     // that runs once for a piece: such code waits for its own instructions.
     auto each_row = [&](const Piece& q, auto&& body) {
       int rr = (warp & 3) * 32 + (lane >> 4);
-      const int first = q.row0 + t * 128 + rr;
+      const int first = q.row0 + t * 128 + rr;  // (not called for B's share of a narrow piece)
       int tok = first / a.G, g = first - tok * a.G;
 #pragma unroll 1
       for (int i = 0; i < 16; ++i, rr += 2) {
@@ -581,9 +626,9 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     // the products that read the Q before are done.
     int k = 0;
     auto take_piece = [&]() {
-      while (t == 1 && k < pieces && tail.piece[k].n_rows <= 128) ++k;
+      while (t == 1 && k < pieces && tail.piece[k].n_rows <= 128 && tail.piece[k].nblk < 2) ++k;
       if (k == pieces) return false;
-      if (tail.piece[k].nblk > 0)
+      if (tail.piece[k].nblk > 0 && (t == 0 || tail.piece[k].n_rows > 128))
         each_row(tail.piece[k], [&](int rr, bool in, int64_t token, int head) {
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (in ? token * a.q_stride + head * 128 : 0);
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(chunk_at(rr, lane & 15))),
@@ -592,9 +637,18 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
         });
       return true;
     };
+    uint32_t n_ml = 0, n_ob = 0;  // phases of B_ML and, seen by A, of B's B_O
+    bool joining = false;         // B: A has still to read its last narrow piece's O
+    float2* ml = reinterpret_cast<float2*>(sm + C::OFF_ML);
     bool more = take_piece();
     while (ok && more) {
       const Piece pc = tail.piece[k++];
+      // A narrow piece (up to 128 rows) has its key blocks dealt to A and B in
+      // turn, as if they were two row blocks, and A joins the two results: a
+      // single row block's chain of products and softmaxes would be longer
+      // than K and V take to arrive.
+      const bool narrow = pc.n_rows <= 128, two = narrow && pc.nblk > 1;
+      const int row = narrow ? r : t * 128 + r;  // of the tile
       const bool live = row < pc.n_rows;
       const bool any = __any_sync(kFull, live);  // a warp without rows only keeps step
       const bool whole = pc.slot < 0;
@@ -602,18 +656,24 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
       // that whole rows are written; a partial one (whose layout puts a
       // column's rows side by side), and one of a few rows, straight from
       // registers, with the next piece's Q already on its way.
-      const bool staged = whole && (a.parts == 0 || pc.n_rows > 128);
-      if (pc.nblk > 0) {
+      const bool staged = whole && (a.parts == 0 || !narrow);
+      if (pc.nblk > 0 && (t == 0 || !narrow)) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(bar(B_Q + t));
       }
       float m_ref = -INFINITY, l = 0.f;
-      int valid = pc.L - pc.j0 * C::BK;  // keys from the block's first on
-      for (int j = 0; j < pc.nblk; ++j, valid -= C::BK) {
+      const int step = narrow ? 2 : 1;
+      int valid = pc.L - (pc.j0 + (narrow ? t : 0)) * C::BK;  // keys from the block's first on
+      for (int j = narrow ? t : 0; j < pc.nblk; j += step, valid -= step * C::BK) {
         ok = __all_sync(kFull, mbar_wait(bar(B_S + t), n_s++ & 1));
         if (!ok) break;
         tc_fence_after();
+        if (joining) {  // (B's O is written over by what its next P starts)
+          joining = false;
+          ok = __all_sync(kFull, mbar_wait(bar(B_JOINED), (n_ml - 1) & 1));
+          if (!ok) break;
+        }
         if (any) {
           float s[128];
           tmem_ld64(scol, s);
@@ -673,14 +733,42 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
         mbar_arrive(bar(B_P + t));
       }
 
-      // ---- the piece's result (S of its last block has come: Q is read)
+      // ---- the piece's result (S of its last block has come: Q is read; in a
+      // narrow piece B may still be at its own last block, which A waits for)
+      if (!ok) break;
+      if (two && t == 1) {
+        ml[r] = make_float2(m_ref, l);
+        mbar_arrive(bar(B_ML));
+        ++n_ml;
+        ++n_o;
+        joining = true;
+        more = take_piece();
+        continue;
+      }
+      if (two) {
+        ok = __all_sync(kFull, mbar_wait(bar(B_ML), n_ml++ & 1));
+        if (ok) ok = __all_sync(kFull, mbar_wait(bar(B_O + 1), n_ob & 1));
+      }
+      n_ob += two || (!narrow && pc.nblk > 0);
       if (ok && !staged) more = take_piece();
       if (ok && pc.nblk > 0) ok = __all_sync(kFull, mbar_wait(bar(B_O + t), n_o++ & 1));
       if (!ok) break;
       tc_fence_after();
+      // weights of A's own result and of B's
+      float wa = 1.f, wb = 0.f;
+      if (two) {
+        const float2 other = ml[r];
+        const float m = fmaxf(m_ref, other.x);
+        wa = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
+        wb = other.x == -INFINITY ? 0.f : ex2(other.x - m);
+        l = l * wa + other.y * wb;
+        m_ref = m;
+      }
       if (any) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse = l > 0.f ? (m_ref + lg2(l)) * kLn2 : -INFINITY;
+        wa *= inv;
+        wb *= inv;
         const size_t slot = pc.slot;
         const int tok = (pc.row0 + row) / a.G, g = (pc.row0 + row) - tok * a.G;
         const size_t out_row = (size_t(pc.first) + tok) * a.Hq + size_t(pc.h) * a.G + g;
@@ -689,17 +777,23 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
           float o[32];
           if (pc.nblk > 0) {
             tmem_ld32(ocol + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= wa;
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0.f;
           }
+          if (two) {
+            float ob[32];
+            tmem_ld32(ocol + 128 + c0, ob);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(ob[i], wb, o[i]);
+          }
           if (whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint4 x = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                         pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                         pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                         pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              const uint4 x = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                         pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
               if (staged)
                 *reinterpret_cast<uint4*>(chunk_at(r, c0 / 8 + i)) = x;
               else if (live)
@@ -709,7 +803,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
             float4* dst = reinterpret_cast<float4*>(a.o_part) + (slot * 32 + c0 / 4) * a.part_rows + row;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              dst[size_t(i) * a.part_rows] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+              dst[size_t(i) * a.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
         if (staged) {
@@ -725,6 +819,10 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
           if (!whole) a.lse_part[slot * a.part_rows + row] = lse;
           else if (a.lse) a.lse[out_row] = lse;
         }
+      }
+      if (two) {  // B's O and (m, l) are read
+        tc_fence_before();
+        mbar_arrive(bar(B_JOINED));
       }
       if (staged) more = take_piece();
     }

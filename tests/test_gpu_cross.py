@@ -193,3 +193,22 @@ def test_captured_calls_follow_the_device_lengths():
             results.append((out.clone(), ls.clone()))
         assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
         assert (results[0][0][:cut[0]] == 3).all() and (results[0][0][cut[2]:] == 3).all()
+
+
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_several_items_per_cta(seed):
+    """Between one and four items per SM, of all kinds in a row: one row and hundreds, no key, one block, many."""
+    rng = np.random.default_rng(seed)
+    B = 50
+    lens = [int(x) for x in rng.choice([0, 1, 100, 128, 129, 257, 400, 900], B)]
+    counts = [int(x) for x in rng.choice([0, 1, 2, 40, 64, 70, 140], B)]
+    c = Cache(lens, kv_heads=4, heads=8, device="cuda", seed=55 + seed)
+    run(c, counts)
+
+
+@pytest.mark.parametrize("keys", [1, 128, 129, 256, 257, 1000, 5000])
+@pytest.mark.parametrize("tokens", [1, 64, 65])
+def test_one_head(keys, tokens):
+    """A single item: up to 128 rows its key blocks go to both row blocks in turn, cut or not."""
+    c = Cache([keys], kv_heads=1, heads=2, page=32, device="cuda", seed=59)
+    run(c, [tokens])
