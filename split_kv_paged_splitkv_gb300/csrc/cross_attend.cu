@@ -57,8 +57,7 @@ struct Cross {
   static constexpr int NST = 5;
   static constexpr int OFF_RING = 2 * TILE;      // after Q's two row blocks
   static constexpr int OFF_BAR = OFF_RING + NST * TILE;
-  static constexpr int OFF_ML = OFF_BAR + 512;   // [128] (maximum, sum) of row block B
-  static constexpr int SMEM = 1024 + OFF_ML + 1024;
+  static constexpr int SMEM = 1024 + OFF_BAR + 512;
   static constexpr int SOFTMAX_WARPS = 8;
   // warps: the producers of K and of V, the issuer of the MMAs
   static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 2;
@@ -272,6 +271,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
       "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st2(uint32_t taddr, float x, float y) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+               "f"(x), "f"(y)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld2(uint32_t taddr, float& x, float& y) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=f"(x), "=f"(y)
+               : "r"(taddr)
+               : "memory");
 }
 
 // 8 columns, without a wait.
@@ -639,7 +650,6 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     };
     uint32_t n_ml = 0, n_ob = 0;  // phases of B_ML and, seen by A, of B's B_O
     bool joining = false;         // B: A has still to read its last narrow piece's O
-    float2* ml = reinterpret_cast<float2*>(sm + C::OFF_ML);
     bool more = take_piece();
     while (ok && more) {
       const Piece pc = tail.piece[k++];
@@ -737,7 +747,10 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
       // narrow piece B may still be at its own last block, which A waits for)
       if (!ok) break;
       if (two && t == 1) {
-        ml[r] = make_float2(m_ref, l);
+        // (m, l) into the last two columns of S_B, behind P_B: they are S's again
+        // only when the next product is issued, after A's next Q
+        tmem_st2(scol + 126, m_ref, l);
+        tc_fence_before();
         mbar_arrive(bar(B_ML));
         ++n_ml;
         ++n_o;
@@ -757,7 +770,8 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
       // weights of A's own result and of B's
       float wa = 1.f, wb = 0.f;
       if (two) {
-        const float2 other = ml[r];
+        float2 other;
+        tmem_ld2(scol + 128 + 126, other.x, other.y);
         const float m = fmaxf(m_ref, other.x);
         wa = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
         wb = other.x == -INFINITY ? 0.f : ex2(other.x - m);
@@ -838,62 +852,107 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   }
 }
 
-// Joins the partial results of the item whose first piece is blockIdx.x: its
-// pieces have consecutive slots.  32 rows of the item, a lane each; a warp
-// takes every eighth group of four dims, read side by side for the rows.
-constexpr int kMergeWarps = 8;
-__global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __grid_constant__ CrossArgs a) {
+// Joins the partial results of the cut items (an item's pieces have consecutive
+// slots).  A unit is 32 rows of an item, a lane each; the CTAs take the units
+// of all cut items in turn (a CTA for every possible unit would be 2,432, whose
+// start alone takes 4 us).  A warp takes every eighth group of four dims, which
+// lie side by side for the rows; the log-sum-exps and results of four pieces
+// are loaded at once, and the sums rescaled when later ones are larger.
+constexpr int kMergeWarps = 8, kMergeAtOnce = 4, kMergeGroups = 32 / kMergeWarps;
+constexpr int kMergeWords = (2 * kSmCount + 31) / 32;  // of a bit per piece
+__global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __grid_constant__ CrossArgs a, int units) {
   __shared__ uint2 rows_out[32][33];  // bf16 rows (of 32 pieces of 8 bytes, and one to spread the banks)
   launch_dependents();
   wait_prerequisites();
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const CrossSplit sp = a.split[c];
-  const int r0 = blockIdx.y * 32, row = r0 + lane;
-  if (sp.cuts == 0 || r0 >= sp.rows) return;
-  const int last = c + sp.cuts - 1;
-  const bool live = row < sp.rows;
-  auto slot = [&](int k) { return size_t(k); };
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int k = c; k <= last; ++k)
-    if (live) M = fmaxf(M, a.lse_part[slot(k) * a.part_rows + row]);
-  float sum = 0.f;
-  float4 acc[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned firsts[kMergeWords];  // the pieces that are the first of a cut item
+  {
+    int cuts[kMergeWords];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = c; k <= last; ++k) {
-    if (!live) continue;
-    const float ls = a.lse_part[slot(k) * a.part_rows + row];
-    const float4* src = reinterpret_cast<const float4*>(a.o_part) + (slot(k) * 32 + warp) * a.part_rows + row;
-    float4 x[4];
+    for (int i = 0; i < kMergeWords; ++i) cuts[i] = i * 32 + lane < 2 * a.parts ? a.split[i * 32 + lane].cuts : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = src[size_t(i) * kMergeWarps * a.part_rows];
-    const float w = M == -INFINITY ? 0.f : ex2((ls - M) * 1.4426950408889634f);
-    sum += w;
+    for (int i = 0; i < kMergeWords; ++i) firsts[i] = __ballot_sync(kFull, cuts[i] > 0);
+  }
+  for (int u = blockIdx.x;; u += gridDim.x) {
+    int q = u / units, c = -1;  // the q-th cut item, its first piece
+    const int r0 = (u - q * units) * 32;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[i].x += w * x[i].x;
-      acc[i].y += w * x[i].y;
-      acc[i].z += w * x[i].z;
-      acc[i].w += w * x[i].w;
+    for (int i = 0; i < kMergeWords; ++i) {
+      const int n = __popc(firsts[i]);
+      if (c < 0 && q < n) {
+        unsigned m = firsts[i];
+        for (; q > 0; --q) m &= m - 1;
+        c = i * 32 + __ffs(m) - 1;
+      }
+      q -= n;
     }
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (c < 0) break;
+    const CrossSplit sp = a.split[c];
+    if (r0 >= sp.rows) continue;
+    const int row = r0 + lane;
+    const bool live = row < sp.rows;
+    float M = -INFINITY, sum = 0.f;
+    float4 acc[kMergeGroups];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    rows_out[lane][warp + i * kMergeWarps] =
-        make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
-  __syncthreads();
-  // whole rows out, a warp to a row
-  for (int i = warp; i < 32 && r0 + i < sp.rows; i += kMergeWarps) {
-    const int tok = (sp.row0 + r0 + i) / a.G, g = (sp.row0 + r0 + i) - tok * a.G;
-    const size_t out_row = (size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g;
-    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128)[lane] = rows_out[i][lane];
-  }
-  if (warp == 0 && live && a.lse) {
-    const int tok = (sp.row0 + row) / a.G, g = (sp.row0 + row) - tok * a.G;
-    a.lse[(size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g] = sum > 0.f ? M + lg2(sum) * kLn2 : -INFINITY;
+    for (int i = 0; i < kMergeGroups; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < sp.cuts; k0 += kMergeAtOnce) {
+      float ls[kMergeAtOnce];
+      float4 v[kMergeAtOnce][kMergeGroups];
+#pragma unroll
+      for (int k = 0; k < kMergeAtOnce; ++k) {
+        const size_t slot = c + k0 + k;
+        const bool in = live && k0 + k < sp.cuts;
+        ls[k] = in ? a.lse_part[slot * a.part_rows + row] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kMergeGroups; ++i)
+          if (in) v[k][i] = reinterpret_cast<const float4*>(a.o_part)[(slot * 32 + warp + i * kMergeWarps) * a.part_rows + row];
+      }
+      float m = M;
+#pragma unroll
+      for (int k = 0; k < kMergeAtOnce; ++k) m = fmaxf(m, ls[k]);
+      if (m == -INFINITY) continue;
+      const float old = ex2((M - m) * 1.4426950408889634f);
+      M = m;
+      sum *= old;
+#pragma unroll
+      for (int i = 0; i < kMergeGroups; ++i) {
+        acc[i].x *= old;
+        acc[i].y *= old;
+        acc[i].z *= old;
+        acc[i].w *= old;
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeAtOnce; ++k) {
+        if (ls[k] == -INFINITY) continue;  // (a piece that is none, or without weight)
+        const float w = ex2((ls[k] - m) * 1.4426950408889634f);
+        sum += w;
+#pragma unroll
+        for (int i = 0; i < kMergeGroups; ++i) {
+          acc[i].x += w * v[k][i].x;
+          acc[i].y += w * v[k][i].y;
+          acc[i].z += w * v[k][i].z;
+          acc[i].w += w * v[k][i].w;
+        }
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    __syncthreads();  // (the rows of the unit before are out)
+#pragma unroll
+    for (int i = 0; i < kMergeGroups; ++i)
+      rows_out[lane][warp + i * kMergeWarps] =
+          make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+    __syncthreads();
+    // whole rows out, a warp to a row
+    for (int i = warp; i < 32 && r0 + i < sp.rows; i += kMergeWarps) {
+      const int tok = (sp.row0 + r0 + i) / a.G, g = (sp.row0 + r0 + i) - tok * a.G;
+      const size_t out_row = (size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g;
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128)[lane] = rows_out[i][lane];
+    }
+    if (warp == 0 && live && a.lse) {
+      const int tok = (sp.row0 + row) / a.G, g = (sp.row0 + row) - tok * a.G;
+      a.lse[(size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g] = sum > 0.f ? M + lg2(sum) * kLn2 : -INFINITY;
+    }
   }
 }
 
@@ -942,10 +1001,11 @@ cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& t
   cudaError_t e = cudaLaunchKernelEx(&cfg, cross_attend_kernel, a, *reinterpret_cast<const CUtensorMap*>(&tk),
                                      *reinterpret_cast<const CUtensorMap*>(&tv));
   if (e != cudaSuccess || a.parts == 0) return e;
-  cfg.gridDim = dim3(unsigned(2 * a.parts), unsigned((a.part_rows + 31) / 32), 1);
+  const int units = (a.part_rows + 31) / 32;  // of an item
+  cfg.gridDim = dim3(unsigned(units > 1 ? 2 * a.parts : a.parts), 1, 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, cross_merge_kernel, a);
+  return cudaLaunchKernelEx(&cfg, cross_merge_kernel, a, units);
 }
 
 }  // namespace splitkv
