@@ -497,8 +497,8 @@ void splitkv_rope_destroy(splitkv_rope_t* rope);
  *   k, v           bf16 [Hkv][Dk] and [Hkv][Dv] per token; v NULL with
  *                  v_shares_k
  *   kv_scale, k_scale, v_scale  e4m3 caches store round(x / scale) with
- *                  saturation at +-448: kv_scale, or per KV head where k_scale
- *                  and v_scale (fp32 [Hkv], device) are given
+ *                  saturation at +-448 (NaN stays NaN): kv_scale, or per KV head
+ *                  where k_scale and v_scale (fp32 [Hkv], device) are given
  *   q_out          bf16, strided like q; may be q itself
  *   k_pages, v_pages  the pools, in desc->kv_layout
  *   key_weights, key_positions  state arrays or NULL: the new slots get weight

@@ -126,11 +126,11 @@ def _ptr(x):
     raise TypeError(f"cannot take the address of {type(x)}")
 
 
-def _stream(s):
+def _stream(s, device=None):
     if s is None:
         import torch
         # (the handle alone: making a Stream object costs ten times as much)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -334,6 +334,8 @@ def _addr(name, x, dtype, numel, device):
     kernels run."""
     if x is None or type(x) is int:
         return x
+    if not hasattr(x, "data_ptr"):
+        raise TypeError(f"{name} must be a tensor, an address or None, got {type(x)}")
     if x.dtype is dtype and x.numel() >= numel and x.get_device() == device and x.is_contiguous():
         return x.data_ptr()
     if x.dtype is not dtype or not x.is_contiguous():
@@ -415,7 +417,7 @@ def splitkv_append(desc: splitkv_desc_t, rope, positions, q, k, v, block_table, 
         _addr("v_pages", v_pages, z.pool_dtype, z.v_pool, dev),
         _addr("key_weights", key_weights, f32, z.state, dev),
         _addr("key_positions", key_positions, i32, z.state, dev), _addr("status", status, i32, 1, dev),
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def splitkv_key_weights(desc: splitkv_desc_t, q, k_pages, block_table, seq_lens, lse, scale: float,
@@ -432,7 +434,7 @@ def splitkv_key_weights(desc: splitkv_desc_t, q, k_pages, block_table, seq_lens,
         _addr("k_scale", k_scale, f32, z.kv_heads, dev), decay,
         _addr("weights_in", weights_in, f32, z.state, dev),
         _addr("weights_out", weights_out, f32, z.state, dev), _addr("status", status, i32, 1, dev),
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def splitkv_evict_workspace_size(desc: splitkv_desc_t, budget: int) -> int:
@@ -457,7 +459,7 @@ def splitkv_evict(desc: splitkv_desc_t, budget: int, sink: int, recent: int, k_p
         _addr("positions_out", positions_out, i32, z.state, dev),
         _addr("seq_lens_out", seq_lens_out, i32, z.batch, dev),
         _addr("workspace", workspace, z.torch.uint8, 0, dev), workspace_bytes,
-        _addr("status", status, i32, 1, dev), _stream(stream)))
+        _addr("status", status, i32, 1, dev), _stream(stream, dev)))
 
 
 def splitkv_cross_workspace_size(desc: splitkv_desc_t, n_tokens: int) -> int:
@@ -483,7 +485,7 @@ def splitkv_cross_attend(desc: splitkv_desc_t, cu_tokens, q, k_pages, v_pages, b
         scale, _addr("out", out, z.torch.bfloat16, n * z.heads * z.v_dim, dev),
         _addr("lse", lse, z.torch.float32, n * z.heads, dev),
         _addr("workspace", workspace, z.torch.uint8, 0, dev), workspace_bytes,
-        _addr("status", status, i32, 1, dev), _stream(stream)))
+        _addr("status", status, i32, 1, dev), _stream(stream, dev)))
 
 
 def splitkv_last_error() -> str:

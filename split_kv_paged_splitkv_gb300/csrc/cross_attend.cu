@@ -985,9 +985,9 @@ int cross_box_rows(const splitkv_desc_t& d) {
 
 cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  static cudaError_t attr =
-      cudaFuncSetAttribute(cross_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cross::SMEM);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(cross_attend_kernel), Cross::SMEM, allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;
@@ -998,7 +998,7 @@ cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& t
   cfg.stream = s;
   cfg.attrs = la;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cross_attend_kernel, a, *reinterpret_cast<const CUtensorMap*>(&tk),
+  e = cudaLaunchKernelEx(&cfg, cross_attend_kernel, a, *reinterpret_cast<const CUtensorMap*>(&tk),
                                      *reinterpret_cast<const CUtensorMap*>(&tv));
   if (e != cudaSuccess || a.parts == 0) return e;
   const int units = (a.part_rows + 31) / 32;  // of an item

@@ -561,9 +561,9 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
     nc *= 2;
   const int64_t per = ((cap + nc - 1) / nc + 3) & ~int64_t(3);
   const int rank_cap = int(per <= kRankCap ? per : kRankCap);
-  static cudaError_t attr =
-      cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRankCap * 4);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_shared_memory(reinterpret_cast<const void*>(select_kernel), kRankCap * 4, allowed);
+  if (e != cudaSuccess) return e;
 
   cudaLaunchAttribute la[2];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

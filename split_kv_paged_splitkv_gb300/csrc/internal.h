@@ -1,6 +1,7 @@
 // Internal declarations shared by the planner, the C-ABI layer and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <vector>
@@ -248,6 +249,10 @@ struct CrossArgs {
   int32_t part_rows;  // rows of an item, at most
   int32_t merge_cost;  // of cutting items, in key blocks
 };
+
+// Once per device and kernel: opts in to `bytes` of dynamic shared memory on the
+// current device.  `done` is the kernel's own, a bit per device.
+cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream);
 cudaError_t launch_key_weights(const WeightArgs& a, bool fp8, void* stream);

@@ -301,9 +301,7 @@ template <bool FP8, int NRG>
 cudaError_t launch_weights_t(const WeightArgs& a, cudaStream_t s) {
   constexpr int STAGES = 2;
   constexpr int SMEM = kWarps * STAGES * (FP8 ? 2048 : 4096);
-  static cudaError_t attr = cudaFuncSetAttribute(key_weights_kernel<FP8, NRG, STAGES>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (attr != cudaSuccess) return attr;
+  static_assert(SMEM <= 48 * 1024, "no opt-in needed");
   // as many CTAs as the GPU holds at once
   int dev = 0, sms = 0, per_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -1,7 +1,9 @@
-"""Convenience wrapper: plan, torch-allocated workspace and outputs, one decode.
+"""Convenience wrappers: plans, torch-allocated workspaces and outputs.
 
 Marshalling only -- torch allocates device memory and provides the stream;
-the computation is ``splitkv_decode`` in libsplitkv.
+the computation is in libsplitkv.  ``DecodeSession`` is one decode over given
+caches; ``CacheSession`` holds a paged cache through its life: append, decode,
+weigh, evict, cross attention.
 """
 from __future__ import annotations
 
@@ -11,7 +13,9 @@ from . import (SPLITKV_BF16, SPLITKV_COMBINE_SEPARATE, SPLITKV_FP8_E4M3, SPLITKV
                SPLITKV_LAYOUT_NHD, make_desc, splitkv_combine_workspace, splitkv_decode,
                splitkv_decode_partials,
                splitkv_decode_kv_scales, splitkv_plan, splitkv_plan_fixed,
-               splitkv_plan_upload, splitkv_read_stats)
+               splitkv_plan_upload, splitkv_read_stats, splitkv_append,
+               splitkv_cross_attend, splitkv_cross_workspace_size, splitkv_evict,
+               splitkv_evict_workspace_size, splitkv_key_weights)
 
 
 class DecodeSession:
@@ -89,3 +93,95 @@ class DecodeSession:
     def stats(self):
         """(per-CTA log [n][4], device status word) -- synchronises the stream."""
         return splitkv_read_stats(self.plan, self.workspace, self.stream)
+
+
+class CacheSession:
+    """A paged cache and the calls that fill, read, weigh and prune it.
+
+    ``desc`` (``make_desc``) describes the cache and the decode step; the pools,
+    ``block_table`` and ``seq_lens`` are the caller's tensors, in the layout of
+    ``DecodeSession``.  ``seq_lens`` lives on the device: the caller raises it by
+    the new tokens before ``append``, ``evict`` lowers it.  Nothing here reads
+    a length on the host, so a whole step can be captured into a CUDA graph.
+
+    With ``track`` the session keeps the accumulated weight and the position of
+    every cached key, which ``weigh`` and ``evict`` need.  A session's calls
+    share its workspaces and outputs: one stream at a time.
+    """
+
+    def __init__(self, desc, k_pages, v_pages, block_table, seq_lens, *, scale, rope=None, kv_scale=1.0,
+                 k_scale=None, v_scale=None, num_splits=16, track=False):
+        dev = k_pages.device
+        self.desc, self.rope = desc, rope
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.block_table, self.seq_lens = block_table, seq_lens
+        self.scale, self.kv_scale = float(scale), float(kv_scale)
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.num_splits = num_splits
+        self.plan = None  # made by the first decode
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        slots = (desc.batch, desc.num_kv_heads, desc.max_pages_per_seq * desc.page_size)
+        self.key_weights = torch.zeros(slots, device=dev) if track else None
+        self.key_positions = torch.zeros(slots, dtype=torch.int32, device=dev) if track else None
+        self.evict_workspace = None
+
+    def append(self, positions, q, k, v, cu_tokens=None, q_out=None, stream=None):
+        """Rotates the new tokens' queries (returned) and keys and stores their
+        keys and values (``splitkv_append``); ``q`` may be None."""
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        splitkv_append(self.desc, self.rope, positions, q, k, v, self.block_table, self.seq_lens, q_out,
+                       self.k_pages, self.v_pages, cu_tokens=cu_tokens, kv_scale=self.kv_scale,
+                       k_scale=self.k_scale, v_scale=self.v_scale, key_weights=self.key_weights,
+                       key_positions=self.key_positions, status=self.status, stream=stream)
+        return q_out
+
+    def decode(self, q, out=None, lse=None, stream=None):
+        """Causal decode attention of ``q`` [B][T][Hq][Dk] through a capacity plan."""
+        d = self.desc
+        if self.plan is None:
+            self.plan = splitkv_plan_fixed(d, self.num_splits)
+            self.workspace = torch.empty(max(self.plan.workspace_size, 256), dtype=torch.uint8, device=q.device)
+            splitkv_plan_upload(self.plan, self.workspace, self.workspace.numel(), stream)
+        if out is None:
+            out = torch.empty((d.batch, d.q_tokens, d.num_q_heads, d.v_dim), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((d.batch, d.q_tokens, d.num_q_heads), dtype=torch.float32, device=q.device)
+        args = (self.plan, self.workspace, q, self.k_pages, self.v_pages, self.block_table, self.seq_lens,
+                self.num_splits, self.scale)
+        if self.k_scale is not None:
+            splitkv_decode_kv_scales(*args, self.k_scale, self.v_scale, out, lse, stream)
+        else:
+            splitkv_decode(*args, self.kv_scale, out, lse, stream)
+        return out, lse
+
+    def weigh(self, q, lse, decay=1.0, stream=None):
+        """Adds the attention every cached key got from ``q`` (``lse`` from ``decode``)."""
+        splitkv_key_weights(self.desc, q, self.k_pages, self.block_table, self.seq_lens, lse, self.scale,
+                            self.kv_scale, decay, self.key_weights, self.key_weights, k_scale=self.k_scale,
+                            status=self.status, stream=stream)
+
+    def evict(self, budget, sink=0, recent=0, stream=None):
+        """Cuts every sequence to ``budget`` keys per KV head, in place."""
+        size = splitkv_evict_workspace_size(self.desc, budget)
+        if self.evict_workspace is None or self.evict_workspace.numel() < size:
+            self.evict_workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=self.k_pages.device)
+        splitkv_evict(self.desc, budget, sink, recent, self.k_pages, self.v_pages, self.block_table,
+                      self.seq_lens, self.key_weights, self.key_positions, self.key_weights,
+                      self.key_positions, self.seq_lens, self.evict_workspace, status=self.status,
+                      stream=stream)
+
+    def cross_attend(self, q, cu_tokens=None, stream=None):
+        """Attention of ``q`` [n][Hq][128] over all keys of its sequence, without a causal mask."""
+        n = q.shape[0]
+        size = splitkv_cross_workspace_size(self.desc, n)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+        out = torch.empty((n, self.desc.num_q_heads, 128), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((n, self.desc.num_q_heads), dtype=torch.float32, device=q.device)
+        splitkv_cross_attend(self.desc, cu_tokens, q, self.k_pages, self.v_pages, self.block_table, self.seq_lens,
+                             self.scale, out, lse, workspace, status=self.status, stream=stream)
+        return out, lse
+
+    def read_status(self):
+        """Device status bits of append, weigh, evict and cross_attend so far (synchronises)."""
+        return int(self.status.item())
