@@ -15,12 +15,18 @@
 //
 // Two kernels.  select_kernel: one cluster per (sequence, head); the rank of
 // a key is a 32-bit number (protected in the top bit, then the bits of the
-// weight, whose order is that of non-negative floats), its n-th largest value
+// weight, whose order is that of non-negative floats).  The n-th largest rank
 // is found by radix selection in three digits over histograms that the
-// cluster's CTAs add up in the shared memory of the first; then prefix sums give every freed slot and every moving key its place in the
-// list.  move_kernel copies the rows, persistent over the groups' lists.
-// Bound: 8 bytes of state per key read once (the ranks stay in
-// shared memory), 8 written per kept key, each moved row read and written once.
+// cluster's CTAs add up in the shared memory of the first; then prefix sums
+// give every freed slot and every moving key its place in the list.
+// move_kernel copies the rows, persistent over the groups' lists.
+//
+// Bound: 8 bytes of state per key read once, 8 written per kept key, each moved
+// row read and written once.  Many rows: the moves' bytes (32 sequences x 8
+// heads of 0 .. 131k keys, half kept: 224 us, of which the moves take 153 at
+// 5.7 TB/s of scattered 256-byte rows; floor 136).  One sequence: the chain of
+// barriers and passes of the selection (64k latent rows: 24 us, floor 2.2;
+// 5.9k keys of 2 heads: 14.4 us, of which two dependent launches take about 4).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -37,8 +43,13 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBatch = 4;              // 16-byte vectors a lane loads at a time
 constexpr int kBins = 2048;            // 11-bit digits: bits 31-21, 20-10, and 9-0
+constexpr int kAlike = 2048;           // ranks set aside for the third digit
 constexpr int kMaxCluster = 8;
-constexpr int kRankCap = 46080;        // ranks a CTA can keep in shared memory (180 KB)
+// Ranks a CTA keeps in shared memory; a CTA with more slots makes them anew in
+// each pass, from the L2.  32 KB leave room for two CTAs per SM: 64k latent
+// rows 24.4 us (29.5 with none kept); 256 groups of up to 131k keys 223.7 us
+// (225.8 with all of a CTA's kept, at one CTA per SM).
+constexpr int kRankCap = 8192;
 constexpr int kMoveThreads = 256;
 constexpr int kFewBatch = 32, kManyBatch = 64;  // moves a CTA takes at a time
 constexpr int kMoveGroups = 1024;      // groups whose prefix a CTA holds at a time
@@ -120,6 +131,8 @@ __device__ __forceinline__ void copy_rows(const EvictArgs& a, const Rows<N>& row
 struct SelShared {
   uint32_t hist[kBins];      // this CTA's
   uint32_t total[3][kBins];  // the cluster's, a digit each, in its first CTA
+  uint32_t alike[kAlike];    // ranks with the first digit found, for the third
+  uint32_t n_alike;          // (more than kAlike: not all are there)
   int32_t warp_sum[kSelWarps];
   int32_t pub[4];    // read by the cluster: largest position, equals, holes, movers
   int32_t found[3];  // digit, keys above it, keys of it
@@ -242,6 +255,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   if (cr == 0)
     for (int i = threadIdx.x; i < 3 * kBins / 4; i += kSelThreads)
       reinterpret_cast<uint4*>(sh.total)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) sh.n_alike = 0;
   newest = __reduce_max_sync(kFull, newest);
   if (lane == 0) sh.warp_sum[warp] = newest;
   __syncthreads();
@@ -266,22 +280,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     if (rank_pos) y = *reinterpret_cast<const int4*>(pos + j);
     return make_uint4(rank(x.x, y.x), rank(x.y, y.y), rank(x.z, y.z), rank(x.w, y.w));
   };
-  if (in_smem) {  // (a lane's own slots: no barrier)
-    #pragma unroll 1
-    for (int j0 = wlo; j0 < whi; j0 += 128 * kBatch) {
-      uint4 x[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int j = j0 + u * 128 + lane * 4;
-        if (j < whi) x[u] = ranks_at(j, *reinterpret_cast<const uint4*>(ranks + (j - lo)));
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int j = j0 + u * 128 + lane * 4;
-        if (j < whi) *reinterpret_cast<uint4*>(ranks + (j - lo)) = x[u];
-      }
-    }
-  }
   // Visits this warp's slots in order, four to a lane: body(first slot of the
   // lane, ranks, mask of its slots that exist).
   auto visit = [&](auto&& body) {
@@ -315,18 +313,60 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     for (int e = 0; e < kPer; e += 4)
       if (low >= 0) *reinterpret_cast<uint4*>(sh.hist + low + e) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    visit([&](int, const uint32_t (&r)[4], uint32_t live) {
+    // Counts four ranks of each lane; with the second digit, those that share
+    // the first are put aside, so that the third need not look at all again.
+    auto tally = [&](const uint32_t (&r)[4], uint32_t live) {
       // equal ranks throughout the warp's 128 slots: one addition
       const uint32_t r0 = __shfl_sync(kFull, r[0], 0);
       const bool same = live == 15u && r[0] == r0 && r[1] == r0 && r[2] == r0 && r[3] == r0;
       if (__all_sync(kFull, same)) {
-        if (lane == 0 && (r0 & mask) == T) atomicAdd(sh.hist + ((r0 >> shift) & (nbins - 1)), 128u);
+        if (lane == 0 && (r0 & mask) == T) {
+          atomicAdd(sh.hist + ((r0 >> shift) & (nbins - 1)), 128u);
+          if (d == 1) atomicAdd(&sh.n_alike, uint32_t(kAlike + 1));
+        }
         return;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if ((live >> e & 1) && (r[e] & mask) == T) atomicAdd(sh.hist + ((r[e] >> shift) & (nbins - 1)), 1u);
-    });
+        if ((live >> e & 1) && (r[e] & mask) == T) {
+          atomicAdd(sh.hist + ((r[e] >> shift) & (nbins - 1)), 1u);
+          if (d == 1) {
+            const uint32_t at = atomicAdd(&sh.n_alike, 1u);
+            if (at < kAlike) sh.alike[at] = r[e];
+          }
+        }
+    };
+    if (d == 0 && in_smem) {
+      // the weights in shared memory become ranks (a lane's own slots: no barrier)
+#pragma unroll 1
+      for (int j0 = wlo; j0 < whi; j0 += 128 * kBatch) {
+        int4 y[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int j = j0 + u * 128 + lane * 4;
+          y[u] = make_int4(0, 0, 0, 0);
+          if (rank_pos && j < whi) y[u] = *reinterpret_cast<const int4*>(pos + j);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (j0 + u * 128 >= whi) break;  // (the same for the warp)
+          const int j = j0 + u * 128 + lane * 4;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (j < whi) {
+            x = *reinterpret_cast<const uint4*>(ranks + (j - lo));
+            x = make_uint4(rank(x.x, y[u].x), rank(x.y, y[u].y), rank(x.z, y[u].z), rank(x.w, y[u].w));
+            *reinterpret_cast<uint4*>(ranks + (j - lo)) = x;
+          }
+          const uint32_t r[4] = {x.x, x.y, x.z, x.w};
+          tally(r, j >= whi ? 0u : whi - j >= 4 ? 15u : (1u << (whi - j)) - 1);
+        }
+      }
+    } else if (d == 2 && sh.n_alike <= kAlike) {
+      for (uint32_t i = threadIdx.x; i < sh.n_alike; i += kSelThreads)
+        if ((sh.alike[i] & mask) == T) atomicAdd(sh.hist + (sh.alike[i] & (nbins - 1)), 1u);
+    } else {
+      visit([&](int, const uint32_t (&r)[4], uint32_t live) { tally(r, live); });
+    }
     __syncthreads();
     // This CTA's counts (of few bins) into the first CTA's sums, which all read.
     uint32_t* total = cluster.map_shared_rank(sh.total[d], 0);
@@ -551,10 +591,10 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // CTAs per (sequence, head): one for each 2048 slots of capacity while the
-  // groups do not fill the GPU, and one for each 32,768 slots in any case (128
-  // KB of ranks).  5.9k slots of 2 heads: 14.8 us with four, 17.0 with eight,
-  // 16.5 with one; 64k slots of one: 32 with four, 26 with eight; 256 heads of
-  // 131k: 227 with four, 233 with eight, 281 with two.
+  // groups do not fill the GPU, and one for each 32,768 slots in any case.
+  // 5.9k slots of 2 heads: 14.4 us with four, 16.0 with eight, 15.8 with one;
+  // 64k slots of one: 24.4 with eight, 39 with four, 58 with two, and 26.4 with
+  // sixteen; 256 groups of 131k: 224 with four, 238 with eight, 261 with two.
   int nc = 1;
   while (nc < kMaxCluster && ((cap > int64_t(nc) * 2048 && int64_t(groups) * nc * 2 <= int64_t(sms) * 4) ||
                               cap > int64_t(nc) * 32768))
@@ -587,8 +627,8 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   mv.numAttrs = 1;
   mv.blockDim = dim3(kMoveThreads, 1, 1);
   // Few moves go in small batches, so that more SMs take part (12k rows of 576
-  // bytes: 24.5 us in batches of 32, 26.4 of 64), many in large ones, for bytes
-  // in flight (840k pairs of 256-byte rows: 266 us and 233).
+  // bytes: 24.4 us in batches of 32, 26.2 of 64), many in large ones, for bytes
+  // in flight (840k pairs of 256-byte rows: 253 us and 224).
   const bool few = int64_t(groups) * a.max_moves <= int64_t(sms) * 256;
   const int batch = few ? kFewBatch : kManyBatch;
   const int64_t most = int64_t(groups) * ((a.max_moves + batch - 1) / batch);
