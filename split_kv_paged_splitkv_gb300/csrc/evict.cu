@@ -23,10 +23,10 @@
 //
 // Bound: 8 bytes of state per key read once, 8 written per kept key, each moved
 // row read and written once.  Many rows: the moves' bytes (32 sequences x 8
-// heads of 0 .. 131k keys, half kept: 224 us, of which the moves take 153 at
-// 5.7 TB/s of scattered 256-byte rows; floor 136).  One sequence: the chain of
-// barriers and passes of the selection (64k latent rows: 24 us, floor 2.2;
-// 5.9k keys of 2 heads: 14.4 us, of which two dependent launches take about 4).
+// heads of up to 131k keys cut to 16k: 220 us, of which the moves take 150 at
+// 5.8 TB/s of scattered 256-byte rows; floor 136).  One sequence: the chain of
+// barriers and passes of the selection (64k latent rows: 25 us, floor 2.2;
+// 5.9k keys of 2 heads: 13.8 us, of which two dependent launches take about 4).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -50,8 +50,8 @@ constexpr int kMaxCluster = 8;
 // rows 24.4 us (29.5 with none kept); 256 groups of up to 131k keys 223.7 us
 // (225.8 with all of a CTA's kept, at one CTA per SM).
 constexpr int kRankCap = 8192;
-constexpr int kMoveThreads = 256;
-constexpr int kFewBatch = 32, kManyBatch = 64;  // moves a CTA takes at a time
+constexpr int kMoveThreads = 128, kMovePerSm = 8;
+constexpr int kFewBatch = 16, kManyBatch = 32;  // moves a CTA takes at a time
 constexpr int kMoveGroups = 1024;      // groups whose prefix a CTA holds at a time
 
 // Rows of the pools that a batch of moves reads and writes.
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
 // batches form one line of which a CTA takes every gridDim.x-th.  While the
 // rows of a batch are in flight, the first threads look up the next one's.
 template <int BATCH, int UNROLL>
-__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, kMovePerSm) move_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ int32_t upto[kMoveGroups];  // batches of the groups up to and with this one
   __shared__ int32_t part[kMoveThreads / 32];
   __shared__ Rows<BATCH> rows[2];
@@ -626,16 +626,17 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   mv.attrs = la;
   mv.numAttrs = 1;
   mv.blockDim = dim3(kMoveThreads, 1, 1);
-  // Few moves go in small batches, so that more SMs take part (12k rows of 576
-  // bytes: 24.4 us in batches of 32, 26.2 of 64), many in large ones, for bytes
-  // in flight (840k pairs of 256-byte rows: 253 us and 224).
+  // Eight small CTAs per SM, so that some load while others wait at a barrier
+  // (840k pairs of 256-byte rows: 219.8 us; four of 256 threads 223.7).  Few
+  // moves go in small batches, so that more SMs take part (2.7k of those pairs:
+  // 13.8 us in batches of 16, 15.0 of 32), many in large ones, for bytes in flight.
   const bool few = int64_t(groups) * a.max_moves <= int64_t(sms) * 256;
   const int batch = few ? kFewBatch : kManyBatch;
   const int64_t most = int64_t(groups) * ((a.max_moves + batch - 1) / batch);
-  const int64_t grid = most < int64_t(sms) * 4 ? (most > 0 ? most : 1) : int64_t(sms) * 4;
+  const int64_t grid = most < int64_t(sms) * kMovePerSm ? (most > 0 ? most : 1) : int64_t(sms) * kMovePerSm;
   mv.gridDim = dim3(unsigned(grid), 1, 1);
-  return few ? cudaLaunchKernelEx(&mv, move_kernel<kFewBatch, kFewBatch / 8>, a)
-             : cudaLaunchKernelEx(&mv, move_kernel<kManyBatch, kManyBatch / 8>, a);
+  return few ? cudaLaunchKernelEx(&mv, move_kernel<kFewBatch, kFewBatch / 4>, a)
+             : cudaLaunchKernelEx(&mv, move_kernel<kManyBatch, kManyBatch / 4>, a);
 }
 
 }  // namespace splitkv
