@@ -482,7 +482,7 @@ void splitkv_rope_destroy(splitkv_rope_t* rope);
  * tokens [cu_tokens[b], cu_tokens[b + 1]), becomes key
  * j = seq_lens[b] - (cu_tokens[b + 1] - n): the lengths count the new tokens,
  * as for splitkv_decode.  Tokens outside [cu_tokens[0], cu_tokens[B]) are
- * padding: nothing of theirs is read or written.
+ * padding: their rows may hold anything, and nothing is written for them.
  *   desc           the cache (q_tokens counts only without cu_tokens; there is
  *                  no limit on query rows per KV head here): qk_dim = v_dim =
  *                  128, or one KV head with qk_dim 576 and v_dim 512
@@ -565,7 +565,8 @@ splitkv_status splitkv_key_weights(const splitkv_desc_t* desc, const void* q, co
  * A length outside [0, max_pages_per_seq * P] sets SPLITKV_DEVERR_SEQLEN and
  * its sequence is left as it is; a page id out of range sets
  * SPLITKV_DEVERR_PAGE and the rows that it would hold are not moved.
- * Two kernels; results do not depend on the order of execution.
+ * Two kernels; results do not depend on the order of execution.  EINVAL from
+ * 2^28 pairs of sequence and KV head on.
  */
 size_t splitkv_evict_workspace_size(const splitkv_desc_t* desc, int32_t budget);
 splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t sink,
@@ -588,7 +589,7 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
  *                q_tokens tokens for every sequence.  Tokens outside
  *                [cu_tokens[0], cu_tokens[B]) are left as they are
  *   q            bf16, token n's heads [Hq][128] at q + n * q_stride (elements,
- *                a multiple of 8)
+ *                a multiple of 8 below 2^31)
  *   scale        softmax scale, positive
  *   out          bf16 [n_tokens][Hq][128]; must not overlap q
  *   lse          fp32 [n_tokens][Hq] natural-log LSE of the scaled scores, or
@@ -598,7 +599,7 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
  *                aligned, used by this call alone until it has finished
  * A length outside [0, max_pages_per_seq * P] sets SPLITKV_DEVERR_SEQLEN and
  * counts as 0; a page id out of range sets SPLITKV_DEVERR_PAGE (page 0 is read
- * in its place).  One kernel, or two where the keys are split (few tokens).
+ * in its place).  One kernel, or two where there are few tokens.
  * EUNSUPPORTED for e4m3 caches and other row widths.
  */
 size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens);

@@ -18,7 +18,10 @@
 //
 // Bound: the bytes of q (read and written), k and v (read, and written in the
 // cache's type); a decode step of a few tokens is bound by one chain of
-// loads, so nothing but the token's own loads precedes its stores.
+// loads, so nothing but the token's own loads precedes its stores.  Measured:
+// 26k prompt tokens of 40 rows of 128: 99 us, 5.4 TB/s (floor 79 at the copy's
+// 6.8: rows of 256 bytes go to as many places); one token 3.2 us, 32 in e4m3
+// 3.7, of which a launch is most.
 //
 // One thread handles 32-byte units (two 16-byte chunks of a head row, the
 // two halves of the same eight pairs where pairs are half a row apart), so
@@ -302,7 +305,8 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
 }
 
 // A call of few tokens takes one unit per thread, to use more of the GPU's
-// SMs; a long one four, for bytes in flight.
+// SMs (32 tokens: 3.7 us, with four 8.8); a long one four, for bytes in flight
+// (26k tokens: 99 us, with one 239).
 constexpr int64_t kFewUnits = 1 << 17;
 
 template <int DK, int DV, bool FP8>

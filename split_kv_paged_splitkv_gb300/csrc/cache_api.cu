@@ -70,6 +70,15 @@ int64_t max_moves(const splitkv_desc_t& d, int32_t budget) {
   return budget >= cap ? 0 : (budget < cap - budget ? budget : cap - budget);
 }
 
+// Eviction starts up to eight CTAs for each (sequence, KV head).
+splitkv_status validate_groups(const splitkv_desc_t* d) {
+  splitkv_status st = validate_cache(d);
+  if (st != SPLITKV_OK) return st;
+  if (int64_t(d->batch) * d->num_kv_heads >= (int64_t(1) << 28))
+    return fail(SPLITKV_EINVAL, "batch * num_kv_heads must be below 2^28");
+  return SPLITKV_OK;
+}
+
 splitkv_status validate_cross(const splitkv_desc_t* d, int32_t n_tokens) {
   splitkv_status st = validate_cache(d);
   if (st != SPLITKV_OK) return st;
@@ -289,7 +298,7 @@ splitkv_status splitkv_key_weights(const splitkv_desc_t* desc, const void* q, co
 }
 
 size_t splitkv_evict_workspace_size(const splitkv_desc_t* desc, int32_t budget) {
-  if (validate_cache(desc) != SPLITKV_OK || budget < 1) return 0;
+  if (validate_groups(desc) != SPLITKV_OK || budget < 1) return 0;
   const size_t groups = size_t(desc->batch) * desc->num_kv_heads;
   return align256(groups * 8) + align256(groups * 2 * size_t(max_moves(*desc, budget)) * 4) + 256;
 }
@@ -301,7 +310,7 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
                              float* weights_out, int32_t* positions_out, int32_t* seq_lens_out,
                              void* workspace, size_t workspace_bytes, int32_t* status,
                              void* stream) {
-  splitkv_status st = validate_cache(desc);
+  splitkv_status st = validate_groups(desc);
   if (st != SPLITKV_OK) return st;
   const splitkv_desc_t& d = *desc;
   if (budget < 1) return fail(SPLITKV_EINVAL, "budget must be >= 1");
@@ -388,8 +397,8 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   for (const void* p : words)
     if (misaligned(p, 4)) return fail(SPLITKV_EINVAL, "index arrays and lse must be 4-byte aligned");
   const int64_t row = int64_t(d.num_q_heads) * 128;
-  if (q_stride < row || q_stride % 8)
-    return fail(SPLITKV_EINVAL, "q_stride must be a multiple of 8 elements and hold a token's heads");
+  if (q_stride < row || q_stride % 8 || q_stride > (int64_t(1) << 31) - 8)
+    return fail(SPLITKV_EINVAL, "q_stride must be a multiple of 8 elements, hold a token's heads and be below 2^31");
   if (n_tokens > 0 && overlap(q, size_t((n_tokens - 1) * q_stride + row) * 2, out, size_t(n_tokens) * row * 2))
     return fail(SPLITKV_EINVAL, "out overlaps q");
   if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPLITKV_EINVAL, "scale must be positive and finite");
@@ -397,7 +406,6 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   CrossArgs a{};
   a.parts = cross_parts(d, n_tokens);
   a.part_rows = cross_part_rows(d, n_tokens);
-  a.merge_cost = a.part_rows > 64 ? 5 : 3;
   if (a.parts > 0) {
     if (!workspace) return fail(SPLITKV_EWORKSPACE, "workspace is NULL");
     if (misaligned(workspace, 16)) return fail(SPLITKV_EINVAL, "workspace must be 16-byte aligned");

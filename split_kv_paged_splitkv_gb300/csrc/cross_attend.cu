@@ -23,18 +23,27 @@
 // finished S also say that the PV before it is done (P read, O at rest).
 //
 // K and V blocks pass in that order through one ring of five 32 KB slots that
-// one producer warp fills by TMA, one box per page piece and 64-column half,
-// 128-byte swizzled; K is read K-major, V with its dims on N.
+// two producer warps, one for K and one for V, fill by TMA, one box per page
+// piece and 64-column half, 128-byte swizzled; K is read K-major, V with its
+// dims on N.
 // TMEM columns: S_A [0, 128), S_B [128, 256), O_A [256, 384), O_B [384, 512).
 //
 // Many items (prompts): a CTA per item; the bound is 4 * 128 * rows * L
-// operations.  Few items (a decoder token over the encoder's states, short
-// prompts; the bound is the bytes of K and V, or the longest item): one CTA
+// operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 780 to
+// 810 us, 1,320 to 1,370 TFLOP/s (floor 552 at 1,938), at 1,370 of the GPU's
+// 1,400 W and with the tensor pipe waiting for the softmax's turn of the row
+// blocks.
+//
+// Few items (a decoder token over the encoder's states, short prompts): one CTA
 // per SM, which finds by the device lengths how finely to cut the items' keys
 // and walks its pieces (the ring and the barriers run on across them); cut
-// items leave partial results that merge_kernel joins by their log-sum-exps.
-// An item of up to 128 rows uses the second row block for every other key
-// block of the same rows.
+// items leave partial results that cross_merge_kernel joins by their
+// log-sum-exps.  An item of up to 128 rows uses the second row block for every
+// other key block of the same rows.  Bound: the bytes of K and V, at HBM's rate
+// once the copies flow, behind a start of 5 us (the plan, the first blocks) and
+// the merge's 2 (one token of 8 requests over 1.2k keys of 16 heads: 32 us,
+// floor 11.6), or the longest piece's chain of products (prompts of 37 to 900
+// tokens over 1 to 4.1k keys: 24.4 us, floor 2.9).
 //
 // P is rounded to bf16 for the second product (half a step, 2^-8 of a weight,
 // as in the decode kernels); sums, maxima and O are fp32.
@@ -140,7 +149,9 @@ __device__ __forceinline__ int cuts_of(int nb, float t) {
 // Few items: every item of nb key blocks is cut into ceil(nb / t) equal pieces,
 // and CTA c takes pieces c, c + parts, ... of the line of all items' pieces.
 // Lane i weighs t = ceil(longest nb / (i + 1)): the blocks of the CTA with most,
-// two more for each of its pieces, and a.merge_cost if anything is cut.
+// two more for each of its pieces, and two if anything is cut.  (What that
+// chooses for 16 heads: two key blocks stay whole, 12.5 us with one token and
+// 12.7 cut; four are cut, 13.1 and 14.8 whole, and with 256 tokens 17.3 and 20.2.)
 __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& tail) {
   int tiles = 0, nb = 1;
   auto read = [&](int b0) {  // lane: sequence b0 + lane
@@ -178,7 +189,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
     n *= a.Hkv;
     // (cut pieces have a slot each; uncut items need none)
     const bool fits = lane == 0 || n <= 2 * a.parts;
-    const uint32_t cost = (n + a.parts - 1) / a.parts * (uint32_t(t) + 2) + (n > items ? a.merge_cost : 0);
+    const uint32_t cost = (n + a.parts - 1) / a.parts * (uint32_t(t) + 2) + (n > items ? 2 : 0);
     const int best = __reduce_min_sync(kFull, fits ? cost * 32 + lane : ~0u) & 31;
     T = __shfl_sync(kFull, t, best);
     P = __shfl_sync(kFull, n, best);
@@ -840,6 +851,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
       }
       if (staged) more = take_piece();
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out)
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
   }
 

@@ -247,7 +247,6 @@ struct CrossArgs {
   int32_t n_tokens, batch, T, Hq, Hkv, G, P, max_pages, num_pages, box_rows;
   int32_t parts;      // CTAs that share all items' key blocks; 0: a CTA per item
   int32_t part_rows;  // rows of an item, at most
-  int32_t merge_cost;  // of cutting items, in key blocks
 };
 
 // Once per device and kernel: opts in to `bytes` of dynamic shared memory on the

@@ -12,9 +12,14 @@
 // operands use the same one, so each lane owns 16-byte pieces of two key rows
 // that are its A operand as they lie (four lanes read 64 consecutive bytes),
 // and query pieces chosen the same way are its B operand.  A lane copies its
-// pieces of the next tiles into shared memory asynchronously and reads back
-// only what it copied itself: a ring per warp with no barrier at all, and up
-// to ten tiles of a warp in flight.
+// pieces of the next tile into shared memory asynchronously and reads back
+// only what it copied itself: no barrier at all, and the bytes in flight come
+// from the number of warps (32 KB of a CTA's four; a third tile of a warp in
+// flight costs more in CTAs per SM than it gives: 171 us against 165 below).
+//
+// Measured: 32 sequences of up to 131k keys, 8 heads, bf16: 165 us, 6.4 TB/s of
+// the 6.8 a copy gets; 8 of 32k in e4m3: 27.2 us (floor 20.2, the rest the
+// start and its chain of loads); one of 5.9k: 4.2 us, the chain alone.
 //
 // Work is split by the device lengths: the 16-key tiles of all (sequence, KV
 // head) pairs form one line, cut into equal contiguous parts, one per warp.

@@ -152,6 +152,12 @@ def test_evict_refusals(kw):
     refused(EINVAL, call_evict, desc(), **kw)
 
 
+def test_evict_refuses_more_groups_than_a_grid_holds():
+    d = desc(B=1 << 27, Hkv=2, maxp=1)
+    assert "2^28" in refused(EINVAL, call_evict, d) and skv.splitkv_evict_workspace_size(d, 1) == 0
+    assert skv.splitkv_evict_workspace_size(desc(B=(1 << 27) - 1, Hkv=2, maxp=1), 1) > 0
+
+
 def test_evict_workspace():
     d = desc(B=3, Hkv=2, maxp=8, P=16)  # 128 slots
     refused(EWORKSPACE, call_evict, d, workspace=None)
@@ -194,7 +200,8 @@ def test_cross_refuses_other_caches_and_small_workspaces():
     assert skv.splitkv_cross_workspace_size(d, 0) == 0 and skv.splitkv_cross_workspace_size(d, -1) == 0
     call_cross(d, cu_tokens=A, n_tokens=0)  # nothing to do, nothing launched
     lib = skv._lib.splitkv_cross_attend
-    assert lib(ctypes.byref(d), 1, None, A, 1016, A, A, A, A, 0.1, 1 << 40, None, A, 1 << 40, None, 0) == EINVAL
+    for stride in (1016, 1025, 1 << 31, 1 << 62, -1024):
+        assert lib(ctypes.byref(d), 1, None, A, stride, A, A, A, A, 0.1, 1 << 40, None, A, 1 << 40, None, 0) == EINVAL
 
 
 def test_tensor_arguments_are_checked():
