@@ -483,6 +483,7 @@ void splitkv_rope_destroy(splitkv_rope_t* rope);
  * j = seq_lens[b] - (cu_tokens[b + 1] - n): the lengths count the new tokens,
  * as for splitkv_decode.  Tokens outside [cu_tokens[0], cu_tokens[B]) are
  * padding: their rows may hold anything, and nothing is written for them.
+ * With n_tokens = 0 nothing is done.
  *   desc           the cache (q_tokens counts only without cu_tokens; there is
  *                  no limit on query rows per KV head here): qk_dim = v_dim =
  *                  128, or one KV head with qk_dim 576 and v_dim 512
@@ -581,8 +582,8 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
  * splitkv_cross_attend -- attention of query tokens over a paged cache of
  * another length, without a causal mask: every token of sequence b attends to
  * all seq_lens[b] keys (an encoder's states, written once with
- * splitkv_append).  Any number of tokens per sequence, one (a decode step) to
- * whole prompts.
+ * splitkv_append).  Any number of tokens per sequence, none, one (a decode
+ * step) to whole prompts; with n_tokens = 0 nothing is done.
  *   desc         the cache, bf16, qk_dim = v_dim = 128 (q_tokens counts only
  *                without cu_tokens; any number of query rows per KV head)
  *   cu_tokens    int32 [B + 1], not decreasing, within [0, n_tokens], or NULL:

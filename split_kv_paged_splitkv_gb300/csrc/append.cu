@@ -320,7 +320,6 @@ cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t s) {
 
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.n_tokens == 0) return cudaSuccess;
   if (qk_dim == 128 && v_dim == 128)
     return fp8 ? launch_append_t<128, 128, true>(a, s) : launch_append_t<128, 128, false>(a, s);
   return fp8 ? launch_append_t<576, 512, true>(a, s) : launch_append_t<576, 512, false>(a, s);

@@ -179,6 +179,7 @@ splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* 
   if (n_tokens < 0) return fail(SPLITKV_EINVAL, "n_tokens must be >= 0");
   if (!cu_tokens && int64_t(d.batch) * d.q_tokens != n_tokens)
     return fail(SPLITKV_EINVAL, "without cu_tokens, n_tokens (%d) must be batch * q_tokens", n_tokens);
+  if (n_tokens == 0) return SPLITKV_OK;
   if (!k || !block_table || !seq_lens || !k_pages)
     return fail(SPLITKV_EINVAL, "k, block_table, seq_lens and k_pages must not be NULL");
   if (!q != !q_out) return fail(SPLITKV_EINVAL, "q and q_out must both be given or both be NULL");
@@ -203,7 +204,7 @@ splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* 
       k_stride < k_row || k_stride % 8 || k_stride > big || (v && (v_stride < v_row || v_stride % 8 || v_stride > big)))
     return fail(SPLITKV_EINVAL,
                 "token strides must be multiples of 8 elements, hold a token's heads and be below 2^31");
-  if (q && n_tokens > 0 && !(q == q_out && q_stride == q_out_stride) &&
+  if (q && !(q == q_out && q_stride == q_out_stride) &&
       overlap(q, size_t((n_tokens - 1) * q_stride + q_row) * 2, q_out,
               size_t((n_tokens - 1) * q_out_stride + q_row) * 2))
     return fail(SPLITKV_EINVAL, "q_out overlaps q without being q");
@@ -388,6 +389,7 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   const splitkv_desc_t& d = *desc;
   if (!cu_tokens && int64_t(d.batch) * d.q_tokens != n_tokens)
     return fail(SPLITKV_EINVAL, "without cu_tokens, n_tokens (%d) must be batch * q_tokens", n_tokens);
+  if (n_tokens == 0) return SPLITKV_OK;
   if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !out)
     return fail(SPLITKV_EINVAL, "q, k_pages, v_pages, block_table, seq_lens and out must not be NULL");
   const void* wide[] = {q, k_pages, v_pages, out};
@@ -399,10 +401,9 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   const int64_t row = int64_t(d.num_q_heads) * 128;
   if (q_stride < row || q_stride % 8 || q_stride > (int64_t(1) << 31) - 8)
     return fail(SPLITKV_EINVAL, "q_stride must be a multiple of 8 elements, hold a token's heads and be below 2^31");
-  if (n_tokens > 0 && overlap(q, size_t((n_tokens - 1) * q_stride + row) * 2, out, size_t(n_tokens) * row * 2))
+  if (overlap(q, size_t((n_tokens - 1) * q_stride + row) * 2, out, size_t(n_tokens) * row * 2))
     return fail(SPLITKV_EINVAL, "out overlaps q");
   if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPLITKV_EINVAL, "scale must be positive and finite");
-  if (n_tokens == 0) return SPLITKV_OK;
   CrossArgs a{};
   a.parts = cross_parts(d, n_tokens);
   a.part_rows = cross_part_rows(d, n_tokens);

@@ -7,6 +7,8 @@ weigh, evict, cross attention.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (SPLITKV_BF16, SPLITKV_COMBINE_SEPARATE, SPLITKV_FP8_E4M3, SPLITKV_LAYOUT_HND,
@@ -15,7 +17,8 @@ from . import (SPLITKV_BF16, SPLITKV_COMBINE_SEPARATE, SPLITKV_FP8_E4M3, SPLITKV
                splitkv_decode_kv_scales, splitkv_plan, splitkv_plan_fixed,
                splitkv_plan_upload, splitkv_read_stats, splitkv_append,
                splitkv_cross_attend, splitkv_cross_workspace_size, splitkv_evict,
-               splitkv_evict_workspace_size, splitkv_key_weights)
+               splitkv_evict_workspace_size, splitkv_key_weights, SPLITKV_EUNSUPPORTED,
+               SplitKVError)
 
 
 class DecodeSession:
@@ -95,6 +98,14 @@ class DecodeSession:
         return splitkv_read_stats(self.plan, self.workspace, self.stream)
 
 
+def _on(stream):
+    """What is allocated here belongs to ``stream`` (a torch stream, a handle or
+    None for the current one), and its memory is reused in that stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class CacheSession:
     """A paged cache and the calls that fill, read, weigh and prune it.
 
@@ -106,7 +117,9 @@ class CacheSession:
 
     With ``track`` the session keeps the accumulated weight and the position of
     every cached key, which ``weigh`` and ``evict`` need.  A session's calls
-    share its workspaces and outputs: one stream at a time.
+    share its workspaces: one stream (or replayed graph) at a time.  It is made
+    outside of captures; the workspaces that it makes then serve every call and
+    graph of its life.  Results belong to the stream of the call.
     """
 
     def __init__(self, desc, k_pages, v_pages, block_table, seq_lens, *, scale, rope=None, kv_scale=1.0,
@@ -118,18 +131,29 @@ class CacheSession:
         self.scale, self.kv_scale = float(scale), float(kv_scale)
         self.k_scale, self.v_scale = k_scale, v_scale
         self.num_splits = num_splits
-        self.plan = None  # made by the first decode
+        try:
+            self.plan = splitkv_plan_fixed(desc, num_splits)
+            self.workspace = torch.empty(max(self.plan.workspace_size, 256), dtype=torch.uint8, device=dev)
+            splitkv_plan_upload(self.plan, self.workspace, self.workspace.numel())
+        except SplitKVError as e:  # (a cache that the decode does not serve may still be filled, and read by cross_attend)
+            if e.status != SPLITKV_EUNSUPPORTED:
+                raise
+            self.plan = None
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         slots = (desc.batch, desc.num_kv_heads, desc.max_pages_per_seq * desc.page_size)
         self.key_weights = torch.zeros(slots, device=dev) if track else None
         self.key_positions = torch.zeros(slots, dtype=torch.int32, device=dev) if track else None
-        self.evict_workspace = None
+        # (most is needed for a budget of half the slots)
+        size = splitkv_evict_workspace_size(desc, max(1, slots[2] // 2)) if track else 0
+        self.evict_workspace = torch.empty(size, dtype=torch.uint8, device=dev) if track else None
+        torch.cuda.current_stream(dev).synchronize()  # (the calls may come on any stream)
 
     def append(self, positions, q, k, v, cu_tokens=None, q_out=None, stream=None):
         """Rotates the new tokens' queries (returned) and keys and stores their
         keys and values (``splitkv_append``); ``q`` may be None."""
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            with _on(stream):
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         splitkv_append(self.desc, self.rope, positions, q, k, v, self.block_table, self.seq_lens, q_out,
                        self.k_pages, self.v_pages, cu_tokens=cu_tokens, kv_scale=self.kv_scale,
                        k_scale=self.k_scale, v_scale=self.v_scale, key_weights=self.key_weights,
@@ -140,13 +164,12 @@ class CacheSession:
         """Causal decode attention of ``q`` [B][T][Hq][Dk] through a capacity plan."""
         d = self.desc
         if self.plan is None:
-            self.plan = splitkv_plan_fixed(d, self.num_splits)
-            self.workspace = torch.empty(max(self.plan.workspace_size, 256), dtype=torch.uint8, device=q.device)
-            splitkv_plan_upload(self.plan, self.workspace, self.workspace.numel(), stream)
-        if out is None:
-            out = torch.empty((d.batch, d.q_tokens, d.num_q_heads, d.v_dim), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((d.batch, d.q_tokens, d.num_q_heads), dtype=torch.float32, device=q.device)
+            splitkv_plan_fixed(d, self.num_splits)  # (raises, with the reason)
+        with _on(stream):
+            if out is None:
+                out = torch.empty((d.batch, d.q_tokens, d.num_q_heads, d.v_dim), dtype=torch.bfloat16, device=q.device)
+            if lse is None:
+                lse = torch.empty((d.batch, d.q_tokens, d.num_q_heads), dtype=torch.float32, device=q.device)
         args = (self.plan, self.workspace, q, self.k_pages, self.v_pages, self.block_table, self.seq_lens,
                 self.num_splits, self.scale)
         if self.k_scale is not None:
@@ -163,9 +186,6 @@ class CacheSession:
 
     def evict(self, budget, sink=0, recent=0, stream=None):
         """Cuts every sequence to ``budget`` keys per KV head, in place."""
-        size = splitkv_evict_workspace_size(self.desc, budget)
-        if self.evict_workspace is None or self.evict_workspace.numel() < size:
-            self.evict_workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=self.k_pages.device)
         splitkv_evict(self.desc, budget, sink, recent, self.k_pages, self.v_pages, self.block_table,
                       self.seq_lens, self.key_weights, self.key_positions, self.key_weights,
                       self.key_positions, self.seq_lens, self.evict_workspace, status=self.status,
@@ -175,9 +195,10 @@ class CacheSession:
         """Attention of ``q`` [n][Hq][128] over all keys of its sequence, without a causal mask."""
         n = q.shape[0]
         size = splitkv_cross_workspace_size(self.desc, n)
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
-        out = torch.empty((n, self.desc.num_q_heads, 128), dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((n, self.desc.num_q_heads), dtype=torch.float32, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+            out = torch.empty((n, self.desc.num_q_heads, 128), dtype=torch.bfloat16, device=q.device)
+            lse = torch.empty((n, self.desc.num_q_heads), dtype=torch.float32, device=q.device)
         splitkv_cross_attend(self.desc, cu_tokens, q, self.k_pages, self.v_pages, self.block_table, self.seq_lens,
                              self.scale, out, lse, workspace, status=self.status, stream=stream)
         return out, lse

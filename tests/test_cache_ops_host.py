@@ -204,6 +204,15 @@ def test_cross_refuses_other_caches_and_small_workspaces():
         assert lib(ctypes.byref(d), 1, None, A, stride, A, A, A, A, 0.1, 1 << 40, None, A, 1 << 40, None, 0) == EINVAL
 
 
+def test_calls_without_tokens():
+    import torch
+    none = torch.zeros((0, 2, 128), dtype=torch.bfloat16)
+    call_append(desc(), cu_tokens=A, n_tokens=0, k=None, v=None, q=None, q_out=None, positions=None)
+    assert skv._lib.splitkv_cross_attend(ctypes.byref(desc()), 0, A, none.data_ptr(), 1024, A, A, A, A, 0.1, None, None, None, 0,
+                                         None, 0) == skv.SPLITKV_OK
+    refused(EINVAL, call_append, desc(), n_tokens=0)  # without cu_tokens: a token per sequence
+
+
 def test_tensor_arguments_are_checked():
     import torch
     d = desc()

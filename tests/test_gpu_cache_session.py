@@ -177,3 +177,69 @@ def test_encoder_states_and_cross_attention():
             want, size = p @ v64[kt:kt + L, h // 3], p @ np.abs(v64[kt:kt + L, h // 3])
             assert (np.abs(got - want) <= (2.0 ** -8 + 1e-3) * size + EPS16 * np.abs(want)).all()
         at, kt = at + m, kt + L
+
+
+def session_of(seed, lens=(160, 160), **kw):
+    c = Cache(list(lens), device="cuda", seed=seed)
+    return c, CacheSession(c.desc, c.k, c.v, c.table, c.lens, scale=0.1, track=True, num_splits=4, **kw)
+
+
+def test_a_call_on_another_stream_keeps_its_memory():
+    """What a call allocates is not handed out again on the current stream before the call has run."""
+    c, s = session_of(66)
+    q = torch.randn((2, c.heads, 128), device="cuda").to(torch.bfloat16)
+    want = [x.clone() for x in s.cross_attend(q)]
+    size = skv.splitkv_cross_workspace_size(c.desc, 2)
+    assert size > 0
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+    got = s.cross_attend(q, stream=side)
+    others = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(bool((x == 7).all()) for x in others)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_captured_without_a_call_before():
+    """The first calls of a session lie in a graph, and eager calls between its replays use the same workspaces."""
+    results = []
+    for captured in (False, True):
+        c, s = session_of(67)
+        g = torch.Generator(device="cuda").manual_seed(68)
+        q = torch.randn((2, 1, c.heads, 128), generator=g, device="cuda").to(torch.bfloat16)
+        out, lse = torch.zeros_like(q), torch.zeros((2, 1, c.heads), device="cuda")
+
+        def step():
+            s.decode(q, out, lse)
+            s.weigh(q, lse)
+            s.evict(30)
+
+        graph = torch.cuda.CUDAGraph()
+        if captured:
+            with torch.cuda.graph(graph):
+                step()
+        seen = []
+        for n in (160, 90):
+            s.decode(q, out, lse)
+            s.weigh(q, lse)
+            s.evict(100)  # (a larger workspace)
+            c.lens.fill_(n)
+            graph.replay() if captured else step()
+            seen += [x.clone() for x in (out, lse, c.lens, s.key_weights)]
+        torch.cuda.synchronize()
+        assert s.read_status() == 0 and c.lens.tolist() == [30, 30]
+        results.append(seen + [c.k.clone(), c.v.clone()])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_a_call_without_tokens():
+    c, s = session_of(69)
+    none = torch.zeros((0, c.heads, 128), dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros((0, c.Hkv, 128), dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert s.append(torch.zeros((1, 0), dtype=torch.int32, device="cuda"), none, k, k, cu_tokens=cu).shape == none.shape
+    out, lse = s.cross_attend(none, cu_tokens=cu)
+    assert out.shape == none.shape and lse.shape == (0, c.heads)
