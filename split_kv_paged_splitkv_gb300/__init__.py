@@ -13,10 +13,8 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import re
-import types
 
 import numpy as np
 
@@ -313,57 +311,17 @@ def splitkv_debug_gather(desc: splitkv_desc_t, pages, row_elems: int, block_tabl
 
 # ------------------------------------------------------------ cache operators
 
-@functools.lru_cache(maxsize=256)
-def _sizes(desc_bytes: bytes):
-    """Element counts of a call's arrays, by the descriptor's content."""
+_marshal = None
+
+
+def _call():
+    """(the compiled marshalling, torch's current device: the calls' kernels run there)."""
+    global _marshal
     import torch
-    d = splitkv_desc_t.from_buffer_copy(desc_bytes)
-    rows = d.num_pages_total * d.num_kv_heads * d.page_size
-    return types.SimpleNamespace(
-        torch=torch, pool_dtype=torch.uint8 if d.kv_dtype == SPLITKV_FP8_E4M3 else torch.bfloat16,
-        k_pool=rows * d.qk_dim, v_pool=rows * d.v_dim, table=d.batch * d.max_pages_per_seq, batch=d.batch,
-        state=d.batch * d.num_kv_heads * d.max_pages_per_seq * d.page_size, heads=d.num_q_heads,
-        kv_heads=d.num_kv_heads, k_dim=d.qk_dim, v_dim=d.v_dim, k_token=d.num_kv_heads * d.qk_dim,
-        q_rows=d.batch * d.q_tokens * d.num_q_heads)
-
-
-def _addr(name, x, dtype, numel, device):
-    """The address of a tensor argument (addresses and None pass unchecked),
-    after checking its type, that its elements are adjacent, that there are
-    enough of them, and that it is on torch's current device, where the call's
-    kernels run."""
-    if x is None or type(x) is int:
-        return x
-    if not hasattr(x, "data_ptr"):
-        raise TypeError(f"{name} must be a tensor, an address or None, got {type(x)}")
-    if x.dtype is dtype and x.numel() >= numel and x.get_device() == device and x.is_contiguous():
-        return x.data_ptr()
-    if x.dtype is not dtype or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor, got {x.dtype}")
-    if x.numel() < numel:
-        raise ValueError(f"{name} has {x.numel()} elements, the call needs {numel}")
-    raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
-
-
-def _token_rows(name, x, tokens, heads, dim, z, device):
-    """(address, token stride) of a bf16 tensor [tokens][heads][dim] whose tokens may be strided."""
-    if x is None or type(x) is int:
-        return x, heads * dim
-    if x.dim() == 4 and x.is_contiguous():
-        x = x.flatten(0, 1)
-    if x.dtype is not z.torch.bfloat16 or x.shape != (tokens, heads, dim):
-        raise ValueError(f"{name} must be a bfloat16 tensor [{tokens}][{heads}][{dim}], got {x.dtype} {tuple(x.shape)}")
-    stride = x.stride()
-    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
-        raise ValueError(f"the heads of a token of {name} must be adjacent")
-    if x.get_device() != device:
-        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
-    return x.data_ptr(), stride[0] if tokens > 1 else heads * dim
-
-
-def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    if _marshal is None:
+        from . import _binding
+        _marshal = _binding
+    return _marshal, torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
 class Rope:
@@ -399,42 +357,19 @@ def splitkv_append(desc: splitkv_desc_t, rope, positions, q, k, v, block_table, 
     """Rotates queries and keys of new tokens (``rope`` None: rotates nothing)
     and writes the keys and values into the pages.  ``n_tokens`` is needed only
     where ``k`` is an address."""
-    z, dev = _sizes(bytes(desc)), _current_device()
-    i32, f32 = z.torch.int32, z.torch.float32
-    n = n_tokens if n_tokens is not None else k.numel() // z.k_token if k is not None else 0
-    qp, qs = _token_rows("q", q, n, z.heads, z.k_dim, z, dev)
-    op, os_ = _token_rows("q_out", q_out, n, z.heads, z.k_dim, z, dev)
-    kp, ks = _token_rows("k", k, n, z.kv_heads, z.k_dim, z, dev)
-    vp, vs = _token_rows("v", v, n, z.kv_heads, z.v_dim, z, dev)
-    _check(_lib.splitkv_append(
-        ctypes.byref(desc), None if rope is None else rope.handle, n,
-        _addr("cu_tokens", cu_tokens, i32, z.batch + 1, dev),
-        _addr("positions", positions, i32, n * (rope.n_axes if rope is not None else 1), dev),
-        qp, qs, kp, ks, vp, vs, _addr("block_table", block_table, i32, z.table, dev),
-        _addr("seq_lens", seq_lens, i32, z.batch, dev), kv_scale,
-        _addr("k_scale", k_scale, f32, z.kv_heads, dev), _addr("v_scale", v_scale, f32, z.kv_heads, dev),
-        op, os_, _addr("k_pages", k_pages, z.pool_dtype, z.k_pool, dev),
-        _addr("v_pages", v_pages, z.pool_dtype, z.v_pool, dev),
-        _addr("key_weights", key_weights, f32, z.state, dev),
-        _addr("key_positions", key_positions, i32, z.state, dev), _addr("status", status, i32, 1, dev),
-        _stream(stream, dev)))
+    b, dev = _call()
+    _check(b.append(dev, desc, None if rope is None else rope.handle, 1 if rope is None else rope.n_axes, n_tokens,
+                    positions, q, k, v, block_table, seq_lens, q_out, k_pages, v_pages, cu_tokens, kv_scale,
+                    k_scale, v_scale, key_weights, key_positions, status, _stream(stream, dev)))
 
 
 def splitkv_key_weights(desc: splitkv_desc_t, q, k_pages, block_table, seq_lens, lse, scale: float,
                         kv_scale: float, decay: float, weights_in, weights_out, k_scale=None,
                         status=None, stream=None):
     """Adds the attention every cached key got from ``q`` (``lse`` from the decode call)."""
-    z, dev = _sizes(bytes(desc)), _current_device()
-    i32, f32 = z.torch.int32, z.torch.float32
-    _check(_lib.splitkv_key_weights(
-        ctypes.byref(desc), _addr("q", q, z.torch.bfloat16, z.q_rows * z.k_dim, dev),
-        _addr("k_pages", k_pages, z.pool_dtype, z.k_pool, dev),
-        _addr("block_table", block_table, i32, z.table, dev), _addr("seq_lens", seq_lens, i32, z.batch, dev),
-        _addr("lse", lse, f32, z.q_rows, dev), scale, kv_scale,
-        _addr("k_scale", k_scale, f32, z.kv_heads, dev), decay,
-        _addr("weights_in", weights_in, f32, z.state, dev),
-        _addr("weights_out", weights_out, f32, z.state, dev), _addr("status", status, i32, 1, dev),
-        _stream(stream, dev)))
+    b, dev = _call()
+    _check(b.key_weights(dev, desc, q, k_pages, block_table, seq_lens, lse, scale, kv_scale, decay, weights_in,
+                         weights_out, k_scale, status, _stream(stream, dev)))
 
 
 def splitkv_evict_workspace_size(desc: splitkv_desc_t, budget: int) -> int:
@@ -445,21 +380,10 @@ def splitkv_evict(desc: splitkv_desc_t, budget: int, sink: int, recent: int, k_p
                   block_table, seq_lens, weights_in, positions_in, weights_out, positions_out,
                   seq_lens_out, workspace, workspace_bytes=None, status=None, stream=None):
     """Cuts every sequence to at most ``budget`` keys per KV head, the best by weight."""
-    z, dev = _sizes(bytes(desc)), _current_device()
-    i32, f32 = z.torch.int32, z.torch.float32
-    if workspace_bytes is None:
-        workspace_bytes = 0 if workspace is None else workspace.numel()
-    _check(_lib.splitkv_evict(
-        ctypes.byref(desc), budget, sink, recent, _addr("k_pages", k_pages, z.pool_dtype, z.k_pool, dev),
-        _addr("v_pages", v_pages, z.pool_dtype, z.v_pool, dev),
-        _addr("block_table", block_table, i32, z.table, dev), _addr("seq_lens", seq_lens, i32, z.batch, dev),
-        _addr("weights_in", weights_in, f32, z.state, dev),
-        _addr("positions_in", positions_in, i32, z.state, dev),
-        _addr("weights_out", weights_out, f32, z.state, dev),
-        _addr("positions_out", positions_out, i32, z.state, dev),
-        _addr("seq_lens_out", seq_lens_out, i32, z.batch, dev),
-        _addr("workspace", workspace, z.torch.uint8, 0, dev), workspace_bytes,
-        _addr("status", status, i32, 1, dev), _stream(stream, dev)))
+    b, dev = _call()
+    _check(b.evict(dev, desc, budget, sink, recent, k_pages, v_pages, block_table, seq_lens, weights_in,
+                   positions_in, weights_out, positions_out, seq_lens_out, workspace, workspace_bytes, status,
+                   _stream(stream, dev)))
 
 
 def splitkv_cross_workspace_size(desc: splitkv_desc_t, n_tokens: int) -> int:
@@ -471,21 +395,9 @@ def splitkv_cross_attend(desc: splitkv_desc_t, cu_tokens, q, k_pages, v_pages, b
                          n_tokens=None, stream=None):
     """Attention of ragged query tokens over all keys of each sequence's cache.
     ``n_tokens`` is needed only where ``q`` is an address."""
-    z, dev = _sizes(bytes(desc)), _current_device()
-    i32 = z.torch.int32
-    n = n_tokens if n_tokens is not None else q.numel() // (z.heads * z.k_dim) if q is not None else 0
-    qp, qs = _token_rows("q", q, n, z.heads, z.k_dim, z, dev)
-    if workspace_bytes is None:
-        workspace_bytes = 0 if workspace is None else workspace.numel()
-    _check(_lib.splitkv_cross_attend(
-        ctypes.byref(desc), n, _addr("cu_tokens", cu_tokens, i32, z.batch + 1, dev), qp, qs,
-        _addr("k_pages", k_pages, z.pool_dtype, z.k_pool, dev),
-        _addr("v_pages", v_pages, z.pool_dtype, z.v_pool, dev),
-        _addr("block_table", block_table, i32, z.table, dev), _addr("seq_lens", seq_lens, i32, z.batch, dev),
-        scale, _addr("out", out, z.torch.bfloat16, n * z.heads * z.v_dim, dev),
-        _addr("lse", lse, z.torch.float32, n * z.heads, dev),
-        _addr("workspace", workspace, z.torch.uint8, 0, dev), workspace_bytes,
-        _addr("status", status, i32, 1, dev), _stream(stream, dev)))
+    b, dev = _call()
+    _check(b.cross_attend(dev, desc, n_tokens, cu_tokens, q, k_pages, v_pages, block_table, seq_lens, scale, out,
+                          lse, workspace, workspace_bytes, status, _stream(stream, dev)))
 
 
 def splitkv_last_error() -> str:

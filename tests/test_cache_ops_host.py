@@ -262,3 +262,34 @@ def test_plain_weights_sum_to_the_rows():
     q, k = rng.standard_normal((3, 4, 128)), rng.standard_normal((20, 2, 128))
     w = key_weights(q, k, lse_of(q, k, 0.1, 3), 0.1, 3)
     assert np.allclose(w.sum(1), 3 * 2)
+
+
+# ------------------------------------------------------------------ the compiled marshalling
+
+def test_wrong_kinds_of_arguments_raise():
+    import torch
+    d = desc()
+    with pytest.raises(TypeError):
+        call_evict(b"not a descriptor")
+    with pytest.raises(OverflowError):
+        call_evict(d, budget=1 << 40)
+    with pytest.raises(TypeError):
+        call_evict(d, budget="a")
+    for bad in ("q", np.zeros(8), object()):
+        with pytest.raises(TypeError):
+            call_cross(d, q=bad)
+    with pytest.raises(TypeError):
+        call_cross(d, scale=None)
+    with pytest.raises(TypeError):
+        call_cross(d, n_tokens=None)  # q is an address
+    with pytest.raises(ValueError):  # enough elements of the right type, but not on the device (nor with memory)
+        call_cross(d, q=torch.zeros((2, 8, 128), dtype=torch.bfloat16, device="meta"))
+    with pytest.raises(ValueError):
+        call_cross(d, q=torch.zeros((2, 8, 128), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        call_evict(d, weights_in=torch.zeros((2, 2, 128)).transpose(0, 1))
+    refused(EINVAL, call_cross, d, q=None, n_tokens=None)
+    # counts that pass 64 bits ask for more elements than any tensor has
+    huge = desc(B=2**31 - 1, Hkv=2**10, Hq=2**10, maxp=2**26, P=16, N=1)
+    with pytest.raises(ValueError):
+        call_evict(huge, weights_in=torch.zeros(16))
