@@ -25,8 +25,9 @@
 // row read and written once.  Many rows: the moves' bytes (32 sequences x 8
 // heads of up to 131k keys cut to 16k: 220 us, of which the moves take 150 at
 // 5.8 TB/s of scattered 256-byte rows; floor 136).  One sequence: the chain of
-// barriers and passes of the selection (64k latent rows: 25 us, floor 2.2;
-// 5.9k keys of 2 heads: 13.8 us, of which two dependent launches take about 4).
+// barriers and passes of the selection: a digit's exchange within the cluster
+// takes 2 us whatever its size (64k latent rows: 24.5 us, floor 2.2; 5.9k keys
+// of 2 heads: 12.3 us, of which two dependent launches take about 4).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -46,9 +47,9 @@ constexpr int kBins = 2048;            // 11-bit digits: bits 31-21, 20-10, and 
 constexpr int kAlike = 2048;           // ranks set aside for the third digit
 constexpr int kMaxCluster = 8;
 // Ranks a CTA keeps in shared memory; a CTA with more slots makes them anew in
-// each pass, from the L2.  32 KB leave room for two CTAs per SM: 64k latent
-// rows 24.4 us (29.5 with none kept); 256 groups of up to 131k keys 223.7 us
-// (225.8 with all of a CTA's kept, at one CTA per SM).
+// each pass, from the L2: 64k latent rows, 8192 a CTA, 24.1 us (29.4 with none
+// kept); 256 groups of up to 131k keys, whose CTAs have more, 219.7 us (218.5
+// with all kept, in 176 KB and at one CTA per SM).
 constexpr int kRankCap = 8192;
 constexpr int kMoveThreads = 128, kMovePerSm = 8;
 constexpr int kFewBatch = 16, kManyBatch = 32;  // moves a CTA takes at a time
@@ -133,26 +134,30 @@ struct SelShared {
   uint32_t total[3][kBins];  // the cluster's, a digit each, in its first CTA
   uint32_t alike[kAlike];    // ranks with the first digit found, for the third
   uint32_t n_alike;          // (more than kAlike: not all are there)
-  int32_t warp_sum[kSelWarps];
+  int32_t warp_max[kSelWarps];
+  int2 warp_sum[2][kSelWarps];  // of warps_prefix, in turn
   int32_t pub[4];    // read by the cluster: largest position, equals, holes, movers
   int32_t found[3];  // digit, keys above it, keys of it
 };
 
-// Exclusive prefix over the CTA's warps of one value per warp; `total`
-// receives the sum.
-__device__ __forceinline__ int warps_prefix(int mine, int warp, int lane, int32_t* sums, int* total) {
-  __syncthreads();  // (sums may still be read from the call before)
+// Exclusive prefixes over the CTA's warps of two values per warp; `total`
+// receives the sums.  Calls use the two rows of `sums` in turn: a row is written
+// again only behind the barrier of the call between, which its readers reach.
+__device__ __forceinline__ int2 warps_prefix(int2 mine, int warp, int lane, int2* sums, int2* total) {
   if (lane == 0) sums[warp] = mine;
   __syncthreads();
-  const int v = lane < kSelWarps ? sums[lane] : 0;
-  int x = v;
+  const int2 v = lane < kSelWarps ? sums[lane] : make_int2(0, 0);
+  int2 x = v;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += y;
+  for (int o = 1; o < kSelWarps; o <<= 1) {
+    const int y0 = __shfl_up_sync(kFull, x.x, o), y1 = __shfl_up_sync(kFull, x.y, o);
+    if (lane >= o) {
+      x.x += y0;
+      x.y += y1;
+    }
   }
-  *total = __shfl_sync(kFull, x, 31);
-  return __shfl_sync(kFull, x - v, warp);
+  *total = make_int2(__shfl_sync(kFull, x.x, kSelWarps - 1), __shfl_sync(kFull, x.y, kSelWarps - 1));
+  return make_int2(__shfl_sync(kFull, x.x - v.x, warp), __shfl_sync(kFull, x.y - v.y, warp));
 }
 
 // Sum over the lanes before this one of popcounts of 4-bit masks, in slot
@@ -193,6 +198,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   float* wo = a.w_out + size_t(group) * cap;
   int32_t* po = a.pos_out ? a.pos_out + size_t(group) * cap : nullptr;
   const bool rank_pos = a.sink > 0 || a.recent > 0;
+  auto of = [&](auto* mine, int c) {  // the same variable of the cluster's CTA c
+    return nc > 1 ? cluster.map_shared_rank(mine, c) : mine;
+  };
 
   // This CTA's slots [lo, hi) and this warp's [wlo, whi): multiples of 4, so
   // that a lane takes four at a time (a row of the state is padded to 16).
@@ -252,21 +260,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     }
     return;
   }
-  if (cr == 0)
-    for (int i = threadIdx.x; i < 3 * kBins / 4; i += kSelThreads)
-      reinterpret_cast<uint4*>(sh.total)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < (cr == 0 ? 4 : 1) * (kBins / 4); i += kSelThreads)  // (hist, then total)
+    reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x == 0) sh.n_alike = 0;
   newest = __reduce_max_sync(kFull, newest);
-  if (lane == 0) sh.warp_sum[warp] = newest;
+  if (lane == 0) sh.warp_max[warp] = newest;
   __syncthreads();
-  if (warp == 0) {
-    newest = __reduce_max_sync(kFull, sh.warp_sum[lane % kSelWarps]);
-    if (lane == 0) sh.pub[0] = newest;
-  }
-  cluster.sync();  // (the cleared totals, too)
+  newest = __reduce_max_sync(kFull, sh.warp_max[lane % kSelWarps]);
+  if (nc > 1) {
+    if (threadIdx.x == 0) sh.pub[0] = newest;
+    cluster.sync();  // (the cleared totals, too)
 #pragma unroll
-  for (int c = 0; c < kMaxCluster; ++c)
-    if (c < nc) newest = max(newest, cluster.map_shared_rank(sh.pub, c)[0]);
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (c < nc) newest = max(newest, of(sh.pub, c)[0]);
+  }
   const int64_t after = int64_t(newest) - a.recent;  // protected: positions beyond it
 
   // The rank of a weight and its position; negative weights and NaN count as 0.
@@ -300,7 +307,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
 
   // ---- radix selection: the n-th largest rank T, `above` keys beyond it
   uint32_t T = 0;  // the digits found so far
-  int above = 0;
+  int above = 0, turn = 0;  // turn: of warps_prefix
 #pragma unroll 1  // (code that runs once waits for its instructions)
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
@@ -308,11 +315,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     const uint32_t mask = d == 0 ? 0u : ~0u << (shift + bits);
     // Thread i has the kPer bins from nbins - kPer * (i + 1) on.
     constexpr int kPer = kBins / kSelThreads;
+    static_assert(kPer == 4, "a vector of bins");
     const int low = nbins - kPer * (int(threadIdx.x) + 1);
-#pragma unroll
-    for (int e = 0; e < kPer; e += 4)
-      if (low >= 0) *reinterpret_cast<uint4*>(sh.hist + low + e) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    uint32_t* hist = sh.hist;
     // Counts four ranks of each lane; with the second digit, those that share
     // the first are put aside, so that the third need not look at all again.
     auto tally = [&](const uint32_t (&r)[4], uint32_t live) {
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
       const bool same = live == 15u && r[0] == r0 && r[1] == r0 && r[2] == r0 && r[3] == r0;
       if (__all_sync(kFull, same)) {
         if (lane == 0 && (r0 & mask) == T) {
-          atomicAdd(sh.hist + ((r0 >> shift) & (nbins - 1)), 128u);
+          atomicAdd(hist + ((r0 >> shift) & (nbins - 1)), 128u);
           if (d == 1) atomicAdd(&sh.n_alike, uint32_t(kAlike + 1));
         }
         return;
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if ((live >> e & 1) && (r[e] & mask) == T) {
-          atomicAdd(sh.hist + ((r[e] >> shift) & (nbins - 1)), 1u);
+          atomicAdd(hist + ((r[e] >> shift) & (nbins - 1)), 1u);
           if (d == 1) {
             const uint32_t at = atomicAdd(&sh.n_alike, 1u);
             if (at < kAlike) sh.alike[at] = r[e];
@@ -363,44 +368,37 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
       }
     } else if (d == 2 && sh.n_alike <= kAlike) {
       for (uint32_t i = threadIdx.x; i < sh.n_alike; i += kSelThreads)
-        if ((sh.alike[i] & mask) == T) atomicAdd(sh.hist + (sh.alike[i] & (nbins - 1)), 1u);
+        if ((sh.alike[i] & mask) == T) atomicAdd(hist + (sh.alike[i] & (nbins - 1)), 1u);
     } else {
       visit([&](int, const uint32_t (&r)[4], uint32_t live) { tally(r, live); });
     }
     __syncthreads();
     // This CTA's counts (of few bins) into the first CTA's sums, which all read.
-    uint32_t* total = cluster.map_shared_rank(sh.total[d], 0);
+    uint4 v = make_uint4(0, 0, 0, 0);
     if (low >= 0) {
-#pragma unroll
-      for (int e = 0; e < kPer; e += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(sh.hist + low + e);
-        if (v.x) atomicAdd(total + low + e, v.x);
-        if (v.y) atomicAdd(total + low + e + 1, v.y);
-        if (v.z) atomicAdd(total + low + e + 2, v.z);
-        if (v.w) atomicAdd(total + low + e + 3, v.w);
-      }
+      v = *reinterpret_cast<const uint4*>(hist + low);
+      if (d < 2) *reinterpret_cast<uint4*>(hist + low) = make_uint4(0, 0, 0, 0);  // (for the next digit)
     }
-    cluster.sync();
-    int c[kPer], sum = 0;  // from the highest bin down
-#pragma unroll
-    for (int e = 0; e < kPer; e += 4) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (low >= 0) v = *reinterpret_cast<const uint4*>(total + low + e);
-      c[kPer - 1 - e] = int(v.x);
-      c[kPer - 2 - e] = int(v.y);
-      c[kPer - 3 - e] = int(v.z);
-      c[kPer - 4 - e] = int(v.w);
+    if (nc > 1) {
+      uint32_t* total = cluster.map_shared_rank(sh.total[d], 0);
+      if (v.x) atomicAdd(total + low, v.x);
+      if (v.y) atomicAdd(total + low + 1, v.y);
+      if (v.z) atomicAdd(total + low + 2, v.z);
+      if (v.w) atomicAdd(total + low + 3, v.w);
+      cluster.sync();
+      if (low >= 0) v = *reinterpret_cast<const uint4*>(total + low);
     }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) sum += c[e];
+    const int c[kPer] = {int(v.w), int(v.z), int(v.y), int(v.x)};  // from the highest bin down
+    const int sum = (c[0] + c[1]) + (c[2] + c[3]);
     int x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kFull, x, o);
       if (lane >= o) x += y;
     }
-    int all;
-    int start = above + x - sum + warps_prefix(__shfl_sync(kFull, x, 31), warp, lane, sh.warp_sum, &all);
+    int2 all;
+    int start = above + x - sum +
+                warps_prefix(make_int2(__shfl_sync(kFull, x, 31), 0), warp, lane, sh.warp_sum[turn++ & 1], &all).x;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {  // `start`: keys above this bin
       if (start < n && start + c[e] >= n) {
@@ -413,6 +411,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     __syncthreads();
     T |= uint32_t(sh.found[0]) << shift;
     above = sh.found[1];
+    // all keys that share the digits so far stay: the other digits do not matter
+    // (5.9k keys of 2 heads: 12.3 us, 13.6 without)
+    if (above + sh.found[2] == n) break;
   }
   const int need = n - above;  // keys of rank T that stay: the lowest slots
   const bool ties = need < sh.found[2];
@@ -420,17 +421,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   // ---- keys of rank T before this warp's slots, if not all of them stay
   int eq_at = 0;
   if (ties) {
-    int eq = 0, eq_cta;
+    int eq = 0;
+    int2 eq_cta;
     visit([&](int, const uint32_t (&r)[4], uint32_t live) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) eq += (live >> e & 1) && r[e] == T;
     });
-    eq_at = warps_prefix(__reduce_add_sync(kFull, eq), warp, lane, sh.warp_sum, &eq_cta);
-    if (threadIdx.x == 0) sh.pub[1] = eq_cta;
-    cluster.sync();
+    eq_at = warps_prefix(make_int2(__reduce_add_sync(kFull, eq), 0), warp, lane, sh.warp_sum[turn++ & 1], &eq_cta).x;
+    if (nc > 1) {
+      if (threadIdx.x == 0) sh.pub[1] = eq_cta.x;
+      cluster.sync();
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c)
-      if (c < cr) eq_at += cluster.map_shared_rank(sh.pub, c)[1];
+      for (int c = 0; c < kMaxCluster; ++c)
+        if (c < cr) eq_at += of(sh.pub, c)[1];
+    }
   }
 
   // ---- what is freed below slot n and what moves from behind it
@@ -460,23 +464,27 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     holes += __popc(hole);
     movers += __popc(mover);
   });
-  int hole_at, mover_at, holes_cta, movers_cta;
-  hole_at = warps_prefix(__reduce_add_sync(kFull, holes), warp, lane, sh.warp_sum, &holes_cta);
-  mover_at = warps_prefix(__reduce_add_sync(kFull, movers), warp, lane, sh.warp_sum, &movers_cta);
-  if (threadIdx.x == 0) {
-    sh.pub[2] = holes_cta;
-    sh.pub[3] = movers_cta;
-  }
-  cluster.sync();
-  int moves = 0;
+  int2 cta;
+  const int2 at = warps_prefix(make_int2(__reduce_add_sync(kFull, holes), __reduce_add_sync(kFull, movers)), warp, lane,
+                               sh.warp_sum[turn & 1], &cta);
+  int hole_at = at.x, mover_at = at.y, moves = cta.y;
+  if (nc > 1) {
+    if (threadIdx.x == 0) {
+      sh.pub[2] = cta.x;
+      sh.pub[3] = cta.y;
+    }
+    cluster.sync();
+    moves = 0;
 #pragma unroll
-  for (int c = 0; c < kMaxCluster; ++c) {
-    if (c >= nc) break;
-    const int32_t* p = cluster.map_shared_rank(sh.pub, c);
-    const int ho = p[2], mo = p[3];
-    hole_at += c < cr ? ho : 0;
-    mover_at += c < cr ? mo : 0;
-    moves += mo;
+    for (int c = 0; c < kMaxCluster; ++c) {
+      if (c >= nc) break;
+      const int32_t* p = of(sh.pub, c);
+      const int ho = p[2], mo = p[3];
+      hole_at += c < cr ? ho : 0;
+      mover_at += c < cr ? mo : 0;
+      moves += mo;
+    }
+    cluster.barrier_arrive();  // (this CTA reads no more of the others')
   }
   int32_t* src = a.moves + size_t(group) * 2 * a.max_moves;
   int32_t* dst = src + a.max_moves;
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     a.meta[2 * group] = moves;
     a.meta[2 * group + 1] = n;
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (nc > 1) cluster.barrier_wait();  // no CTA leaves while another reads its shared memory
 }
 
 // The moves of all groups, in batches of BATCH moves of one group; the
@@ -592,9 +600,10 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   if (e != cudaSuccess) return e;
   // CTAs per (sequence, head): one for each 2048 slots of capacity while the
   // groups do not fill the GPU, and one for each 32,768 slots in any case.
-  // 5.9k slots of 2 heads: 14.4 us with four, 16.0 with eight, 15.8 with one;
-  // 64k slots of one: 24.4 with eight, 39 with four, 58 with two, and 26.4 with
-  // sixteen; 256 groups of 131k: 224 with four, 238 with eight, 261 with two.
+  // 5.9k slots of 2 heads: 12.2 us with four, 14.1 with eight, 12.2 with one;
+  // 64k slots of one: 24.1 with eight, 39 with four, 58 with two, and 2 more
+  // with sixteen than with eight; 256 groups of 131k: 219.7 with four, 229 with
+  // eight, 255 with two.
   int nc = 1;
   while (nc < kMaxCluster && ((cap > int64_t(nc) * 2048 && int64_t(groups) * nc * 2 <= int64_t(sms) * 4) ||
                               cap > int64_t(nc) * 32768))
@@ -627,9 +636,10 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   mv.numAttrs = 1;
   mv.blockDim = dim3(kMoveThreads, 1, 1);
   // Eight small CTAs per SM, so that some load while others wait at a barrier
-  // (840k pairs of 256-byte rows: 219.8 us; four of 256 threads 223.7).  Few
+  // (840k pairs of 256-byte rows: 219.4 us; four of 256 threads 223.7).  Few
   // moves go in small batches, so that more SMs take part (2.7k of those pairs:
-  // 13.8 us in batches of 16, 15.0 of 32), many in large ones, for bytes in flight.
+  // 12.2 us in batches of 16, 13.3 of 32; 12k rows of 576 bytes: 24.1 and 25.6),
+  // many in large ones, for bytes in flight.
   const bool few = int64_t(groups) * a.max_moves <= int64_t(sms) * 256;
   const int batch = few ? kFewBatch : kManyBatch;
   const int64_t most = int64_t(groups) * ((a.max_moves + batch - 1) / batch);
