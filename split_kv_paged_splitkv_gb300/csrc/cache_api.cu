@@ -64,6 +64,10 @@ splitkv_status check_scales(bool fp8, float kv_scale, const float* k_scale, cons
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// The records of cross attention's cut items (each has two of 2 * parts pieces at
+// least), and their number.
+size_t split_bytes(size_t parts) { return align256(parts * sizeof(CrossSplit) + sizeof(int32_t)); }
+
 // Moves of one (sequence, head), at most: the kept keys behind the budget.
 int64_t max_moves(const splitkv_desc_t& d, int32_t budget) {
   const int64_t cap = int64_t(d.max_pages_per_seq) * d.page_size;
@@ -375,7 +379,7 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
 size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
   if (validate_cross(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
   const size_t parts = size_t(cross_parts(*desc, n_tokens));
-  return align256(2 * parts * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float)) + align256(2 * parts * sizeof(CrossSplit));
+  return align256(2 * parts * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float)) + split_bytes(parts);
 }
 
 splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens,
@@ -416,7 +420,8 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
     a.o_part = static_cast<float*>(workspace);
     a.lse_part = a.o_part + size_t(2) * a.parts * a.part_rows * 128;
     a.split = reinterpret_cast<CrossSplit*>(static_cast<unsigned char*>(workspace) + need -
-                                            align256(size_t(2) * a.parts * sizeof(CrossSplit)));
+                                            split_bytes(a.parts));
+    a.n_split = reinterpret_cast<int32_t*>(a.split + a.parts);
   }
   a.q = q;
   a.cu = cu_tokens;

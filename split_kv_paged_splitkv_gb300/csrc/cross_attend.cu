@@ -128,12 +128,6 @@ struct Tail {
 };
 static_assert(B_COUNT * 8 + sizeof(Tail) <= 512, "barriers, then the tail");
 
-// Row tiles of sequence b.
-__device__ __forceinline__ int tiles_of(const CrossArgs& a, int b) {
-  int first;
-  return (tokens_of(a, b, &first) * a.G + Cross::ROWS - 1) / Cross::ROWS;
-}
-
 // Pieces of about t key blocks that an item of nb is cut into.  (In floating
 // point, for speed: any count in 1 .. nb is right, as long as all agree on it.)
 __device__ __forceinline__ int cuts_of(int nb, float t) {
@@ -153,11 +147,14 @@ __device__ __forceinline__ int cuts_of(int nb, float t) {
 // chooses for 16 heads: two key blocks stay whole, 12.5 us with one token and
 // 12.7 cut; four are cut, 13.1 and 14.8 whole, and with 256 tokens 17.3 and 20.2.)
 __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& tail) {
-  int tiles = 0, nb = 1;
+  int first = 0, rows = 0, L = 0, tiles = 0, nb = 1;
   auto read = [&](int b0) {  // lane: sequence b0 + lane
     const int b = b0 + lane;
-    tiles = b < a.batch ? tiles_of(a, b) : 0;
-    nb = b < a.batch ? blocks_of(keys_of(a, b)) : 1;
+    const bool in = b < a.batch;
+    L = in ? keys_of(a, b) : 0;
+    rows = in ? tokens_of(a, b, &first) * a.G : 0;
+    tiles = (rows + Cross::ROWS - 1) / Cross::ROWS;
+    nb = blocks_of(L);
   };
   auto before = [&](int n, int* total) {  // sum over the lanes before this one
     int x = n;
@@ -197,7 +194,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
   int k = 0;
   for (int p = blockIdx.x; a.parts == 0 ? k == 0 : p < P && k < kMaxPieces; p += a.parts, ++k) {
     Piece q;
-    int cuts = 0, passed = 0, total;
+    int passed = 0, cut_items = 0, total;  // pieces and cut items of the sequences before
     bool found = false;
     for (int b0 = 0; b0 < a.batch && !found; b0 += 32) {
       if (a.batch > 32 || a.parts == 0) read(b0);
@@ -206,34 +203,47 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
       const int at = passed + before(n, &total);
       const unsigned m = __ballot_sync(kFull, p >= at && p < at + n);
       passed += total;
+      const int mine = s > 1 ? tiles * a.Hkv : 0;
       if (m) {
         const int f = __ffs(m) - 1;
         found = true;
-        q.b = b0 + f;
-        cuts = __shfl_sync(kFull, s, f);
-        const int in = p - __shfl_sync(kFull, at, f), item = in / cuts, cut = in - item * cuts;
+        const int cuts = __shfl_sync(kFull, s, f);
+        const int in = p - __shfl_sync(kFull, at, f);
+        const int item = cuts > 1 ? in / cuts : in, cut = in - item * cuts;
         const int ts = __shfl_sync(kFull, tiles, f), blocks = __shfl_sync(kFull, nb, f);
-        const int tile = a.parts > 0 ? item % ts : item;
-        q.h = a.parts > 0 ? item / ts : int(blockIdx.y);
-        q.n_rows = tokens_of(a, q.b, &q.first) * a.G - tile * Cross::ROWS;
+        const int h = a.parts == 0 ? int(blockIdx.y) : ts > 1 ? item / ts : item;
+        const int tile = a.parts > 0 ? item - h * ts : item;
+        q.b = b0 + f;
+        q.h = h;
+        q.first = __shfl_sync(kFull, first, f);
         q.row0 = tile * Cross::ROWS;
-        q.L = keys_of(a, q.b);
-        q.j0 = blocks * cut / cuts;
-        q.nblk = q.L > 0 ? blocks * (cut + 1) / cuts - q.j0 : 0;
+        q.n_rows = __shfl_sync(kFull, rows, f) - q.row0;
+        q.L = __shfl_sync(kFull, L, f);
+        const int base = cuts > 1 ? blocks / cuts : blocks, over = blocks - base * cuts;  // `over` pieces have one more
+        q.j0 = cut * base + min(cut, over);
+        q.nblk = q.L > 0 ? base + (cut < over) : 0;
         q.slot = cuts > 1 ? p : -1;
-        // the merge's record, with the first piece of a cut item
-        if (lane == 0 && k < 2 && a.parts > 0) {
-          const CrossSplit r = {cuts > 1 && cut == 0 ? cuts : 0, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
-          a.split[p] = r;
+        if (cuts > 1 && cut == 0) {  // the merge's record, with the first piece of a cut item
+          cut_items += __reduce_add_sync(kFull, lane < f ? mine : 0);
+          const CrossSplit r = {cuts, p, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
+          if (lane == 0) a.split[cut_items + item] = r;
         }
+      } else {
+        cut_items += __reduce_add_sync(kFull, mine);
       }
     }
     if (!found) break;
     if (lane == 0) tail.piece[k] = q;
   }
-  if (lane == 0) {
-    tail.pieces = k;
-    for (int i = k; i < 2 && a.parts > 0; ++i) a.split[blockIdx.x + i * a.parts].cuts = 0;
+  if (lane == 0) tail.pieces = k;
+  // the number of those records
+  if (a.parts > 0 && blockIdx.x == 0) {
+    int cut_items = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      if (a.batch > 32) read(b0);
+      cut_items += __reduce_add_sync(kFull, cuts_of(nb, T) > 1 ? tiles * a.Hkv : 0);
+    }
+    if (lane == 0) *a.n_split = cut_items;
   }
 }
 
@@ -413,7 +423,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
-      mbar_init(bar(B_FULL + s), 1);
+      mbar_init(bar(B_FULL + s), 2);  // (a half by each producer)
       mbar_init(bar(B_EMPTY + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -438,10 +448,9 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   wait_prerequisites();
   if (warp == C::ISSUER) {
     plan_pieces(a, lane, tail);
-    // one CTA reports lengths that the cache cannot hold
-    if (a.status && blockIdx.x == 0 && blockIdx.y == 0)
-      for (int i = lane; i < a.batch; i += 32)
-        if (a.seq_lens[i] != keys_of(a, i)) atomicOr(a.status, SPLITKV_DEVERR_SEQLEN);
+  } else if (a.parts > 0) {  // (meanwhile: where the pages' ids begin)
+    for (int b = threadIdx.x; b < a.batch; b += C::SOFTMAX_WARPS * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.block_table + size_t(b) * a.max_pages));
   }
   tc_fence_before();
   __syncthreads();
@@ -452,19 +461,19 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   if (warp == C::PRODUCER || warp == C::PRODUCER + 1) {
     // ------------------------------------------------------------- producers
     // Of all pieces, key block j's K is ring item 2 j, its V item 2 j + 1; item
-    // i lies in slot i % NST.  One warp copies the K, one the V (a warp issues
-    // a box in some 100 cycles: one alone would bring 64 KB in 3,200).  A block
-    // is BK / br groups of br keys of one page each; lane g holds the page of
-    // group g.  Groups behind the last key are not read.
-    const int v = warp - C::PRODUCER;
-    const CUtensorMap* tm = v ? &tv : &tk;
+    // i lies in slot i % NST.  Each of the two warps copies a 64-column half of
+    // every item (a warp issues a box in some 100 cycles: one alone would take
+    // 1,600 for a block in pages of 16 keys).  A block is BK / br groups of br
+    // keys of one page each; lane g holds the page of group g.  Groups behind the
+    // last key are not read.
+    const int half = warp - C::PRODUCER;
     const int br = a.box_rows;
     bool ok = true;
-    int item = v;
+    int item = 0;
     for (int k = 0; k < pieces && ok; ++k) {
       const Piece pc = tail.piece[k];
       const int32_t* trow = a.block_table + size_t(pc.b) * a.max_pages;
-      for (int j = 0; j < pc.nblk; ++j, item += 2) {
+      for (int j = 0; j < pc.nblk && ok; ++j) {
         const int key0 = (pc.j0 + j) * C::BK;
         const int np = (min(C::BK, pc.L - key0) + br - 1) / br;
         int ph = 0, in = 0;
@@ -477,31 +486,33 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
             ph = 0;
           }
         }
-        const int st = item % C::NST;
-        if (item >= C::NST) ok = __all_sync(kFull, mbar_wait(bar(B_EMPTY + st), (item / C::NST - 1) & 1));
-        if (!ok) break;
-        mbar_arrive_expect_tx_warp(bar(B_FULL + st), uint32_t(np * br * 256));
-        const uint32_t dst = smem_u32(sm + C::OFF_RING + st * C::TILE);
-        for (int g = 0; g < np; ++g) {
-          const int pg = __shfl_sync(kFull, ph, g), kp = __shfl_sync(kFull, in, g);
-          tma_load_5d_warp(dst + g * br * 128, tm, bar(B_FULL + st), 0, kp, 0, pc.h, pg);
-          tma_load_5d_warp(dst + C::HALF + g * br * 128, tm, bar(B_FULL + st), 0, kp, 1, pc.h, pg);
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v, ++item) {
+          const int st = item % C::NST;
+          if (item >= C::NST) ok = __all_sync(kFull, mbar_wait(bar(B_EMPTY + st), (item / C::NST - 1) & 1));
+          if (!ok) break;
+          mbar_arrive_expect_tx_warp(bar(B_FULL + st), uint32_t(np * br * 128));
+          const uint32_t dst = smem_u32(sm + C::OFF_RING + st * C::TILE) + half * C::HALF;
+          const CUtensorMap* tm = v ? &tv : &tk;
+          for (int g = 0; g < np; ++g) {
+            const int pg = __shfl_sync(kFull, ph, g), kp = __shfl_sync(kFull, in, g);
+            tma_load_5d_warp(dst + g * br * 128, tm, bar(B_FULL + st), 0, kp, half, pc.h, pg);
+          }
         }
       }
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
-    // Stay until every copy has landed: the last item of each slot, or after a
-    // wait that ran out this warp's own last ones.
-    if (lane == 0) {
-      int items = 0;
-      for (int k = 0; k < pieces; ++k) items += 2 * tail.piece[k].nblk;
-      const int end = ok ? items : item;  // (item: the one that was not issued)
-      for (int i = ok ? end - 1 : end - 2; i >= 0 && i >= end - C::NST; i -= ok ? 1 : 2)
-        if (!mbar_wait(bar(B_FULL + i % C::NST), (i / C::NST) & 1)) break;
-    }
+    // Stay until every copy has landed: the last item of each slot.
+    if (lane == 0)
+      for (int i = item - 1; i >= 0 && i >= item - C::NST; --i)  // (item: the first that was not issued)
+        mbar_wait(bar(B_FULL + i % C::NST), (i / C::NST) & 1);
   } else if (warp == C::ISSUER) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, 0, 0), idesc_pv = umma_idesc_bf16(128, 128, 0, 1);
+    // one CTA reports lengths that the cache cannot hold
+    if (a.status && blockIdx.x == 0 && blockIdx.y == 0)
+      for (int i = lane; i < a.batch; i += 32)
+        if (a.seq_lens[i] != keys_of(a, i)) atomicOr(a.status, SPLITKV_DEVERR_SEQLEN);
     bool ok = true;
     int item = 0;                      // ring items consumed
     uint32_t n_q = 0, n_p = 0;  // phases of B_Q and B_P so far, a bit per row block
@@ -871,35 +882,15 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
 // lie side by side for the rows; the log-sum-exps and results of four pieces
 // are loaded at once, and the sums rescaled when later ones are larger.
 constexpr int kMergeWarps = 8, kMergeAtOnce = 4, kMergeGroups = 32 / kMergeWarps;
-constexpr int kMergeWords = (2 * kSmCount + 31) / 32;  // of a bit per piece
 __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __grid_constant__ CrossArgs a, int units) {
   __shared__ uint2 rows_out[32][33];  // bf16 rows (of 32 pieces of 8 bytes, and one to spread the banks)
   launch_dependents();
   wait_prerequisites();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned firsts[kMergeWords];  // the pieces that are the first of a cut item
-  {
-    int cuts[kMergeWords];
-#pragma unroll
-    for (int i = 0; i < kMergeWords; ++i) cuts[i] = i * 32 + lane < 2 * a.parts ? a.split[i * 32 + lane].cuts : 0;
-#pragma unroll
-    for (int i = 0; i < kMergeWords; ++i) firsts[i] = __ballot_sync(kFull, cuts[i] > 0);
-  }
-  for (int u = blockIdx.x;; u += gridDim.x) {
-    int q = u / units, c = -1;  // the q-th cut item, its first piece
-    const int r0 = (u - q * units) * 32;
-#pragma unroll
-    for (int i = 0; i < kMergeWords; ++i) {
-      const int n = __popc(firsts[i]);
-      if (c < 0 && q < n) {
-        unsigned m = firsts[i];
-        for (; q > 0; --q) m &= m - 1;
-        c = i * 32 + __ffs(m) - 1;
-      }
-      q -= n;
-    }
-    if (c < 0) break;
-    const CrossSplit sp = a.split[c];
+  const int last = *a.n_split * units;
+  for (int u = blockIdx.x; u < last; u += gridDim.x) {
+    const int q = u / units, r0 = (u - q * units) * 32;  // the q-th cut item, its rows from r0 on
+    const CrossSplit sp = a.split[q];
     if (r0 >= sp.rows) continue;
     const int row = r0 + lane;
     const bool live = row < sp.rows;
@@ -913,7 +904,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __g
       float4 v[kMergeAtOnce][kMergeGroups];
 #pragma unroll
       for (int k = 0; k < kMergeAtOnce; ++k) {
-        const size_t slot = c + k0 + k;
+        const size_t slot = sp.slot + k0 + k;
         const bool in = live && k0 + k < sp.cuts;
         ls[k] = in ? a.lse_part[slot * a.part_rows + row] : -INFINITY;
 #pragma unroll

@@ -224,10 +224,10 @@ struct EvictArgs {
 
 constexpr int kSmCount = 152;  // SMs that cross attention plans for
 
-// A piece of cross attention's items, for the merge: the number of pieces that
-// its item is cut into if it is the first of them, else 0.
+// A cut item of cross attention, for the merge: its number of pieces, the slot of
+// the first, its sequence's first token, head, first row and rows.
 struct CrossSplit {
-  int32_t cuts, first, head, row0, rows;  // first: token of the sequence
+  int32_t cuts, slot, first, head, row0, rows;
 };
 
 struct CrossArgs {
@@ -240,7 +240,8 @@ struct CrossArgs {
   float* o_part;      // [2 parts][32][part_rows][4]: partial results, in groups of four
                       //   dims
   float* lse_part;    // [2 parts][part_rows]
-  CrossSplit* split;  // [2 parts]
+  CrossSplit* split;  // [parts]
+  int32_t* n_split;   // how many of them there are
   int32_t* status;    // or null
   int64_t q_stride;   // elements per token
   float qk_scale_log2;
