@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
         const size_t slot = pc.slot;
         const int tok = (pc.row0 + row) / a.G, g = (pc.row0 + row) - tok * a.G;
         const size_t out_row = (size_t(pc.first) + tok) * a.Hq + size_t(pc.h) * a.G + g;
-#pragma unroll 1
+#pragma unroll 2
         for (int c0 = 0; c0 < 128; c0 += 32) {
           float o[32];
           if (pc.nblk > 0) {
