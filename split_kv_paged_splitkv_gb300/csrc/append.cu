@@ -19,7 +19,7 @@
 // Bound: the bytes of q (read and written), k and v (read, and written in the
 // cache's type); a decode step of a few tokens is bound by one chain of
 // loads, so nothing but the token's own loads precedes its stores.  Measured:
-// 26k prompt tokens of 40 rows of 128: 99 us, 5.4 TB/s (floor 79 at the copy's
+// 26k prompt tokens of 40 rows of 128: 98 us, 5.5 TB/s (floor 79 at the copy's
 // 6.8: rows of 256 bytes go to as many places); one token 3.2 us, 32 in e4m3
 // 3.7, of which a launch is most.
 //
@@ -288,7 +288,7 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
   // below 2^32 or the CTA has one token (0: that token's, however many units)
   a.per_tok_magic = per_tok > 65536 ? 0 : unsigned(((uint64_t(1) << 32) + per_tok - 1) / per_tok);
   // A CTA's units.  In a long call two passes share the lookup of the places
-  // and the sines (26k tokens of 40 rows: 99 us, with one pass 106).
+  // and the sines (26k tokens of 40 rows: 99 us, with one pass 106, both with four units).
   constexpr int units = (U == 1 ? 1 : 2) * U * kThreads;
   const int tpc = per_tok >= units ? 1 : min(kMaxTok, units / per_tok);
   const int64_t slices = (int64_t(per_tok) * tpc + units - 1) / units;
@@ -305,15 +305,15 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
 }
 
 // A call of few tokens takes one unit per thread, to use more of the GPU's
-// SMs (32 tokens: 3.7 us, with four 8.8); a long one four, for bytes in flight
-// (26k tokens: 99 us, with one 239).
+// SMs (32 tokens: 3.7 us, with four 8.8); a long one two, for bytes in flight
+// (26k tokens: 97.8 us, with one 239, with four 99.2, with six 126).
 constexpr int64_t kFewUnits = 1 << 17;
 
 template <int DK, int DV, bool FP8>
 cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t s) {
   const int per_tok = (a.q ? a.Hq * (DK / 16) : 0) + a.Hkv * (DK / 16 + (a.v ? DV / 16 : 0));
   return int64_t(per_tok) * a.n_tokens <= kFewUnits ? launch_append_u<DK, DV, FP8, 1>(a, per_tok, s)
-                                                    : launch_append_u<DK, DV, FP8, 4>(a, per_tok, s);
+                                                    : launch_append_u<DK, DV, FP8, 2>(a, per_tok, s);
 }
 
 }  // namespace

@@ -119,6 +119,7 @@ struct Piece {
   int slot;                                    // of its partial result; -1: the whole item
 };
 constexpr int kMaxPieces = 4;  // of a CTA
+constexpr int kPieceCost = 2, kCutCost = 2;  // in key blocks: of each piece, and of cutting anything
 
 // Behind the barriers.
 struct Tail {
@@ -143,7 +144,7 @@ __device__ __forceinline__ int cuts_of(int nb, float t) {
 // Few items: every item of nb key blocks is cut into ceil(nb / t) equal pieces,
 // and CTA c takes pieces c, c + parts, ... of the line of all items' pieces.
 // Lane i weighs t = ceil(longest nb / (i + 1)): the blocks of the CTA with most,
-// two more for each of its pieces, and two if anything is cut.  (What that
+// kPieceCost for each of its pieces, and kCutCost if anything is cut.  (What that
 // chooses for 16 heads: two key blocks stay whole, 12.5 us with one token and
 // 12.7 cut; four are cut, 13.1 and 14.8 whole, and with 256 tokens 17.3 and 20.2.)
 __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& tail) {
@@ -186,7 +187,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
     n *= a.Hkv;
     // (cut pieces have a slot each; uncut items need none)
     const bool fits = lane == 0 || n <= 2 * a.parts;
-    const uint32_t cost = (n + a.parts - 1) / a.parts * (uint32_t(t) + 2) + (n > items ? 2 : 0);
+    const uint32_t cost = (n + a.parts - 1) / a.parts * (uint32_t(t) + kPieceCost) + (n > items ? kCutCost : 0);
     const int best = __reduce_min_sync(kFull, fits ? cost * 32 + lane : ~0u) & 31;
     T = __shfl_sync(kFull, t, best);
     P = __shfl_sync(kFull, n, best);
@@ -1004,6 +1005,11 @@ cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& t
   e = cudaLaunchKernelEx(&cfg, cross_attend_kernel, a, *reinterpret_cast<const CUtensorMap*>(&tk),
                                      *reinterpret_cast<const CUtensorMap*>(&tv));
   if (e != cudaSuccess || a.parts == 0) return e;
+  // With an item per CTA at most, a cut costs 1 + kPieceCost + kCutCost at least:
+  // items of so few key blocks that none costs more are never cut (a token over
+  // 256 keys of 16 heads: 9.4 us, with the merge's launch 10.9).
+  const int64_t blocks = (int64_t(a.max_pages) * a.P + Cross::BK - 1) / Cross::BK;
+  if (row_tiles * a.Hkv <= a.parts && blocks <= 1 + kCutCost) return e;
   const int units = (a.part_rows + 31) / 32;  // of an item
   cfg.gridDim = dim3(unsigned(units > 1 ? 2 * a.parts : a.parts), 1, 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
