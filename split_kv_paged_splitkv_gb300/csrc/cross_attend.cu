@@ -120,6 +120,7 @@ struct Piece {
 };
 constexpr int kMaxPieces = 4;  // of a CTA
 constexpr int kPieceCost = 2, kCutCost = 2;  // in key blocks: of each piece, and of cutting anything
+constexpr int kLineCost = 8;  // and of an even line of all key blocks
 
 // Behind the barriers.
 struct Tail {
@@ -135,6 +136,86 @@ __device__ __forceinline__ int cuts_of(int nb, float t) {
   return max(1, min(nb, int(ceilf(__fdividef(float(nb), t) - 1e-3f))));
 }
 
+// Lane's sequence of a plan: its first token, query rows, keys, row tiles, and
+// the key blocks of each of its items.
+struct Lane {
+  int first, rows, L, tiles, nb;
+};
+__device__ __forceinline__ Lane lane_of(const CrossArgs& a, int b) {
+  Lane x = {0, 0, 0, 0, 1};
+  if (b < a.batch) {
+    x.L = keys_of(a, b);
+    x.rows = tokens_of(a, b, &x.first) * a.G;
+    x.tiles = (x.rows + Cross::ROWS - 1) / Cross::ROWS;
+    x.nb = blocks_of(x.L);
+  }
+  return x;
+}
+
+// Sum over the lanes before this one.
+__device__ __forceinline__ int lanes_before(int n, int lane, int* total) {
+  int x = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  *total = __shfl_sync(kFull, x, 31);
+  return x - n;
+}
+
+// The even line of plan_pieces: all items' key blocks, `line` in number (parts to
+// 2^23), one after the other, of which CTA c takes those from lo(c) on.  No item
+// is shorter than half a CTA's share, so it has three pieces at most.  (One token
+// of 10 requests, 160 items over 152 CTAs, 1.5k keys: 39.6 us, in whole items
+// 49.7; 4k keys: 75.8 and 110.9.  kLineCost is what leaves 8 requests, 27.6 us
+// and as a line 30.2, and 16, 51.8 and 55.3, as they are.)
+__device__ __noinline__ void plan_line(const CrossArgs& a, int lane, int line, Tail& tail) {
+  auto lo = [&](int c) { return int(unsigned(line) * unsigned(c) / unsigned(a.parts)); };
+  auto cta_of = [&](int y) { return int((unsigned(y + 1) * unsigned(a.parts) - 1) / unsigned(line)); };
+  const int c = blockIdx.x, hi = lo(c + 1);
+  CrossSplit r = {0, 0, 2, 0, 0, 0, 0};
+  int k = 0;
+  for (int x = lo(c); x < hi && k < kMaxPieces; ++k) {
+    Piece q;
+    int passed = 0, total;
+    bool found = false;
+    for (int b0 = 0; b0 < a.batch && !found; b0 += 32) {
+      const Lane s = lane_of(a, b0 + lane);
+      const int n = s.tiles * a.Hkv * s.nb;
+      const int at = passed + lanes_before(n, lane, &total);
+      const unsigned m = __ballot_sync(kFull, x >= at && x < at + n);
+      passed += total;
+      if (m) {
+        const int f = __ffs(m) - 1;
+        found = true;
+        const int blocks = __shfl_sync(kFull, s.nb, f), ts = __shfl_sync(kFull, s.tiles, f);
+        const int in = x - __shfl_sync(kFull, at, f), item = in / blocks;
+        q.b = b0 + f;
+        q.h = ts > 1 ? item / ts : item;
+        q.row0 = (item - q.h * ts) * Cross::ROWS;
+        q.first = __shfl_sync(kFull, s.first, f);
+        q.n_rows = __shfl_sync(kFull, s.rows, f) - q.row0;
+        q.L = __shfl_sync(kFull, s.L, f);
+        q.j0 = in - item * blocks;
+        const int len = min(blocks - q.j0, hi - x);
+        q.nblk = q.L > 0 ? len : 0;
+        q.slot = len < blocks ? 2 * c + (k > 0) : -1;  // (only a CTA's first and last piece can be cut)
+        if (len < blocks && q.j0 == 0)                 // (the last)
+          r = {cta_of(x + blocks - 1) - c + 1, q.slot, 2, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
+        x += len;
+      }
+    }
+    if (!found) break;
+    if (lane == 0) tail.piece[k] = q;
+  }
+  if (lane == 0) {
+    tail.pieces = k;
+    a.split[c] = r;
+    if (c == 0) *a.n_split = a.parts;
+  }
+}
+
 // By a warp: which pieces this CTA computes.
 //
 // A CTA per item (a.parts = 0): row tile blockIdx.x of all sequences' (the grid
@@ -144,37 +225,25 @@ __device__ __forceinline__ int cuts_of(int nb, float t) {
 // Few items: every item of nb key blocks is cut into ceil(nb / t) equal pieces,
 // and CTA c takes pieces c, c + parts, ... of the line of all items' pieces.
 // Lane i weighs t = ceil(longest nb / (i + 1)): the blocks of the CTA with most,
-// kPieceCost for each of its pieces, and kCutCost if anything is cut.  (What that
+// kPieceCost for each of its pieces, and kCutCost if anything is cut.  Where few
+// rows keep the partial results small and the items, of like lengths, do not fill
+// the last round of CTAs, an even line may cost less still (plan_line).  (What that
 // chooses for 16 heads: two key blocks stay whole, 12.5 us with one token and
 // 12.7 cut; four are cut, 13.1 and 14.8 whole, and with 256 tokens 17.3 and 20.2.)
 __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& tail) {
-  int first = 0, rows = 0, L = 0, tiles = 0, nb = 1;
-  auto read = [&](int b0) {  // lane: sequence b0 + lane
-    const int b = b0 + lane;
-    const bool in = b < a.batch;
-    L = in ? keys_of(a, b) : 0;
-    rows = in ? tokens_of(a, b, &first) * a.G : 0;
-    tiles = (rows + Cross::ROWS - 1) / Cross::ROWS;
-    nb = blocks_of(L);
-  };
-  auto before = [&](int n, int* total) {  // sum over the lanes before this one
-    int x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, x, o);
-      if (lane >= o) x += y;
-    }
-    *total = __shfl_sync(kFull, x, 31);
-    return x - n;
-  };
+  Lane mine;
+  auto read = [&](int b0) { mine = lane_of(a, b0 + lane); };
   float T = 0.f;
   int P = 0, items = 0;
   if (a.parts > 0) {
-    int longest = 1;
+    int longest = 1, shortest = INT32_MAX, widest = 0, all = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
       read(b0);
-      items += __reduce_add_sync(kFull, tiles);
-      longest = max(longest, __reduce_max_sync(kFull, tiles > 0 ? nb : 1));
+      items += __reduce_add_sync(kFull, mine.tiles);
+      longest = max(longest, __reduce_max_sync(kFull, mine.tiles > 0 ? mine.nb : 1));
+      shortest = min(shortest, __reduce_min_sync(kFull, mine.tiles > 0 ? mine.nb : INT32_MAX));
+      widest = max(widest, __reduce_max_sync(kFull, mine.rows));
+      all = min(1 << 24, all + __reduce_add_sync(kFull, int(min(int64_t(1) << 24, int64_t(mine.tiles) * a.Hkv * mine.nb))));
     }
     items *= a.Hkv;
     const float t = ceilf(__fdividef(longest, lane + 1));
@@ -182,7 +251,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
       if (a.batch > 32) read(b0);
       for (int i = 0; i < min(32, a.batch - b0); ++i)
-        n += __shfl_sync(kFull, tiles, i) * cuts_of(__shfl_sync(kFull, nb, i), t);
+        n += __shfl_sync(kFull, mine.tiles, i) * cuts_of(__shfl_sync(kFull, mine.nb, i), t);
     }
     n *= a.Hkv;
     // (cut pieces have a slot each; uncut items need none)
@@ -191,6 +260,13 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
     const int best = __reduce_min_sync(kFull, fits ? cost * 32 + lane : ~0u) & 31;
     T = __shfl_sync(kFull, t, best);
     P = __shfl_sync(kFull, n, best);
+    if (widest <= 128 && all >= a.parts && all < (1 << 23)) {
+      const int share = (all + a.parts - 1) / a.parts;
+      if (share <= 2 * shortest && uint32_t(share + kLineCost) < __shfl_sync(kFull, cost, best)) {
+        plan_line(a, lane, all, tail);
+        return;
+      }
+    }
   }
   int k = 0;
   for (int p = blockIdx.x; a.parts == 0 ? k == 0 : p < P && k < kMaxPieces; p += a.parts, ++k) {
@@ -199,38 +275,38 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
     bool found = false;
     for (int b0 = 0; b0 < a.batch && !found; b0 += 32) {
       if (a.batch > 32 || a.parts == 0) read(b0);
-      const int s = a.parts > 0 ? cuts_of(nb, T) : 1;
-      const int n = a.parts > 0 ? tiles * a.Hkv * s : tiles;
-      const int at = passed + before(n, &total);
+      const int s = a.parts > 0 ? cuts_of(mine.nb, T) : 1;
+      const int n = a.parts > 0 ? mine.tiles * a.Hkv * s : mine.tiles;
+      const int at = passed + lanes_before(n, lane, &total);
       const unsigned m = __ballot_sync(kFull, p >= at && p < at + n);
       passed += total;
-      const int mine = s > 1 ? tiles * a.Hkv : 0;
+      const int cut_here = s > 1 ? mine.tiles * a.Hkv : 0;
       if (m) {
         const int f = __ffs(m) - 1;
         found = true;
         const int cuts = __shfl_sync(kFull, s, f);
         const int in = p - __shfl_sync(kFull, at, f);
         const int item = cuts > 1 ? in / cuts : in, cut = in - item * cuts;
-        const int ts = __shfl_sync(kFull, tiles, f), blocks = __shfl_sync(kFull, nb, f);
+        const int ts = __shfl_sync(kFull, mine.tiles, f), blocks = __shfl_sync(kFull, mine.nb, f);
         const int h = a.parts == 0 ? int(blockIdx.y) : ts > 1 ? item / ts : item;
         const int tile = a.parts > 0 ? item - h * ts : item;
         q.b = b0 + f;
         q.h = h;
-        q.first = __shfl_sync(kFull, first, f);
+        q.first = __shfl_sync(kFull, mine.first, f);
         q.row0 = tile * Cross::ROWS;
-        q.n_rows = __shfl_sync(kFull, rows, f) - q.row0;
-        q.L = __shfl_sync(kFull, L, f);
+        q.n_rows = __shfl_sync(kFull, mine.rows, f) - q.row0;
+        q.L = __shfl_sync(kFull, mine.L, f);
         const int base = cuts > 1 ? blocks / cuts : blocks, over = blocks - base * cuts;  // `over` pieces have one more
         q.j0 = cut * base + min(cut, over);
         q.nblk = q.L > 0 ? base + (cut < over) : 0;
         q.slot = cuts > 1 ? p : -1;
         if (cuts > 1 && cut == 0) {  // the merge's record, with the first piece of a cut item
-          cut_items += __reduce_add_sync(kFull, lane < f ? mine : 0);
-          const CrossSplit r = {cuts, p, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
+          cut_items += __reduce_add_sync(kFull, lane < f ? cut_here : 0);
+          const CrossSplit r = {cuts, p, 1, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
           if (lane == 0) a.split[cut_items + item] = r;
         }
       } else {
-        cut_items += __reduce_add_sync(kFull, mine);
+        cut_items += __reduce_add_sync(kFull, cut_here);
       }
     }
     if (!found) break;
@@ -242,7 +318,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
     int cut_items = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
       if (a.batch > 32) read(b0);
-      cut_items += __reduce_add_sync(kFull, cuts_of(nb, T) > 1 ? tiles * a.Hkv : 0);
+      cut_items += __reduce_add_sync(kFull, cuts_of(mine.nb, T) > 1 ? mine.tiles * a.Hkv : 0);
     }
     if (lane == 0) *a.n_split = cut_items;
   }
@@ -892,7 +968,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __g
   for (int u = blockIdx.x; u < last; u += gridDim.x) {
     const int q = u / units, r0 = (u - q * units) * 32;  // the q-th cut item, its rows from r0 on
     const CrossSplit sp = a.split[q];
-    if (r0 >= sp.rows) continue;
+    if (sp.cuts == 0 || r0 >= sp.rows) continue;
     const int row = r0 + lane;
     const bool live = row < sp.rows;
     float M = -INFINITY, sum = 0.f;
@@ -905,7 +981,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __g
       float4 v[kMergeAtOnce][kMergeGroups];
 #pragma unroll
       for (int k = 0; k < kMergeAtOnce; ++k) {
-        const size_t slot = sp.slot + k0 + k;
+        const size_t slot = k0 + k ? (sp.slot & -sp.step) + (k0 + k) * sp.step : sp.slot;
         const bool in = live && k0 + k < sp.cuts;
         ls[k] = in ? a.lse_part[slot * a.part_rows + row] : -INFINITY;
 #pragma unroll

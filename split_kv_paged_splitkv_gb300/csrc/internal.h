@@ -224,10 +224,11 @@ struct EvictArgs {
 
 constexpr int kSmCount = 152;  // SMs that cross attention plans for
 
-// A cut item of cross attention, for the merge: its number of pieces, the slot of
-// the first, its sequence's first token, head, first row and rows.
+// A cut item of cross attention, for the merge: its number of pieces (0: none such),
+// the slot of the first, how far apart the others' are (1, or 2 from the even slot
+// at or before the first on), its sequence's first token, head, first row and rows.
 struct CrossSplit {
-  int32_t cuts, slot, first, head, row0, rows;
+  int32_t cuts, slot, step, first, head, row0, rows;
 };
 
 struct CrossArgs {

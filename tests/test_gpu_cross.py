@@ -212,3 +212,17 @@ def test_one_head(keys, tokens):
     """A single item: up to 128 rows its key blocks go to both row blocks in turn, cut or not."""
     c = Cache([keys], kv_heads=1, heads=2, page=32, device="cuda", seed=59)
     run(c, [tokens])
+
+
+@pytest.mark.parametrize("batch,kv_heads,heads,tokens", [(10, 16, 16, 1), (12, 16, 32, 3), (170, 1, 1, 1), (21, 8, 64, 8)])
+def test_slightly_more_items_than_sms(batch, kv_heads, heads, tokens):
+    """Items of like lengths that would leave the last round of CTAs nearly empty: cut anywhere, pieces of several
+    items in a CTA."""
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in rng.integers(900, 1700, batch)]
+    counts = [int(x) for x in rng.integers(1, tokens + 1, batch)]
+    c = Cache(lens, kv_heads=kv_heads, heads=heads, device="cuda", seed=70 + batch)
+    run(c, counts)
+    c.lens_host = [min(x, -(-y // c.P) * c.P) for x, y in zip(lens[::-1], lens)]
+    c.lens.copy_(torch.tensor(c.lens_host))
+    run(c, counts, pad=3, before=2)
