@@ -23,14 +23,13 @@
 // finished S also say that the PV before it is done (P read, O at rest).
 //
 // K and V blocks pass in that order through one ring of five 32 KB slots that
-// two producer warps, one for K and one for V, fill by TMA, one box per page
-// piece and 64-column half, 128-byte swizzled; K is read K-major, V with its
-// dims on N.
+// two producer warps fill by TMA, each a 64-column half of every slot, one box
+// per page piece, 128-byte swizzled; K is read K-major, V with its dims on N.
 // TMEM columns: S_A [0, 128), S_B [128, 256), O_A [256, 384), O_B [384, 512).
 //
 // Many items (prompts): a CTA per item; the bound is 4 * 128 * rows * L
-// operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 780 to
-// 810 us, 1,320 to 1,370 TFLOP/s (floor 552 at 1,938), at 1,370 of the GPU's
+// operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 745 to
+// 775 us, 1,380 to 1,435 TFLOP/s (floor 552 at 1,938), near the GPU's limit of
 // 1,400 W and with the tensor pipe waiting for the softmax's turn of the row
 // blocks.
 //
@@ -39,11 +38,18 @@
 // and walks its pieces (the ring and the barriers run on across them); cut
 // items leave partial results that cross_merge_kernel joins by their
 // log-sum-exps.  An item of up to 128 rows uses the second row block for every
-// other key block of the same rows.  Bound: the bytes of K and V, at HBM's rate
-// once the copies flow, behind a start of 5 us (the plan, the first blocks) and
-// the merge's 2 (one token of 8 requests over 1.2k keys of 16 heads: 32 us,
-// floor 11.6), or the longest piece's chain of products (prompts of 37 to 900
-// tokens over 1 to 4.1k keys: 24.4 us, floor 2.9).
+// other key block of the same rows.  Bound: the bytes of K and V, some 43 bytes
+// a nanosecond into each SM once the copies flow, behind a start of 5 us (2.3
+// the plan, 2.6 the first blocks), an end of 3 (the last softmax, P . V, the
+// result) and the merge's 1.5 (one token of 8 requests over 1.2k keys of 16
+// heads: 27.7 us, floor 11.6), or the longest piece's chain of products and the
+// 32-bit partial results (prompts of 37 to 900 tokens over 1 to 4.1k keys:
+// 21.6 us, floor 2.9).
+//
+// The code that runs once in a piece is kept small: it waits for its own
+// instructions, and the softmax's loop runs slower beside more of them (the
+// epilogue's columns unrolled by two: 754 us for the prompts above, rolled
+// 800; the rescaling of O unrolled as well: 810).
 //
 // P is rounded to bf16 for the second product (half a step, 2^-8 of a weight,
 // as in the decode kernels); sums, maxima and O are fp32.
