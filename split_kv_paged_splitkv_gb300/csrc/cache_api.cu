@@ -379,6 +379,7 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
 size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
   if (validate_cross(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
   const size_t parts = size_t(cross_parts(*desc, n_tokens));
+  if (parts == 0) return 0;
   return align256(2 * parts * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float)) + split_bytes(parts);
 }
 
