@@ -378,8 +378,8 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
 
 size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
   if (validate_cross(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
-  const size_t parts = size_t(cross_parts(*desc, n_tokens));
-  if (parts == 0) return 0;
+  if (cross_deal(*desc, n_tokens) == CrossDeal::kItems) return 0;
+  const size_t parts = kSmCount;
   return align256(2 * parts * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float)) + split_bytes(parts);
 }
 
@@ -410,7 +410,9 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
     return fail(SPLITKV_EINVAL, "out overlaps q");
   if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPLITKV_EINVAL, "scale must be positive and finite");
   CrossArgs a{};
-  a.parts = cross_parts(d, n_tokens);
+  const CrossDeal deal = cross_deal(d, n_tokens);
+  a.parts = deal == CrossDeal::kItems ? 0 : kSmCount;
+  a.line = deal == CrossDeal::kLine;
   a.part_rows = cross_part_rows(d, n_tokens);
   if (a.parts > 0) {
     if (!workspace) return fail(SPLITKV_EWORKSPACE, "workspace is NULL");

@@ -27,9 +27,10 @@
 // per page piece, 128-byte swizzled; K is read K-major, V with its dims on N.
 // TMEM columns: S_A [0, 128), S_B [128, 256), O_A [256, 384), O_B [384, 512).
 //
-// Many items (prompts): a CTA per item; the bound is 4 * 128 * rows * L
-// operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 745 to
-// 775 us, 1,380 to 1,435 TFLOP/s (floor 552 at 1,938), near the GPU's limit of
+// Many items: a CTA per item (prompts), or a line of all items' key blocks that the
+// CTAs share (batches of few rows a sequence; cross_deal has the rule).  The bound
+// of prompts is 4 * 128 * rows * L operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 740 to
+// 775 us, 1,380 to 1,445 TFLOP/s (floor 552 at 1,938), near the GPU's limit of
 // 1,400 W and with the tensor pipe waiting for the softmax's turn of the row
 // blocks.
 //
@@ -72,7 +73,8 @@ struct Cross {
   static constexpr int NST = 5;
   static constexpr int OFF_RING = 2 * TILE;      // after Q's two row blocks
   static constexpr int OFF_BAR = OFF_RING + NST * TILE;
-  static constexpr int SMEM = 1024 + OFF_BAR + 512;
+  static constexpr int TAIL = 1536;              // barriers, plan
+  static constexpr int SMEM = 1024 + OFF_BAR + TAIL;
   static constexpr int SOFTMAX_WARPS = 8;
   // warps: the producers of K and of V, the issuer of the MMAs
   static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 2;
@@ -126,15 +128,25 @@ struct Piece {
 };
 constexpr int kMaxPieces = 4;  // of a CTA
 constexpr int kPieceCost = 2, kCutCost = 2;  // in key blocks: of each piece, and of cutting anything
-constexpr int kLineCost = 8;  // and of an even line of all key blocks
+constexpr int kLineCost = 8;  // and of a line of all key blocks
+
+// Where a warp is in a line: the next key block, and the item that holds it (of
+// sequence b, from block `off` on) with its sequence's numbers.
+struct Walk {
+  int64_t x;
+  int b, item, off, first, rows, L, tiles, nb;
+};
 
 // Behind the barriers.
 struct Tail {
-  uint32_t tmem;  // written by the allocation
-  int32_t pieces;
+  uint32_t tmem;   // written by the allocation
+  int32_t pieces;  // in `piece`; -1: the line's blocks [lo, hi), `share` to a CTA
+  int64_t lo, hi, share;
   Piece piece[kMaxPieces];
+  Walk walk[Cross::THREADS / 32];
+  Piece now[Cross::THREADS / 32];
 };
-static_assert(B_COUNT * 8 + sizeof(Tail) <= 512, "barriers, then the tail");
+static_assert(B_COUNT * 8 + sizeof(Tail) <= Cross::TAIL, "barriers, then the tail");
 
 // Pieces of about t key blocks that an item of nb is cut into.  (In floating
 // point, for speed: any count in 1 .. nb is right, as long as all agree on it.)
@@ -159,130 +171,210 @@ __device__ __forceinline__ Lane lane_of(const CrossArgs& a, int b) {
 }
 
 // Sum over the lanes before this one.
-__device__ __forceinline__ int lanes_before(int n, int lane, int* total) {
-  int x = n;
+template <class T>
+__device__ __forceinline__ T lanes_before(T n, int lane, T* total) {
+  T x = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, x, o);
+    const T y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x += y;
   }
   *total = __shfl_sync(kFull, x, 31);
   return x - n;
 }
 
-// The even line of plan_pieces: all items' key blocks, `line` in number (parts to
-// 2^23), one after the other, of which CTA c takes those from lo(c) on.  No item
-// is shorter than half a CTA's share, so it has three pieces at most.  (One token
-// of 10 requests, 160 items over 152 CTAs, 1.5k keys: 39.6 us, in whole items
-// 49.7; 4k keys: 75.8 and 110.9.  kLineCost is what leaves 8 requests, 27.6 us
-// and as a line 30.2, and 16, 51.8 and 55.3, as they are.)
-__device__ __noinline__ void plan_line(const CrossArgs& a, int lane, int line, Tail& tail) {
-  auto lo = [&](int c) { return int(unsigned(line) * unsigned(c) / unsigned(a.parts)); };
-  auto cta_of = [&](int y) { return int((unsigned(y + 1) * unsigned(a.parts) - 1) / unsigned(line)); };
-  const int c = blockIdx.x, hi = lo(c + 1);
-  CrossSplit r = {0, 0, 2, 0, 0, 0, 0};
-  int k = 0;
-  for (int x = lo(c); x < hi && k < kMaxPieces; ++k) {
-    Piece q;
-    int passed = 0, total;
-    bool found = false;
-    for (int b0 = 0; b0 < a.batch && !found; b0 += 32) {
-      const Lane s = lane_of(a, b0 + lane);
-      const int n = s.tiles * a.Hkv * s.nb;
-      const int at = passed + lanes_before(n, lane, &total);
-      const unsigned m = __ballot_sync(kFull, x >= at && x < at + n);
-      passed += total;
-      if (m) {
-        const int f = __ffs(m) - 1;
-        found = true;
-        const int blocks = __shfl_sync(kFull, s.nb, f), ts = __shfl_sync(kFull, s.tiles, f);
-        const int in = x - __shfl_sync(kFull, at, f), item = in / blocks;
-        q.b = b0 + f;
-        q.h = ts > 1 ? item / ts : item;
-        q.row0 = (item - q.h * ts) * Cross::ROWS;
-        q.first = __shfl_sync(kFull, s.first, f);
-        q.n_rows = __shfl_sync(kFull, s.rows, f) - q.row0;
-        q.L = __shfl_sync(kFull, s.L, f);
-        q.j0 = in - item * blocks;
-        const int len = min(blocks - q.j0, hi - x);
-        q.nblk = q.L > 0 ? len : 0;
-        q.slot = len < blocks ? 2 * c + (k > 0) : -1;  // (only a CTA's first and last piece can be cut)
-        if (len < blocks && q.j0 == 0)                 // (the last)
-          r = {cta_of(x + blocks - 1) - c + 1, q.slot, 2, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
-        x += len;
-      }
+// The line of plan_pieces: all items' key blocks, one after the other (sequence,
+// KV head, row tile), of which CTA c takes `share` from c * share on, whole items
+// but for the first and the last (the last CTAs may have less; equal parts cut
+// more items and were up to 9 % slower).  Here: where this CTA begins.
+//
+// Few items, of like lengths and few rows, that do not fill the last round of
+// CTAs: one token of 10 requests, 160 items over 152 CTAs, 1.5k keys, takes 42.7
+// us, in whole items 49.7; over 4k keys 79 and 111.  kLineCost is what leaves 8
+// requests, 27.7 us and as a line 30.2, and 16, 51.8 and 55.3, as they are.
+__device__ __noinline__ void plan_line(const CrossArgs& a, int lane, int64_t all, Tail& tail) {
+  const int64_t share = (all + a.parts - 1) / a.parts;
+  const int64_t lo = min(all, int64_t(blockIdx.x) * share), hi = min(all, lo + share);
+  Walk w = {lo, 0, 0, 0, 0, 0, 0, 0, 1};
+  int64_t passed = 0, total;
+  for (int b0 = 0; lo < hi && b0 < a.batch; b0 += 32) {
+    const Lane s = lane_of(a, b0 + lane);
+    const int64_t n = int64_t(s.tiles) * a.Hkv * s.nb;
+    const int64_t at = passed + lanes_before(n, lane, &total);
+    const unsigned m = __ballot_sync(kFull, lo >= at && lo < at + n);
+    passed += total;
+    if (m) {
+      const int f = __ffs(m) - 1;
+      w.b = b0 + f;
+      w.first = __shfl_sync(kFull, s.first, f);
+      w.rows = __shfl_sync(kFull, s.rows, f);
+      w.L = __shfl_sync(kFull, s.L, f);
+      w.tiles = __shfl_sync(kFull, s.tiles, f);
+      w.nb = __shfl_sync(kFull, s.nb, f);
+      const int64_t in = lo - __shfl_sync(kFull, at, f);
+      w.item = int(in / w.nb);
+      w.off = int(in - int64_t(w.item) * w.nb);
+      break;
     }
-    if (!found) break;
-    if (lane == 0) tail.piece[k] = q;
   }
+  if (lane < Cross::THREADS / 32) tail.walk[lane] = w;
   if (lane == 0) {
-    tail.pieces = k;
-    a.split[c] = r;
-    if (c == 0) *a.n_split = a.parts;
+    tail.pieces = -1;
+    tail.lo = lo;
+    tail.hi = hi;
+    tail.share = share;
+    a.split[blockIdx.x].cuts = 0;
+    if (blockIdx.x == 0) *a.n_split = a.parts;
   }
+}
+
+// A CTA per item: row tile blockIdx.x of all sequences' (the grid counts tiles for
+// any split of the tokens among the sequences), head blockIdx.y.
+__device__ __noinline__ void plan_one(const CrossArgs& a, int lane, Tail& tail) {
+  const int p = blockIdx.x;
+  int passed = 0, total;
+  bool found = false;
+  for (int b0 = 0; b0 < a.batch && !found; b0 += 32) {
+    const Lane s = lane_of(a, b0 + lane);
+    const int at = passed + lanes_before(s.tiles, lane, &total);
+    const unsigned m = __ballot_sync(kFull, p >= at && p < at + s.tiles);
+    passed += total;
+    if (m) {
+      found = true;
+      const int f = __ffs(m) - 1;
+      Piece q;
+      q.b = b0 + f;
+      q.h = blockIdx.y;
+      q.first = __shfl_sync(kFull, s.first, f);
+      q.row0 = (p - __shfl_sync(kFull, at, f)) * Cross::ROWS;
+      q.n_rows = __shfl_sync(kFull, s.rows, f) - q.row0;
+      q.L = __shfl_sync(kFull, s.L, f);
+      q.j0 = 0;
+      q.nblk = q.L > 0 ? __shfl_sync(kFull, s.nb, f) : 0;
+      q.slot = -1;
+      if (lane == 0) tail.piece[0] = q;
+    }
+  }
+  if (lane == 0) tail.pieces = found;
+}
+
+// By warp `me`, in a line: its next piece, into tail.now[me]; false behind the last.
+__device__ __noinline__ bool next_piece(const CrossArgs& a, Tail& tail, int me, int lane) {
+  Walk& walk = tail.walk[me];
+  __syncwarp();  // (the piece before has been read)
+  Walk w = walk;
+  if (w.x >= tail.hi) return false;
+  const int len = int(min(int64_t(w.nb - w.off), tail.hi - w.x));
+  Piece q;
+  q.b = w.b;
+  q.h = w.tiles > 1 ? w.item / w.tiles : w.item;
+  q.first = w.first;
+  q.row0 = (w.item - q.h * w.tiles) * Cross::ROWS;
+  q.n_rows = w.rows - q.row0;
+  q.L = w.L;
+  q.j0 = w.off;
+  q.nblk = w.L > 0 ? len : 0;
+  q.slot = len < w.nb ? 2 * int(blockIdx.x) + (w.x > tail.lo) : -1;
+  if (me == Cross::ISSUER && lane == 0 && len < w.nb && w.off == 0) {  // (the CTA's last piece: an item's first)
+    const int last = int((w.x + w.nb - 1) / tail.share);               // CTA of the item's last block
+    const CrossSplit r = {last - int(blockIdx.x) + 1, q.slot, 2, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
+    a.split[blockIdx.x] = r;
+  }
+  w.x += len;
+  w.off += len;
+  if (w.off == w.nb && w.x < tail.hi) {
+    w.off = 0;
+    if (++w.item == w.tiles * a.Hkv) {  // the next sequence with tokens
+      w.item = 0;
+      Lane s;
+      do s = lane_of(a, ++w.b); while (s.tiles == 0 && w.b < a.batch);
+      w.first = s.first;
+      w.rows = s.rows;
+      w.L = s.L;
+      w.tiles = s.tiles;
+      w.nb = s.nb;
+    }
+  }
+  __syncwarp();
+  if (lane == 0) {
+    tail.now[me] = q;
+    walk = w;
+  }
+  __syncwarp();
+  return true;
 }
 
 // By a warp: which pieces this CTA computes.
 //
-// A CTA per item (a.parts = 0): row tile blockIdx.x of all sequences' (the grid
-// counts tiles for any split of the tokens among the sequences), head
-// blockIdx.y.
+// A CTA per item (a.parts = 0): plan_one.  A line whatever the lengths (a.line):
+// plan_line.
 //
 // Few items: every item of nb key blocks is cut into ceil(nb / t) equal pieces,
 // and CTA c takes pieces c, c + parts, ... of the line of all items' pieces.
 // Lane i weighs t = ceil(longest nb / (i + 1)): the blocks of the CTA with most,
 // kPieceCost for each of its pieces, and kCutCost if anything is cut.  Where few
 // rows keep the partial results small and the items, of like lengths, do not fill
-// the last round of CTAs, an even line may cost less still (plan_line).  (What that
+// the last round of CTAs, a line may cost less still.  (What that
 // chooses for 16 heads: two key blocks stay whole, 12.5 us with one token and
 // 12.7 cut; four are cut, 13.1 and 14.8 whole, and with 256 tokens 17.3 and 20.2.)
 __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& tail) {
+  if (a.parts == 0) {
+    plan_one(a, lane, tail);
+    return;
+  }
   Lane mine;
   auto read = [&](int b0) { mine = lane_of(a, b0 + lane); };
-  float T = 0.f;
-  int P = 0, items = 0;
-  if (a.parts > 0) {
-    int longest = 1, shortest = INT32_MAX, widest = 0, all = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      read(b0);
-      items += __reduce_add_sync(kFull, mine.tiles);
-      longest = max(longest, __reduce_max_sync(kFull, mine.tiles > 0 ? mine.nb : 1));
-      shortest = min(shortest, __reduce_min_sync(kFull, mine.tiles > 0 ? mine.nb : INT32_MAX));
-      widest = max(widest, __reduce_max_sync(kFull, mine.rows));
-      all = min(1 << 24, all + __reduce_add_sync(kFull, int(min(int64_t(1) << 24, int64_t(mine.tiles) * a.Hkv * mine.nb))));
+  int items = 0, longest = 1, shortest = INT32_MAX, widest = 0;
+  int64_t all = 0;  // key blocks
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    read(b0);
+    const int64_t blocks = int64_t(mine.tiles) * a.Hkv * mine.nb;
+    if (a.line) {
+      int64_t sum;
+      lanes_before(blocks, lane, &sum);
+      all += sum;
+      continue;
     }
-    items *= a.Hkv;
-    const float t = ceilf(__fdividef(longest, lane + 1));
-    int n = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      if (a.batch > 32) read(b0);
-      for (int i = 0; i < min(32, a.batch - b0); ++i)
-        n += __shfl_sync(kFull, mine.tiles, i) * cuts_of(__shfl_sync(kFull, mine.nb, i), t);
-    }
-    n *= a.Hkv;
-    // (cut pieces have a slot each; uncut items need none)
-    const bool fits = lane == 0 || n <= 2 * a.parts;
-    const uint32_t cost = (n + a.parts - 1) / a.parts * (uint32_t(t) + kPieceCost) + (n > items ? kCutCost : 0);
-    const int best = __reduce_min_sync(kFull, fits ? cost * 32 + lane : ~0u) & 31;
-    T = __shfl_sync(kFull, t, best);
-    P = __shfl_sync(kFull, n, best);
-    if (widest <= 128 && all >= a.parts && all < (1 << 23)) {
-      const int share = (all + a.parts - 1) / a.parts;
-      if (share <= 2 * shortest && uint32_t(share + kLineCost) < __shfl_sync(kFull, cost, best)) {
-        plan_line(a, lane, all, tail);
-        return;
-      }
-    }
+    all += __reduce_add_sync(kFull, int(min(int64_t(1) << 26, blocks)));  // (items are few: more need not be exact)
+    items += __reduce_add_sync(kFull, mine.tiles);
+    longest = max(longest, __reduce_max_sync(kFull, mine.tiles > 0 ? mine.nb : 1));
+    shortest = min(shortest, __reduce_min_sync(kFull, mine.tiles > 0 ? mine.nb : INT32_MAX));
+    widest = max(widest, __reduce_max_sync(kFull, mine.rows));
+  }
+  if (a.line) {
+    plan_line(a, lane, all, tail);
+    return;
+  }
+  items *= a.Hkv;
+  const float t = ceilf(__fdividef(longest, lane + 1));
+  int n = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    if (a.batch > 32) read(b0);
+    for (int i = 0; i < min(32, a.batch - b0); ++i)
+      n += __shfl_sync(kFull, mine.tiles, i) * cuts_of(__shfl_sync(kFull, mine.nb, i), t);
+  }
+  n *= a.Hkv;
+  // (cut pieces have a slot each; uncut items need none)
+  const bool fits = lane == 0 || n <= 2 * a.parts;
+  const uint32_t cost = (n + a.parts - 1) / a.parts * (uint32_t(t) + kPieceCost) + (n > items ? kCutCost : 0);
+  const int best = __reduce_min_sync(kFull, fits ? cost * 32 + lane : ~0u) & 31;
+  const float T = __shfl_sync(kFull, t, best);
+  const int P = __shfl_sync(kFull, n, best);
+  const int64_t share = (all + a.parts - 1) / a.parts;
+  if (widest <= 128 && all >= a.parts && all < (1 << 26) && share <= 2 * int64_t(shortest) &&
+      share + kLineCost < __shfl_sync(kFull, cost, best)) {
+    plan_line(a, lane, all, tail);
+    return;
   }
   int k = 0;
-  for (int p = blockIdx.x; a.parts == 0 ? k == 0 : p < P && k < kMaxPieces; p += a.parts, ++k) {
+  for (int p = blockIdx.x; p < P && k < kMaxPieces; p += a.parts, ++k) {
     Piece q;
     int passed = 0, cut_items = 0, total;  // pieces and cut items of the sequences before
     bool found = false;
     for (int b0 = 0; b0 < a.batch && !found; b0 += 32) {
-      if (a.batch > 32 || a.parts == 0) read(b0);
-      const int s = a.parts > 0 ? cuts_of(mine.nb, T) : 1;
-      const int n = a.parts > 0 ? mine.tiles * a.Hkv * s : mine.tiles;
+      if (a.batch > 32) read(b0);
+      const int s = cuts_of(mine.nb, T);
+      const int n = mine.tiles * a.Hkv * s;
       const int at = passed + lanes_before(n, lane, &total);
       const unsigned m = __ballot_sync(kFull, p >= at && p < at + n);
       passed += total;
@@ -294,8 +386,8 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
         const int in = p - __shfl_sync(kFull, at, f);
         const int item = cuts > 1 ? in / cuts : in, cut = in - item * cuts;
         const int ts = __shfl_sync(kFull, mine.tiles, f), blocks = __shfl_sync(kFull, mine.nb, f);
-        const int h = a.parts == 0 ? int(blockIdx.y) : ts > 1 ? item / ts : item;
-        const int tile = a.parts > 0 ? item - h * ts : item;
+        const int h = ts > 1 ? item / ts : item;
+        const int tile = item - h * ts;
         q.b = b0 + f;
         q.h = h;
         q.first = __shfl_sync(kFull, mine.first, f);
@@ -320,7 +412,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
   }
   if (lane == 0) tail.pieces = k;
   // the number of those records
-  if (a.parts > 0 && blockIdx.x == 0) {
+  if (blockIdx.x == 0) {
     int cut_items = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
       if (a.batch > 32) read(b0);
@@ -531,7 +623,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   wait_prerequisites();
   if (warp == C::ISSUER) {
     plan_pieces(a, lane, tail);
-  } else if (a.parts > 0) {  // (meanwhile: where the pages' ids begin)
+  } else {  // (meanwhile: where the pages' ids begin)
     for (int b = threadIdx.x; b < a.batch; b += C::SOFTMAX_WARPS * 32)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(a.block_table + size_t(b) * a.max_pages));
   }
@@ -540,6 +632,11 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tail.tmem);
   const int pieces = *reinterpret_cast<volatile int32_t*>(&tail.pieces);
+  int n_taken = 0;  // by this warp
+  auto take = [&]() -> const Piece* {
+    if (pieces >= 0) return n_taken < pieces ? &tail.piece[n_taken++] : nullptr;
+    return next_piece(a, tail, warp, lane) ? &tail.now[warp] : nullptr;
+  };
 
   if (warp == C::PRODUCER || warp == C::PRODUCER + 1) {
     // ------------------------------------------------------------- producers
@@ -553,8 +650,9 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     const int br = a.box_rows;
     bool ok = true;
     int item = 0;
-    for (int k = 0; k < pieces && ok; ++k) {
-      const Piece pc = tail.piece[k];
+    const Piece* taken;
+    while (ok && (taken = take()) != nullptr) {
+      const Piece pc = *taken;
       const int32_t* trow = a.block_table + size_t(pc.b) * a.max_pages;
       for (int j = 0; j < pc.nblk && ok; ++j) {
         const int key0 = (pc.j0 + j) * C::BK;
@@ -631,8 +729,9 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
       }
       return true;
     };
-    for (int k = 0; k < pieces && ok; ++k) {
-      const Piece pc = tail.piece[k];
+    const Piece* taken;
+    while (ok && (taken = take()) != nullptr) {
+      const Piece pc = *taken;
       if (pc.nblk == 0) continue;
       if (pc.n_rows <= 128) {
         // narrow: A takes the even key blocks, B the odd ones, of the same rows
@@ -740,12 +839,14 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     // The next piece with rows of this row block: its query rows, swizzled, on
     // their way into shared memory (rows behind the last are zero).  Not before
     // the products that read the Q before are done.
-    int k = 0;
+    const Piece* next = nullptr;
     auto take_piece = [&]() {
-      while (t == 1 && k < pieces && tail.piece[k].n_rows <= 128 && tail.piece[k].nblk < 2) ++k;
-      if (k == pieces) return false;
-      if (tail.piece[k].nblk > 0 && (t == 0 || tail.piece[k].n_rows > 128))
-        each_row(tail.piece[k], [&](int rr, bool in, int64_t token, int head) {
+      do {
+        next = take();
+        if (next == nullptr) return false;
+      } while (t == 1 && next->n_rows <= 128 && next->nblk < 2);
+      if (next->nblk > 0 && (t == 0 || next->n_rows > 128))
+        each_row(*next, [&](int rr, bool in, int64_t token, int head) {
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (in ? token * a.q_stride + head * 128 : 0);
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(chunk_at(rr, lane & 15))),
                        "l"(src + 8 * (lane & 15)), "r"(in ? 16 : 0)
@@ -757,7 +858,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
     bool joining = false;         // B: A has still to read its last narrow piece's O
     bool more = take_piece();
     while (ok && more) {
-      const Piece pc = tail.piece[k++];
+      const Piece pc = *next;
       // A narrow piece (up to 128 rows) has its key blocks dealt to A and B in
       // turn, as if they were two row blocks, and A joins the two results: a
       // single row block's chain of products and softmaxes would be longer
@@ -771,7 +872,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
       // that whole rows are written; a partial one (whose layout puts a
       // column's rows side by side), and one of a few rows, straight from
       // registers, with the next piece's Q already on its way.
-      const bool staged = whole && (a.parts == 0 || !narrow);
+      const bool staged = whole && !narrow;
       if (pc.nblk > 0 && (t == 0 || !narrow)) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1051,11 +1152,17 @@ int64_t cross_row_tiles(const splitkv_desc_t& d, int64_t n_tokens) {
   return full + some;
 }
 
-// CTAs that share the line of key blocks, or 0: a CTA per item.  With four
-// items per SM the unequal ends of a grid of items cost less than an eighth,
-// and the items of a head run side by side, so that its K and V come from L2.
-int cross_parts(const splitkv_desc_t& d, int64_t n_tokens) {
-  return cross_row_tiles(d, n_tokens) * d.num_kv_heads >= kMaxPieces * kSmCount ? 0 : kSmCount;
+// How the items are dealt.  Few: pieces of a cost.  Many of few rows (half a tile
+// a sequence, on average): a line, so that a CTA's K and V keep coming while it goes
+// from one item to the next (one token of 512 requests, 8 heads, 512 keys: 280 us,
+// a CTA per item 405).  Many of more rows: a CTA per item, for its results pass
+// through the shared memory that the next item's queries need (80 prompts of 40
+// to 80 tokens, 32 heads on 8, 512 keys: 99 us, as a line 116; prompts of 4k
+// tokens the same either way).
+CrossDeal cross_deal(const splitkv_desc_t& d, int64_t n_tokens) {
+  if (cross_row_tiles(d, n_tokens) * d.num_kv_heads <= kMaxPieces * kSmCount) return CrossDeal::kPieces;
+  const int64_t rows = n_tokens * (d.num_q_heads / d.num_kv_heads);
+  return 2 * rows <= Cross::ROWS * int64_t(d.batch) ? CrossDeal::kLine : CrossDeal::kItems;
 }
 
 int cross_part_rows(const splitkv_desc_t& d, int64_t n_tokens) {

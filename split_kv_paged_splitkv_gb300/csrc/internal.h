@@ -248,6 +248,7 @@ struct CrossArgs {
   float qk_scale_log2;
   int32_t n_tokens, batch, T, Hq, Hkv, G, P, max_pages, num_pages, box_rows;
   int32_t parts;      // CTAs that share all items' key blocks; 0: a CTA per item
+  int32_t line;       // an even line of all items' key blocks, whatever their lengths
   int32_t part_rows;  // rows of an item, at most
 };
 
@@ -259,7 +260,8 @@ cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, 
 cudaError_t launch_key_weights(const WeightArgs& a, bool fp8, void* stream);
 cudaError_t launch_evict(const EvictArgs& a, void* stream);
 int64_t cross_row_tiles(const splitkv_desc_t& d, int64_t n_tokens);
-int cross_parts(const splitkv_desc_t& d, int64_t n_tokens);
+enum class CrossDeal { kPieces, kLine, kItems };
+CrossDeal cross_deal(const splitkv_desc_t& d, int64_t n_tokens);
 int cross_part_rows(const splitkv_desc_t& d, int64_t n_tokens);
 int cross_box_rows(const splitkv_desc_t& d);  // keys of one TMA box
 cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv,

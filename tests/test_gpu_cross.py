@@ -226,3 +226,28 @@ def test_slightly_more_items_than_sms(batch, kv_heads, heads, tokens):
     c.lens_host = [min(x, -(-y // c.P) * c.P) for x, y in zip(lens[::-1], lens)]
     c.lens.copy_(torch.tensor(c.lens_host))
     run(c, counts, pad=3, before=2)
+
+
+@pytest.mark.parametrize("seed", [1, 2])
+def test_many_items_of_few_rows(seed):
+    """More than four items per SM, of half a row tile on average: dealt as a line, cut at the CTAs' bounds; lengths,
+    tokens and empty sequences of all kinds, more than 32 sequences, some of several row tiles."""
+    rng = np.random.default_rng(seed)
+    B = 90
+    lens = [int(x) for x in rng.choice([0, 1, 100, 128, 129, 257, 400, 700], B)]
+    counts = [int(x) for x in rng.choice([0, 1, 2, 9, 40, 65], B, p=[.2, .4, .2, .1, .05, .05])]
+    counts[7] = 150
+    c = Cache(lens, kv_heads=8, heads=32, device="cuda", seed=80 + seed)
+    assert sum(counts) * 4 <= 128 * B and (sum(counts) * 4 // 256 + B) * 8 > 4 * 152
+    run(c, counts, before=2, pad=1)
+
+
+def test_many_items_but_few_tokens():
+    """The bound on the items is high, most sequences have no token: fewer key blocks than SMs in the line."""
+    B = 100
+    counts = [0] * B
+    counts[3], counts[50], counts[97] = 1, 90, 9
+    lens = [40] * B
+    lens[50], lens[97] = 300, 0
+    c = Cache(lens, kv_heads=8, heads=8, device="cuda", seed=85)
+    run(c, counts)
