@@ -335,7 +335,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
       all += sum;
       continue;
     }
-    all += __reduce_add_sync(kFull, int(min(int64_t(1) << 26, blocks)));  // (items are few: more need not be exact)
+    all += __reduce_add_sync(kFull, int(min(int64_t(1) << 25, blocks)));  // (items are few: more need not be exact)
     items += __reduce_add_sync(kFull, mine.tiles);
     longest = max(longest, __reduce_max_sync(kFull, mine.tiles > 0 ? mine.nb : 1));
     shortest = min(shortest, __reduce_min_sync(kFull, mine.tiles > 0 ? mine.nb : INT32_MAX));
@@ -361,7 +361,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
   const float T = __shfl_sync(kFull, t, best);
   const int P = __shfl_sync(kFull, n, best);
   const int64_t share = (all + a.parts - 1) / a.parts;
-  if (widest <= 128 && all >= a.parts && all < (1 << 26) && share <= 2 * int64_t(shortest) &&
+  if (widest <= 128 && all >= a.parts && all < (1 << 25) && share <= 2 * int64_t(shortest) &&
       share + kLineCost < __shfl_sync(kFull, cost, best)) {
     plan_line(a, lane, all, tail);
     return;
