@@ -251,3 +251,17 @@ def test_many_items_but_few_tokens():
     lens[50], lens[97] = 300, 0
     c = Cache(lens, kv_heads=8, heads=8, device="cuda", seed=85)
     run(c, counts)
+
+
+@pytest.mark.parametrize("seed,G", [(1, 4), (2, 3)])
+def test_many_items_of_many_rows(seed, G):
+    """More than four items per SM, of more than half a row tile on average: a CTA for each, found by a search."""
+    rng = np.random.default_rng(seed)
+    B = 70
+    lens = [int(x) for x in rng.choice([0, 1, 100, 129, 300], B)]
+    counts = [int(x) for x in rng.choice([0, 1, 60, 64, 86, 130], B)]
+    c = Cache(lens, kv_heads=8, heads=8 * G, device="cuda", seed=90 + seed)
+    assert sum(counts) * G > 128 * B and skv.splitkv_cross_workspace_size(c.desc, sum(counts)) == 0
+    run(c, counts, before=3, pad=2)
+    c = Cache([200] * B, kv_heads=8, heads=8 * G, tokens=60, device="cuda", seed=92 + seed)
+    run(c, [60] * B, cu=False)
