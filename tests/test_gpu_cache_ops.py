@@ -172,6 +172,16 @@ def test_append_many_heads_and_tokens():
     run_append(c, [1] * 70)
 
 
+@pytest.mark.parametrize("batch", [33, 100, 1100])
+def test_append_many_sequences(batch):
+    rng = np.random.default_rng(batch)
+    counts = [int(x) for x in rng.choice([0, 0, 1, 2], batch)]
+    counts[-1] = 0
+    lens = [n + int(x) for n, x in zip(counts, rng.integers(0, 40, batch))]
+    run_append(Cache(lens, kv_heads=1, heads=1, device="cuda", seed=7), counts, pad=3)
+    run_append(Cache([1] * batch, kv_heads=1, heads=1, device="cuda", seed=8), [1] * batch)
+
+
 def test_append_reports_slots_and_pages():
     c = Cache([16, 40, 20], device="cuda", seed=9)
     c.lens[0] = 2         # shorter than its three tokens: the first has no slot
