@@ -19,7 +19,7 @@
 // Bound: the bytes of q (read and written), k and v (read, and written in the
 // cache's type); a decode step of a few tokens is bound by one chain of
 // loads, so nothing but the token's own loads precedes its stores.  Measured:
-// 26k prompt tokens of 40 rows of 128: 98 us, 5.5 TB/s (floor 79 at the copy's
+// 26k prompt tokens of 40 rows of 128: 95 us, 5.7 TB/s (floor 79 at the copy's
 // 6.8: rows of 256 bytes go to as many places); one token 3.2 us, 32 in e4m3
 // 3.7, of which a launch is most.
 //
@@ -80,6 +80,8 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int n, int
   const int ended = lo + __popc(__ballot_sync(kFull, lane < len && cu[lo + lane + 1] <= n));
   return ended < batch && cu[0] <= n ? ended : -1;
 }
+
+constexpr int kPasses = 5;  // over a CTA's units, at most
 
 // U: units of a thread in flight.
 template <int DK, int DV, bool FP8, int U>
@@ -293,11 +295,28 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
   // i * magic >> 32 is i / per_tok for every unit i of a CTA, as i * per_tok is
   // below 2^32 or the CTA has one token (0: that token's, however many units)
   a.per_tok_magic = per_tok > 65536 ? 0 : unsigned(((uint64_t(1) << 32) + per_tok - 1) / per_tok);
-  // A CTA's units.  In a long call two passes share the lookup of the places
-  // and the sines (26k tokens of 40 rows: 99 us, with one pass 106, both with four units).
-  constexpr int units = (U == 1 ? 1 : 2) * U * kThreads;
-  const int tpc = per_tok >= units ? 1 : min(kMaxTok, units / per_tok);
-  const int64_t slices = (int64_t(per_tok) * tpc + units - 1) / units;
+  // A CTA's tokens.  In a long call the first number, of two passes or more over
+  // its units (which share the lookup of the places and the sines: 26k tokens of
+  // 40 rows, 99 us, with one pass 106), that leaves at most a twelfth of the
+  // threads idle in the last, or else the best within kPasses (29k tokens of 17
+  // latent rows, e4m3: four tokens 172 us, one 230).  A token of more units than
+  // that goes to several CTAs.
+  constexpr int pass = U * kThreads, most = (U == 1 ? 1 : kPasses) * pass;
+  const int64_t slices = (int64_t(per_tok) + most - 1) / most;
+  int most_tok = max(1, min(kMaxTok, most / per_tok)), tpc = most_tok;
+  if (U > 1) {
+    // (two CTAs per SM at least)
+    tpc = most_tok = max(1, min(most_tok, a.n_tokens / (2 * kSmCount)));
+    double least = 1e30;
+    for (int t = 1; t <= most_tok && least > 1. / 12; ++t) {
+      const int units = t * per_tok;
+      const double idle = double((pass - units % pass) % pass) / units;
+      if (units > pass && idle < least) {
+        least = idle;
+        tpc = t;
+      }
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.n_tokens + tpc - 1) / tpc, unsigned(slices > 65535 ? 65535 : slices), 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -312,7 +331,8 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
 
 // A call of few tokens takes one unit per thread, to use more of the GPU's
 // SMs (32 tokens: 3.7 us, with four 8.8); a long one two, for bytes in flight
-// (26k tokens: 97.8 us, with one 239, with four 99.2, with six 126).
+// (26k tokens: 97.8 us, with one 239, with four 99.2, with six 126; in e4m3
+// 100, with four 137).
 constexpr int64_t kFewUnits = 1 << 17;
 
 template <int DK, int DV, bool FP8>
