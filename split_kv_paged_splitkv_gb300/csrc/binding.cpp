@@ -98,21 +98,34 @@ class Args {
   // A tensor of at least `numel` adjacent elements of `type` on the call's
   // device; addresses and None pass unchecked.
   template <class T>
-  T* tensor(const char* name, ScalarType type, int64_t numel, int64_t device, int64_t* has = nullptr) {
+  T* tensor(const char* name, ScalarType type, int64_t numel, int64_t device) {
     PyObject* x = next();
     if (!x) return nullptr;
     if (x == Py_None || PyLong_Check(x)) return static_cast<T*>(raw(x));
-    if (!is_tensor(name, x)) return nullptr;
-    const at::Tensor& t = THPVariable_Unpack(x);
-    if (t.scalar_type() != type || !t.is_contiguous())
-      ok_ = wrong(PyExc_ValueError, "%s must be a contiguous %s tensor, got %s", name, c10::toString(type),
-                  c10::toString(t.scalar_type()));
-    else if (t.numel() < numel)
-      ok_ = wrong(PyExc_ValueError, "%s has %lld elements, the call needs %lld", name, (long long)t.numel(),
+    const at::Tensor* t = typed(name, x, type);
+    if (!t) return nullptr;
+    if (t->numel() < numel)
+      ok_ = wrong(PyExc_ValueError, "%s has %lld elements, the call needs %lld", name, (long long)t->numel(),
                   (long long)numel);
-    else if (on(name, t, device)) {
-      if (has) *has = t.numel();
-      return static_cast<T*>(t.data_ptr());
+    else if (on(name, *t, device))
+      return static_cast<T*>(t->data_ptr());
+    return nullptr;
+  }
+  // Two arguments: a workspace and its bytes.  None for the bytes means all of the
+  // tensor's; a number is at most those (the kernels write as many).
+  void* workspace(int64_t device, size_t* bytes) {
+    PyObject* x = next();
+    const int64_t given = ok_ && a_[i_] == Py_None ? (next(), -1) : count("workspace_bytes");
+    if (!ok_) return nullptr;
+    *bytes = given < 0 ? 0 : size_t(given);
+    if (x == Py_None || PyLong_Check(x)) return raw(x);
+    const at::Tensor* t = typed("workspace", x, ScalarType::Byte);
+    if (!t) return nullptr;
+    if (given > t->numel()) {
+      ok_ = wrong(PyExc_ValueError, "workspace_bytes is %lld, workspace has %lld", (long long)given, (long long)t->numel());
+    } else if (on("workspace", *t, device)) {
+      if (given < 0) *bytes = size_t(t->numel());
+      return t->data_ptr();
     }
     return nullptr;
   }
@@ -169,6 +182,20 @@ class Args {
     void* p = PyLong_AsVoidPtr(x);
     ok_ = !(!p && PyErr_Occurred());
     return p;
+  }
+  // A non-negative integer.
+  int64_t count(const char* name) {
+    const int64_t v = integer();
+    if (ok_ && v < 0) ok_ = wrong(PyExc_ValueError, "%s must be >= 0, got %lld", name, (long long)v);
+    return v;
+  }
+  const at::Tensor* typed(const char* name, PyObject* x, ScalarType type) {
+    if (!is_tensor(name, x)) return nullptr;
+    const at::Tensor& t = THPVariable_Unpack(x);
+    if (t.scalar_type() == type && t.is_contiguous()) return &t;
+    ok_ = wrong(PyExc_ValueError, "%s must be a contiguous %s tensor, got %s", name, c10::toString(type),
+                c10::toString(t.scalar_type()));
+    return nullptr;
   }
   bool is_tensor(const char* name, PyObject* x) {
     if (!THPVariable_Check(x))
@@ -272,15 +299,6 @@ PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// workspace_bytes, or the workspace's own where it is None.
-size_t bytes_of(Args& in, PyObject* given, int64_t own) {
-  if (given == Py_None) {
-    in.address();
-    return size_t(own);
-  }
-  return size_t(in.integer());
-}
-
 PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   Args in(a, n_args, 18);
   return guarded(in, [&]() -> int {
@@ -297,9 +315,8 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     auto* w_out = in.tensor<float>("weights_out", kFloat, z.state, dev);
     auto* p_out = in.tensor<int32_t>("positions_out", kInt, z.state, dev);
     auto* lens_out = in.tensor<int32_t>("seq_lens_out", kInt, d.batch, dev);
-    int64_t own = 0;
-    void* workspace = in.tensor<void>("workspace", ScalarType::Byte, 0, dev, &own);
-    const size_t bytes = in.ok() ? bytes_of(in, a[15], own) : 0;
+    size_t bytes = 0;
+    void* workspace = in.workspace(dev, &bytes);
     auto* status = in.tensor<int32_t>("status", kInt, 1, dev);
     void* stream = in.address();
     if (!in.ok()) return 0;
@@ -318,7 +335,7 @@ PyObject* cross_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const splitkv_desc_t& d = z.d;
     const int64_t n = in.tokens(4, times({d.num_q_heads, d.qk_dim}));
     auto* cu = in.tensor<int32_t>("cu_tokens", kInt, int64_t(d.batch) + 1, dev);
-    int64_t qs, own = 0;
+    int64_t qs;
     void* q = in.rows("q", n, d.num_q_heads, d.qk_dim, dev, &qs);
     void* k_pages = in.tensor<void>("k_pages", z.pool, z.k_pool, dev);
     void* v_pages = in.tensor<void>("v_pages", z.pool, z.v_pool, dev);
@@ -327,8 +344,8 @@ PyObject* cross_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const float scale = in.real();
     void* out = in.tensor<void>("out", ScalarType::BFloat16, times({n, d.num_q_heads, d.v_dim}), dev);
     auto* lse = in.tensor<float>("lse", kFloat, times({n, d.num_q_heads}), dev);
-    void* workspace = in.tensor<void>("workspace", ScalarType::Byte, 0, dev, &own);
-    const size_t bytes = in.ok() ? bytes_of(in, a[13], own) : 0;
+    size_t bytes = 0;
+    void* workspace = in.workspace(dev, &bytes);
     auto* status = in.tensor<int32_t>("status", kInt, 1, dev);
     void* stream = in.address();
     if (!in.ok()) return 0;
