@@ -310,6 +310,8 @@ def splitkv_debug_gather(desc: splitkv_desc_t, pages, row_elems: int, block_tabl
 
 
 # ------------------------------------------------------------ cache operators
+# Tensors are contiguous (token rows apart, whose tokens may be strided) and may be longer
+# than the call needs in their first dimension: rows of another length are refused.
 
 _marshal = None
 

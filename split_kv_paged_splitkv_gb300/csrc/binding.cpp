@@ -34,11 +34,41 @@ bool wrong(PyObject* kind, const char* format, ...) {
   return false;
 }
 
-// Element counts of a call's arrays.
+// The shape of an array, as the kernels index it.
+struct Shape {
+  int64_t dim[4];
+  int n;
+  Shape(std::initializer_list<int64_t> dims) : dim{}, n(0) {
+    for (int64_t x : dims) dim[n++] = x;
+  }
+  int64_t numel() const { return n ? times({dim[0], row()}) : 1; }
+  int64_t row() const {  // elements of an entry of the first dimension
+    int64_t r = 1;
+    for (int i = 1; i < n; ++i) r = times({r, dim[i]});
+    return r;
+  }
+  // Whether a contiguous tensor has these elements where they are looked for: it
+  // has no others, or its others are at the end, so that what lies apart by its
+  // first dimension's stride are rows of the array.  (A buffer with room for more
+  // in another dimension has rows of another length.)
+  bool lies_in(const at::Tensor& t) const {
+    if (t.numel() == numel()) return true;
+    int64_t first = 0, has = 1, want = 1;
+    while (first < t.dim() - 1 && t.size(first) == 1) ++first;
+    for (int64_t k = t.dim() - 1; k > first; --k) has = times({has, t.size(k)});
+    int outer = 0;
+    while (outer < n - 1 && dim[outer] == 1) ++outer;
+    for (int k = n - 1; k > outer; --k)
+      if ((want = times({want, dim[k]})) == has) return true;
+    return outer == n - 1;  // a single row
+  }
+};
+
+// The shapes of a call's arrays.
 struct Sizes {
-  splitkv_desc_t d;
-  int64_t k_pool, v_pool, table, state;
-  ScalarType pool;
+  splitkv_desc_t d{};
+  Shape k_pool{}, v_pool{}, table{}, state{};
+  ScalarType pool{};
 };
 
 bool sizes(PyObject* desc, Sizes& z) {
@@ -48,12 +78,14 @@ bool sizes(PyObject* desc, Sizes& z) {
   if (fits) memcpy(&z.d, b.buf, sizeof(z.d));
   PyBuffer_Release(&b);
   if (!fits) return wrong(PyExc_TypeError, "desc must be a splitkv_desc_t");
-  const int64_t rows = times({z.d.num_pages_total, z.d.num_kv_heads, z.d.page_size});
-  z.k_pool = times({rows, z.d.qk_dim});
-  z.v_pool = times({rows, z.d.v_dim});
-  z.table = times({z.d.batch, z.d.max_pages_per_seq});
-  z.state = times({z.table, z.d.num_kv_heads, z.d.page_size});
-  z.pool = z.d.kv_dtype == SPLITKV_FP8_E4M3 ? ScalarType::Byte : ScalarType::BFloat16;
+  const splitkv_desc_t& d = z.d;
+  const bool nhd = d.kv_layout == SPLITKV_LAYOUT_NHD;
+  const int64_t outer = nhd ? d.page_size : d.num_kv_heads, inner = nhd ? d.num_kv_heads : d.page_size;
+  z.k_pool = {d.num_pages_total, outer, inner, d.qk_dim};
+  z.v_pool = {d.num_pages_total, outer, inner, d.v_dim};
+  z.table = {d.batch, d.max_pages_per_seq};
+  z.state = {d.batch, d.num_kv_heads, times({d.max_pages_per_seq, d.page_size})};
+  z.pool = d.kv_dtype == SPLITKV_FP8_E4M3 ? ScalarType::Byte : ScalarType::BFloat16;
   return true;
 }
 
@@ -67,7 +99,7 @@ class Args {
   bool ok() const { return ok_; }
 
   Sizes desc() {
-    Sizes z{};
+    Sizes z;
     if (PyObject* x = next()) ok_ = sizes(x, z);
     return z;
   }
@@ -95,18 +127,21 @@ class Args {
     PyObject* x = next();
     return x ? raw(x) : nullptr;
   }
-  // A tensor of at least `numel` adjacent elements of `type` on the call's
+  // A contiguous tensor that holds an array of `type` and `shape`, on the call's
   // device; addresses and None pass unchecked.
   template <class T>
-  T* tensor(const char* name, ScalarType type, int64_t numel, int64_t device) {
+  T* tensor(const char* name, ScalarType type, const Shape& shape, int64_t device) {
     PyObject* x = next();
     if (!x) return nullptr;
     if (x == Py_None || PyLong_Check(x)) return static_cast<T*>(raw(x));
     const at::Tensor* t = typed(name, x, type);
     if (!t) return nullptr;
-    if (t->numel() < numel)
+    if (t->numel() < shape.numel())
       ok_ = wrong(PyExc_ValueError, "%s has %lld elements, the call needs %lld", name, (long long)t->numel(),
-                  (long long)numel);
+                  (long long)shape.numel());
+    else if (!shape.lies_in(*t))
+      ok_ = wrong(PyExc_ValueError, "%s has %lld elements, but not in %lld rows of %lld and more behind them", name,
+                  (long long)t->numel(), (long long)shape.dim[0], (long long)shape.row());
     else if (on(name, *t, device))
       return static_cast<T*>(t->data_ptr());
     return nullptr;
@@ -247,23 +282,23 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const auto* rope = static_cast<const splitkv_rope_t*>(in.address());
     const int64_t axes = in.integer();
     const int64_t n = in.tokens(7, times({d.num_kv_heads, d.qk_dim}));
-    auto* positions = in.tensor<int32_t>("positions", kInt, times({n, axes}), dev);
+    auto* positions = in.tensor<int32_t>("positions", kInt, {axes, n}, dev);
     int64_t qs, ks, vs, os;
     void* q = in.rows("q", n, d.num_q_heads, d.qk_dim, dev, &qs);
     void* k = in.rows("k", n, d.num_kv_heads, d.qk_dim, dev, &ks);
     void* v = in.rows("v", n, d.num_kv_heads, d.v_dim, dev, &vs);
     auto* table = in.tensor<int32_t>("block_table", kInt, z.table, dev);
-    auto* lens = in.tensor<int32_t>("seq_lens", kInt, d.batch, dev);
+    auto* lens = in.tensor<int32_t>("seq_lens", kInt, {d.batch}, dev);
     void* q_out = in.rows("q_out", n, d.num_q_heads, d.qk_dim, dev, &os);
     void* k_pages = in.tensor<void>("k_pages", z.pool, z.k_pool, dev);
     void* v_pages = in.tensor<void>("v_pages", z.pool, z.v_pool, dev);
-    auto* cu = in.tensor<int32_t>("cu_tokens", kInt, int64_t(d.batch) + 1, dev);
+    auto* cu = in.tensor<int32_t>("cu_tokens", kInt, {int64_t(d.batch) + 1}, dev);
     const float kv_scale = in.real();
-    auto* k_scale = in.tensor<float>("k_scale", kFloat, d.num_kv_heads, dev);
-    auto* v_scale = in.tensor<float>("v_scale", kFloat, d.num_kv_heads, dev);
+    auto* k_scale = in.tensor<float>("k_scale", kFloat, {d.num_kv_heads}, dev);
+    auto* v_scale = in.tensor<float>("v_scale", kFloat, {d.num_kv_heads}, dev);
     auto* weights = in.tensor<float>("key_weights", kFloat, z.state, dev);
     auto* key_positions = in.tensor<int32_t>("key_positions", kInt, z.state, dev);
-    auto* status = in.tensor<int32_t>("status", kInt, 1, dev);
+    auto* status = in.tensor<int32_t>("status", kInt, {1}, dev);
     void* stream = in.address();
     if (!in.ok()) return 0;
     return call([&] {
@@ -279,17 +314,16 @@ PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t dev = in.integer();
     const Sizes z = in.desc();
     const splitkv_desc_t& d = z.d;
-    const int64_t rows = times({d.batch, d.q_tokens, d.num_q_heads});
-    void* q = in.tensor<void>("q", ScalarType::BFloat16, times({rows, d.qk_dim}), dev);
+    void* q = in.tensor<void>("q", ScalarType::BFloat16, {d.batch, d.q_tokens, d.num_q_heads, d.qk_dim}, dev);
     void* k_pages = in.tensor<void>("k_pages", z.pool, z.k_pool, dev);
     auto* table = in.tensor<int32_t>("block_table", kInt, z.table, dev);
-    auto* lens = in.tensor<int32_t>("seq_lens", kInt, d.batch, dev);
-    auto* lse = in.tensor<float>("lse", kFloat, rows, dev);
+    auto* lens = in.tensor<int32_t>("seq_lens", kInt, {d.batch}, dev);
+    auto* lse = in.tensor<float>("lse", kFloat, {d.batch, d.q_tokens, d.num_q_heads}, dev);
     const float scale = in.real(), kv_scale = in.real(), decay = in.real();
     auto* w_in = in.tensor<float>("weights_in", kFloat, z.state, dev);
     auto* w_out = in.tensor<float>("weights_out", kFloat, z.state, dev);
-    auto* k_scale = in.tensor<float>("k_scale", kFloat, d.num_kv_heads, dev);
-    auto* status = in.tensor<int32_t>("status", kInt, 1, dev);
+    auto* k_scale = in.tensor<float>("k_scale", kFloat, {d.num_kv_heads}, dev);
+    auto* status = in.tensor<int32_t>("status", kInt, {1}, dev);
     void* stream = in.address();
     if (!in.ok()) return 0;
     return call([&] {
@@ -309,15 +343,15 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     void* k_pages = in.tensor<void>("k_pages", z.pool, z.k_pool, dev);
     void* v_pages = in.tensor<void>("v_pages", z.pool, z.v_pool, dev);
     auto* table = in.tensor<int32_t>("block_table", kInt, z.table, dev);
-    auto* lens = in.tensor<int32_t>("seq_lens", kInt, d.batch, dev);
+    auto* lens = in.tensor<int32_t>("seq_lens", kInt, {d.batch}, dev);
     auto* w_in = in.tensor<float>("weights_in", kFloat, z.state, dev);
     auto* p_in = in.tensor<int32_t>("positions_in", kInt, z.state, dev);
     auto* w_out = in.tensor<float>("weights_out", kFloat, z.state, dev);
     auto* p_out = in.tensor<int32_t>("positions_out", kInt, z.state, dev);
-    auto* lens_out = in.tensor<int32_t>("seq_lens_out", kInt, d.batch, dev);
+    auto* lens_out = in.tensor<int32_t>("seq_lens_out", kInt, {d.batch}, dev);
     size_t bytes = 0;
     void* workspace = in.workspace(dev, &bytes);
-    auto* status = in.tensor<int32_t>("status", kInt, 1, dev);
+    auto* status = in.tensor<int32_t>("status", kInt, {1}, dev);
     void* stream = in.address();
     if (!in.ok()) return 0;
     return call([&] {
@@ -334,19 +368,19 @@ PyObject* cross_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const Sizes z = in.desc();
     const splitkv_desc_t& d = z.d;
     const int64_t n = in.tokens(4, times({d.num_q_heads, d.qk_dim}));
-    auto* cu = in.tensor<int32_t>("cu_tokens", kInt, int64_t(d.batch) + 1, dev);
+    auto* cu = in.tensor<int32_t>("cu_tokens", kInt, {int64_t(d.batch) + 1}, dev);
     int64_t qs;
     void* q = in.rows("q", n, d.num_q_heads, d.qk_dim, dev, &qs);
     void* k_pages = in.tensor<void>("k_pages", z.pool, z.k_pool, dev);
     void* v_pages = in.tensor<void>("v_pages", z.pool, z.v_pool, dev);
     auto* table = in.tensor<int32_t>("block_table", kInt, z.table, dev);
-    auto* lens = in.tensor<int32_t>("seq_lens", kInt, d.batch, dev);
+    auto* lens = in.tensor<int32_t>("seq_lens", kInt, {d.batch}, dev);
     const float scale = in.real();
-    void* out = in.tensor<void>("out", ScalarType::BFloat16, times({n, d.num_q_heads, d.v_dim}), dev);
-    auto* lse = in.tensor<float>("lse", kFloat, times({n, d.num_q_heads}), dev);
+    void* out = in.tensor<void>("out", ScalarType::BFloat16, {n, d.num_q_heads, d.v_dim}, dev);
+    auto* lse = in.tensor<float>("lse", kFloat, {n, d.num_q_heads}, dev);
     size_t bytes = 0;
     void* workspace = in.workspace(dev, &bytes);
-    auto* status = in.tensor<int32_t>("status", kInt, 1, dev);
+    auto* status = in.tensor<int32_t>("status", kInt, {1}, dev);
     void* stream = in.address();
     if (!in.ok()) return 0;
     return call([&] {
