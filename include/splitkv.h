@@ -595,7 +595,8 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
  *   out          bf16 [n_tokens][Hq][128]; must not overlap q
  *   lse          fp32 [n_tokens][Hq] natural-log LSE of the scaled scores, or
  *                NULL.  A token of a sequence without keys gets out = 0 and
- *                lse = -inf
+ *                lse = -inf.  A row with a NaN or +inf among its scores gets NaN
+ *                in both
  *   workspace    splitkv_cross_workspace_size bytes (0: may be NULL; 40 MB at
  *                most), 16-byte aligned, used by this call alone until it has
  *                finished

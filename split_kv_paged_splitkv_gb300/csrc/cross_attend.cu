@@ -502,6 +502,13 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return m;
 }
 
+// NaN if either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+  return m;
+}
+
 // Two sums at once.
 __device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
   asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"
@@ -993,8 +1000,9 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
         m_ref = m;
       }
       if (any) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const float lse = l > 0.f ? (m_ref + lg2(l)) * kLn2 : -INFINITY;
+        // (a row without keys has l = 0; a NaN or a score of +inf makes l NaN, and the row)
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float lse = l == 0.f ? -INFINITY : (m_ref + lg2(l)) * kLn2;
         wa *= inv;
         wb *= inv;
         const size_t slot = pc.slot;
@@ -1105,7 +1113,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __g
       }
       float m = M;
 #pragma unroll
-      for (int k = 0; k < kMergeAtOnce; ++k) m = fmaxf(m, ls[k]);
+      for (int k = 0; k < kMergeAtOnce; ++k) m = max_nan(m, ls[k]);  // (a NaN piece makes the row NaN)
       if (m == -INFINITY) continue;
       const float old = ex2((M - m) * 1.4426950408889634f);
       M = m;
@@ -1131,7 +1139,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __g
         }
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     __syncthreads();  // (the rows of the unit before are out)
 #pragma unroll
     for (int i = 0; i < kMergeGroups; ++i)
@@ -1146,7 +1154,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __g
     }
     if (warp == 0 && live && a.lse) {
       const int tok = (sp.row0 + row) / a.G, g = (sp.row0 + row) - tok * a.G;
-      a.lse[(size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g] = sum > 0.f ? M + lg2(sum) * kLn2 : -INFINITY;
+      a.lse[(size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g] = sum == 0.f ? -INFINITY : M + lg2(sum) * kLn2;
     }
   }
 }
