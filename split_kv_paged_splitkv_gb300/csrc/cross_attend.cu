@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
         if (lane < np) {
           const int key = key0 + lane * br, lp = key / a.P;
           in = key - lp * a.P;
-          ph = __ldg(trow + lp);
+          ph = trow[lp];
           if (ph < 0 || ph >= a.num_pages) {
             if (a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
             ph = 0;

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
       if (!FP8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(qp) + ci + 4 * i) : make_uint4(0, 0, 0, 0);
+          const uint4 x = live ? reinterpret_cast<const uint4*>(qp)[ci + 4 * i] : make_uint4(0, 0, 0, 0);
           qf[rg][2 * i][0] = x.x;
           qf[rg][2 * i][1] = x.y;
           qf[rg][2 * i + 1][0] = x.z;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            x[i][e] = live ? __ldg(reinterpret_cast<const uint4*>(qp) + 2 * (ci + 4 * i) + e) : make_uint4(0, 0, 0, 0);
+            x[i][e] = live ? reinterpret_cast<const uint4*>(qp)[2 * (ci + 4 * i) + e] : make_uint4(0, 0, 0, 0);
             const uint32_t v[4] = {x[i][e].x, x[i][e].y, x[i][e].z, x[i][e].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
         ls[rg][e] = INFINITY;  // (a row that is none, or has no keys, weighs nothing)
         if (r < rph) {
           const int rt = r / a.G, rgq = r - rt * a.G;
-          const float v = __ldg(a.lse + (size_t(b) * a.T + rt) * a.Hq + size_t(h) * a.G + rgq);
+          const float v = a.lse[(size_t(b) * a.T + rt) * a.Hq + size_t(h) * a.G + rgq];
           if (v != -INFINITY) {
             ls[rg][e] = v * kLog2e;
             lim[rg][e] = L - a.T + rt;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
           tiles0 = tl;
           if (tl + lane < end) {
             const int lp = (tl + lane) * 16 / a.P, kp = (tl + lane) * 16 - lp * a.P;
-            int ph = __ldg(trow + lp);
+            int ph = trow[lp];
             if (ph < 0 || ph >= a.num_pages) {
               if (a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
               ph = 0;
