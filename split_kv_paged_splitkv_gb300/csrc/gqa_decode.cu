@@ -189,7 +189,7 @@ __device__ __forceinline__ void merge_and_store(const DecodeArgs& a, int tid, co
     }
   }
   float lse_n = -INFINITY;
-  const float osc = a.v_scale ? __ldg(a.v_scale + h0 + hs) : a.o_scale;
+  const float osc = a.v_scale ? a.v_scale[h0 + hs] : a.o_scale;
   // (lsum is a sum of at most a few million terms of at most 1: far below
   // the 2^126 where the fast divide loses range)
   const float inv = lsum > 0.f ? __fdividef(osc, lsum) : 0.f;
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(Gqa<FP8, HPI, NRG, NST>::THREADS, Gqa<FP8, HPI
       const int cnt = min(C::PT_CHUNK, pg_end - pc);
       __syncwarp();
       for (int x = lane; x < cnt; x += 32) {
-        int ph = __ldg(trow + pc + x);
+        int ph = trow[pc + x];
         if (ph < 0 || ph >= a.num_pages) {
           if (pw == 0) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
           ph = 0;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(Gqa<FP8, HPI, NRG, NST>::THREADS, Gqa<FP8, HPI
   const int hkv = h0 + hs;
   const int rph = a.T * a.G;           // query rows per KV head
   // scores -> log2 units: scale (and the e4m3 K scale, per KV head if given)
-  const float qk_l2 = a.k_scale ? a.qk_scale_log2 * __ldg(a.k_scale + hkv) : a.qk_scale_log2;
+  const float qk_l2 = a.k_scale ? a.qk_scale_log2 * a.k_scale[hkv] : a.qk_scale_log2;
   // Per query row of this lane's scores (rows 2ti, 2ti + 1 of the slot's row
   // group): qk_l2 times the inverse of the power of two the row's f16 query
   // fragments were scaled by (e4m3 path; 1 for bf16).
@@ -528,8 +528,8 @@ __global__ void __launch_bounds__(Gqa<FP8, HPI, NRG, NST>::THREADS, Gqa<FP8, HPI
                                   ((size_t(b) * a.T + t) * a.Hq + size_t(hkv) * a.G + g) * 128;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          qf[ks][0] = __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 2 * ti));
-          qf[ks][1] = __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 2 * ti + 8));
+          qf[ks][0] = *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 2 * ti);
+          qf[ks][1] = *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 2 * ti + 8);
         }
       } else {
 #pragma unroll
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(Gqa<FP8, HPI, NRG, NST>::THREADS, Gqa<FP8, HPI
         for (int ks = 0; ks < 8; ++ks) {
           // k = 2ti, 2ti+1 <-> d = 16ks+4ti, +1 ; k = 2ti+8, 2ti+9 <-> d = 16ks+4ti+2, +3
           // (the byte order of the e4m3 K operand, see the QK product below)
-          const uint2 raw = __ldg(reinterpret_cast<const uint2*>(qp + ks * 16 + 4 * ti));
+          const uint2 raw = *reinterpret_cast<const uint2*>(qp + ks * 16 + 4 * ti);
           f[ks][0] = __uint_as_float(raw.x << 16);
           f[ks][1] = __uint_as_float(raw.x & 0xffff0000u);
           f[ks][2] = __uint_as_float(raw.y << 16);

@@ -189,7 +189,7 @@ struct PageWalk {
       const int my = chunk0 + lane;
       phys = 0;
       if (my < p1) {
-        phys = __ldg(trow + my);
+        phys = trow[my];
         if (phys < 0 || phys >= a.num_pages) {
           if (report) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
           phys = 0;
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
         float amax = 0.f;
 #pragma unroll 4
         for (int v = 0; v < C::DK / 8; ++v) {
-          const uint4 x = __ldg(qrow + v);
+          const uint4 x = qrow[v];
           const uint32_t wv[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
         uint32_t w[32];
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
-          const uint4 x = __ldg(src + v);
+          const uint4 x = src[v];
           w[4 * v] = cvt(x.x);
           w[4 * v + 1] = cvt(x.y);
           w[4 * v + 2] = cvt(x.z);
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
         uint8_t* dst = sm + C::OFF_Q + k * C::Q_CH + r * 128;
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
-          const uint4 x = __ldg(src + v);
+          const uint4 x = src[v];
           *reinterpret_cast<uint4*>(dst + ((v ^ (r & 7)) << 4)) =
               make_uint4(cvt(x.x), cvt(x.y), cvt(x.z), cvt(x.w));
         }

@@ -20,3 +20,12 @@ def test_no_read_only_loads_beside_a_running_writer(name):
     text = code(name)
     assert "wait_prerequisites" in text
     assert not re.search(r"__ldg\s*\(|ld\.global\.nc|__restrict__", text)
+
+
+@pytest.mark.parametrize("name", ["gqa_decode.cu", "mla_decode.cu"])
+def test_the_decode_reads_its_inputs_with_plain_loads(name):
+    """The append that turned the queries may be the kernel before, and lets the decode start before it has written
+    them."""
+    text = code(name)
+    assert "wait_prerequisites" in text
+    assert not re.search(r"__ldg\s*\(|ld\.global\.nc", text)
