@@ -597,9 +597,9 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
  *                NULL.  A token of a sequence without keys gets out = 0 and
  *                lse = -inf.  A row with a NaN or +inf among its scores gets NaN
  *                in both
- *   workspace    splitkv_cross_workspace_size bytes (0: may be NULL; 40 MB at
- *                most), 16-byte aligned, used by this call alone until it has
- *                finished
+ *   workspace    splitkv_cross_workspace_size bytes (0: may be NULL; 40,161,536
+ *                at most), 16-byte aligned, used by this call alone until it
+ *                has finished
  * A length outside [0, max_pages_per_seq * P] sets SPLITKV_DEVERR_SEQLEN and
  * counts as 0; a page id out of range sets SPLITKV_DEVERR_PAGE (page 0 is read
  * in its place).  One kernel or two.

@@ -126,3 +126,23 @@ def test_one_row_may_be_longer():
                                      (call_evict, "weights_in", (200,), FLOAT), (call_cross, "block_table", (64,), INT)):
         with pytest.raises(ValueError, match=f"{name} is not on the current CUDA device"):
             call(d, **{name: torch.zeros(shape, dtype=dtype)})
+
+
+# ------------------------------------------------------------------ the documented bound of a workspace
+
+def test_cross_workspace_bound():
+    """No call needs more than the header says, and some need all of it."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "splitkv.h")) as f:
+        bound = re.search(r"splitkv_cross_workspace_size bytes \(0: may be NULL;\s*\*?\s*([\d,]+)\s*\*?\s*at\s*\*?\s*most\)", f.read())
+    assert bound, "the header names the bound in bytes"
+    most = 0
+    for kv in (1, 2, 8, 16, 608, 65535):
+        for group in (1, 4, 32, 300):
+            for batch in (1, 3, 600, 5000):
+                d = desc(B=batch, Hq=kv * group, Hkv=kv, maxp=1 << 12, N=16)
+                for n in (1, 5, 128, 4000, 1 << 17):
+                    most = max(most, skv.splitkv_cross_workspace_size(d, n))
+    assert most == int(bound.group(1).replace(",", ""))
