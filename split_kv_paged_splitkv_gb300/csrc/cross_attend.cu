@@ -106,15 +106,16 @@ __device__ __forceinline__ int keys_of(const CrossArgs& a, int b) {
   return L >= 0 && L <= int64_t(a.max_pages) * a.P ? L : 0;
 }
 
-// First token and number of tokens of sequence b, within [0, n_tokens].
+// First token and number of tokens of sequence b, within [0, n_tokens] whatever the
+// offsets are.
 __device__ __forceinline__ int tokens_of(const CrossArgs& a, int b, int* first) {
   if (!a.cu) {
     *first = b * a.T;
     return a.T;
   }
-  const int t0 = min(max(a.cu[b], 0), a.n_tokens), t1 = min(a.cu[b + 1], a.n_tokens);
+  const int t0 = min(max(a.cu[b], 0), a.n_tokens), t1 = min(max(a.cu[b + 1], t0), a.n_tokens);
   *first = t0;
-  return max(t1 - t0, 0);
+  return t1 - t0;
 }
 
 // Key blocks of an item over n_keys keys; an item without keys counts as one
