@@ -128,6 +128,11 @@ struct Piece {
   int slot;                                    // of its partial result; -1: the whole item
 };
 constexpr int kMaxPieces = 4;  // of a CTA
+// Where the plan stops counting a KV head's pieces.  A call's items are at most
+// kMaxPieces * kSmCount, cut into 32 each; offsets out of order may give every
+// sequence all tokens, and a wrapped count would pass for one that fits.
+constexpr int kManyPieces = 32767;
+static_assert(kMaxPieces * kSmCount * 32 <= kManyPieces && int64_t(kManyPieces) * 65535 < (int64_t(1) << 31), "no call's count");
 constexpr int kPieceCost = 2, kCutCost = 2;  // in key blocks: of each piece, and of cutting anything
 constexpr int kLineCost = 8;  // and of a line of all key blocks
 
@@ -360,7 +365,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail& 
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     if (a.batch > 32) read(b0);
     for (int i = 0; i < min(32, a.batch - b0); ++i)
-      n += __shfl_sync(kFull, mine.tiles, i) * cuts_of(__shfl_sync(kFull, mine.nb, i), t);
+      n = min(n + __shfl_sync(kFull, mine.tiles, i) * cuts_of(__shfl_sync(kFull, mine.nb, i), t), kManyPieces);
   }
   n *= a.Hkv;
   // (cut pieces have a slot each; uncut items need none)

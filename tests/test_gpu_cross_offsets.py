@@ -82,3 +82,15 @@ def test_wrong_offsets_write_nothing_else(deal):
     state = dict(k=c.k, v=c.v, table=c.table, lens=c.lens, most=float(c.v.abs().max()))
     for cu in offsets(counts, n, np.random.default_rng(6)):
         run(c.desc, state, q, cu)
+
+
+def test_more_pieces_than_32_bits_count():
+    """One token, which the offsets give to every other one of 240,000 sequences of 608 heads: 2.3e9 pieces if each is cut
+    into 32."""
+    B, heads, P = 240000, 608, 4112  # 33 key blocks
+    k = torch.randn((1, heads, P, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.rand((1, heads, P, 128), device="cuda").to(torch.bfloat16)
+    state = dict(k=k, v=v, table=torch.zeros((B, 1), dtype=torch.int32, device="cuda"),
+                 lens=torch.full((B,), P, dtype=torch.int32, device="cuda"), most=1.0)
+    q = torch.randn((1, heads, 128), device="cuda").to(torch.bfloat16)
+    run(skv.make_desc(B, 1, heads, heads, 128, 128, P, 1, 1), state, q, np.arange(B + 1) % 2)
