@@ -36,7 +36,7 @@ size_t state_bytes(const splitkv_desc_t& d) {
 splitkv_status validate_cache(const splitkv_desc_t* d) {
   splitkv_status st = validate_shape(d);
   if (st != SPLITKV_OK) return st;
-  if (int64_t(d->max_pages_per_seq) * d->page_size > (int64_t(1) << 31) - 4096)
+  if (int64_t(d->max_pages_per_seq) * d->page_size > kMaxSlots)
     return fail(SPLITKV_EINVAL, "max_pages_per_seq * page_size must be at most 2^31 - 4096");
   const bool rows128 = d->qk_dim == 128 && d->v_dim == 128 && !d->v_shares_k;
   const bool latent = d->qk_dim == 576 && d->v_dim == 512 && d->num_kv_heads == 1;

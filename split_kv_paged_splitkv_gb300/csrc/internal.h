@@ -152,6 +152,8 @@ cudaError_t launch_mla_debug_gather(const TmaDesc& t, bool fp8, const int32_t* t
 
 // ---------------------------------------------------- cache operators
 
+// Key slots of a sequence, at most (the kernels round numbers of keys up in 32 bits).
+constexpr int64_t kMaxSlots = (int64_t(1) << 31) - 4096;
 constexpr int kMaxRotPairs = 64;  // rotated pairs of a head row
 constexpr int kMaxAxes = 4;       // position axes
 

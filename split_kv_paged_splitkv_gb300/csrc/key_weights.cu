@@ -73,10 +73,11 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
   wait_prerequisites();
 
   // tiles of the whole batch, then this warp's part [i0, i1)
+  static_assert(32 * ((kMaxSlots + 15) / 16) < int64_t(1) << 32, "32 sequences' tiles are added up in 32 bits, unsigned");
   int64_t total = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const int bl = b0 + lane;
-    int n = bl < a.batch ? (seq_len(a, bl, blockIdx.x == 0 && threadIdx.x < 32) + 15) >> 4 : 0;
+    uint32_t n = bl < a.batch ? (seq_len(a, bl, blockIdx.x == 0 && threadIdx.x < 32) + 15) >> 4 : 0;
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
     total += int64_t(n) * a.Hkv;
@@ -92,17 +93,17 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const __grid_c
   for (int b0 = 0; b < 0; b0 += 32) {
     const int bl = b0 + lane;
     const int n = bl < a.batch ? (seq_len(a, bl, false) + 15) >> 4 : 0;
-    int sum = n;  // tiles of a head, up to and with sequence bl
+    uint32_t sum = n;  // tiles of a head, up to and with sequence bl
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kFull, sum, o);
+      const uint32_t v = __shfl_up_sync(kFull, sum, o);
       if (lane >= o) sum += v;
     }
     const unsigned past = __ballot_sync(kFull, before + int64_t(sum) * a.Hkv > i0);
     if (past) {
       const int first = __ffs(past) - 1;
       const int per = __shfl_sync(kFull, n, first);
-      const int64_t at = i0 - before - int64_t(__shfl_sync(kFull, sum, first) - per) * a.Hkv;
+      const int64_t at = i0 - before - (int64_t(__shfl_sync(kFull, sum, first)) - per) * a.Hkv;
       b = b0 + first;
       h = int(at / per);
       tile = int(at - int64_t(h) * per);
