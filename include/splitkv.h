@@ -467,7 +467,8 @@ typedef struct splitkv_rope_s splitkv_rope_t;
  *   pairing        splitkv_rope_pairing
  *   base           freq_i = base^(-2 i / rot_dim), unless
  *   freqs_host     [rot_dim / 2] radians per position, or NULL (|f| < 1e6)
- * Angles are exact to 2^-31 half turns for every int32 position.  Free with
+ * Angles are right to 2^-25 half turns (1e-7 rad) for every int32 position and
+ * the frequencies as doubles.  Free with
  * splitkv_rope_destroy (NULL is ignored); a call holds its own copy.
  */
 splitkv_status splitkv_rope_create(int32_t rot_offset, int32_t rot_dim, int32_t n_axes,
@@ -583,7 +584,9 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
  * another length, without a causal mask: every token of sequence b attends to
  * all seq_lens[b] keys (an encoder's states, written once with
  * splitkv_append).  Any number of tokens per sequence, none, one (a decode
- * step) to whole prompts; with n_tokens = 0 nothing is done.
+ * step) to whole prompts; with n_tokens = 0 nothing is done.  For one token per
+ * sequence and up to 32 query rows per KV head splitkv_decode computes the same
+ * (its causal limit hides nothing then), in less time with a fitting split count.
  *   desc         the cache, bf16, qk_dim = v_dim = 128 (q_tokens counts only
  *                without cu_tokens; any number of query rows per KV head)
  *   cu_tokens    int32 [B + 1], not decreasing, within [0, n_tokens], or NULL:

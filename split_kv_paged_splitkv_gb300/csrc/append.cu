@@ -11,9 +11,10 @@
 // Angles.  A position times a frequency needs more digits than 32-bit
 // arithmetic has (2^20 * 1.0 rad leaves 2^-4 rad of it).  freq_i is held as a
 // fraction of a full turn in 64-bit fixed point, so position * freq modulo a
-// turn is one wrapping 64-bit product, off by at most |position| * 2^-65
-// turns; its top 32 bits, as a signed number of half turns in [-1, 1), go to
-// sincospif.  Rotation is in fp32, rounded once: to bf16, or to e4m3 after
+// turn is one wrapping 64-bit product, off by at most |position| * 3 * 2^-65
+// turns (the table's entries are added up from two rounded parts); its top 32
+// bits, as a signed number of half turns in [-1, 1) rounded to 24 bits (off by
+// 2^-25 half turns at most), go to sincospif.  Rotation is in fp32, rounded once: to bf16, or to e4m3 after
 // the division by the cache's scale.
 //
 // Bound: the bytes of q (read and written), k and v (read, and written in the

@@ -76,7 +76,7 @@ struct Cross {
   static constexpr int TAIL = 1536;              // barriers, plan
   static constexpr int SMEM = 1024 + OFF_BAR + TAIL;
   static constexpr int SOFTMAX_WARPS = 8;
-  // warps: the producers of K and of V, the issuer of the MMAs
+  // warps: two producers (a half of every K and V block each), the issuer of the MMAs
   static constexpr int PRODUCER = SOFTMAX_WARPS, ISSUER = SOFTMAX_WARPS + 2;
   static constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
   static constexpr uint32_t TMEM_COLS = 512, S_COL = 0, O_COL = 256;  // + 128 per row block
@@ -1083,8 +1083,8 @@ __global__ void __launch_bounds__(Cross::THREADS, 1)
 
 // Joins the partial results of the cut items (an item's pieces have consecutive
 // slots).  A unit is 32 rows of an item, a lane each; the CTAs take the units
-// of all cut items in turn (a CTA for every possible unit would be 2,432, whose
-// start alone takes 4 us).  A warp takes every eighth group of four dims, which
+// of all cut items in turn (a CTA for every possible unit would be 1,216, of which
+// most calls have no use).  A warp takes every eighth group of four dims, which
 // lie side by side for the rows; the log-sum-exps and results of four pieces
 // are loaded at once, and the sums rescaled when later ones are larger.
 constexpr int kMergeWarps = 8, kMergeAtOnce = 4, kMergeGroups = 32 / kMergeWarps;

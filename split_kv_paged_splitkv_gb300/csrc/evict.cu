@@ -25,9 +25,10 @@
 // row read and written once.  Many rows: the moves' bytes (32 sequences x 8
 // heads of up to 131k keys cut to 16k: 220 us, of which the moves take 150 at
 // 5.8 TB/s of scattered 256-byte rows; floor 136).  One sequence: the chain of
-// barriers and passes of the selection: a digit's exchange within the cluster
-// takes 2 us whatever its size (64k latent rows: 24.5 us, floor 2.2; 5.9k keys
-// of 2 heads: 12.3 us, of which two dependent launches take about 4).
+// barriers and passes of the selection: each of up to five passes over the ranks
+// is a chain of shared-memory reads and shuffles, and a digit's exchange within
+// the cluster takes 2 us whatever its size (64k latent rows: 24.1 us, floor 2.2;
+// 5.9k keys of 2 heads: 12.1 us, of which two dependent launches take about 4).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -600,7 +601,8 @@ cudaError_t launch_evict(const EvictArgs& a, void* stream) {
   if (e != cudaSuccess) return e;
   // CTAs per (sequence, head): one for each 2048 slots of capacity while the
   // groups do not fill the GPU, and one for each 32,768 slots in any case.
-  // 5.9k slots of 2 heads: 12.2 us with four, 14.1 with eight, 12.2 with one;
+  // 5.9k slots of 2 heads: 12.2 us with four, 14.1 with eight, and 12.2 with one
+  // too, whose longer passes cost what it saves in exchanges;
   // 64k slots of one: 24.1 with eight, 39 with four, 58 with two, and 2 more
   // with sixteen than with eight; 256 groups of 131k: 219.7 with four, 229 with
   // eight, 255 with two.

@@ -27,7 +27,7 @@ enum class Family { kGqa, kMla, kNone };
 Family family_of(const splitkv_desc_t& d);
 
 // KV heads one work item covers (consecutive, from the item's h_kv): for the
-// e4m3 GQA path with at most 8 query rows per head, 2 when Hkv is even (one
+// e4m3 GQA path with at most 16 query rows per head, 2 when Hkv is even (one
 // TMA box brings a 16-key tile of both), else 1; otherwise 1.
 int heads_per_item(const splitkv_desc_t& d);
 
@@ -224,7 +224,9 @@ struct EvictArgs {
   int32_t k_row, v_row;   // bytes of one key's row
 };
 
-constexpr int kSmCount = 152;  // SMs that cross attention plans for
+// SMs that cross attention plans for, and append's long calls.  (Where fewer are to
+// be had the grid takes a second round; results do not depend on it.)
+constexpr int kSmCount = 152;
 
 // A cut item of cross attention, for the merge: its number of pieces (0: none such),
 // the slot of the first, how far apart the others' are (1, or 2 from the even slot
