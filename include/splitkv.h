@@ -263,6 +263,9 @@ splitkv_status splitkv_plan_upload(const splitkv_plan_t* plan, void* workspace,
  *   lse          fp32 [B][T][Hq], natural-log LSE of the scaled scores; may be
  *                NULL
  *   workspace    uploaded with splitkv_plan_upload for this plan
+ * Attended keys and queries hold no NaN: a row that meets one in a key is NaN in
+ * `out`, but not in `lse`, which is that of the splits without it (-inf if there
+ * is none); a row with a NaN query may come out as one without keys.
  * Launches one kernel (FUSED) or two (SEPARATE, second with programmatic
  * dependent launch).
  */
