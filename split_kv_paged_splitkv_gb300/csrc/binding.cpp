@@ -50,12 +50,13 @@ struct Shape {
   // Whether a contiguous tensor has these elements where they are looked for: it
   // has no others, or its others are at the end, so that what lies apart by its
   // first dimension's stride are rows of the array.  (A buffer with room for more
-  // in another dimension has rows of another length.)
-  bool lies_in(const at::Tensor& t) const {
-    if (t.numel() == numel()) return true;
+  // in another dimension has rows of another length.)  `by_row`: without others,
+  // too, it has the array's rows or is flat.
+  bool lies_in(const at::Tensor& t, bool by_row) const {
     int64_t first = 0, has = 1, want = 1;
     while (first < t.dim() - 1 && t.size(first) == 1) ++first;
     for (int64_t k = t.dim() - 1; k > first; --k) has = times({has, t.size(k)});
+    if (t.numel() == numel() && (!by_row || has == 1)) return true;
     int outer = 0;
     while (outer < n - 1 && dim[outer] == 1) ++outer;
     for (int k = n - 1; k > outer; --k)
@@ -130,7 +131,7 @@ class Args {
   // A contiguous tensor that holds an array of `type` and `shape`, on the call's
   // device; addresses and None pass unchecked.
   template <class T>
-  T* tensor(const char* name, ScalarType type, const Shape& shape, int64_t device) {
+  T* tensor(const char* name, ScalarType type, const Shape& shape, int64_t device, bool by_row = false) {
     PyObject* x = next();
     if (!x) return nullptr;
     if (x == Py_None || PyLong_Check(x)) return static_cast<T*>(raw(x));
@@ -139,8 +140,8 @@ class Args {
     if (t->numel() < shape.numel())
       ok_ = wrong(PyExc_ValueError, "%s has %lld elements, the call needs %lld", name, (long long)t->numel(),
                   (long long)shape.numel());
-    else if (!shape.lies_in(*t))
-      ok_ = wrong(PyExc_ValueError, "%s has %lld elements, but not in %lld rows of %lld and more behind them", name,
+    else if (!shape.lies_in(*t, by_row))
+      ok_ = wrong(PyExc_ValueError, "%s has %lld elements, but does not begin with %lld rows of %lld", name,
                   (long long)t->numel(), (long long)shape.dim[0], (long long)shape.row());
     else if (on(name, *t, device))
       return static_cast<T*>(t->data_ptr());
@@ -282,7 +283,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const auto* rope = static_cast<const splitkv_rope_t*>(in.address());
     const int64_t axes = in.integer();
     const int64_t n = in.tokens(7, times({d.num_kv_heads, d.qk_dim}));
-    auto* positions = in.tensor<int32_t>("positions", kInt, {axes, n}, dev);
+    // ([n][axes], easily given instead, has as many elements)
+    auto* positions = in.tensor<int32_t>("positions", kInt, {axes, n}, dev, true);
     int64_t qs, ks, vs, os;
     void* q = in.rows("q", n, d.num_q_heads, d.qk_dim, dev, &qs);
     void* k = in.rows("k", n, d.num_kv_heads, d.qk_dim, dev, &ks);

@@ -146,3 +146,11 @@ def test_cross_workspace_bound():
                 for n in (1, 5, 128, 4000, 1 << 17):
                     most = max(most, skv.splitkv_cross_workspace_size(d, n))
     assert most == int(bound.group(1).replace(",", ""))
+
+
+@pytest.mark.parametrize("shape", [(4, 3), (2, 6), (6, 2), (12, 1, 1), (1, 4, 3)])
+def test_positions_go_by_axis(shape):
+    """[tokens][axes] has as many elements as [axes][tokens], in another order."""
+    taken = shape == (12, 1, 1)  # (no rows of its own: taken as it lies)
+    with pytest.raises(ValueError, match="positions is not on" if taken else "positions.*rows of"):
+        call_append(desc(**D), positions=torch.zeros(shape, dtype=INT), **AXES)
