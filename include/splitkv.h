@@ -407,7 +407,8 @@ enum {
   SPLITKV_DEVERR_TIMEOUT = 1,    /* a bounded wait on a shared-memory barrier gave up */
   SPLITKV_DEVERR_SEQLEN = 2,     /* device seq_lens differs from the plan's, or is not
                                     one the cache can hold                            */
-  SPLITKV_DEVERR_PAGE = 4        /* a block-table entry was outside [0, num_pages)    */
+  SPLITKV_DEVERR_PAGE = 4,       /* a block-table entry was outside [0, num_pages)    */
+  SPLITKV_DEVERR_PATH = 8        /* an accepted path does not rise within its tree    */
 };
 
 /*
@@ -439,7 +440,8 @@ splitkv_status splitkv_debug_gather(const splitkv_desc_t* desc, const void* page
  * and a position (int32), arrays [B][Hkv][max_pages_per_seq * P].  Entries at
  * or behind a sequence's length mean nothing.
  *
- * Pages that a call writes (append: those of the new keys; evict: those of
+ * Pages that a call writes (append: those of the new keys; tree_commit: those of
+ * the drafted keys; evict: those of
  * the first min(L, budget) keys) belong to one sequence: two sequences that
  * share such a page overwrite one another's keys.
  *
@@ -520,6 +522,44 @@ splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* 
                               const float* v_scale, void* q_out, int64_t q_out_stride,
                               void* k_pages, void* v_pages, float* key_weights,
                               int32_t* key_positions, int32_t* status, void* stream);
+
+/* Norms of splitkv_append_norm: rows divided by their root mean square. */
+typedef struct splitkv_norm {
+  const float* q_weight;  /* fp32 (device, 16-byte aligned), a factor for each column of
+                             a query head row, [128], or [Hq][128] with q_per_head;
+                             NULL: ones                                         */
+  const float* k_weight;  /* the same for key rows: [128] or [Hkv][128]; [512] for
+                             latent rows                                        */
+  float eps;              /* positive                                           */
+  int32_t norm_q, norm_k; /* which rows are normalised                          */
+  int32_t q_per_head, k_per_head;
+} splitkv_norm_t;
+
+/*
+ * splitkv_append_norm -- splitkv_append of query and key rows that are normalised
+ * first, each head row x by itself:
+ *
+ *     x_i * w_i / sqrt(mean_i(x_i^2) + eps)
+ *
+ * then rotated and stored, with one rounding at the end.  Of latent rows (qk_dim
+ * 576) the key's first 512 columns are normalised, whatever is rotated, and queries
+ * are not (EUNSUPPORTED with norm_q).  Values are stored as they are.  A row's sum
+ * of squares is held in fp32: components up to 2^59 in magnitude.
+ *   norm    which rows, their weights (host struct; the weights may be written by
+ *           the kernel before)
+ *   others  as splitkv_append
+ * EINVAL for a weight of rows that are not normalised, and for an eps that is not
+ * positive and finite.
+ */
+splitkv_status splitkv_append_norm(const splitkv_desc_t* desc, const splitkv_norm_t* norm,
+                                   const splitkv_rope_t* rope, int32_t n_tokens,
+                                   const int32_t* cu_tokens, const int32_t* positions,
+                                   const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, const int32_t* block_table,
+                                   const int32_t* seq_lens, float kv_scale, const float* k_scale,
+                                   const float* v_scale, void* q_out, int64_t q_out_stride,
+                                   void* k_pages, void* v_pages, float* key_weights,
+                                   int32_t* key_positions, int32_t* status, void* stream);
 
 /*
  * splitkv_key_weights -- how much attention every cached key got from the
@@ -618,6 +658,35 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
                                     const int32_t* block_table, const int32_t* seq_lens,
                                     float scale, void* out, float* lse, void* workspace,
                                     size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * splitkv_tree_commit -- keeps the accepted tokens of a drafted tree.  The last T_b
+ * of sequence b's L = seq_lens[b] keys are those of its drafted tokens, token i in
+ * slot L - T_b + i (as splitkv_append stored them).  With the accepted path p_0 <
+ * p_1 < ... < p_(n-1), n = path_lens[b], the keys and values of the tokens p_i (and
+ * their state) move to slots L - T_b + i, in place, and the sequence's length
+ * becomes L - T_b + n.  What lies behind it means nothing.
+ *   desc         the cache (q_tokens counts only without cu_tokens; qk_dim = v_dim =
+ *                128, or the latent rows)
+ *   path         int32 [B][max_path], numbers of drafted tokens within [0, T_b),
+ *                rising; entries from path_lens[b] on are not looked at
+ *   path_lens    int32 [B], 0 .. min(T_b, max_path)
+ *   cu_tokens    int32 [B + 1], T_b = cu_tokens[b + 1] - cu_tokens[b], or NULL:
+ *                q_tokens for every sequence
+ *   key_weights, key_positions  state arrays or NULL
+ *   seq_lens_out int32 [B]: the new lengths; may be seq_lens
+ * A sequence of length 0 stays as it is.  A length outside [0, max_pages_per_seq *
+ * P], or below T_b, sets SPLITKV_DEVERR_SEQLEN, a path that does not rise within
+ * [0, T_b) or is longer than max_path SPLITKV_DEVERR_PATH: the sequence and its
+ * length stay as they are.  A page id out of range sets SPLITKV_DEVERR_PAGE and the
+ * row that it would hold, or that it should come from, is not moved.  One kernel.
+ */
+splitkv_status splitkv_tree_commit(const splitkv_desc_t* desc, int32_t max_path, const int32_t* path,
+                                   const int32_t* path_lens, const int32_t* cu_tokens, void* k_pages,
+                                   void* v_pages, const int32_t* block_table,
+                                   const int32_t* seq_lens, float* key_weights,
+                                   int32_t* key_positions, int32_t* seq_lens_out, int32_t* status,
+                                   void* stream);
 
 /* Thread-local description of the last error returned on this thread. */
 const char* splitkv_last_error(void);

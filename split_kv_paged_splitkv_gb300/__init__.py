@@ -28,7 +28,7 @@ SPLITKV_COMBINE_FUSED, SPLITKV_COMBINE_SEPARATE = 0, 1
 SPLITKV_LAYOUT_HND, SPLITKV_LAYOUT_NHD = 0, 1
 SPLITKV_ITEM_FIELDS = 8
 SPLITKV_RANGE_FIELDS = 5
-SPLITKV_DEVERR_TIMEOUT, SPLITKV_DEVERR_SEQLEN, SPLITKV_DEVERR_PAGE = 1, 2, 4
+SPLITKV_DEVERR_TIMEOUT, SPLITKV_DEVERR_SEQLEN, SPLITKV_DEVERR_PAGE, SPLITKV_DEVERR_PATH = 1, 2, 4, 8
 SPLITKV_ROPE_HALVES, SPLITKV_ROPE_NEIGHBOURS = 0, 1
 ITEM_FIELD_NAMES = ("b", "h_kv", "split", "num_splits", "page_begin", "page_end", "slot", "group")
 
@@ -38,6 +38,12 @@ class splitkv_desc_t(ctypes.Structure):
         "batch", "q_tokens", "num_q_heads", "num_kv_heads", "qk_dim", "v_dim", "page_size",
         "max_pages_per_seq", "num_pages_total", "kv_dtype", "v_shares_k", "combine_mode",
         "kv_layout")]
+
+
+class splitkv_norm_t(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("norm_q", ctypes.c_int32), ("norm_k", ctypes.c_int32), ("q_per_head", ctypes.c_int32),
+                ("k_per_head", ctypes.c_int32)]
 
 
 class SplitKVError(RuntimeError):
@@ -79,6 +85,9 @@ _SIGNATURES = {
     "splitkv_append": (_i32, [ctypes.POINTER(splitkv_desc_t), _vp, _i32, _vp, _vp, _vp, _i64, _vp, _i64,
                               _vp, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
                               _vp]),
+    "splitkv_append_norm": (_i32, [ctypes.POINTER(splitkv_desc_t), ctypes.POINTER(splitkv_norm_t), _vp, _i32, _vp,
+                                   _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _vp,
+                                   _vp, _vp, _vp, _vp, _vp]),
     "splitkv_key_weights": (_i32, [ctypes.POINTER(splitkv_desc_t), _vp, _vp, _vp, _vp, _vp, _f32, _f32,
                                    _vp, _f32, _vp, _vp, _vp, _vp]),
     "splitkv_evict_workspace_size": (_sz, [ctypes.POINTER(splitkv_desc_t), _i32]),
@@ -87,6 +96,8 @@ _SIGNATURES = {
     "splitkv_cross_workspace_size": (_sz, [ctypes.POINTER(splitkv_desc_t), _i32]),
     "splitkv_cross_attend": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, _vp, _vp, _i64, _vp, _vp, _vp,
                                     _vp, _f32, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "splitkv_tree_commit": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _vp, _vp]),
     "splitkv_last_error": (ctypes.c_char_p, []),
 }
 
@@ -365,6 +376,21 @@ def splitkv_append(desc: splitkv_desc_t, rope, positions, q, k, v, block_table, 
                     k_scale, v_scale, key_weights, key_positions, status, _stream(stream, dev)))
 
 
+def splitkv_append_norm(desc: splitkv_desc_t, rope, positions, q, k, v, block_table, seq_lens, q_out,
+                        k_pages, v_pages, norm_q: bool = True, norm_k: bool = True, q_weight=None,
+                        k_weight=None, eps: float = 1e-6, cu_tokens=None, kv_scale: float = 1.0,
+                        k_scale=None, v_scale=None, key_weights=None, key_positions=None, status=None,
+                        n_tokens=None, stream=None):
+    """splitkv_append of rows that are first divided by their root mean square: the query head rows with
+    ``norm_q``, the key rows with ``norm_k`` (of latent rows, whose queries are not normalised, the first
+    512 columns).  Weights are fp32 ``[columns]`` or ``[heads][columns]``."""
+    b, dev = _call()
+    _check(b.append_norm(dev, desc, None if rope is None else rope.handle, 1 if rope is None else rope.n_axes, n_tokens,
+                         positions, q, k, v, block_table, seq_lens, q_out, k_pages, v_pages, cu_tokens, kv_scale,
+                         k_scale, v_scale, key_weights, key_positions, status, _stream(stream, dev), int(norm_q),
+                         int(norm_k), q_weight, k_weight, eps))
+
+
 def splitkv_key_weights(desc: splitkv_desc_t, q, k_pages, block_table, seq_lens, lse, scale: float,
                         kv_scale: float, decay: float, weights_in, weights_out, k_scale=None,
                         status=None, stream=None):
@@ -400,6 +426,20 @@ def splitkv_cross_attend(desc: splitkv_desc_t, cu_tokens, q, k_pages, v_pages, b
     b, dev = _call()
     _check(b.cross_attend(dev, desc, n_tokens, cu_tokens, q, k_pages, v_pages, block_table, seq_lens, scale, out,
                           lse, workspace, workspace_bytes, status, _stream(stream, dev)))
+
+
+def splitkv_tree_commit(desc: splitkv_desc_t, path, path_lens, k_pages, v_pages, block_table, seq_lens,
+                        seq_lens_out, cu_tokens=None, key_weights=None, key_positions=None, status=None,
+                        max_path=None, stream=None):
+    """Keeps the drafted tokens ``path`` ``[B][max_path]`` (the first ``path_lens[b]`` of a row) of every
+    sequence.  ``max_path`` is needed only where ``path`` is an address."""
+    b, dev = _call()
+    if max_path is None:
+        if path is None or isinstance(path, int):
+            raise TypeError("max_path is needed where path is an address")
+        max_path = path.shape[-1]
+    _check(b.tree_commit(dev, desc, max_path, path, path_lens, k_pages, v_pages, block_table, seq_lens, seq_lens_out,
+                         cu_tokens, key_weights, key_positions, status, _stream(stream, dev)))
 
 
 def splitkv_last_error() -> str:

@@ -24,6 +24,14 @@
 // 6.8: rows of 256 bytes go to as many places); one token 3.2 us, 32 in e4m3
 // 3.7, of which a launch is most.
 //
+// With norms (splitkv_append_norm) the query and key rows are first divided by
+// their root mean square and multiplied by a weight for each column:
+//     x_i <- x_i * rsqrt(mean(x^2) + eps) * w_i,
+// all in fp32, so that norm, rotation and store round once.  The mean of a row of
+// 128 is a sum over the eight lanes that hold its units; a latent row's 36 units
+// lie across warps, so a warp adds up its 512 columns by itself while the token's
+// place is looked up (1 KB read again, beside the 147 KB of the token's queries).
+//
 // One thread handles 32-byte units (two 16-byte chunks of a head row, the
 // two halves of the same eight pairs where pairs are half a row apart), so
 // every load and store is 16 bytes wide; a CTA computes the sines and cosines
@@ -82,10 +90,28 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int n, int
   return ended < batch && cu[0] <= n ? ended : -1;
 }
 
+// f * factor * weight, the weight of chunk c of its row (null: ones).
+__device__ __forceinline__ void normed(float (&f)[8], float factor, const float* weight, int c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] *= factor;
+  if (weight == nullptr) return;
+  const float4 lo = reinterpret_cast<const float4*>(weight)[2 * c], hi = reinterpret_cast<const float4*>(weight)[2 * c + 1];
+  const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] *= w[e];
+}
+
+__device__ __forceinline__ float squares(const float (&f)[8]) {
+  float x = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x = fmaf(f[e], f[e], x);
+  return x;
+}
+
 constexpr int kPasses = 5;  // over a CTA's units, at most
 
-// U: units of a thread in flight.
-template <int DK, int DV, bool FP8, int U>
+// U: units of a thread in flight.  NORM: rows may be normalised (a.norm_q, a.norm_k).
+template <int DK, int DV, bool FP8, int U, bool NORM>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a,
                                                           int tok_per_cta) {
   constexpr int UK = DK / 16, UV = DV / 16;  // units of a q or k row, of a v row
@@ -93,6 +119,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   // Cosines and sines of two pairs of a chunk to a float4 (c, c, s, s), the
   // chunks of a row side by side: its lanes read consecutive 16 bytes.
   __shared__ float4 cs[kMaxTok * kMaxRotPairs / 2];
+  constexpr bool LATENT = DK != DV;           // rows of 576: the first DV columns of the keys are normalised
+  __shared__ float factor[NORM && LATENT ? kMaxTok : 1];  // of the tokens' latent rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   launch_dependents();
@@ -196,6 +224,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
           if (err && lane == 0 && a.status && blockIdx.y == 0) atomicOr(a.status, err);
         }
         if (lane == 0) tok[i] = t;
+        if (NORM && LATENT && a.norm_k) {
+          const uint4* src = reinterpret_cast<const uint4*>(k + int64_t(i) * int(a.k_stride));
+          float x = 0.f;
+#pragma unroll
+          for (int c = 0; c < DV / 8; c += 32) {
+            float f[8];
+            unpack8(src[c + lane], f);
+            x += squares(f);
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+          if (lane == 0) factor[i] = rsqrtf(fmaf(x, 1.f / DV, a.eps));
+        }
       }
       for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
         const int t = i / half, p = i - t * half;
@@ -229,6 +270,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       float f0[8], f1[8];
       unpack8(x0[r], f0);
       unpack8(x1[r], f1);
+      if (NORM && LATENT) {
+        if (kind == 1 && a.norm_k) {
+          if (c0 < DV / 8) normed(f0, factor[t], a.k_weight, c0);
+          if (c1 < DV / 8) normed(f1, factor[t], a.k_weight, c1);
+        }
+      } else if (NORM && kind < 2 && (kind ? a.norm_k : a.norm_q)) {
+        // (a row's units are eight neighbouring lanes', none of which or all are here)
+        float x = squares(f0) + squares(f1);
+#pragma unroll
+        for (int o = 4; o; o >>= 1) x += __shfl_xor_sync(0xffu << (lane & 24), x, o);
+        x = rsqrtf(fmaf(x, 1.f / DK, a.eps));
+        const float* w = kind ? a.k_weight : a.q_weight;
+        if (w && (kind ? a.k_per_head : a.q_per_head)) w += row * DK;
+        normed(f0, x, w, c0);
+        normed(f1, x, w, c1);
+      }
       if (kind < 2 && rotc) {
         const float4* w = cs + t * (kMaxRotPairs / 2);
         auto turn = [](float& u, float& v, float c, float s) {
@@ -290,7 +347,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
 }
 
-template <int DK, int DV, bool FP8, int U>
+template <int DK, int DV, bool FP8, int U, bool NORM>
 cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s) {
   AppendArgs a = args;
   // i * magic >> 32 is i / per_tok for every unit i of a CTA, as i * per_tok is
@@ -327,7 +384,7 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
   la[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = la;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<DK, DV, FP8, U>, a, tpc);
+  return cudaLaunchKernelEx(&cfg, append_kernel<DK, DV, FP8, U, NORM>, a, tpc);
 }
 
 // A call of few tokens takes one unit per thread, to use more of the GPU's
@@ -336,20 +393,26 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
 // 100, with four 137).
 constexpr int64_t kFewUnits = 1 << 17;
 
-template <int DK, int DV, bool FP8>
+template <int DK, int DV, bool FP8, bool NORM>
 cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t s) {
   const int per_tok = (a.q ? a.Hq * (DK / 16) : 0) + a.Hkv * (DK / 16 + (a.v ? DV / 16 : 0));
-  return int64_t(per_tok) * a.n_tokens <= kFewUnits ? launch_append_u<DK, DV, FP8, 1>(a, per_tok, s)
-                                                    : launch_append_u<DK, DV, FP8, 2>(a, per_tok, s);
+  return int64_t(per_tok) * a.n_tokens <= kFewUnits ? launch_append_u<DK, DV, FP8, 1, NORM>(a, per_tok, s)
+                                                    : launch_append_u<DK, DV, FP8, 2, NORM>(a, per_tok, s);
+}
+
+template <bool NORM>
+cudaError_t launch_append_n(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, cudaStream_t s) {
+  if (qk_dim == 128 && v_dim == 128)
+    return fp8 ? launch_append_t<128, 128, true, NORM>(a, s) : launch_append_t<128, 128, false, NORM>(a, s);
+  return fp8 ? launch_append_t<576, 512, true, NORM>(a, s) : launch_append_t<576, 512, false, NORM>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (qk_dim == 128 && v_dim == 128)
-    return fp8 ? launch_append_t<128, 128, true>(a, s) : launch_append_t<128, 128, false>(a, s);
-  return fp8 ? launch_append_t<576, 512, true>(a, s) : launch_append_t<576, 512, false>(a, s);
+  return a.norm_q || a.norm_k ? launch_append_n<true>(a, qk_dim, v_dim, fp8, s)
+                              : launch_append_n<false>(a, qk_dim, v_dim, fp8, s);
 }
 
 }  // namespace splitkv

@@ -165,6 +165,22 @@ class Args {
     }
     return nullptr;
   }
+  // A norm's weights: contiguous fp32 [columns], or [heads][columns] (`per_head`); an
+  // address is of the first kind.
+  const float* weight(const char* name, int64_t heads, int64_t columns, int64_t device, int32_t* per_head) {
+    PyObject* x = next();
+    if (!x) return nullptr;
+    if (x == Py_None || PyLong_Check(x)) return static_cast<const float*>(raw(x));
+    const at::Tensor* t = typed(name, x, ScalarType::Float);
+    if (!t) return nullptr;
+    *per_head = t->dim() == 2;
+    if (!(t->dim() == 1 || (t->dim() == 2 && t->size(0) == heads)) || t->size(t->dim() - 1) != columns)
+      ok_ = wrong(PyExc_ValueError, "%s must be a float tensor [%lld] or [%lld][%lld]", name, (long long)columns,
+                  (long long)heads, (long long)columns);
+    else if (on(name, *t, device))
+      return static_cast<const float*>(t->data_ptr());
+    return nullptr;
+  }
   // The tokens of a bf16 tensor (`per_token` elements each), or of an argument
   // that says so where it is an address.  Looks ahead: nothing is taken.
   int64_t tokens(int tensor_at, int64_t per_token) {
@@ -274,8 +290,9 @@ int call(F&& f) {
 
 constexpr ScalarType kInt = ScalarType::Int, kFloat = ScalarType::Float;
 
-PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  Args in(a, n_args, 22);
+// append, and append_norm, whose norm follows (norm_q, norm_k, q_weight, k_weight, eps).
+PyObject* append_any(PyObject* const* a, Py_ssize_t n_args, bool with_norm) {
+  Args in(a, n_args, with_norm ? 27 : 22);
   return guarded(in, [&]() -> int {
     const int64_t dev = in.integer();
     const Sizes z = in.desc();
@@ -302,13 +319,28 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     auto* key_positions = in.tensor<int32_t>("key_positions", kInt, z.state, dev);
     auto* status = in.tensor<int32_t>("status", kInt, {1}, dev);
     void* stream = in.address();
+    splitkv_norm_t norm{};
+    if (with_norm) {
+      norm.norm_q = in.int32("norm_q");
+      norm.norm_k = in.int32("norm_k");
+      norm.q_weight = in.weight("q_weight", d.num_q_heads, d.qk_dim == 576 ? d.v_dim : d.qk_dim, dev, &norm.q_per_head);
+      norm.k_weight = in.weight("k_weight", d.num_kv_heads, d.qk_dim == 576 ? d.v_dim : d.qk_dim, dev, &norm.k_per_head);
+      norm.eps = in.real();
+    }
     if (!in.ok()) return 0;
     return call([&] {
-      return splitkv_append(&d, rope, int32_t(n), cu, positions, q, qs, k, ks, v, vs, table, lens, kv_scale, k_scale,
-                            v_scale, q_out, os, k_pages, v_pages, weights, key_positions, status, stream);
+      return with_norm ? splitkv_append_norm(&d, &norm, rope, int32_t(n), cu, positions, q, qs, k, ks, v, vs, table, lens,
+                                             kv_scale, k_scale, v_scale, q_out, os, k_pages, v_pages, weights,
+                                             key_positions, status, stream)
+                       : splitkv_append(&d, rope, int32_t(n), cu, positions, q, qs, k, ks, v, vs, table, lens, kv_scale,
+                                        k_scale, v_scale, q_out, os, k_pages, v_pages, weights, key_positions, status,
+                                        stream);
     });
   });
 }
+
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n_args) { return append_any(a, n_args, false); }
+PyObject* append_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args) { return append_any(a, n_args, true); }
 
 PyObject* key_weights(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   Args in(a, n_args, 15);
@@ -392,8 +424,37 @@ PyObject* cross_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  Args in(a, n_args, 15);
+  return guarded(in, [&]() -> int {
+    const int64_t dev = in.integer();
+    const Sizes z = in.desc();
+    const splitkv_desc_t& d = z.d;
+    const int32_t max_path = in.int32("max_path");
+    // (a wider array has rows of another length)
+    auto* path = in.tensor<int32_t>("path", kInt, {d.batch, max_path}, dev, true);
+    auto* path_lens = in.tensor<int32_t>("path_lens", kInt, {d.batch}, dev);
+    void* k_pages = in.tensor<void>("k_pages", z.pool, z.k_pool, dev);
+    void* v_pages = in.tensor<void>("v_pages", z.pool, z.v_pool, dev);
+    auto* table = in.tensor<int32_t>("block_table", kInt, z.table, dev);
+    auto* lens = in.tensor<int32_t>("seq_lens", kInt, {d.batch}, dev);
+    auto* lens_out = in.tensor<int32_t>("seq_lens_out", kInt, {d.batch}, dev);
+    auto* cu = in.tensor<int32_t>("cu_tokens", kInt, {int64_t(d.batch) + 1}, dev);
+    auto* weights = in.tensor<float>("key_weights", kFloat, z.state, dev);
+    auto* positions = in.tensor<int32_t>("key_positions", kInt, z.state, dev);
+    auto* status = in.tensor<int32_t>("status", kInt, {1}, dev);
+    void* stream = in.address();
+    if (!in.ok()) return 0;
+    return call([&] {
+      return splitkv_tree_commit(&d, max_path, path, path_lens, cu, k_pages, v_pages, table, lens, weights, positions,
+                                 lens_out, status, stream);
+    });
+  });
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {FAST(append), FAST(key_weights), FAST(evict), FAST(cross_attend), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef kMethods[] = {FAST(append), FAST(append_norm), FAST(key_weights), FAST(evict), FAST(cross_attend),
+                          FAST(tree_commit), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,5 +1,5 @@
-// C-ABI layer of the cache operators: append with rotary positions, key
-// weights, eviction, cross attention.  Argument validation, workspace layout, launches.
+// C-ABI layer of the cache operators: append with norms and rotary positions, key
+// weights, eviction, cross attention, the commit of drafted trees.  Argument validation, workspace layout, launches.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -168,14 +168,14 @@ splitkv_status splitkv_rope_create(int32_t rot_offset, int32_t rot_dim, int32_t 
 
 void splitkv_rope_destroy(splitkv_rope_t* rope) { delete rope; }
 
-splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* rope,
-                              int32_t n_tokens, const int32_t* cu_tokens, const int32_t* positions,
-                              const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                              const void* v, int64_t v_stride, const int32_t* block_table,
-                              const int32_t* seq_lens, float kv_scale, const float* k_scale,
-                              const float* v_scale, void* q_out, int64_t q_out_stride,
-                              void* k_pages, void* v_pages, float* key_weights,
-                              int32_t* key_positions, int32_t* status, void* stream) {
+static splitkv_status append(const splitkv_desc_t* desc, const splitkv_norm_t* norm, const splitkv_rope_t* rope,
+                             int32_t n_tokens, const int32_t* cu_tokens, const int32_t* positions,
+                             const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const int32_t* block_table,
+                             const int32_t* seq_lens, float kv_scale, const float* k_scale,
+                             const float* v_scale, void* q_out, int64_t q_out_stride,
+                             void* k_pages, void* v_pages, float* key_weights,
+                             int32_t* key_positions, int32_t* status, void* stream) {
   splitkv_status st = validate_cache(desc);
   if (st != SPLITKV_OK) return st;
   const splitkv_desc_t& d = *desc;
@@ -183,6 +183,16 @@ splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* 
   if (n_tokens < 0) return fail(SPLITKV_EINVAL, "n_tokens must be >= 0");
   if (!cu_tokens && int64_t(d.batch) * d.q_tokens != n_tokens)
     return fail(SPLITKV_EINVAL, "without cu_tokens, n_tokens (%d) must be batch * q_tokens", n_tokens);
+  if (norm) {
+    if ((norm->norm_q || norm->norm_k) && !(norm->eps > 0.f && norm->eps < 1e30f))
+      return fail(SPLITKV_EINVAL, "eps must be positive and finite");
+    if ((norm->q_weight && !norm->norm_q) || (norm->k_weight && !norm->norm_k))
+      return fail(SPLITKV_EINVAL, "a weight is given for rows that are not normalised");
+    if (norm->norm_q && d.qk_dim != 128)
+      return fail(SPLITKV_EUNSUPPORTED, "queries of latent caches are not normalised (norm_q must be 0)");
+    if (misaligned(norm->q_weight, 16) || misaligned(norm->k_weight, 16))
+      return fail(SPLITKV_EINVAL, "the weights of the norms must be 16-byte aligned");
+  }
   if (n_tokens == 0) return SPLITKV_OK;
   if (!k || !block_table || !seq_lens || !k_pages)
     return fail(SPLITKV_EINVAL, "k, block_table, seq_lens and k_pages must not be NULL");
@@ -245,9 +255,46 @@ splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* 
   a.num_pages = d.num_pages_total;
   a.nhd = d.kv_layout == SPLITKV_LAYOUT_NHD;
   if (rope) a.rope = *rope;
+  if (norm) {
+    a.norm_q = q && norm->norm_q;
+    a.norm_k = norm->norm_k;
+    a.q_weight = norm->q_weight;
+    a.k_weight = norm->k_weight;
+    a.q_per_head = norm->q_per_head;
+    a.k_per_head = norm->k_per_head;
+    a.eps = norm->eps;
+  }
   cudaError_t e = launch_append(a, d.qk_dim, d.v_dim, fp8, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launching the append kernel");
   return SPLITKV_OK;
+}
+
+splitkv_status splitkv_append(const splitkv_desc_t* desc, const splitkv_rope_t* rope,
+                              int32_t n_tokens, const int32_t* cu_tokens, const int32_t* positions,
+                              const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const int32_t* block_table,
+                              const int32_t* seq_lens, float kv_scale, const float* k_scale,
+                              const float* v_scale, void* q_out, int64_t q_out_stride,
+                              void* k_pages, void* v_pages, float* key_weights,
+                              int32_t* key_positions, int32_t* status, void* stream) {
+  return append(desc, nullptr, rope, n_tokens, cu_tokens, positions, q, q_stride, k, k_stride, v, v_stride, block_table,
+                seq_lens, kv_scale, k_scale, v_scale, q_out, q_out_stride, k_pages, v_pages, key_weights, key_positions,
+                status, stream);
+}
+
+splitkv_status splitkv_append_norm(const splitkv_desc_t* desc, const splitkv_norm_t* norm,
+                                   const splitkv_rope_t* rope,
+                                   int32_t n_tokens, const int32_t* cu_tokens, const int32_t* positions,
+                                   const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, const int32_t* block_table,
+                                   const int32_t* seq_lens, float kv_scale, const float* k_scale,
+                                   const float* v_scale, void* q_out, int64_t q_out_stride,
+                                   void* k_pages, void* v_pages, float* key_weights,
+                                   int32_t* key_positions, int32_t* status, void* stream) {
+  if (!norm) return fail(SPLITKV_EINVAL, "norm is NULL");
+  return append(desc, norm, rope, n_tokens, cu_tokens, positions, q, q_stride, k, k_stride, v, v_stride, block_table,
+                seq_lens, kv_scale, k_scale, v_scale, q_out, q_out_stride, k_pages, v_pages, key_weights, key_positions,
+                status, stream);
 }
 
 splitkv_status splitkv_key_weights(const splitkv_desc_t* desc, const void* q, const void* k_pages,
@@ -451,6 +498,54 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   if (st != SPLITKV_OK) return st;
   cudaError_t e = launch_cross(a, cross_row_tiles(d, n_tokens), tk, tv, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launching the cross attention kernels");
+  return SPLITKV_OK;
+}
+
+splitkv_status splitkv_tree_commit(const splitkv_desc_t* desc, int32_t max_path, const int32_t* path,
+                                   const int32_t* path_lens, const int32_t* cu_tokens, void* k_pages,
+                                   void* v_pages, const int32_t* block_table, const int32_t* seq_lens,
+                                   float* key_weights, int32_t* key_positions, int32_t* seq_lens_out,
+                                   int32_t* status, void* stream) {
+  splitkv_status st = validate_cache(desc);
+  if (st != SPLITKV_OK) return st;
+  const splitkv_desc_t& d = *desc;
+  if (max_path < 1) return fail(SPLITKV_EINVAL, "max_path must be >= 1");
+  if (!path || !path_lens || !k_pages || !block_table || !seq_lens || !seq_lens_out)
+    return fail(SPLITKV_EINVAL, "path, path_lens, k_pages, block_table, seq_lens and seq_lens_out must not be NULL");
+  if (d.v_shares_k ? v_pages != nullptr : v_pages == nullptr)
+    return fail(SPLITKV_EINVAL, d.v_shares_k ? "v_pages must be NULL when v_shares_k" : "v_pages is NULL");
+  if (misaligned(k_pages, 16) || misaligned(v_pages, 16))
+    return fail(SPLITKV_EINVAL, "the pages must be 16-byte aligned");
+  const void* words[] = {path, path_lens, cu_tokens, block_table, seq_lens, key_weights, key_positions, seq_lens_out, status};
+  for (const void* p : words)
+    if (misaligned(p, 4)) return fail(SPLITKV_EINVAL, "index and state arrays must be 4-byte aligned");
+  if (half_shared(seq_lens, seq_lens_out, size_t(d.batch) * 4))
+    return fail(SPLITKV_EINVAL, "seq_lens_out overlaps seq_lens without being it");
+  CommitArgs a{};
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.path = path;
+  a.path_lens = path_lens;
+  a.cu = cu_tokens;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.key_weights = key_weights;
+  a.key_positions = key_positions;
+  a.lens_out = seq_lens_out;
+  a.status = status;
+  a.batch = d.batch;
+  a.T = d.q_tokens;
+  a.Hkv = d.num_kv_heads;
+  a.P = d.page_size;
+  a.max_pages = d.max_pages_per_seq;
+  a.num_pages = d.num_pages_total;
+  a.nhd = d.kv_layout == SPLITKV_LAYOUT_NHD;
+  a.max_path = max_path;
+  const int elem = d.kv_dtype == SPLITKV_FP8_E4M3 ? 1 : 2;
+  a.k_row = d.qk_dim * elem;
+  a.v_row = d.v_shares_k ? 0 : d.v_dim * elem;
+  cudaError_t e = launch_tree_commit(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the commit kernel");
   return SPLITKV_OK;
 }
 

@@ -190,6 +190,10 @@ struct AppendArgs {
   int32_t n_tokens, batch, T, Hq, Hkv, P, max_pages, num_pages, nhd;
   uint32_t per_tok_magic;    // set by the launch: 2^32 / units of a token, rounded up
   splitkv_rope_s rope;       // rot_dim 0: nothing is rotated
+  const float* q_weight;     // of the norms: a row's columns, for every head with q_per_head; null: ones
+  const float* k_weight;
+  float eps;
+  int32_t norm_q, norm_k, q_per_head, k_per_head;
 };
 
 struct WeightArgs {
@@ -222,6 +226,22 @@ struct EvictArgs {
   int32_t batch, Hkv, P, max_pages, num_pages, nhd;
   int32_t budget, sink, recent, max_moves;
   int32_t k_row, v_row;   // bytes of one key's row
+};
+
+struct CommitArgs {
+  void* k_pages;
+  void* v_pages;             // or null
+  const int32_t* path;       // [batch][max_path]
+  const int32_t* path_lens;
+  const int32_t* cu;         // [batch + 1] or null: T tokens per sequence
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  float* key_weights;        // [batch][Hkv][max_pages * P] or null
+  int32_t* key_positions;    // likewise
+  int32_t* lens_out;         // may be seq_lens
+  int32_t* status;           // or null
+  int32_t batch, T, Hkv, P, max_pages, num_pages, nhd, max_path;
+  int32_t k_row, v_row;      // bytes of one key's row
 };
 
 // SMs that cross attention plans for, and append's long calls.  (Where fewer are to
@@ -263,6 +283,7 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint6
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream);
 cudaError_t launch_key_weights(const WeightArgs& a, bool fp8, void* stream);
 cudaError_t launch_evict(const EvictArgs& a, void* stream);
+cudaError_t launch_tree_commit(const CommitArgs& a, void* stream);
 int64_t cross_row_tiles(const splitkv_desc_t& d, int64_t n_tokens);
 enum class CrossDeal { kPieces, kLine, kItems };
 CrossDeal cross_deal(const splitkv_desc_t& d, int64_t n_tokens);
