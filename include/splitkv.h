@@ -660,6 +660,54 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
                                     size_t workspace_bytes, int32_t* status, void* stream);
 
 /*
+ * splitkv_tree_attend -- attention of a tree of drafted tokens over the cache that
+ * holds their keys (stored with splitkv_append or splitkv_append_norm).  With L =
+ * seq_lens[b], sequence b's T_b tokens are the last T_b of its L keys, token i's key
+ * in slot L - T_b + i.  A token sees every key before slot L - T_b, and of the
+ * drafted ones those that its mask names: bit i of the mask (bit i % 32 of word i /
+ * 32) for the key of token i.  A tree's mask has a token's own bit and those of the
+ * tokens on its way from the first; any other mask is served as well, one of zeros
+ * too.  Any number of tokens per sequence, none or more than the mask has bits (keys
+ * from 32 * mask_words on are seen by none); bits from T_b on are not looked at.
+ * With n_tokens = 0 nothing is done.  Nothing is planned; all lengths are read on the
+ * device.
+ *   desc         the cache, bf16 or e4m3, qk_dim = v_dim = 128 (q_tokens counts only
+ *                without cu_tokens; any number of query rows per KV head); or the
+ *                latent rows that splitkv_decode serves (128 query heads, q_tokens
+ *                <= 16 for every sequence, cu_tokens NULL, tokens of q adjacent)
+ *   cu_tokens    int32 [B + 1], not decreasing, within [0, n_tokens], or NULL:
+ *                q_tokens tokens for every sequence.  Tokens outside
+ *                [cu_tokens[0], cu_tokens[B]) are left as they are
+ *   tree_mask    uint32 [n_tokens][mask_words], 1 <= mask_words <= 32
+ *   q            bf16, token n's heads [Hq][Dk] at q + n * q_stride (elements, a
+ *                multiple of 8 below 2^31)
+ *   scale        softmax scale, positive
+ *   kv_scale, k_scale, v_scale  of e4m3 caches: kv_scale, or per KV head where
+ *                k_scale and v_scale (fp32 [Hkv], device) are given (rows of 128)
+ *   out          bf16 [n_tokens][Hq][Dv]; must not overlap q
+ *   lse          fp32 [n_tokens][Hq] natural-log LSE of the scaled scores, or
+ *                NULL.  A token that sees no key gets out = 0 and lse = -inf
+ *   workspace    splitkv_tree_workspace_size bytes (0: may be NULL), 16-byte
+ *                aligned, used by this call alone until it has finished
+ * Keys that no token sees (padding of a tree) may hold anything.  A NaN or infinity
+ * in a key that a token does not see leaves it as it is; in the value of a drafted key
+ * it may reach every token whose rows share a tile of 256 with a token that sees it
+ * (latent rows: it does not).
+ * A length outside [0, max_pages_per_seq * P], or below T_b and not 0, sets
+ * SPLITKV_DEVERR_SEQLEN and counts as 0; a page id out of range sets
+ * SPLITKV_DEVERR_PAGE (page 0 is read in its place).  One kernel or two.
+ */
+size_t splitkv_tree_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens);
+splitkv_status splitkv_tree_attend(const splitkv_desc_t* desc, int32_t n_tokens,
+                                   const int32_t* cu_tokens, const uint32_t* tree_mask,
+                                   int32_t mask_words, const void* q, int64_t q_stride,
+                                   const void* k_pages, const void* v_pages,
+                                   const int32_t* block_table, const int32_t* seq_lens, float scale,
+                                   float kv_scale, const float* k_scale, const float* v_scale,
+                                   void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   int32_t* status, void* stream);
+
+/*
  * splitkv_tree_commit -- keeps the accepted tokens of a drafted tree.  The last T_b
  * of sequence b's L = seq_lens[b] keys are those of its drafted tokens, token i in
  * slot L - T_b + i (as splitkv_append stored them).  With the accepted path p_0 <

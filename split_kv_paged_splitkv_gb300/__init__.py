@@ -96,6 +96,9 @@ _SIGNATURES = {
     "splitkv_cross_workspace_size": (_sz, [ctypes.POINTER(splitkv_desc_t), _i32]),
     "splitkv_cross_attend": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, _vp, _vp, _i64, _vp, _vp, _vp,
                                     _vp, _f32, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "splitkv_tree_workspace_size": (_sz, [ctypes.POINTER(splitkv_desc_t), _i32]),
+    "splitkv_tree_attend": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp,
+                                   _vp, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "splitkv_tree_commit": (_i32, [ctypes.POINTER(splitkv_desc_t), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                    _vp, _vp, _vp, _vp]),
     "splitkv_last_error": (ctypes.c_char_p, []),
@@ -426,6 +429,26 @@ def splitkv_cross_attend(desc: splitkv_desc_t, cu_tokens, q, k_pages, v_pages, b
     b, dev = _call()
     _check(b.cross_attend(dev, desc, n_tokens, cu_tokens, q, k_pages, v_pages, block_table, seq_lens, scale, out,
                           lse, workspace, workspace_bytes, status, _stream(stream, dev)))
+
+
+def splitkv_tree_workspace_size(desc: splitkv_desc_t, n_tokens: int) -> int:
+    return int(_lib.splitkv_tree_workspace_size(ctypes.byref(desc), n_tokens))
+
+
+def splitkv_tree_attend(desc: splitkv_desc_t, cu_tokens, tree_mask, q, k_pages, v_pages, block_table, seq_lens,
+                        scale: float, out, lse, workspace, kv_scale: float = 1.0, k_scale=None, v_scale=None,
+                        workspace_bytes=None, status=None, n_tokens=None, mask_words=None, stream=None):
+    """Attention of drafted tokens over their sequence's cache: the keys before the drafted ones, and of
+    those the ones that a token's row of ``tree_mask`` (int32 ``[n][words]``, bit i: token i) names.
+    ``n_tokens`` and ``mask_words`` are needed only where ``q`` and ``tree_mask`` are addresses."""
+    b, dev = _call()
+    if mask_words is None:
+        if tree_mask is None or isinstance(tree_mask, int):
+            raise TypeError("mask_words is needed where tree_mask is an address")
+        mask_words = tree_mask.shape[-1]
+    _check(b.tree_attend(dev, desc, n_tokens, cu_tokens, mask_words, tree_mask, q, k_pages, v_pages, block_table,
+                         seq_lens, scale, kv_scale, k_scale, v_scale, out, lse, workspace, workspace_bytes, status,
+                         _stream(stream, dev)))
 
 
 def splitkv_tree_commit(desc: splitkv_desc_t, path, path_lens, k_pages, v_pages, block_table, seq_lens,

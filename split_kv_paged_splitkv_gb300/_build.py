@@ -17,7 +17,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsplitkv.so")
 SOURCES = ["plan.cpp", "api.cu", "gqa_decode.cu", "mla_decode.cu", "combine.cu", "noalloc.cu",
            "refresh.cu", "cache_api.cu", "append.cu", "key_weights.cu", "evict.cu",
-           "cross_attend.cu", "tree_commit.cu"]
+           "cross_attend.cu", "tree_attend.cu", "tree_commit.cu"]
 BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -115,19 +115,31 @@ splitkv_status make_u8_map(TmaDesc* out, const void* base, int dim, int64_t rows
 splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys) {
   auto fn = encode_fn();
   if (!fn) return fail(SPLITKV_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint64_t row = 256u, P = cuuint64_t(d.page_size), H = cuuint64_t(d.num_kv_heads);
+  const bool fp8 = d.kv_dtype == SPLITKV_FP8_E4M3;
+  const cuuint64_t row = fp8 ? 128u : 256u, P = cuuint64_t(d.page_size), H = cuuint64_t(d.num_kv_heads);
   const bool nhd = d.kv_layout == SPLITKV_LAYOUT_NHD;
   CUtensorMap m;
-  cuuint64_t gdim[5] = {64u, P, 2u, H, cuuint64_t(d.num_pages_total)};
+  cuuint64_t gdim[5] = {fp8 ? 128u : 64u, P, fp8 ? 1u : 2u, H, cuuint64_t(d.num_pages_total)};
   cuuint64_t gstride[4] = {nhd ? row * H : row, 128u, nhd ? row : row * P, row * P * H};
-  cuuint32_t box[5] = {64u, cuuint32_t(keys), 1u, 1u, 1u};
+  cuuint32_t box[5] = {fp8 ? 128u : 64u, cuuint32_t(keys), 1u, 1u, 1u};
   cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
-  CUresult r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), gdim, gstride, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  CUresult r = fn(&m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base),
+                  gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SPLITKV_ECUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
   std::memcpy(out, &m, sizeof(m));
   return SPLITKV_OK;
+}
+
+splitkv_status make_mla_maps(TmaDesc* tk, TmaDesc* tv, const void* k_pages, const void* v_pages,
+                             const splitkv_desc_t& d) {
+  const int64_t rows_total = int64_t(d.num_pages_total) * d.num_kv_heads * d.page_size;
+  const int box_rows = d.page_size < 64 ? d.page_size : 64;
+  splitkv_status st = d.kv_dtype == SPLITKV_FP8_E4M3 ? make_u8_map(tk, k_pages, d.qk_dim, rows_total, box_rows)
+                                                     : make_bf16_map(tk, k_pages, d.qk_dim, rows_total, box_rows);
+  if (st != SPLITKV_OK || d.v_shares_k) return st;
+  return make_bf16_map(tv, v_pages, d.v_dim, rows_total, box_rows);
 }
 
 splitkv_status cuda_fail(cudaError_t e, const char* what) {
@@ -468,21 +480,14 @@ splitkv_status decode_impl(const splitkv_plan_t* plan, void* workspace, const vo
   }
   a.deep_ring = plan->n_items <= sms ? 1 : 0;
 
-  const int64_t rows_total = int64_t(d.num_pages_total) * d.num_kv_heads * d.page_size;
   if (family_of(d) == Family::kMla) {
     // Latent cache rows of 576 bf16 (boxes of min(P, 64) rows, one page at
     // most), and with a separate V tensor its rows of 512; the query rows are read by the
     // kernel's threads.  The partials are always merged by the separate
     // combine kernel.
     TmaDesc tk, tv;
-    const int box_rows = d.page_size < 64 ? d.page_size : 64;
-    splitkv_status st = fp8 ? make_u8_map(&tk, k_pages, d.qk_dim, rows_total, box_rows)
-                            : make_bf16_map(&tk, k_pages, d.qk_dim, rows_total, box_rows);
+    splitkv_status st = make_mla_maps(&tk, &tv, k_pages, v_pages, d);
     if (st != SPLITKV_OK) return st;
-    if (!d.v_shares_k) {
-      st = make_bf16_map(&tv, v_pages, d.v_dim, rows_total, box_rows);
-      if (st != SPLITKV_OK) return st;
-    }
     a.fused = 0;
     cudaError_t e = launch_mla(a, tk, d.v_shares_k ? nullptr : &tv, fp8, stream);
     if (e != cudaSuccess) return cuda_fail(e, "launching the MLA split-KV kernel");

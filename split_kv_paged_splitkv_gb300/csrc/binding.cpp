@@ -424,6 +424,40 @@ PyObject* cross_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+PyObject* tree_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  Args in(a, n_args, 21);
+  return guarded(in, [&]() -> int {
+    const int64_t dev = in.integer();
+    const Sizes z = in.desc();
+    const splitkv_desc_t& d = z.d;
+    const int64_t n = in.tokens(6, times({d.num_q_heads, d.qk_dim}));
+    auto* cu = in.tensor<int32_t>("cu_tokens", kInt, {int64_t(d.batch) + 1}, dev);
+    const int32_t words = in.int32("mask_words");
+    // (a wider mask has rows of another length)
+    auto* mask = in.tensor<uint32_t>("tree_mask", kInt, {n, words}, dev, true);
+    int64_t qs;
+    void* q = in.rows("q", n, d.num_q_heads, d.qk_dim, dev, &qs);
+    void* k_pages = in.tensor<void>("k_pages", z.pool, z.k_pool, dev);
+    void* v_pages = in.tensor<void>("v_pages", z.pool, z.v_pool, dev);
+    auto* table = in.tensor<int32_t>("block_table", kInt, z.table, dev);
+    auto* lens = in.tensor<int32_t>("seq_lens", kInt, {d.batch}, dev);
+    const float scale = in.real(), kv_scale = in.real();
+    auto* k_scale = in.tensor<float>("k_scale", kFloat, {d.num_kv_heads}, dev);
+    auto* v_scale = in.tensor<float>("v_scale", kFloat, {d.num_kv_heads}, dev);
+    void* out = in.tensor<void>("out", ScalarType::BFloat16, {n, d.num_q_heads, d.v_dim}, dev);
+    auto* lse = in.tensor<float>("lse", kFloat, {n, d.num_q_heads}, dev);
+    size_t bytes = 0;
+    void* workspace = in.workspace(dev, &bytes);
+    auto* status = in.tensor<int32_t>("status", kInt, {1}, dev);
+    void* stream = in.address();
+    if (!in.ok()) return 0;
+    return call([&] {
+      return splitkv_tree_attend(&d, int32_t(n), cu, mask, words, q, qs, k_pages, v_pages, table, lens, scale, kv_scale,
+                                 k_scale, v_scale, out, lse, workspace, bytes, status, stream);
+    });
+  });
+}
+
 PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   Args in(a, n_args, 15);
   return guarded(in, [&]() -> int {
@@ -454,7 +488,7 @@ PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FAST(append), FAST(append_norm), FAST(key_weights), FAST(evict), FAST(cross_attend),
-                          FAST(tree_commit), {nullptr, nullptr, 0, nullptr}};
+                          FAST(tree_attend), FAST(tree_commit), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,5 +1,5 @@
 // C-ABI layer of the cache operators: append with norms and rotary positions, key
-// weights, eviction, cross attention, the commit of drafted trees.  Argument validation, workspace layout, launches.
+// weights, eviction, cross attention, attention and commit of drafted trees.  Argument validation, workspace layout, launches.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -68,6 +68,38 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 // least), and their number.
 size_t split_bytes(size_t parts) { return align256(parts * sizeof(CrossSplit) + sizeof(int32_t)); }
 
+// The workspace of a call that is not dealt as whole items.
+size_t cross_bytes(const splitkv_desc_t& d, int32_t n_tokens) {
+  const size_t parts = kSmCount;
+  return align256(2 * parts * cross_part_rows(d, n_tokens) * 129 * sizeof(float)) + split_bytes(parts);
+}
+
+// The shape of a call of cross attention's kernel, how its items are dealt, and where
+// in the workspace what lies.
+void fill_cross(CrossArgs& a, const splitkv_desc_t& d, int32_t n_tokens, void* workspace) {
+  const CrossDeal deal = cross_deal(d, n_tokens);
+  a.parts = deal == CrossDeal::kItems ? 0 : kSmCount;
+  a.line = deal == CrossDeal::kLine;
+  a.part_rows = cross_part_rows(d, n_tokens);
+  if (a.parts > 0) {
+    a.o_part = static_cast<float*>(workspace);
+    a.lse_part = a.o_part + size_t(2) * a.parts * a.part_rows * 128;
+    a.split = reinterpret_cast<CrossSplit*>(static_cast<unsigned char*>(workspace) + cross_bytes(d, n_tokens) -
+                                            split_bytes(a.parts));
+    a.n_split = reinterpret_cast<int32_t*>(a.split + a.parts);
+  }
+  a.n_tokens = n_tokens;
+  a.batch = d.batch;
+  a.T = d.q_tokens;
+  a.Hq = d.num_q_heads;
+  a.Hkv = d.num_kv_heads;
+  a.G = d.num_q_heads / d.num_kv_heads;
+  a.P = d.page_size;
+  a.max_pages = d.max_pages_per_seq;
+  a.num_pages = d.num_pages_total;
+  a.box_rows = cross_box_rows(d);
+}
+
 // Moves of one (sequence, head), at most: the kept keys behind the budget.
 int64_t max_moves(const splitkv_desc_t& d, int32_t budget) {
   const int64_t cap = int64_t(d.max_pages_per_seq) * d.page_size;
@@ -91,6 +123,54 @@ splitkv_status validate_cross(const splitkv_desc_t* d, int32_t n_tokens) {
   if (n_tokens < 0 || int64_t(n_tokens) * d->num_q_heads >= (int64_t(1) << 31) || d->num_kv_heads > 65535)
     return fail(SPLITKV_EINVAL, "n_tokens must be >= 0 with n_tokens * num_q_heads < 2^31, and num_kv_heads at most 65535");
   return SPLITKV_OK;
+}
+
+splitkv_status validate_tree(const splitkv_desc_t* d, int32_t n_tokens) {
+  splitkv_status st = validate_cache(d);
+  if (st != SPLITKV_OK) return st;
+  if (n_tokens < 0 || int64_t(n_tokens) * d->num_q_heads >= (int64_t(1) << 31) || d->num_kv_heads > 65535)
+    return fail(SPLITKV_EINVAL, "n_tokens must be >= 0 with n_tokens * num_q_heads < 2^31, and num_kv_heads at most 65535");
+  if (d->qk_dim == 128) return SPLITKV_OK;
+  if (family_of(*d) != Family::kMla)
+    return fail(SPLITKV_EUNSUPPORTED, "trees over latent rows need 128 query heads, q_tokens <= 16, pages of 16, 32 or a "
+                "multiple of 64, and in e4m3 the values in the rows");
+  if (n_tokens != 0 && int64_t(d->batch) * d->q_tokens != n_tokens)
+    return fail(SPLITKV_EINVAL, "over latent rows n_tokens (%d) must be batch * q_tokens", n_tokens);
+  return SPLITKV_OK;
+}
+
+// The workspace of a tree over latent rows: the splits of every sequence, where what
+// lies (bytes from its start), and its size.
+struct LatentTree {
+  int32_t splits, items;
+  size_t groups, log, status, lse, o, total;
+};
+LatentTree latent_tree(const splitkv_desc_t& d) {
+  LatentTree w;
+  // As many splits as cost least over a full cache, in its blocks of 64 keys: the longest
+  // in each round of CTAs (two for every token, sequence and split, one to an SM), and
+  // some 12 blocks' time to begin and to end it.  (12 tokens over 64k rows: 6 splits in
+  // one round; 16 tokens 9 splits in two rather than 4 in one.)
+  const int64_t blocks = (int64_t(d.max_pages_per_seq) * d.page_size + 63) / 64;
+  int64_t least = INT64_MAX;
+  w.splits = 1;
+  for (int s = 1; s <= kMaxSplits && s <= d.max_pages_per_seq; ++s) {
+    const int64_t rounds = (int64_t(d.batch) * s * 2 * d.q_tokens + kSmCount - 1) / kSmCount;
+    const int64_t cost = rounds * ((blocks + s - 1) / s + 12);
+    if (cost < least) {
+      least = cost;
+      w.splits = s;
+    }
+  }
+  const int64_t items = int64_t(d.batch) * w.splits, rows = items * d.q_tokens * d.num_q_heads;
+  w.items = int32_t(items);
+  w.groups = 0;
+  w.log = w.groups + align256(size_t(d.batch) * kGroupFields * 4);
+  w.status = w.log + align256(size_t(items) * 2 * d.q_tokens * kLogFields * 4);
+  w.lse = w.status + 256;
+  w.o = w.lse + (w.splits > 1 ? align256(size_t(rows) * 4) : 0);
+  w.total = w.o + (w.splits > 1 ? size_t(rows) * d.v_dim * 4 : 0);
+  return w;
 }
 
 }  // namespace
@@ -426,8 +506,7 @@ splitkv_status splitkv_evict(const splitkv_desc_t* desc, int32_t budget, int32_t
 size_t splitkv_cross_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
   if (validate_cross(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
   if (cross_deal(*desc, n_tokens) == CrossDeal::kItems) return 0;
-  const size_t parts = kSmCount;
-  return align256(2 * parts * cross_part_rows(*desc, n_tokens) * 129 * sizeof(float)) + split_bytes(parts);
+  return cross_bytes(*desc, n_tokens);
 }
 
 splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens,
@@ -456,23 +535,15 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   if (overlap(q, size_t((n_tokens - 1) * q_stride + row) * 2, out, size_t(n_tokens) * row * 2))
     return fail(SPLITKV_EINVAL, "out overlaps q");
   if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPLITKV_EINVAL, "scale must be positive and finite");
-  CrossArgs a{};
-  const CrossDeal deal = cross_deal(d, n_tokens);
-  a.parts = deal == CrossDeal::kItems ? 0 : kSmCount;
-  a.line = deal == CrossDeal::kLine;
-  a.part_rows = cross_part_rows(d, n_tokens);
-  if (a.parts > 0) {
+  const size_t need = splitkv_cross_workspace_size(desc, n_tokens);
+  if (need > 0) {
     if (!workspace) return fail(SPLITKV_EWORKSPACE, "workspace is NULL");
     if (misaligned(workspace, 16)) return fail(SPLITKV_EINVAL, "workspace must be 16-byte aligned");
-    const size_t need = splitkv_cross_workspace_size(desc, n_tokens);
     if (workspace_bytes < need)
       return fail(SPLITKV_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
-    a.o_part = static_cast<float*>(workspace);
-    a.lse_part = a.o_part + size_t(2) * a.parts * a.part_rows * 128;
-    a.split = reinterpret_cast<CrossSplit*>(static_cast<unsigned char*>(workspace) + need -
-                                            split_bytes(a.parts));
-    a.n_split = reinterpret_cast<int32_t*>(a.split + a.parts);
   }
+  CrossArgs a{};
+  fill_cross(a, d, n_tokens, workspace);
   a.q = q;
   a.cu = cu_tokens;
   a.block_table = block_table;
@@ -482,22 +553,135 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   a.status = status;
   a.q_stride = q_stride;
   a.qk_scale_log2 = scale * kLog2e;
-  a.n_tokens = n_tokens;
-  a.batch = d.batch;
-  a.T = d.q_tokens;
-  a.Hq = d.num_q_heads;
-  a.Hkv = d.num_kv_heads;
-  a.G = d.num_q_heads / d.num_kv_heads;
-  a.P = d.page_size;
-  a.max_pages = d.max_pages_per_seq;
-  a.num_pages = d.num_pages_total;
-  a.box_rows = cross_box_rows(d);
   TmaDesc tk, tv;
   st = make_half_map(&tk, k_pages, d, a.box_rows);
   if (st == SPLITKV_OK) st = make_half_map(&tv, v_pages, d, a.box_rows);
   if (st != SPLITKV_OK) return st;
   cudaError_t e = launch_cross(a, cross_row_tiles(d, n_tokens), tk, tv, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launching the cross attention kernels");
+  return SPLITKV_OK;
+}
+
+size_t splitkv_tree_workspace_size(const splitkv_desc_t* desc, int32_t n_tokens) {
+  if (validate_tree(desc, n_tokens) != SPLITKV_OK || n_tokens == 0) return 0;
+  if (desc->qk_dim != 128) return latent_tree(*desc).total;
+  if (cross_deal(*desc, n_tokens) == CrossDeal::kItems) return 0;
+  return cross_bytes(*desc, n_tokens);
+}
+
+splitkv_status splitkv_tree_attend(const splitkv_desc_t* desc, int32_t n_tokens,
+                                   const int32_t* cu_tokens, const uint32_t* tree_mask,
+                                   int32_t mask_words, const void* q, int64_t q_stride,
+                                   const void* k_pages, const void* v_pages,
+                                   const int32_t* block_table, const int32_t* seq_lens, float scale,
+                                   float kv_scale, const float* k_scale, const float* v_scale,
+                                   void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   int32_t* status, void* stream) {
+  splitkv_status st = validate_tree(desc, n_tokens);
+  if (st != SPLITKV_OK) return st;
+  const splitkv_desc_t& d = *desc;
+  const bool fp8 = d.kv_dtype == SPLITKV_FP8_E4M3, latent = d.qk_dim != 128;
+  if (latent && cu_tokens) return fail(SPLITKV_EINVAL, "over latent rows every sequence has q_tokens tokens: cu_tokens must be NULL");
+  if (!cu_tokens && int64_t(d.batch) * d.q_tokens != n_tokens)
+    return fail(SPLITKV_EINVAL, "without cu_tokens, n_tokens (%d) must be batch * q_tokens", n_tokens);
+  if (n_tokens == 0) return SPLITKV_OK;
+  if (!tree_mask || !q || !k_pages || !block_table || !seq_lens || !out)
+    return fail(SPLITKV_EINVAL, "tree_mask, q, k_pages, block_table, seq_lens and out must not be NULL");
+  if (d.v_shares_k ? v_pages != nullptr : v_pages == nullptr)
+    return fail(SPLITKV_EINVAL, d.v_shares_k ? "v_pages must be NULL when v_shares_k" : "v_pages is NULL");
+  if (mask_words < 1 || mask_words > kMaxMaskWords)
+    return fail(SPLITKV_EINVAL, "mask_words (%d) must be in [1, %d]", mask_words, kMaxMaskWords);
+  const void* wide[] = {q, k_pages, v_pages, out};
+  for (const void* p : wide)
+    if (misaligned(p, 16)) return fail(SPLITKV_EINVAL, "q, out and the pages must be 16-byte aligned");
+  const void* words[] = {cu_tokens, tree_mask, block_table, seq_lens, lse, status};
+  for (const void* p : words)
+    if (misaligned(p, 4)) return fail(SPLITKV_EINVAL, "the mask, index arrays and lse must be 4-byte aligned");
+  const int64_t row = int64_t(d.num_q_heads) * d.qk_dim, out_row = int64_t(d.num_q_heads) * d.v_dim;
+  if (q_stride < row || q_stride % 8 || q_stride > (int64_t(1) << 31) - 8)
+    return fail(SPLITKV_EINVAL, "q_stride must be a multiple of 8 elements, hold a token's heads and be below 2^31");
+  if (latent && n_tokens > 1 && q_stride != row)
+    return fail(SPLITKV_EINVAL, "over latent rows the tokens of q must be adjacent");
+  if (overlap(q, size_t((n_tokens - 1) * q_stride + row) * 2, out, size_t(n_tokens) * out_row * 2))
+    return fail(SPLITKV_EINVAL, "out overlaps q");
+  if (!(scale > 0.f) || !(scale < 1e30f)) return fail(SPLITKV_EINVAL, "scale must be positive and finite");
+  st = check_scales(fp8, kv_scale, k_scale, v_scale, true);
+  if (st != SPLITKV_OK) return st;
+  if (latent && k_scale) return fail(SPLITKV_EUNSUPPORTED, "k_scale and v_scale apply to rows of 128 only");
+  const size_t need = splitkv_tree_workspace_size(desc, n_tokens);
+  if (need > 0) {
+    if (!workspace) return fail(SPLITKV_EWORKSPACE, "workspace is NULL");
+    if (misaligned(workspace, 16)) return fail(SPLITKV_EINVAL, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(SPLITKV_EWORKSPACE, "workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
+  }
+  const float qk_scale = scale * kLog2e * (fp8 && !k_scale ? kv_scale : 1.f), o_scale = fp8 ? kv_scale : 1.f;
+  if (latent) {
+    const LatentTree w = latent_tree(d);
+    if (int64_t(w.items) * 2 * d.q_tokens >= (int64_t(1) << 31))
+      return fail(SPLITKV_EINVAL, "batch * q_tokens must be below 2^30");
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    DecodeArgs a{};
+    a.groups = reinterpret_cast<const int32_t*>(ws + w.groups);
+    a.cta_log = reinterpret_cast<int32_t*>(ws + w.log);
+    a.status = status ? status : reinterpret_cast<int32_t*>(ws + w.status);
+    a.lse_part = reinterpret_cast<float*>(ws + w.lse);
+    a.o_part = reinterpret_cast<float*>(ws + w.o);
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.n_items = w.items;
+    a.n_groups = w.splits > 1 ? d.batch : 0;
+    a.batch = d.batch;
+    a.T = d.q_tokens;
+    a.Hq = d.num_q_heads;
+    a.Hkv = 1;
+    a.G = d.num_q_heads;
+    a.P = d.page_size;
+    a.max_pages = d.max_pages_per_seq;
+    a.num_pages = d.num_pages_total;
+    a.rows = d.q_tokens * d.num_q_heads;
+    a.dv = d.v_dim;
+    a.qk_scale_log2 = qk_scale;
+    a.o_scale = o_scale;
+    a.fixed = 1;
+    a.max_splits = w.splits;
+    a.hpi = 1;
+    a.fx = {seq_lens, w.splits, 1, 1, d.page_size, d.q_tokens, int64_t(d.max_pages_per_seq) * d.page_size};
+    a.mask = tree_mask;
+    a.words = mask_words;
+    TmaDesc tk, tv;
+    st = make_mla_maps(&tk, &tv, k_pages, v_pages, d);
+    if (st != SPLITKV_OK) return st;
+    cudaError_t e = launch_mla(a, tk, d.v_shares_k ? nullptr : &tv, fp8, stream);
+    if (e == cudaSuccess) e = launch_combine(a, true, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "launching the tree attention kernels");
+    return SPLITKV_OK;
+  }
+  CrossArgs a{};
+  fill_cross(a, d, n_tokens, workspace);
+  a.q = q;
+  a.cu = cu_tokens;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.lse = lse;
+  a.status = status;
+  a.q_stride = q_stride;
+  a.qk_scale_log2 = qk_scale;
+  a.mask = tree_mask;
+  a.words = mask_words;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.o_scale = o_scale;
+  TmaDesc tk, tv;
+  st = make_half_map(&tk, k_pages, d, a.box_rows);
+  if (st == SPLITKV_OK) st = make_half_map(&tv, v_pages, d, a.box_rows);
+  if (st != SPLITKV_OK) return st;
+  cudaError_t e = launch_tree(a, cross_row_tiles(d, n_tokens), tk, tv, fp8, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the tree attention kernels");
   return SPLITKV_OK;
 }
 

@@ -121,6 +121,8 @@ struct DecodeArgs {
   FixedShape fx;         // capacity plans: the kernels derive items and groups from it
   int32_t deep_ring;     // 1: at most one CTA per SM, so the GQA kernel may take the
                          //    deeper (four-stage) ring instead of sharing the SM
+  const uint32_t* mask;  // drafted trees (MLA): [B][T][words], or null: causal
+  int32_t words;
 };
 
 // Raw 128-byte tensor map storage (CUtensorMap), built by the API layer.
@@ -248,6 +250,9 @@ struct CommitArgs {
 // be had the grid takes a second round; results do not depend on it.)
 constexpr int kSmCount = 152;
 
+// Words of a drafted token's mask, at most.
+constexpr int kMaxMaskWords = 32;
+
 // A cut item of cross attention, for the merge: its number of pieces (0: none such),
 // the slot of the first, how far apart the others' are (1, or 2 from the even slot
 // at or before the first on), its sequence's first token, head, first row and rows.
@@ -274,6 +279,12 @@ struct CrossArgs {
   int32_t parts;      // CTAs that share all items' key blocks; 0: a CTA per item
   int32_t line;       // an even line of all items' key blocks, whatever their lengths
   int32_t part_rows;  // rows of an item, at most
+  // of drafted trees (TREE):
+  const uint32_t* mask;  // [n_tokens][words]
+  const float* k_scale;  // e4m3 per-KV-head scales or null: in qk_scale_log2, and o_scale
+  const float* v_scale;
+  float o_scale;
+  int32_t words;
 };
 
 // Once per device and kernel: opts in to `bytes` of dynamic shared memory on the
@@ -291,9 +302,17 @@ int cross_part_rows(const splitkv_desc_t& d, int64_t n_tokens);
 int cross_box_rows(const splitkv_desc_t& d);  // keys of one TMA box
 cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv,
                          void* stream);
-// Tensor map over a bf16 pool of 128-wide rows, coordinates (64 columns, key
-// in page, column half, KV head, page) in either layout, boxes of `keys` keys
-// and one column half, 128-byte swizzle (api.cu).
+cudaError_t launch_cross_merge(const CrossArgs& a, int64_t row_tiles, void* stream);  // (both kinds')
+cudaError_t launch_tree(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv, bool fp8,
+                        void* stream);
+// Tensor map over a pool of 128-wide rows, coordinates (columns, key in page,
+// column half, KV head, page) in either layout: boxes of `keys` keys and one
+// column half, 128-byte swizzle, of bf16; of `keys` keys and whole rows, as they lie,
+// of e4m3 (one "half") (api.cu).
 splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys);
+// The MLA family's maps of the latent rows and, with v_shares_k = 0, of the separate
+// values (else tv is left as it is) (api.cu).
+splitkv_status make_mla_maps(TmaDesc* tk, TmaDesc* tv, const void* k_pages, const void* v_pages,
+                             const splitkv_desc_t& d);
 
 }  // namespace splitkv

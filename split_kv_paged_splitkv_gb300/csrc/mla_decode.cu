@@ -57,6 +57,12 @@
 // them, warp 7 loads block j's V half over the first four of them, and PV(j)
 // waits for that load.  Shared memory and TMEM are laid out as for the
 // shared latent row; each V-ring slot is filled twice per use.
+//
+// TREE (splitkv_tree_attend): the T query tokens are a drafted tree, and token t
+// sees the keys before the last T and those of the last T that bit i of its mask
+// names.  A CTA has the rows of one token, so a block that reaches past L - T has one
+// 64-bit word of visible keys for all of them: the softmax warps take -inf for the
+// others' scores, and the issuer zeroes their V rows.
 #include <cuda_runtime.h>
 
 #include "fixed_plan.cuh"
@@ -214,7 +220,15 @@ struct PageWalk {
   }
 };
 
-template <bool SEPV, bool SMALLP, bool FP8>
+// The keys of the block from key0 on that a token of a tree sees: those before k_end
+// of the keys before `base`, and of the drafted ones from `base` on by their bits.
+__device__ __forceinline__ uint64_t tree_visible(uint32_t bits, int base, int key0, int k_end) {
+  const int d = base - key0, n = k_end - key0;
+  const uint64_t x = d >= 64 ? ~uint64_t(0) : d > 0 ? (uint64_t(1) << d) - 1 | uint64_t(bits) << d : d > -32 ? bits >> -d : 0;
+  return n >= 64 ? x : n > 0 ? x & ((uint64_t(1) << n) - 1) : 0;
+}
+
+template <bool SEPV, bool SMALLP, bool FP8, bool TREE>
 __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS + 128 : Mla::THREADS), 1)
     mla_splitkv_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv) {
@@ -319,6 +333,8 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
   const int lim = SMALLP ? min(L - a.T + t, k_end - 1) : L - a.T + t;
   launch_dependents();
   wait_prerequisites();
+  // (the mask's bits of drafted tokens that there are not, or of no keys, count as off)
+  const uint32_t bits = TREE ? a.mask[(size_t(b) * a.T + t) * a.words] & ((1u << a.T) - 1) : 0;
   if (threadIdx.x == 0 && h == 0 && t == 0 && a.seq_lens[b] != L)
     atomicOr(a.status, SPLITKV_DEVERR_SEQLEN);
 
@@ -451,6 +467,16 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
             const int r = valid + (x >> 5), ch = (x >> 3) & 3, c16 = x & 7;
             *reinterpret_cast<uint4*>(vst + ch * C::K_CH + r * 128 + c16 * 16) = make_uint4(0, 0, 0, 0);
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        if (TREE && k_begin + jp * C::BK + valid > L - a.T) {
+          // (and those of the drafted keys that the token does not see)
+          const int key0 = k_begin + jp * C::BK;
+          for (uint64_t x = ~tree_visible(bits, L - a.T, key0, k_end); x; x &= x - 1)
+            *reinterpret_cast<uint4*>(vst + (lane >> 3) * C::K_CH + (__ffsll(x) - 1) * 128 + (lane & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          static_assert(C::NV * 8 == 32, "a lane to each piece of a row");
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
@@ -675,7 +701,14 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
       // maximum and is applied inside the exponent below.  Only a block that
       // reaches past the last visible key is masked.
       const int key0 = k_begin + j * C::BK;
-      if (key0 + C::BK - 1 > lim) {
+      if (TREE) {
+        if (key0 + C::BK > min(L - a.T, k_end)) {
+          const uint64_t vis = tree_visible(bits, L - a.T, key0, k_end);
+          const uint32_t v2[2] = {uint32_t(vis), uint32_t(vis >> 32)};
+#pragma unroll
+          for (int k = 0; k < 64; ++k) s[k] = v2[k >> 5] >> (k & 31) & 1 ? s[k] : -INFINITY;
+        }
+      } else if (key0 + C::BK - 1 > lim) {
 #pragma unroll
         for (int k = 0; k < 64; ++k) s[k] = (key0 + k <= lim) ? s[k] : -INFINITY;
       }
@@ -869,11 +902,11 @@ __global__ void __launch_bounds__(128) mla_gather_debug_kernel(const __grid_cons
 
 namespace {
 
-template <bool SEPV, bool SMALLP, bool FP8 = false>
+template <bool SEPV, bool SMALLP, bool FP8, bool TREE>
 cudaError_t launch_mla_t(const DecodeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                          cudaStream_t s) {
   static cudaError_t attr = cudaFuncSetAttribute(
-      mla_splitkv_kernel<SEPV, SMALLP, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Mla::SMEM);
+      mla_splitkv_kernel<SEPV, SMALLP, FP8, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Mla::SMEM);
   if (attr != cudaSuccess) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_items * a.T * 2, 1, 1);
@@ -885,7 +918,26 @@ cudaError_t launch_mla_t(const DecodeArgs& a, const CUtensorMap& mk, const CUten
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_splitkv_kernel<SEPV, SMALLP, FP8>, a, mk, mv);
+  return cudaLaunchKernelEx(&cfg, mla_splitkv_kernel<SEPV, SMALLP, FP8, TREE>, a, mk, mv);
+}
+
+template <bool TREE>
+cudaError_t launch_mla_n(const DecodeArgs& a, const TmaDesc& tk, const TmaDesc* tv, bool fp8, cudaStream_t s) {
+  const CUtensorMap& mk = *reinterpret_cast<const CUtensorMap*>(&tk);
+  // pages of 16 or 32 keys: several boxes per 64-key block
+  const bool small = a.P < Mla::BK;
+  if (fp8) {
+    if (tv) return cudaErrorInvalidValue;  // FP8 latent caches hold V in the key rows
+    return small ? launch_mla_t<false, true, true, TREE>(a, mk, mk, s)
+                 : launch_mla_t<false, false, true, TREE>(a, mk, mk, s);
+  }
+  if (tv) {
+    const CUtensorMap& mv = *reinterpret_cast<const CUtensorMap*>(tv);
+    return small ? launch_mla_t<true, true, false, TREE>(a, mk, mv, s)
+                 : launch_mla_t<true, false, false, TREE>(a, mk, mv, s);
+  }
+  return small ? launch_mla_t<false, true, false, TREE>(a, mk, mk, s)
+               : launch_mla_t<false, false, false, TREE>(a, mk, mk, s);
 }
 
 }  // namespace
@@ -893,20 +945,8 @@ cudaError_t launch_mla_t(const DecodeArgs& a, const CUtensorMap& mk, const CUten
 cudaError_t launch_mla(const DecodeArgs& a, const TmaDesc& tk, const TmaDesc* tv, bool fp8,
                        void* stream) {
   if (a.n_items == 0) return cudaSuccess;
-  const CUtensorMap& mk = *reinterpret_cast<const CUtensorMap*>(&tk);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // pages of 16 or 32 keys: several boxes per 64-key block
-  const bool small = a.P < Mla::BK;
-  if (fp8) {
-    if (tv) return cudaErrorInvalidValue;  // FP8 latent caches hold V in the key rows
-    return small ? launch_mla_t<false, true, true>(a, mk, mk, s)
-                 : launch_mla_t<false, false, true>(a, mk, mk, s);
-  }
-  if (tv) {
-    const CUtensorMap& mv = *reinterpret_cast<const CUtensorMap*>(tv);
-    return small ? launch_mla_t<true, true>(a, mk, mv, s) : launch_mla_t<true, false>(a, mk, mv, s);
-  }
-  return small ? launch_mla_t<false, true>(a, mk, mk, s) : launch_mla_t<false, false>(a, mk, mk, s);
+  return a.mask ? launch_mla_n<true>(a, tk, tv, fp8, s) : launch_mla_n<false>(a, tk, tv, fp8, s);
 }
 
 cudaError_t launch_mla_debug_gather(const TmaDesc& t, bool fp8, const int32_t* table_row, int32_t P,
