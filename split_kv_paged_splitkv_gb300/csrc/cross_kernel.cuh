@@ -68,9 +68,9 @@
 // one instruction for a pair of codes; bf16 would take four).  The queries are f16
 // then, each row times the power of two that brings its largest component into
 // [2^14, 2^15) (exact, but for components below 2^-29 of it, lost among 2^-25 steps), P
-// is f16 too, and the caches' scales join the scores' and the results'.  With four more
-// warps a thread has 136 registers: the softmax reads 64 columns of S at a time, the
-// first of them twice.
+// is f16 too, and the caches' scales join the scores' and the results'.  16 warps: the
+// softmax's registers come from the others' (2 * 168 + 2 * 88 = 4 * 128; the split holds
+// only in code without calls, so that what cross attention calls is inlined here).
 #pragma once
 
 #include <cuda.h>
@@ -100,8 +100,8 @@ struct Cross {
 };
 template <bool FP8>
 struct CrossCta : Cross {
-  static constexpr int CONVERTER = SOFTMAX_WARPS + 3;  // first of four
-  static constexpr int WARPS = SOFTMAX_WARPS + (FP8 ? 7 : 3);
+  static constexpr int CONVERTER = SOFTMAX_WARPS + 4;  // first of four (warp 11 fills its warpgroup)
+  static constexpr int WARPS = SOFTMAX_WARPS + (FP8 ? 8 : 3);
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TAIL = FP8 ? 2048 : 1536; // barriers, plan
   static constexpr int SMEM = 1024 + OFF_BAR + TAIL;
@@ -235,7 +235,7 @@ __device__ __forceinline__ T lanes_before(T n, int lane, T* total) {
 // us, in whole items 49.7; over 4k keys 79 and 111.  kLineCost is what leaves 8
 // requests, 27.7 us and as a line 30.2, and 16, 51.8 and 55.3, as they are.
 template <bool TREE, int WARPS>
-__device__ __noinline__ void plan_line(const CrossArgs& a, int lane, int64_t all, Tail<WARPS>& tail) {
+__device__ __forceinline__ void plan_line_here(const CrossArgs& a, int lane, int64_t all, Tail<WARPS>& tail) {
   const int64_t share = (all + a.parts - 1) / a.parts;
   const int64_t lo = min(all, int64_t(blockIdx.x) * share), hi = min(all, lo + share);
   Walk w = {lo, 0, 0, 0, 0, 0, 0, 0, 1};
@@ -269,6 +269,18 @@ __device__ __noinline__ void plan_line(const CrossArgs& a, int lane, int64_t all
     a.split[blockIdx.x].cuts = 0;
     if (blockIdx.x == 0) *a.n_split = a.parts;
   }
+}
+
+template <bool TREE, int WARPS>
+__device__ __noinline__ void plan_line_there(const CrossArgs& a, int lane, int64_t all, Tail<WARPS>& tail) {
+  plan_line_here<TREE>(a, lane, all, tail);
+}
+template <bool TREE, int WARPS>
+__device__ __forceinline__ void plan_line(const CrossArgs& a, int lane, int64_t all, Tail<WARPS>& tail) {
+  if constexpr (WARPS == CrossCta<true>::WARPS)
+    plan_line_here<TREE>(a, lane, all, tail);
+  else
+    plan_line_there<TREE>(a, lane, all, tail);
 }
 
 // A CTA per item: head blockIdx.y, and a row tile that is found by a search, 32
@@ -312,7 +324,7 @@ __device__ __forceinline__ void plan_one(const CrossArgs& a, int lane, Tail<WARP
 
 // By warp `me`, in a line: its next piece, into tail.now[me]; false behind the last.
 template <bool TREE, int WARPS>
-__device__ __noinline__ bool next_piece(const CrossArgs& a, Tail<WARPS>& tail, int me, int lane) {
+__device__ __forceinline__ bool next_piece_here(const CrossArgs& a, Tail<WARPS>& tail, int me, int lane) {
   Walk& walk = tail.walk[me];
   __syncwarp();  // (the piece before has been read)
   Walk w = walk;
@@ -355,6 +367,18 @@ __device__ __noinline__ bool next_piece(const CrossArgs& a, Tail<WARPS>& tail, i
   }
   __syncwarp();
   return true;
+}
+
+template <bool TREE, int WARPS>
+__device__ __noinline__ bool next_piece_there(const CrossArgs& a, Tail<WARPS>& tail, int me, int lane) {
+  return next_piece_here<TREE>(a, tail, me, lane);
+}
+template <bool TREE, int WARPS>
+__device__ __forceinline__ bool next_piece(const CrossArgs& a, Tail<WARPS>& tail, int me, int lane) {
+  if constexpr (WARPS == CrossCta<true>::WARPS)
+    return next_piece_here<TREE>(a, tail, me, lane);
+  else
+    return next_piece_there<TREE>(a, tail, me, lane);
 }
 
 // By a warp: which pieces this CTA computes.
@@ -746,6 +770,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     return next_piece<TREE>(a, tail, warp, lane) ? &tail.now[warp] : nullptr;
   };
 
+  if (FP8 && warp >= C::SOFTMAX_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == C::PRODUCER || warp == C::PRODUCER + 1) {
     // ------------------------------------------------------------- producers
     // Of all pieces, key block j's K is ring item 2 j, its V item 2 j + 1; item
@@ -829,24 +854,23 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     // V of key block j of a piece has landed; key slots past the last key may
     // hold anything (even NaN): their V rows are zeroed, so that 0 * V stays 0.
     // So are those of drafted keys that no token of the tile sees.
+    int drafts = 0;  // tokens of the piece's sequence
     auto v_ready = [&](const Piece& pc, int j, int iv) {
       const int valid = pc.L - (pc.j0 + j) * C::BK;
       if constexpr (TREE) {
-        const int d = valid - (pc.row0 + pc.n_rows) / a.G;  // keys of the block before the drafted ones
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-        if (d < C::BK) {
-          uint32_t seen[5] = {0u, 0u, 0u, 0u, 0u};
-          const int t0 = pc.row0 / a.G, t1 = (pc.row0 + min(pc.n_rows, C::ROWS) - 1) / a.G;
-          for (int tok = t0 + lane; tok <= t1; tok += 32) {
-            uint32_t m[5];
-            mask_words(a.mask + (int64_t(pc.first) + tok) * a.words, a.words, d, m);
+        const int d = valid - drafts;  // keys of the block before the drafted ones
+        if (d >= C::BK) return wait(B_READY + iv % C::NST, iv / C::NST);
+        uint32_t vis[4], seen[5] = {0u, 0u, 0u, 0u, 0u};
+        const int t0 = pc.row0 / a.G, t1 = (pc.row0 + min(pc.n_rows, C::ROWS) - 1) / a.G;
+        for (int tok = t0 + lane; tok <= t1; tok += 32) {
+          uint32_t m[5];
+          mask_words(a.mask + (int64_t(pc.first) + tok) * a.words, a.words, d, m);
 #pragma unroll
-            for (int i = 0; i < 5; ++i) seen[i] |= m[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 5; ++i) seen[i] = __reduce_or_sync(kFull, seen[i]);
-          visible(seen, d, valid, vis);
+          for (int i = 0; i < 5; ++i) seen[i] |= m[i];
         }
+#pragma unroll
+        for (int i = 0; i < 5; ++i) seen[i] = __reduce_or_sync(kFull, seen[i]);
+        visible(seen, d, valid, vis);
         if (!wait(B_READY + iv % C::NST, iv / C::NST)) return false;
         uint8_t* v = sm + C::OFF_RING + (iv % C::NST) * C::TILE;
         bool any = false;
@@ -878,6 +902,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     while (ok && (taken = take()) != nullptr) {
       const Piece pc = *taken;
       if (pc.nblk == 0) continue;
+      if (TREE) drafts = (pc.row0 + pc.n_rows) / a.G;
       if (pc.n_rows <= 128) {
         // narrow: A takes the even key blocks, B the odd ones, of the same rows
         const bool q_in = wait(B_Q, n_q);
@@ -895,10 +920,10 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
           tc_fence_after();
           pv(t, iv, j > 1);
           if (j + 2 < pc.nblk) {
+            release(iv);  // (K of the next block but one is waited for in the slot that V before this one left)
             if (!wait(B_READY + ik % C::NST, ik / C::NST)) break;
             tc_fence_after();
             qk(t, 0, ik);
-            release(iv);
             release(ik);
           } else {
             umma_commit_warp(bar(B_O + t));
@@ -954,13 +979,13 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     umma_commit_warp(bar(B_DONE));
     __syncwarp();
     mbar_wait(bar(B_DONE), 0);
-  } else if (FP8 && warp >= C::CONVERTER) {
+  } else if (FP8 && warp >= C::SOFTMAX_WARPS) {
     // ------------------------------------------------------------ converters
     // A warp turns 32 rows of every item (those that hold keys).
     bool ok = true;
     int item = 0;
     const Piece* taken;
-    while (ok && (taken = take()) != nullptr) {
+    while (warp >= C::CONVERTER && ok && (taken = take()) != nullptr) {
       const int nblk = taken->nblk, row0 = 32 * (warp - C::CONVERTER);
       int left = taken->L - taken->j0 * C::BK - row0;
       for (int j = 0; j < nblk && ok; ++j, left -= C::BK)
@@ -978,6 +1003,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
   } else {
     // --------------------------------------------------------- softmax warps
+    if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int t = warp >> 2;                       // row block
     const int r = (warp & 3) * 32 + lane;          // TMEM lane
     // this warp's lanes and the columns of S and, + 256 - 128 t, of O
@@ -1117,46 +1143,27 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
           if (!ok) break;
         }
         if (any) {
-          // (e4m3: 64 columns at a time, the first of them twice)
-          constexpr int kCols = FP8 ? 64 : 128;
-          float s[kCols];
-          float mx = -INFINITY;
-          // Columns [c0, c0 + kCols) of the row's scores, as far as it sees them, and
-          // their maximum on the raw scores (the scale is positive).
-          auto load_scores = [&](int c0) {
-            tmem_ld64(scol + c0, s);
-            if (!FP8) tmem_ld64(scol + c0 + 64, s + kCols - 64);
-            if (TREE && d < C::BK) {
-              uint32_t vis[4];
-              visible(m, d, valid, vis);
-              if (FP8 && c0) {
-                vis[0] = vis[2];
-                vis[1] = vis[3];
-              }
+          float s[128];
+          tmem_ld64(scol, s);
+          tmem_ld64(scol + 64, s + 64);
+          if (TREE && d < C::BK) {
+            uint32_t vis[4];
+            visible(m, d, valid, vis);
 #pragma unroll
-              for (int k = 0; k < kCols; ++k) s[k] = vis[k >> 5] >> (k & 31) & 1 ? s[k] : -INFINITY;
-            } else if (valid < C::BK) {
+            for (int k = 0; k < 128; ++k) s[k] = vis[k >> 5] >> (k & 31) & 1 ? s[k] : -INFINITY;
+          } else if (valid < C::BK) {
 #pragma unroll
-              for (int k = 0; k < kCols; ++k) s[k] = c0 + k < valid ? s[k] : -INFINITY;
-            }
-          };
-          auto add_maximum = [&]() {
-            float m4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(s[i], s[4 + i]);
-#pragma unroll
-            for (int k = 8; k < kCols; k += 8)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[k + i], s[k + 4 + i]);
-            const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * sl2;
-            mx = FP8 ? fmaxf(mx, top) : top;
-          };
-          load_scores(0);
-          add_maximum();
-          if (FP8) {
-            load_scores(64);
-            add_maximum();
+            for (int k = 0; k < 128; ++k) s[k] = k < valid ? s[k] : -INFINITY;
           }
+          // row maximum on the raw scores (the scale is positive)
+          float m4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(s[i], s[4 + i]);
+#pragma unroll
+          for (int k = 8; k < 128; k += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[k + i], s[k + 4 + i]);
+          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * sl2;
           float alpha = 1.f;
           bool rescale = false;
           if (mx > m_ref + C::RESCALE_LOG2 || (m_ref == -INFINITY && mx != -INFINITY)) {
@@ -1178,7 +1185,9 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
           }
           const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
-          auto weigh = [&](int q, uint32_t (&pk)[8]) {  // columns [16 q, 16 q + 16) of s
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t pk[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float x = s[16 * q + 2 * i], y = s[16 * q + 2 * i + 1];
@@ -1188,19 +1197,6 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
               add2(l4[(2 * i) & 3], l4[(2 * i + 1) & 3], x, y);
               pk[i] = FP8 ? pack_f16(x, y) : pack_bf16(x, y);
             }
-          };
-          if constexpr (FP8) {
-            uint32_t late[4][8];  // of the last 64 columns
-#pragma unroll
-            for (int q = 0; q < 4; ++q) weigh(q, late[q]);
-            load_scores(0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_st8(scol + 32 + 8 * q, late[q]);
-          }
-#pragma unroll
-          for (int q = 0; q < kCols / 16; ++q) {
-            uint32_t pk[8];
-            weigh(q, pk);
             tmem_st8(scol + 8 * q, pk);
           }
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
