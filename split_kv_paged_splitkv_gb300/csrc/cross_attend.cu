@@ -6,62 +6,60 @@ namespace splitkv {
 namespace {
 
 // Joins the partial results of the cut items (an item's pieces have consecutive
-// slots).  A unit is 32 rows of an item, a lane each; the CTAs take the units
-// of all cut items in turn (a CTA for every possible unit would be 1,216, of which
-// most calls have no use).  A warp takes every eighth group of four dims, which
-// lie side by side for the rows; the log-sum-exps and results of four pieces
-// are loaded at once, and the sums rescaled when later ones are larger.
-constexpr int kMergeWarps = 8, kMergeAtOnce = 4, kMergeGroups = 32 / kMergeWarps;
-__global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __grid_constant__ CrossArgs a, int units) {
-  __shared__ uint2 rows_out[32][33];  // bf16 rows (of 32 pieces of 8 bytes, and one to spread the banks)
-  launch_dependents();
-  wait_prerequisites();
+// slots).  A unit is 32 rows of an item, a lane each, and all 128 dims or, where there
+// are few (a call of one or two trees), a quarter of them; the CTAs take the units of all cut
+// items in turn (a CTA for every possible unit would be 1,216, of which most calls
+// have no use).  A warp takes every eighth group of four dims, which lie side by side
+// for the rows; the log-sum-exps and results of four pieces, of 16 with a quarter of the dims,
+// are loaded at once, and the sums rescaled, after every four, when later ones are
+// larger.
+constexpr int kMergeWarps = 8, kMergeAtOnce = 4;
+template <int PARTS>
+__device__ __forceinline__ void merge_unit(const CrossArgs& a, const CrossSplit& sp, int r0, int part, uint2 (&rows_out)[32][33]) {
+  constexpr int kGroups = 32 / kMergeWarps / PARTS, kDeep = kMergeAtOnce * PARTS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int last = *a.n_split * units;
-  for (int u = blockIdx.x; u < last; u += gridDim.x) {
-    const int q = u / units, r0 = (u - q * units) * 32;  // the q-th cut item, its rows from r0 on
-    const CrossSplit sp = a.split[q];
-    if (sp.cuts == 0 || r0 >= sp.rows) continue;
-    const int row = r0 + lane;
-    const bool live = row < sp.rows;
-    float M = -INFINITY, sum = 0.f;
-    float4 acc[kMergeGroups];
+  const int row = r0 + lane, g0 = part * (32 / PARTS) + warp;
+  const bool live = row < sp.rows;
+  float M = -INFINITY, sum = 0.f;
+  float4 acc[kGroups];
 #pragma unroll
-    for (int i = 0; i < kMergeGroups; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kGroups; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int k0 = 0; k0 < sp.cuts; k0 += kMergeAtOnce) {
-      float ls[kMergeAtOnce];
-      float4 v[kMergeAtOnce][kMergeGroups];
+  for (int k1 = 0; k1 < sp.cuts; k1 += kDeep) {
+    float ls[kDeep];
+    float4 v[kDeep][kGroups];
 #pragma unroll
-      for (int k = 0; k < kMergeAtOnce; ++k) {
-        const size_t slot = k0 + k ? (sp.slot & -sp.step) + (k0 + k) * sp.step : sp.slot;
-        const bool in = live && k0 + k < sp.cuts;
-        ls[k] = in ? a.lse_part[slot * a.part_rows + row] : -INFINITY;
+    for (int k = 0; k < kDeep; ++k) {
+      const size_t slot = k1 + k ? (sp.slot & -sp.step) + (k1 + k) * sp.step : sp.slot;
+      const bool in = live && k1 + k < sp.cuts;
+      ls[k] = in ? a.lse_part[slot * a.part_rows + row] : -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kMergeGroups; ++i)
-          if (in) v[k][i] = reinterpret_cast<const float4*>(a.o_part)[(slot * 32 + warp + i * kMergeWarps) * a.part_rows + row];
-      }
+      for (int i = 0; i < kGroups; ++i)
+        if (in) v[k][i] = reinterpret_cast<const float4*>(a.o_part)[(slot * 32 + g0 + i * kMergeWarps) * a.part_rows + row];
+    }
+#pragma unroll
+    for (int k0 = 0; k0 < kDeep; k0 += kMergeAtOnce) {
       float m = M;
 #pragma unroll
-      for (int k = 0; k < kMergeAtOnce; ++k) m = max_nan(m, ls[k]);  // (a NaN piece makes the row NaN)
+      for (int k = k0; k < k0 + kMergeAtOnce; ++k) m = max_nan(m, ls[k]);  // (a NaN piece makes the row NaN)
       if (m == -INFINITY) continue;
       const float old = ex2((M - m) * 1.4426950408889634f);
       M = m;
       sum *= old;
 #pragma unroll
-      for (int i = 0; i < kMergeGroups; ++i) {
+      for (int i = 0; i < kGroups; ++i) {
         acc[i].x *= old;
         acc[i].y *= old;
         acc[i].z *= old;
         acc[i].w *= old;
       }
 #pragma unroll
-      for (int k = 0; k < kMergeAtOnce; ++k) {
+      for (int k = k0; k < k0 + kMergeAtOnce; ++k) {
         if (ls[k] == -INFINITY) continue;  // (a piece that is none, or without weight)
         const float w = ex2((ls[k] - m) * 1.4426950408889634f);
         sum += w;
 #pragma unroll
-        for (int i = 0; i < kMergeGroups; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
           acc[i].x += w * v[k][i].x;
           acc[i].y += w * v[k][i].y;
           acc[i].z += w * v[k][i].z;
@@ -69,23 +67,45 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __g
         }
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    __syncthreads();  // (the rows of the unit before are out)
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __syncthreads();  // (the rows of the unit before are out)
 #pragma unroll
-    for (int i = 0; i < kMergeGroups; ++i)
-      rows_out[lane][warp + i * kMergeWarps] =
-          make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
-    __syncthreads();
-    // whole rows out, a warp to a row
-    for (int i = warp; i < 32 && r0 + i < sp.rows; i += kMergeWarps) {
-      const int tok = (sp.row0 + r0 + i) / a.G, g = (sp.row0 + r0 + i) - tok * a.G;
-      const size_t out_row = (size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g;
-      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128)[lane] = rows_out[i][lane];
-    }
-    if (warp == 0 && live && a.lse) {
-      const int tok = (sp.row0 + row) / a.G, g = (sp.row0 + row) - tok * a.G;
-      a.lse[(size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g] = sum == 0.f ? -INFINITY : M + lg2(sum) * kLn2;
-    }
+  for (int i = 0; i < kGroups; ++i)
+    rows_out[lane][warp + i * kMergeWarps] =
+        make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv), pack_bf16(acc[i].z * inv, acc[i].w * inv));
+  __syncthreads();
+  // whole rows (or quarters) out, a warp to PARTS rows
+  constexpr int kLanes = 32 / PARTS;
+  for (int i = warp * PARTS + lane / kLanes; i < 32 && r0 + i < sp.rows; i += kMergeWarps * PARTS) {
+    const int tok = (sp.row0 + r0 + i) / a.G, g = (sp.row0 + r0 + i) - tok * a.G;
+    const size_t out_row = (size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g;
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + out_row * 128)[part * kLanes + lane % kLanes] =
+        rows_out[i][lane % kLanes];
+  }
+  if (warp == 0 && part == 0 && live && a.lse) {
+    const int tok = (sp.row0 + row) / a.G, g = (sp.row0 + row) - tok * a.G;
+    a.lse[(size_t(sp.first) + tok) * a.Hq + size_t(sp.head) * a.G + g] = sum == 0.f ? -INFINITY : M + lg2(sum) * kLn2;
+  }
+}
+
+__global__ void __launch_bounds__(kMergeWarps * 32) cross_merge_kernel(const __grid_constant__ CrossArgs a, int units) {
+  __shared__ uint2 rows_out[32][33];  // bf16 rows (of 32 pieces of 8 bytes, and one to spread the banks)
+  launch_dependents();
+  wait_prerequisites();
+  const int last = *a.n_split * units;
+  if (4 * last <= int(gridDim.x)) {
+    const int u = blockIdx.x >> 2, q = u / units, r0 = (u - q * units) * 32;
+    if (u >= last) return;
+    const CrossSplit sp = a.split[q];
+    if (sp.cuts != 0 && r0 < sp.rows) merge_unit<4>(a, sp, r0, blockIdx.x & 3, rows_out);
+    return;
+  }
+  for (int u = blockIdx.x; u < last; u += gridDim.x) {
+    const int q = u / units, r0 = (u - q * units) * 32;  // the q-th cut item, its rows from r0 on
+    const CrossSplit sp = a.split[q];
+    if (sp.cuts == 0 || r0 >= sp.rows) continue;
+    merge_unit<1>(a, sp, r0, 0, rows_out);
   }
 }
 

@@ -167,9 +167,13 @@ constexpr int kManyPieces = 32767;
 static_assert(kMaxPieces * kSmCount * 32 <= kManyPieces && int64_t(kManyPieces) * 65535 < (int64_t(1) << 31), "no call's count");
 constexpr int kPieceCost = 2, kCutCost = 2;  // in key blocks: of each piece, and of cutting anything
 constexpr int kLineCost = 8;  // and of a line of all key blocks
+// What an item takes of a line beside its key blocks: with it the parts of a tree's
+// line cost the same whatever the items' lengths are.
+template <bool TREE>
+constexpr int kWalkCost = TREE ? 10 : 0;
 
-// Where a warp is in a line: the next key block, and the item that holds it (of
-// sequence b, from block `off` on) with its sequence's numbers.
+// Where a warp is in a line: the next key block (or what an item takes beside them), and
+// the item that holds it (of sequence b, from block `off` on) with its sequence's numbers.
 struct Walk {
   int64_t x;
   int b, item, off, first, rows, L, tiles, nb;
@@ -242,7 +246,7 @@ __device__ __forceinline__ void plan_line_here(const CrossArgs& a, int lane, int
   int64_t passed = 0, total;
   for (int b0 = 0; lo < hi && b0 < a.batch; b0 += 32) {
     const Lane s = lane_of<TREE>(a, b0 + lane);
-    const int64_t n = int64_t(s.tiles) * a.Hkv * s.nb;
+    const int64_t n = int64_t(s.tiles) * a.Hkv * (s.nb + kWalkCost<TREE>);
     const int64_t at = passed + lanes_before(n, lane, &total);
     const unsigned m = __ballot_sync(kFull, lo >= at && lo < at + n);
     passed += total;
@@ -255,8 +259,9 @@ __device__ __forceinline__ void plan_line_here(const CrossArgs& a, int lane, int
       w.tiles = __shfl_sync(kFull, s.tiles, f);
       w.nb = __shfl_sync(kFull, s.nb, f);
       const int64_t in = lo - __shfl_sync(kFull, at, f);
-      w.item = int(in / w.nb);
-      w.off = int(in - int64_t(w.item) * w.nb);
+      const int each = w.nb + kWalkCost<TREE>;
+      w.item = int(in / each);
+      w.off = int(in - int64_t(w.item) * each);
       break;
     }
   }
@@ -328,8 +333,24 @@ __device__ __forceinline__ bool next_piece_here(const CrossArgs& a, Tail<WARPS>&
   Walk& walk = tail.walk[me];
   __syncwarp();  // (the piece before has been read)
   Walk w = walk;
+  auto item_done = [&]() {  // (off: behind its last block)
+    w.x += w.nb + kWalkCost<TREE> - w.off;
+    if (w.x >= tail.hi) return;
+    w.off = 0;
+    if (++w.item == w.tiles * a.Hkv) {  // the next sequence with tokens
+      w.item = 0;
+      Lane s;
+      do s = lane_of<TREE>(a, ++w.b); while (s.tiles == 0 && w.b < a.batch);
+      w.first = s.first;
+      w.rows = s.rows;
+      w.L = s.L;
+      w.tiles = s.tiles;
+      w.nb = s.nb;
+    }
+  };
+  if (TREE && w.x < tail.hi && w.off >= w.nb) item_done();  // (the line's part begins behind an item's blocks)
   if (w.x >= tail.hi) return false;
-  const int len = int(min(int64_t(w.nb - w.off), tail.hi - w.x));
+  const int len = int(min(int64_t(w.nb - w.off), tail.hi - w.x));  // blocks
   Piece q;
   q.b = w.b;
   q.h = w.tiles > 1 ? w.item / w.tiles : w.item;
@@ -347,19 +368,7 @@ __device__ __forceinline__ bool next_piece_here(const CrossArgs& a, Tail<WARPS>&
   }
   w.x += len;
   w.off += len;
-  if (w.off == w.nb && w.x < tail.hi) {
-    w.off = 0;
-    if (++w.item == w.tiles * a.Hkv) {  // the next sequence with tokens
-      w.item = 0;
-      Lane s;
-      do s = lane_of<TREE>(a, ++w.b); while (s.tiles == 0 && w.b < a.batch);
-      w.first = s.first;
-      w.rows = s.rows;
-      w.L = s.L;
-      w.tiles = s.tiles;
-      w.nb = s.nb;
-    }
-  }
+  if (w.off == w.nb && w.x < tail.hi) item_done();
   __syncwarp();
   if (lane == 0) {
     tail.now[me] = q;
@@ -406,7 +415,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail<W
   int64_t all = 0;  // key blocks
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     read(b0);
-    const int64_t blocks = int64_t(mine.tiles) * a.Hkv * mine.nb;
+    const int64_t blocks = int64_t(mine.tiles) * a.Hkv * (mine.nb + kWalkCost<TREE>);
     if (a.line) {
       int64_t sum;
       lanes_before(blocks, lane, &sum);
@@ -439,7 +448,7 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail<W
   const float T = __shfl_sync(kFull, t, best);
   const int P = __shfl_sync(kFull, n, best);
   const int64_t share = (all + a.parts - 1) / a.parts;
-  if (widest <= 128 && all >= a.parts && all < (1 << 25) && share <= 2 * int64_t(shortest) &&
+  if ((TREE || widest <= 128) && all >= a.parts && all < (1 << 25) && (TREE || share <= 2 * int64_t(shortest)) &&
       share + kLineCost < __shfl_sync(kFull, cost, best)) {
     plan_line<TREE>(a, lane, all, tail);
     return;
