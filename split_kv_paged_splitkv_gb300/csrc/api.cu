@@ -132,6 +132,32 @@ splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_
   return SPLITKV_OK;
 }
 
+// A map over [tokens][Hq][128] bf16 rows, `stride` elements to a token.
+static splitkv_status make_rows_map(TmaDesc* out, const void* base, int64_t tokens, int heads, int64_t stride, int G) {
+  auto fn = encode_fn();
+  if (!fn) return fail(SPLITKV_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  CUtensorMap m;
+  cuuint64_t gdim[4] = {64u, 2u, cuuint64_t(heads), cuuint64_t(tokens)};
+  cuuint64_t gstride[3] = {128u, 256u, cuuint64_t(stride) * 2};
+  cuuint32_t box[4] = {64u, 1u, cuuint32_t(G), cuuint32_t(kRowBoxRows / G)};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  CUresult r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gdim, gstride, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SPLITKV_ECUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  std::memcpy(out, &m, sizeof(m));
+  return SPLITKV_OK;
+}
+
+splitkv_status make_cross_maps(CrossMaps* maps, const CrossArgs& a, const void* k_pages, const void* v_pages,
+                               const splitkv_desc_t& d) {
+  splitkv_status st = make_half_map(&maps->k, k_pages, d, a.box_rows);
+  if (st == SPLITKV_OK) st = make_half_map(&maps->v, v_pages, d, a.box_rows);
+  if (st == SPLITKV_OK && a.row_boxes) st = make_rows_map(&maps->q, a.q, a.n_tokens, a.Hq, a.q_stride, a.G);
+  if (st == SPLITKV_OK && a.row_boxes) st = make_rows_map(&maps->out, a.out, a.n_tokens, a.Hq, int64_t(a.Hq) * 128, a.G);
+  return st;
+}
+
 splitkv_status make_mla_maps(TmaDesc* tk, TmaDesc* tv, const void* k_pages, const void* v_pages,
                              const splitkv_desc_t& d) {
   const int64_t rows_total = int64_t(d.num_pages_total) * d.num_kv_heads * d.page_size;

@@ -98,6 +98,7 @@ void fill_cross(CrossArgs& a, const splitkv_desc_t& d, int32_t n_tokens, void* w
   a.max_pages = d.max_pages_per_seq;
   a.num_pages = d.num_pages_total;
   a.box_rows = cross_box_rows(d);
+  a.row_boxes = d.kv_dtype == SPLITKV_BF16 && kRowBoxRows % a.G == 0;
 }
 
 // Moves of one (sequence, head), at most: the kept keys behind the budget.
@@ -553,11 +554,10 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
   a.status = status;
   a.q_stride = q_stride;
   a.qk_scale_log2 = scale * kLog2e;
-  TmaDesc tk, tv;
-  st = make_half_map(&tk, k_pages, d, a.box_rows);
-  if (st == SPLITKV_OK) st = make_half_map(&tv, v_pages, d, a.box_rows);
+  CrossMaps maps{};
+  st = make_cross_maps(&maps, a, k_pages, v_pages, d);
   if (st != SPLITKV_OK) return st;
-  cudaError_t e = launch_cross(a, cross_row_tiles(d, n_tokens), tk, tv, stream);
+  cudaError_t e = launch_cross(a, cross_row_tiles(d, n_tokens), maps, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launching the cross attention kernels");
   return SPLITKV_OK;
 }
@@ -676,11 +676,10 @@ splitkv_status splitkv_tree_attend(const splitkv_desc_t* desc, int32_t n_tokens,
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.o_scale = o_scale;
-  TmaDesc tk, tv;
-  st = make_half_map(&tk, k_pages, d, a.box_rows);
-  if (st == SPLITKV_OK) st = make_half_map(&tv, v_pages, d, a.box_rows);
+  CrossMaps maps{};
+  st = make_cross_maps(&maps, a, k_pages, v_pages, d);
   if (st != SPLITKV_OK) return st;
-  cudaError_t e = launch_tree(a, cross_row_tiles(d, n_tokens), tk, tv, fp8, stream);
+  cudaError_t e = launch_tree(a, cross_row_tiles(d, n_tokens), maps, fp8, stream);
   if (e != cudaSuccess) return cuda_fail(e, "launching the tree attention kernels");
   return SPLITKV_OK;
 }

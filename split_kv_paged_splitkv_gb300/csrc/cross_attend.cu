@@ -142,8 +142,8 @@ int cross_box_rows(const splitkv_desc_t& d) {
   return br;
 }
 
-cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv, void* stream) {
-  cudaError_t e = launch_cross_kernel<false, false>(a, tk, tv, stream);
+cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const CrossMaps& maps, void* stream) {
+  cudaError_t e = launch_cross_kernel<false, false>(a, maps, stream);
   return e == cudaSuccess ? launch_cross_merge(a, row_tiles, stream) : e;
 }
 

@@ -22,6 +22,10 @@
 // QK_B(j+1), ...; they execute in that order, which makes the barrier of a
 // finished S also say that the PV before it is done (P read, O at rest).
 //
+// Where a power of two of at most 32 query heads share a KV head, 32 rows of it are a
+// box of the queries' and the results' tensors: a warp's Q comes, and its whole results
+// go, by TMA.  (Others by 16 bytes a lane, row by row: MEASURED.)
+//
 // K and V blocks pass in that order through one ring of five 32 KB slots that
 // two producer warps fill by TMA, each a 64-column half of every slot, one box
 // per page piece, 128-byte swizzled; K is read K-major, V with its dims on N.
@@ -109,7 +113,7 @@ struct CrossCta : Cross {
 };
 
 enum {
-  B_Q = 0,                       // [2] Q of a row block in shared memory (128 threads)
+  B_Q = 0,                       // [2] Q of a row block in shared memory (128 threads, or 4 warps' copies)
   B_FULL = 2,                    // [NST]
   B_EMPTY = B_FULL + Cross::NST, // [NST]
   B_S = B_EMPTY + Cross::NST,    // [2] S of a row block complete
@@ -124,6 +128,7 @@ enum {
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kRowBox = kRowBoxRows;  // query rows, or rows of the result, of a warp's box
 
 // The length of sequence b, or 0 where the device value is not one the cache
 // can hold.
@@ -725,7 +730,8 @@ __device__ __forceinline__ void convert_rows(uint8_t* raw, int rows, int lane) {
 template <bool TREE, bool FP8>
 __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     cross_attend_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv) {
+                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq,
+                        const __grid_constant__ CUtensorMap to) {
   static_assert(TREE || !FP8, "e4m3 caches are served with TREE");
   using C = CrossCta<FP8>;
   extern __shared__ uint8_t smem_raw[];
@@ -743,7 +749,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       if (FP8) mbar_init(bar(B_CONV + s), 4);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(B_Q + t), 128);
+      mbar_init(bar(B_Q + t), !FP8 && a.row_boxes ? 4 : 128);
       mbar_init(bar(B_S + t), 1);
       mbar_init(bar(B_P + t), 128);
       mbar_init(bar(B_O + t), 1);
@@ -758,6 +764,10 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     if (lane == 0) {
       prefetch_tmap(&tk);
       prefetch_tmap(&tv);
+      if (a.row_boxes) {
+        prefetch_tmap(&tq);
+        prefetch_tmap(&to);
+      }
     }
   }
   launch_dependents();
@@ -871,6 +881,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
         if (d >= C::BK) return wait(B_READY + iv % C::NST, iv / C::NST);
         uint32_t vis[4], seen[5] = {0u, 0u, 0u, 0u, 0u};
         const int t0 = pc.row0 / a.G, t1 = (pc.row0 + min(pc.n_rows, C::ROWS) - 1) / a.G;
+#pragma unroll 2
         for (int tok = t0 + lane; tok <= t1; tok += 32) {
           uint32_t m[5];
           mask_words(a.mask + (int64_t(pc.first) + tok) * a.words, a.words, d, m);
@@ -882,15 +893,16 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
         visible(seen, d, valid, vis);
         if (!wait(B_READY + iv % C::NST, iv / C::NST)) return false;
         uint8_t* v = sm + C::OFF_RING + (iv % C::NST) * C::TILE;
-        bool any = false;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          for (uint32_t hidden = ~vis[w]; hidden; hidden &= hidden - 1) {
-            const int row = 32 * w + __ffs(hidden) - 1;
-            if (lane < 16) *reinterpret_cast<uint4*>(v + (lane & 1) * C::HALF + row * 128 + (lane >> 1) * 16) = make_uint4(0, 0, 0, 0);
-            any = true;
-          }
-        if (any) {
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t x = w < 2 ? (w ? vis[1] : vis[0]) : (w == 2 ? vis[2] : vis[3]);
+          if (~x >> lane & 1)
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i)  // (in eight orders, so that the lanes write to all banks)
+              *reinterpret_cast<uint4*>(v + (i & 1) * C::HALF + (32 * w + lane) * 128 + (((i >> 1) + lane) & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+        }
+        if ((vis[0] & vis[1] & vis[2] & vis[3]) != ~0u) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
@@ -1026,13 +1038,13 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       return sm + t * C::TILE + (ch >> 3) * C::HALF + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4);
     };
     // Visits this warp's 32 rows of a piece, 16 lanes to a row: body(row of the
-    // row block, whether it exists, its token and head).  Rolled, as is all
-    // that runs once for a piece: such code waits for its own instructions.
+    // row block, whether it exists, its token and head).  Rolled, but for four rows at
+    // once, as is all that runs once for a piece: such code waits for its own instructions.
     auto each_row = [&](const Piece& q, auto&& body) {
       int rr = (warp & 3) * 32 + (lane >> 4);
       const int first = q.row0 + t * 128 + rr;  // (not called for B's share of a narrow piece)
       int tok = first / a.G, g = first - tok * a.G;
-#pragma unroll 1
+#pragma unroll 4
       for (int i = 0; i < 16; ++i, rr += 2) {
         body(rr, t * 128 + rr < q.n_rows, int64_t(q.first) + tok, q.h * a.G + g);
         for (g += 2; g >= a.G; g -= a.G) ++tok;
@@ -1090,6 +1102,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     // their way into shared memory (rows behind the last are zero).  Not before
     // the products that read the Q before are done.
     const Piece* next = nullptr;
+    int n_q_boxes = 0;  // pieces whose Q came by boxes
     auto take_piece = [&]() {
       do {
         next = take();
@@ -1099,13 +1112,28 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
         if (next->nblk > 0) query_rows(*next);
         return true;
       }
-      if (next->nblk > 0 && (t == 0 || next->n_rows > 128))
+      if (next->nblk == 0 || (t == 1 && next->n_rows <= 128)) return true;
+      if (a.row_boxes) {
+        // (rows of other sequences' tokens behind the last come along, and are not used)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          mbar_arrive_expect_tx(bar(B_Q + t), 2 * kRowBox * 128);
+          const int token = next->first + (next->row0 + t * 128 + (warp & 3) * kRowBox) / a.G;
+          for (int half = 0; half < 2; ++half)
+            tma_load_4d(smem_u32(sm + t * C::TILE + half * C::HALF + (warp & 3) * kRowBox * 128), &tq, bar(B_Q + t), 0, half,
+                        next->h * a.G, token);
+        }
+        ++n_q_boxes;
+      } else {
         each_row(*next, [&](int rr, bool in, int64_t token, int head) {
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (in ? token * a.q_stride + head * 128 : 0);
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(chunk_at(rr, lane & 15))),
                        "l"(src + 8 * (lane & 15)), "r"(in ? 16 : 0)
                        : "memory");
         });
+      }
       return true;
     };
     uint32_t n_ml = 0, n_ob = 0;  // phases of B_ML and, seen by A, of B's B_O
@@ -1128,7 +1156,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       // column's rows side by side), and one of a few rows, straight from
       // registers, with the next piece's Q already on its way.
       const bool staged = whole && !narrow;
-      if (pc.nblk > 0 && (t == 0 || !narrow)) {
+      if (pc.nblk > 0 && (t == 0 || !narrow) && (FP8 || !a.row_boxes)) {
         if (!FP8) asm volatile("cp.async.wait_all;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(bar(B_Q + t));
@@ -1293,7 +1321,16 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
               dst[size_t(i) * a.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
-        if (staged) {
+        if (staged && !FP8 && a.row_boxes && t * 128 + (warp & 3) * kRowBox + kRowBox <= pc.n_rows) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            const int token = pc.first + (pc.row0 + t * 128 + (warp & 3) * kRowBox) / a.G;
+            for (int half = 0; half < 2; ++half)
+              tma_store_4d(&to, smem_u32(sm + t * C::TILE + half * C::HALF + (warp & 3) * kRowBox * 128), 0, half, pc.h * a.G, token);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else if (staged) {
           __syncwarp();
           each_row(pc, [&](int rr, bool in, int64_t token, int head) {
             if (in)
@@ -1313,7 +1350,11 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       }
       if (staged) more = take_piece();
     }
-    if (!FP8) asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out)
+    if (!FP8) {
+      asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out)
+      if (!ok && n_q_boxes > 0) mbar_wait(bar(B_Q + t), (n_q_boxes - 1) & 1);
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
   }
 
@@ -1327,7 +1368,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
 }
 
 template <bool TREE, bool FP8>
-cudaError_t launch_cross_kernel(const CrossArgs& a, const TmaDesc& tk, const TmaDesc& tv, void* stream) {
+cudaError_t launch_cross_kernel(const CrossArgs& a, const CrossMaps& maps, void* stream) {
   using C = CrossCta<FP8>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(cross_attend_kernel<TREE, FP8>), C::SMEM, allowed);
@@ -1343,8 +1384,9 @@ cudaError_t launch_cross_kernel(const CrossArgs& a, const TmaDesc& tk, const Tma
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = la;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cross_attend_kernel<TREE, FP8>, a, *reinterpret_cast<const CUtensorMap*>(&tk),
-                            *reinterpret_cast<const CUtensorMap*>(&tv));
+  return cudaLaunchKernelEx(&cfg, cross_attend_kernel<TREE, FP8>, a, *reinterpret_cast<const CUtensorMap*>(&maps.k),
+                            *reinterpret_cast<const CUtensorMap*>(&maps.v), *reinterpret_cast<const CUtensorMap*>(&maps.q),
+                            *reinterpret_cast<const CUtensorMap*>(&maps.out));
 }
 
 }  // namespace

@@ -279,6 +279,7 @@ struct CrossArgs {
   int32_t parts;      // CTAs that share all items' key blocks; 0: a CTA per item
   int32_t line;       // an even line of all items' key blocks, whatever their lengths
   int32_t part_rows;  // rows of an item, at most
+  int32_t row_boxes;  // queries and whole results of bf16 caches pass by TMA
   // of drafted trees (TREE):
   const uint32_t* mask;  // [n_tokens][words]
   const float* k_scale;  // e4m3 per-KV-head scales or null: in qk_scale_log2, and o_scale
@@ -300,16 +301,24 @@ enum class CrossDeal { kPieces, kLine, kItems };
 CrossDeal cross_deal(const splitkv_desc_t& d, int64_t n_tokens);
 int cross_part_rows(const splitkv_desc_t& d, int64_t n_tokens);
 int cross_box_rows(const splitkv_desc_t& d);  // keys of one TMA box
-cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv,
-                         void* stream);
+// Cross attention's tensor maps; with row_boxes also of the queries and the results,
+// coordinates (64 columns, column half, head, token), boxes of kRowBoxRows rows (the
+// heads that share a KV head, of as many tokens as that makes).
+constexpr int kRowBoxRows = 32;
+struct CrossMaps {
+  TmaDesc k, v, q, out;
+};
+cudaError_t launch_cross(const CrossArgs& a, int64_t row_tiles, const CrossMaps& maps, void* stream);
 cudaError_t launch_cross_merge(const CrossArgs& a, int64_t row_tiles, void* stream);  // (both kinds')
-cudaError_t launch_tree(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv, bool fp8,
-                        void* stream);
+cudaError_t launch_tree(const CrossArgs& a, int64_t row_tiles, const CrossMaps& maps, bool fp8, void* stream);
 // Tensor map over a pool of 128-wide rows, coordinates (columns, key in page,
 // column half, KV head, page) in either layout: boxes of `keys` keys and one
 // column half, 128-byte swizzle, of bf16; of `keys` keys and whole rows, as they lie,
 // of e4m3 (one "half") (api.cu).
 splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys);
+// The maps of a call of cross attention's kernel (api.cu).
+splitkv_status make_cross_maps(CrossMaps* maps, const CrossArgs& a, const void* k_pages, const void* v_pages,
+                               const splitkv_desc_t& d);
 // The MLA family's maps of the latent rows and, with v_shares_k = 0, of the separate
 // values (else tv is left as it is) (api.cu).
 splitkv_status make_mla_maps(TmaDesc* tk, TmaDesc* tv, const void* k_pages, const void* v_pages,

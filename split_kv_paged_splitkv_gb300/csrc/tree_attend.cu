@@ -4,8 +4,8 @@
 
 namespace splitkv {
 
-cudaError_t launch_tree(const CrossArgs& a, int64_t row_tiles, const TmaDesc& tk, const TmaDesc& tv, bool fp8, void* stream) {
-  cudaError_t e = fp8 ? launch_cross_kernel<true, true>(a, tk, tv, stream) : launch_cross_kernel<true, false>(a, tk, tv, stream);
+cudaError_t launch_tree(const CrossArgs& a, int64_t row_tiles, const CrossMaps& maps, bool fp8, void* stream) {
+  cudaError_t e = fp8 ? launch_cross_kernel<true, true>(a, maps, stream) : launch_cross_kernel<true, false>(a, maps, stream);
   return e == cudaSuccess ? launch_cross_merge(a, row_tiles, stream) : e;
 }
 
