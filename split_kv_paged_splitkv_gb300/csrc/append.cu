@@ -90,6 +90,72 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int batch, int n, int
   return ended < batch && cu[0] <= n ? ended : -1;
 }
 
+// Where the key of token n of sequence b (-1: padding) goes; what is wrong with it goes
+// to the status, if this thread reports.
+__device__ __forceinline__ Token place_in(const AppendArgs& a, int b, int n, bool report) {
+  Token t;
+  t.b = b;
+  t.page = -1;
+  t.slot = t.in_page = 0;
+  if (t.b >= 0) {
+    const int64_t cap = int64_t(a.max_pages) * a.P;
+    const int64_t end = a.cu ? a.cu[t.b + 1] : int64_t(t.b + 1) * a.T;
+    const int64_t slot = int64_t(a.seq_lens[t.b]) - (end - n);
+    int err = 0;
+    if (slot < 0 || slot >= cap) {
+      err = SPLITKV_DEVERR_SEQLEN;
+    } else {
+      const int lp = int(slot) / a.P;
+      const int ph = a.block_table[size_t(t.b) * a.max_pages + lp];
+      if (ph < 0 || ph >= a.num_pages) {
+        err = SPLITKV_DEVERR_PAGE;
+      } else {
+        t.page = ph;
+        t.slot = int(slot);
+        t.in_page = int(slot) - lp * a.P;
+      }
+    }
+    if (err && report && a.status) atomicOr(a.status, err);
+  }
+  return t;
+}
+
+// The same by a warp.
+__device__ __forceinline__ Token place_of(const AppendArgs& a, int n, int lane, bool report) {
+  return place_in(a, a.cu ? find_seq(a.cu, a.batch, n, lane) : n / a.T, n, report && lane == 0);
+}
+
+// The sines and cosines of a CTA's tokens (see `cs` of the kernels).
+__device__ __forceinline__ void sines(const AppendArgs& a, int n0, int ntok, float4* cs) {
+  const int half = a.rope.rot_dim / 2;
+  const int chunk_pairs = a.rope.pairing == SPLITKV_ROPE_HALVES ? 8 : 4, turned = half / chunk_pairs;
+  for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
+    const int t = i / half, p = i - t * half;
+    const int64_t pos = a.positions[size_t(a.rope.axis[p]) * a.n_tokens + n0 + t];
+    const uint64_t phase = uint64_t(pos) * a.rope.turns[p];
+    float s, c;
+    sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s, &c);
+    const int ch = p / chunk_pairs, e = p - ch * chunk_pairs;
+    float* z = reinterpret_cast<float*>(cs + t * (kMaxRotPairs / 2) + (e >> 1) * turned + ch) + (e & 1);
+    z[0] = c;
+    z[2] = s;
+  }
+}
+
+// The state of a CTA's new keys.
+template <int THREADS = kThreads>
+__device__ __forceinline__ void new_state(const AppendArgs& a, int n0, int ntok, const Token* tok, int thread = threadIdx.x) {
+  if (a.key_weights || a.key_positions) {
+    for (int i = thread; i < ntok * a.Hkv; i += THREADS) {
+      const int t = i / a.Hkv, h = i - t * a.Hkv;
+      if (tok[t].page < 0) continue;
+      const size_t at = (size_t(tok[t].b) * a.Hkv + h) * (size_t(a.max_pages) * a.P) + tok[t].slot;
+      if (a.key_weights) a.key_weights[at] = 0.f;
+      if (a.key_positions) a.key_positions[at] = a.positions[n0 + t];
+    }
+  }
+}
+
 // f * factor * weight, the weight of chunk c of its row (null: ones).
 __device__ __forceinline__ void normed(float (&f)[8], float factor, const float* weight, int c) {
 #pragma unroll
@@ -110,7 +176,7 @@ __device__ __forceinline__ float squares(const float (&f)[8]) {
 
 constexpr int kPasses = 5;  // over a CTA's units, at most
 
-// U: units of a thread in flight.  NORM: rows may be normalised (a.norm_q, a.norm_k).
+// U: units of a thread in flight.  NORM: the first DV columns of the (latent) keys are normalised.
 template <int DK, int DV, bool FP8, int U, bool NORM>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a,
                                                           int tok_per_cta) {
@@ -119,8 +185,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   // Cosines and sines of two pairs of a chunk to a float4 (c, c, s, s), the
   // chunks of a row side by side: its lanes read consecutive 16 bytes.
   __shared__ float4 cs[kMaxTok * kMaxRotPairs / 2];
-  constexpr bool LATENT = DK != DV;           // rows of 576: the first DV columns of the keys are normalised
-  __shared__ float factor[NORM && LATENT ? kMaxTok : 1];  // of the tokens' latent rows
+  static_assert(!NORM || DK != DV, "rows of 128 are normalised by append_rows_kernel");
+  __shared__ float factor[NORM ? kMaxTok : 1];  // of the tokens' latent rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   launch_dependents();
@@ -199,32 +265,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       // where the tokens' keys go, and their sines and cosines
       for (int i = warp; i < ntok; i += kThreads / 32) {
         const int n = n0 + i;
-        Token t;
-        t.b = a.cu ? find_seq(a.cu, a.batch, n, lane) : n / a.T;
-        t.page = -1;
-        t.slot = t.in_page = 0;
-        if (t.b >= 0) {
-          const int64_t cap = int64_t(a.max_pages) * a.P;
-          const int64_t end = a.cu ? a.cu[t.b + 1] : int64_t(t.b + 1) * a.T;
-          const int64_t slot = int64_t(a.seq_lens[t.b]) - (end - n);
-          int err = 0;
-          if (slot < 0 || slot >= cap) {
-            err = SPLITKV_DEVERR_SEQLEN;
-          } else {
-            const int lp = int(slot) / a.P;
-            const int ph = a.block_table[size_t(t.b) * a.max_pages + lp];
-            if (ph < 0 || ph >= a.num_pages) {
-              err = SPLITKV_DEVERR_PAGE;
-            } else {
-              t.page = ph;
-              t.slot = int(slot);
-              t.in_page = int(slot) - lp * a.P;
-            }
-          }
-          if (err && lane == 0 && a.status && blockIdx.y == 0) atomicOr(a.status, err);
-        }
+        const Token t = place_of(a, n, lane, blockIdx.y == 0);
         if (lane == 0) tok[i] = t;
-        if (NORM && LATENT && a.norm_k) {
+        if (NORM) {
           const uint4* src = reinterpret_cast<const uint4*>(k + int64_t(i) * int(a.k_stride));
           float x = 0.f;
 #pragma unroll
@@ -238,28 +281,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
           if (lane == 0) factor[i] = rsqrtf(fmaf(x, 1.f / DV, a.eps));
         }
       }
-      for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
-        const int t = i / half, p = i - t * half;
-        const int64_t pos = a.positions[size_t(a.rope.axis[p]) * a.n_tokens + n0 + t];
-        const uint64_t phase = uint64_t(pos) * a.rope.turns[p];
-        float s, c;
-        sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s, &c);
-        const int ch = p / chunk_pairs, e = p - ch * chunk_pairs;
-        float* z = reinterpret_cast<float*>(cs + t * (kMaxRotPairs / 2) + (e >> 1) * turned + ch) + (e & 1);
-        z[0] = c;
-        z[2] = s;
-      }
+      sines(a, n0, ntok, cs);
       __syncthreads();
-      // the state of the new keys
-      if (blockIdx.y == 0 && (a.key_weights || a.key_positions)) {
-        for (int i = threadIdx.x; i < ntok * a.Hkv; i += kThreads) {
-          const int t = i / a.Hkv, h = i - t * a.Hkv;
-          if (tok[t].page < 0) continue;
-          const size_t at = (size_t(tok[t].b) * a.Hkv + h) * (size_t(a.max_pages) * a.P) + tok[t].slot;
-          if (a.key_weights) a.key_weights[at] = 0.f;
-          if (a.key_positions) a.key_positions[at] = a.positions[n0 + t];
-        }
-      }
+      if (blockIdx.y == 0) new_state(a, n0, ntok, tok);
     }
 #pragma unroll
     for (int r = 0; r < U; ++r) {
@@ -270,21 +294,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       float f0[8], f1[8];
       unpack8(x0[r], f0);
       unpack8(x1[r], f1);
-      if (NORM && LATENT) {
-        if (kind == 1 && a.norm_k) {
-          if (c0 < DV / 8) normed(f0, factor[t], a.k_weight, c0);
-          if (c1 < DV / 8) normed(f1, factor[t], a.k_weight, c1);
-        }
-      } else if (NORM && kind < 2 && (kind ? a.norm_k : a.norm_q)) {
-        // (a row's units are eight neighbouring lanes', none of which or all are here)
-        float x = squares(f0) + squares(f1);
-#pragma unroll
-        for (int o = 4; o; o >>= 1) x += __shfl_xor_sync(0xffu << (lane & 24), x, o);
-        x = rsqrtf(fmaf(x, 1.f / DK, a.eps));
-        const float* w = kind ? a.k_weight : a.q_weight;
-        if (w && (kind ? a.k_per_head : a.q_per_head)) w += row * DK;
-        normed(f0, x, w, c0);
-        normed(f1, x, w, c1);
+      if (NORM && kind == 1) {
+        if (c0 < DV / 8) normed(f0, factor[t], a.k_weight, c0);
+        if (c1 < DV / 8) normed(f1, factor[t], a.k_weight, c1);
       }
       if (kind < 2 && rotc) {
         const float4* w = cs + t * (kMaxRotPairs / 2);
@@ -347,9 +359,441 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
 }
 
-template <int DK, int DV, bool FP8, int U, bool NORM>
-cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s) {
-  AppendArgs a = args;
+// Two numbers at once.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float x, float y) {
+  Two z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ void one(Two z, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(z)); }
+__device__ __forceinline__ Two mul2(Two x, Two y) {
+  Two z;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+__device__ __forceinline__ Two fma2(Two x, Two y, Two w) {
+  Two z;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(z) : "l"(x), "l"(y), "l"(w));
+  return z;
+}
+__device__ __forceinline__ Two sub2(Two x, Two y) {
+  Two z;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+
+// Rows of 128 with norms: eight lanes to a row, whatever it is (query, key or value),
+// each with the same two chunks of every row; components go two to an instruction.
+struct RowShape {
+  int nq, nk, per_tok;     // rows of a token: queries, and keys before nk, and values
+  int rot0, rotc, turned;  // rotated chunks, those with pairs of their own
+  bool halves;
+  int w[4];                // float4s of a row of weights that are for this lane's chunks
+  int c0, c1;              // this lane's chunks: the two halves of eight pairs while it
+                           //   counts rotated pairs half a row apart, then the other chunks in order
+  __device__ __forceinline__ RowShape(const AppendArgs& a, int l) {
+    nq = a.q ? a.Hq : 0;
+    nk = nq + a.Hkv;
+    per_tok = nk + a.Hkv;
+    rot0 = a.rope.rot_offset / 8;
+    rotc = a.rope.rot_dim / 8;
+    halves = a.rope.pairing == SPLITKV_ROPE_HALVES;
+    turned = a.rope.rot_dim / 2 / (halves ? 8 : 4);
+    c0 = 2 * l;
+    c1 = c0 + 1;
+    if (halves && rotc) {
+      if (l < rotc / 2) {
+        c0 = rot0 + l;
+        c1 = c0 + rotc / 2;
+      } else {
+        c0 -= rotc;
+        c1 -= rotc;
+        c0 += c0 >= rot0 ? rotc : 0;
+        c1 += c1 >= rot0 ? rotc : 0;
+      }
+    }
+    w[0] = 2 * c0;
+    w[1] = 2 * c0 + 1;
+    w[2] = 2 * c1;
+    w[3] = 2 * c1 + 1;
+  }
+};
+
+// This lane's chunks x0, x1 of row `row` of N tokens, the first of them n (those that
+// `live` says), normalised, turned by `z` (the tokens' sines, one behind the other) and stored.
+// SHARED: the weights are in shared memory, the keys' from k_at on.
+template <bool FP8, int N, bool SHARED>
+__device__ __forceinline__ void append_row(const AppendArgs& a, const RowShape& sh, int64_t n, int row, const Token (&tk)[N],
+                                           const bool (&live)[N], const uint4 (&x0)[N], const uint4 (&x1)[N],
+                                           const float4* z, const ulonglong2* shared = nullptr, int k_at = 0) {
+  const int nq = sh.nq, nk = sh.nk, rot0 = sh.rot0, rotc = sh.rotc, turned = sh.turned, c0 = sh.c0, c1 = sh.c1;
+  const int lane = threadIdx.x & 31;
+  const bool is_q = row < nq, is_k = !is_q && row < nk;
+  const int head = is_q ? row : is_k ? row - nq : row - nk;
+  uint4 y0[N], y1[N];
+  Two f0[N][4], f1[N][4];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    y0[i] = x0[i];
+    y1[i] = x1[i];
+    const uint32_t w0[4] = {x0[i].x, x0[i].y, x0[i].z, x0[i].w}, w1[4] = {x1[i].x, x1[i].y, x1[i].z, x1[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f0[i][e] = two(__uint_as_float(w0[e] << 16), __uint_as_float(w0[e] & 0xffff0000u));
+      f1[i][e] = two(__uint_as_float(w1[e] << 16), __uint_as_float(w1[e] & 0xffff0000u));
+    }
+  }
+  if (is_q || is_k) {
+    if (is_q ? a.norm_q : a.norm_k) {
+      float x[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        Two sq = mul2(f0[i][0], f0[i][0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) sq = fma2(f0[i][e], f0[i][e], sq);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sq = fma2(f1[i][e], f1[i][e], sq);
+        float y;
+        one(sq, x[i], y);
+        x[i] += y;
+      }
+      // (a row's lanes are neighbours, none of which or all are here)
+#pragma unroll
+      for (int o = 4; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffu << (lane & 24), x[i], o);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[i] = rsqrtf(fmaf(x[i], 1.f / 128, a.eps));
+        const Two by = two(x[i], x[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f0[i][e] = mul2(f0[i][e], by);
+          f1[i][e] = mul2(f1[i][e], by);
+        }
+      }
+      if (is_q ? a.q_weight : a.k_weight) {
+        const int row_at = (is_q ? a.q_per_head : a.k_per_head) ? head * 32 : 0;
+        ulonglong2 p0, p1, p2, p3;
+        if (SHARED) {
+          // (a lane's float4s lie 8 apart, so that the lanes' are side by side)
+          const ulonglong2* w = shared + (is_q ? 0 : k_at) + row_at + (lane & 7);
+          p0 = w[0];
+          p1 = w[8];
+          p2 = w[16];
+          p3 = w[24];
+        } else {
+          const ulonglong2* w = reinterpret_cast<const ulonglong2*>(is_q ? a.q_weight : a.k_weight) + row_at;
+          p0 = w[sh.w[0]];
+          p1 = w[sh.w[1]];
+          p2 = w[sh.w[2]];
+          p3 = w[sh.w[3]];
+        }
+        const Two w0[4] = {p0.x, p0.y, p1.x, p1.y}, w1[4] = {p2.x, p2.y, p3.x, p3.y};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f0[i][e] = mul2(f0[i][e], w0[e]);
+            f1[i][e] = mul2(f1[i][e], w1[e]);
+          }
+      }
+    }
+    if (sh.halves) {
+      if (c0 >= rot0 && c0 < rot0 + rotc) {  // then c1 is the other half of the pairs
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const ulonglong2 w =  // cosines, sines
+                *reinterpret_cast<const ulonglong2*>(z + i * (kMaxRotPairs / 2) + e * turned + c0 - rot0);
+            const Two u = f0[i][e];
+            f0[i][e] = sub2(mul2(u, w.x), mul2(f1[i][e], w.y));
+            f1[i][e] = fma2(u, w.y, mul2(f1[i][e], w.x));
+          }
+      }
+    } else {
+      auto both = [&](Two (&f)[4], const float4* zi, int c) {
+        if (c < rot0 || c >= rot0 + rotc) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 w = zi[(e >> 1) * turned + c - rot0];
+          const float co = e & 1 ? w.y : w.x, si = e & 1 ? w.w : w.z;
+          float u, v;
+          one(f[e], u, v);
+          f[e] = two(u * co - v * si, u * si + v * co);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        both(f0[i], z + i * (kMaxRotPairs / 2), c0);
+        both(f1[i], z + i * (kMaxRotPairs / 2), c1);
+      }
+    }
+    if (!FP8 || is_q) {
+      auto pack = [](const Two (&f)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float lo, hi;
+          one(f[e], lo, hi);
+          w[e] = pack_bf16(lo, hi);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        y0[i] = pack(f0[i]);
+        y1[i] = pack(f1[i]);
+      }
+    }
+  }
+  if (is_q) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (!live[i]) continue;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) + (n + i) * a.q_out_stride + row * 128);
+      dst[c0] = y0[i];
+      dst[c1] = y1[i];
+    }
+    return;
+  }
+  void* pool = is_k ? a.k_pages : a.v_pages;
+  const float* per_head = is_k ? a.k_scale : a.v_scale;
+  const float sc = FP8 ? per_head ? per_head[head] : a.kv_scale : 1.f;
+  // (the reciprocal of a power of two is exact, and then so is the product)
+  const uint32_t bits = __float_as_uint(sc);
+  const bool exact = (bits & 0x7fffffu) == 0 && bits >= 0x01000000u && bits < 0x7e000000u;
+  const float inv = __uint_as_float(0x7f000000u - bits);
+  auto codes = [&](const Two (&f)[4]) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) one(f[e], x[2 * e], x[2 * e + 1]);
+    if (exact) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= inv;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], sc);
+    }
+    return make_uint2(pack_e4m3x4(x), pack_e4m3x4(x + 4));
+  };
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!live[i] || tk[i].page < 0) continue;
+    const size_t line = a.nhd ? (size_t(tk[i].page) * a.P + tk[i].in_page) * a.Hkv + head
+                              : (size_t(tk[i].page) * a.Hkv + head) * a.P + tk[i].in_page;
+    if (FP8) {
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + line * 128);
+      dst[c0] = codes(f0[i]);
+      dst[c1] = codes(f1[i]);
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + line * 128);
+      dst[c0] = y0[i];
+      dst[c1] = y1[i];
+    }
+  }
+}
+
+// A short call: a row per lane group in flight, as many CTAs as that makes.
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ AppendArgs a, int tok_per_cta) {
+  constexpr int kGroups = kThreads / 8;
+  __shared__ Token tok[kMaxTok];
+  __shared__ float4 cs[kMaxTok * kMaxRotPairs / 2];  // (as in append_kernel)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  launch_dependents();
+  wait_prerequisites();
+
+  const int n0 = blockIdx.x * tok_per_cta;
+  const int ntok = min(tok_per_cta, a.n_tokens - n0);
+  const RowShape sh(a, threadIdx.x & 7);
+  const int total = ntok * sh.per_tok;
+
+  bool ready = false;
+  for (int base = blockIdx.y * kGroups; base < total || !ready; base += gridDim.y * kGroups) {
+    // The token's own row first (that of padding is within the inputs too): it is in
+    // flight while the tokens' places are looked up.
+    const int j = base + (threadIdx.x >> 3);
+    const int t = int(__umulhi(unsigned(j), a.per_tok_magic)), row = j - t * sh.per_tok;
+    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+    if (j < total) {
+      const int kind = row < sh.nq ? 0 : row < sh.nk ? 1 : 2, head = kind == 0 ? row : kind == 1 ? row - sh.nq : row - sh.nk;
+      const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v);
+      const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+      const uint4* src = reinterpret_cast<const uint4*>(from + (n0 + t) * stride + head * 128);
+      x0 = src[sh.c0];
+      x1 = src[sh.c1];
+    }
+    if (!ready) {
+      ready = true;
+      for (int i = warp; i < ntok; i += kThreads / 32) {
+        const Token p = place_of(a, n0 + i, lane, blockIdx.y == 0);
+        if (lane == 0) tok[i] = p;
+      }
+      sines(a, n0, ntok, cs);
+      __syncthreads();
+      if (blockIdx.y == 0) new_state(a, n0, ntok, tok);
+    }
+    if (j >= total) continue;
+    const Token tk = tok[t];
+    if (tk.b >= 0)
+      append_row<FP8, 1, false>(a, sh, n0 + t, row, {tk}, {true}, {x0}, {x1}, cs + t * (kMaxRotPairs / 2));
+  }
+}
+
+// A long call.  Norm, weights and rotation take a row so long that loads which wait for
+// them leave the memory idle (threads that load their own rows, four CTAs to an SM: 143 us
+// for 32k tokens of 40 rows).  Here two CTAs stay on each SM, and a token's rows come by
+// bulk copies (its heads are adjacent) into a ring of stages of a few tokens, asked for as
+// soon as a stage is free; two warps look up the places and compute the sines of the
+// stages ahead (one warp: 122 us, four, which leave the others fewer registers, 119).
+// Measured: 107 us, 6.1 TB/s (floor 97 at the copy's 6.8).
+struct Stream {
+  int tps;       // tokens of a stage
+  int stages;
+  int w_floats;  // of the weights that are copied to shared memory first: q's, then k's; 0: none
+};
+constexpr int kStreamTok = 4, kStreamStages = 4;  // (tokens: even)
+constexpr int kStreamInfo = 64;  // threads for places and sines
+constexpr int kStreamThreads = kThreads + 32 + kStreamInfo;  // warp 8: copies
+struct StreamInfo {
+  float4 cs[kStreamTok * kMaxRotPairs / 2];
+  Token tok[kStreamTok];
+};
+
+template <bool FP8, bool SHARED>
+__global__ void __launch_bounds__(kStreamThreads, 2) append_stream_kernel(const __grid_constant__ AppendArgs a, const Stream st) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ uint64_t bars[2 * kStreamStages];
+  __shared__ StreamInfo info[kStreamStages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RowShape sh(a, threadIdx.x & 7);
+  const int q_bytes = sh.nq * 256, k_bytes = a.Hkv * 256, tok_bytes = q_bytes + 2 * k_bytes;
+  float* weights = reinterpret_cast<float*>(sm);
+  uint8_t* ring = sm + st.w_floats * 4;
+  auto full = [&](int s) { return smem_u32(bars + s); };
+  auto empty = [&](int s) { return smem_u32(bars + kStreamStages + s); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < st.stages; ++s) {
+      mbar_init(full(s), 1 + kStreamInfo / 32);  // copies; places and sines
+      mbar_init(empty(s), kThreads / 32);
+    }
+    fence_mbar_init();
+  }
+  launch_dependents();
+  wait_prerequisites();
+  const int k_at = !a.q_weight ? 0 : a.q_per_head ? a.Hq * 32 : 32;  // (float4s)
+  if (SHARED) {
+    for (int i = threadIdx.x; i < st.w_floats / 4; i += kStreamThreads) {
+      const float4* from = reinterpret_cast<const float4*>(i < k_at ? a.q_weight : a.k_weight) + ((i < k_at ? i : i - k_at) & ~31);
+      reinterpret_cast<float4*>(weights)[i] = from[RowShape(a, i & 7).w[i >> 3 & 3]];
+    }
+  }
+  __syncthreads();
+
+  const int groups = (a.n_tokens + st.tps - 1) / st.tps;
+  bool ok = true;
+  int it = 0;
+  auto each = [&](auto&& body) {
+    for (int g = blockIdx.x; g < groups && ok; g += gridDim.x, ++it) {
+      const int n0 = g * st.tps;
+      body(it % st.stages, it / st.stages, n0, min(st.tps, a.n_tokens - n0));
+    }
+  };
+  if (warp == kThreads / 32) {
+    // ---- copies
+    each([&](int s, int use, int n0, int ntok) {
+      if (use > 0) ok = __all_sync(kFull, mbar_wait(empty(s), (use - 1) & 1));
+      if (!ok) return;
+      if (lane == 0) mbar_arrive_expect_tx(full(s), uint32_t(ntok * tok_bytes));
+      __syncwarp();
+      if (lane < ntok) {
+        const uint32_t dst = smem_u32(ring) + uint32_t(s * st.tps + lane) * tok_bytes;
+        const int64_t n = n0 + lane;
+        if (q_bytes) bulk_load(dst, static_cast<const __nv_bfloat16*>(a.q) + n * a.q_stride, q_bytes, full(s));
+        bulk_load(dst + q_bytes, static_cast<const __nv_bfloat16*>(a.k) + n * a.k_stride, k_bytes, full(s));
+        bulk_load(dst + q_bytes + k_bytes, static_cast<const __nv_bfloat16*>(a.v) + n * a.v_stride, k_bytes, full(s));
+      }
+    });
+    if (!ok) --it;  // (not asked for)
+    // stay until every copy has landed: the last use of each stage
+    for (int i = it - 1; i >= 0 && i >= it - st.stages; --i) mbar_wait(full(i % st.stages), (i / st.stages) & 1);
+  } else if (warp > kThreads / 32) {
+    // ---- places (the first of the warps) and sines
+    const int part = threadIdx.x - kThreads - 32;
+    const int half = a.rope.rot_dim / 2, chunk_pairs = sh.halves ? 8 : 4;
+    each([&](int s, int use, int n0, int ntok) {
+      if (use > 0) ok = __all_sync(kFull, mbar_wait(empty(s), (use - 1) & 1));
+      if (!ok) return;
+      StreamInfo& to = info[s];
+      if (part < ntok) {
+        const int n = n0 + part;
+        int b = n / a.T;
+        if (a.cu) {
+          int lo = 0, hi = a.batch;  // how many sequences have ended
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.cu[mid + 1] <= n) lo = mid + 1;
+            else hi = mid;
+          }
+          b = lo < a.batch && a.cu[0] <= n ? lo : -1;
+        }
+        to.tok[part] = place_in(a, b, n, true);
+      }
+      for (int p = part; p < half; p += kStreamInfo) {  // (a pair's place once, for all tokens)
+        const int ch = p / chunk_pairs, e = p - ch * chunk_pairs;
+        float* z = reinterpret_cast<float*>(to.cs + (e >> 1) * sh.turned + ch) + (e & 1);
+        const int32_t* at = a.positions + size_t(a.rope.axis[p]) * a.n_tokens + n0;
+        const uint64_t turns = a.rope.turns[p];
+        int32_t pos[kStreamTok];
+#pragma unroll
+        for (int t = 0; t < kStreamTok; ++t) pos[t] = at[min(t, ntok - 1)];
+#pragma unroll
+        for (int t = 0; t < kStreamTok; ++t) {
+          float s, c;
+          sincospif(float(int32_t((uint64_t(int64_t(pos[t])) * turns) >> 32)) * 0x1p-31f, &s, &c);
+          if (t >= ntok) break;
+          z[t * (2 * kMaxRotPairs)] = c;
+          z[t * (2 * kMaxRotPairs) + 2] = s;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(s));
+      if (part < 32) new_state<32>(a, n0, ntok, to.tok, part);
+      __syncwarp();
+    });
+  } else {
+    // ---- rows
+    each([&](int s, int use, int n0, int ntok) {
+      ok = __all_sync(kFull, mbar_wait(full(s), use & 1));
+      if (!ok) return;
+      const uint8_t* rows = ring + size_t(s) * st.tps * tok_bytes;
+      const StreamInfo& from = info[s];
+      // (the same row of two tokens at a time: their latencies overlap, and the weights serve both)
+      for (int j = threadIdx.x >> 3; j < (ntok + 1) / 2 * sh.per_tok; j += kThreads / 8) {
+        const int pair = int(__umulhi(unsigned(j), a.per_tok_magic)), row = j - pair * sh.per_tok, t = 2 * pair;
+        const int t2 = min(t + 1, ntok - 1);
+        const Token tk[2] = {from.tok[t], from.tok[t2]};
+        const bool live[2] = {tk[0].b >= 0, t2 > t && tk[1].b >= 0};
+        if (!live[0] && !live[1]) continue;
+        const uint4* s0 = reinterpret_cast<const uint4*>(rows + t * tok_bytes + row * 256);
+        const uint4* s1 = reinterpret_cast<const uint4*>(rows + t2 * tok_bytes + row * 256);
+        append_row<FP8, 2, SHARED>(a, sh, n0 + t, row, tk, live, {s0[sh.c0], s1[sh.c0]}, {s0[sh.c1], s1[sh.c1]},
+                                   from.cs + t * (kMaxRotPairs / 2), reinterpret_cast<const ulonglong2*>(weights), k_at);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(s));
+    });
+  }
+  if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
+}
+
+// The grid of a call, tokens of a CTA first.  A pass is the units (or rows) that a CTA
+// has in flight; `longer`: a long call.
+dim3 append_grid(AppendArgs& a, int per_tok, int pass, bool longer, int* tok_per_cta) {
   // i * magic >> 32 is i / per_tok for every unit i of a CTA, as i * per_tok is
   // below 2^32 or the CTA has one token (0: that token's, however many units)
   a.per_tok_magic = per_tok > 65536 ? 0 : unsigned(((uint64_t(1) << 32) + per_tok - 1) / per_tok);
@@ -359,10 +803,10 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
   // threads idle in the last, or else the best within kPasses (29k tokens of 17
   // latent rows, e4m3: four tokens 172 us, one 230).  A token of more units than
   // that goes to several CTAs.
-  constexpr int pass = U * kThreads, most = (U == 1 ? 1 : kPasses) * pass;
+  const int most = (longer ? kPasses : 1) * pass;
   const int64_t slices = (int64_t(per_tok) + most - 1) / most;
   int most_tok = max(1, min(kMaxTok, most / per_tok)), tpc = most_tok;
-  if (U > 1) {
+  if (longer) {
     // (two CTAs per SM at least)
     tpc = most_tok = max(1, min(most_tok, a.n_tokens / (2 * kSmCount)));
     double least = 1e30;
@@ -375,8 +819,16 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
       }
     }
   }
+  *tok_per_cta = tpc;
+  return dim3((a.n_tokens + tpc - 1) / tpc, unsigned(slices > 65535 ? 65535 : slices), 1);
+}
+
+cudaError_t launch_append_kernel(void (*kernel)(AppendArgs, int), const AppendArgs& args, int per_tok, int pass, bool longer,
+                                 cudaStream_t s) {
+  AppendArgs a = args;
+  int tpc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.n_tokens + tpc - 1) / tpc, unsigned(slices > 65535 ? 65535 : slices), 1);
+  cfg.gridDim = append_grid(a, per_tok, pass, longer, &tpc);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute la[1];
@@ -384,7 +836,7 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
   la[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = la;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<DK, DV, FP8, U, NORM>, a, tpc);
+  return cudaLaunchKernelEx(&cfg, kernel, a, tpc);
 }
 
 // A call of few tokens takes one unit per thread, to use more of the GPU's
@@ -393,26 +845,60 @@ cudaError_t launch_append_u(const AppendArgs& args, int per_tok, cudaStream_t s)
 // 100, with four 137).
 constexpr int64_t kFewUnits = 1 << 17;
 
-template <int DK, int DV, bool FP8, bool NORM>
+// Rows with norms: what the stages of a CTA of a long call hold, how many they are at
+// least, and the weights beside them (two CTAs to an SM); and the rows of a short call.
+constexpr int kStreamBytes = 80 * 1024, kStreamMin = 2, kStreamWeights = 20 * 1024;
+constexpr int64_t kShortRows = 1 << 16;  // (62k rows: 14.4 us either way, 34k 8.6 and 9.7, 240k 42.9 and 31.6)
+
+template <int DK, int DV, bool FP8, bool NORM = false>
 cudaError_t launch_append_t(const AppendArgs& a, cudaStream_t s) {
   const int per_tok = (a.q ? a.Hq * (DK / 16) : 0) + a.Hkv * (DK / 16 + (a.v ? DV / 16 : 0));
-  return int64_t(per_tok) * a.n_tokens <= kFewUnits ? launch_append_u<DK, DV, FP8, 1, NORM>(a, per_tok, s)
-                                                    : launch_append_u<DK, DV, FP8, 2, NORM>(a, per_tok, s);
+  return int64_t(per_tok) * a.n_tokens <= kFewUnits
+             ? launch_append_kernel(append_kernel<DK, DV, FP8, 1, NORM>, a, per_tok, kThreads, false, s)
+             : launch_append_kernel(append_kernel<DK, DV, FP8, 2, NORM>, a, per_tok, 2 * kThreads, true, s);
 }
 
-template <bool NORM>
-cudaError_t launch_append_n(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, cudaStream_t s) {
-  if (qk_dim == 128 && v_dim == 128)
-    return fp8 ? launch_append_t<128, 128, true, NORM>(a, s) : launch_append_t<128, 128, false, NORM>(a, s);
-  return fp8 ? launch_append_t<576, 512, true, NORM>(a, s) : launch_append_t<576, 512, false, NORM>(a, s);
+template <bool FP8>
+cudaError_t launch_append_rows(const AppendArgs& args, cudaStream_t s) {
+  AppendArgs a = args;
+  const int per_tok = (a.q ? a.Hq : 0) + 2 * a.Hkv, tok_bytes = per_tok * 256;
+  Stream st;
+  st.tps = min(kStreamTok, kStreamBytes / kStreamMin / tok_bytes);
+  if (st.tps > 1) st.tps &= ~1;
+  if (st.tps < 1 || int64_t(per_tok) * a.n_tokens <= kShortRows)
+    return launch_append_kernel(append_rows_kernel<FP8>, a, per_tok, kThreads / 8, false, s);
+  st.stages = min(kStreamStages, kStreamBytes / (st.tps * tok_bytes));
+  st.w_floats = (a.q_weight ? a.q_per_head ? a.Hq * 128 : 128 : 0) + (a.k_weight ? a.k_per_head ? a.Hkv * 128 : 128 : 0);
+  if (st.w_floats * 4 > kStreamWeights) st.w_floats = 0;
+  a.per_tok_magic = unsigned(((uint64_t(1) << 32) + per_tok - 1) / per_tok);
+  static std::atomic<uint64_t> allowed[2];
+  auto* kernel = st.w_floats ? append_stream_kernel<FP8, true> : append_stream_kernel<FP8, false>;
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel), kStreamBytes + kStreamWeights, allowed[st.w_floats != 0]);
+  if (e != cudaSuccess) return e;
+  const int groups = (a.n_tokens + st.tps - 1) / st.tps;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(min(2 * kSmCount, groups)), 1, 1);
+  cfg.blockDim = dim3(kStreamThreads, 1, 1);
+  cfg.dynamicSmemBytes = size_t(st.w_floats) * 4 + size_t(st.stages) * st.tps * tok_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = la;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return a.norm_q || a.norm_k ? launch_append_n<true>(a, qk_dim, v_dim, fp8, s)
-                              : launch_append_n<false>(a, qk_dim, v_dim, fp8, s);
+  if (qk_dim == 128 && v_dim == 128) {
+    if (a.norm_q || a.norm_k) return fp8 ? launch_append_rows<true>(a, s) : launch_append_rows<false>(a, s);
+    return fp8 ? launch_append_t<128, 128, true>(a, s) : launch_append_t<128, 128, false>(a, s);
+  }
+  if (a.norm_k) return fp8 ? launch_append_t<576, 512, true, true>(a, s) : launch_append_t<576, 512, false, true>(a, s);
+  return fp8 ? launch_append_t<576, 512, true>(a, s) : launch_append_t<576, 512, false>(a, s);
 }
 
 }  // namespace splitkv
