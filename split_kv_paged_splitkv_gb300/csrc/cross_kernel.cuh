@@ -1258,8 +1258,12 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
         more = take_piece();
         continue;
       }
+      float2 other = make_float2(0.f, 0.f);
       if (two) {
         ok = __all_sync(kFull, mbar_wait(bar(B_ML), n_ml++ & 1));
+        tc_fence_after();
+        if (ok) tmem_ld2(scol + 128 + 126, other.x, other.y);  // (before the next queries, with which S_B is written)
+        tc_fence_before();
         if (ok) ok = __all_sync(kFull, mbar_wait(bar(B_O + 1), n_ob & 1));
       }
       n_ob += two || (!narrow && pc.nblk > 0);
@@ -1270,8 +1274,6 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       // weights of A's own result and of B's
       float wa = 1.f, wb = 0.f;
       if (two) {
-        float2 other;
-        tmem_ld2(scol + 128 + 126, other.x, other.y);
         const float m = fmaxf(m_ref, other.x);
         wa = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
         wb = other.x == -INFINITY ? 0.f : ex2(other.x - m);
