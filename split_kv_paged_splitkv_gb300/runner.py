@@ -3,7 +3,7 @@
 Marshalling only -- torch allocates device memory and provides the stream;
 the computation is in libsplitkv.  ``DecodeSession`` is one decode over given
 caches; ``CacheSession`` holds a paged cache through its life: append, decode,
-weigh, evict, cross attention.
+weigh, evict, cross attention, and drafted trees that are attended and committed.
 """
 from __future__ import annotations
 
@@ -15,9 +15,10 @@ from . import (SPLITKV_BF16, SPLITKV_COMBINE_SEPARATE, SPLITKV_FP8_E4M3, SPLITKV
                SPLITKV_LAYOUT_NHD, make_desc, splitkv_combine_workspace, splitkv_decode,
                splitkv_decode_partials,
                splitkv_decode_kv_scales, splitkv_plan, splitkv_plan_fixed,
-               splitkv_plan_upload, splitkv_read_stats, splitkv_append,
+               splitkv_plan_upload, splitkv_read_stats, splitkv_append, splitkv_append_norm,
                splitkv_cross_attend, splitkv_cross_workspace_size, splitkv_evict,
-               splitkv_evict_workspace_size, splitkv_key_weights, SPLITKV_EUNSUPPORTED,
+               splitkv_evict_workspace_size, splitkv_key_weights, splitkv_tree_attend,
+               splitkv_tree_commit, splitkv_tree_workspace_size, SPLITKV_EUNSUPPORTED,
                SplitKVError)
 
 
@@ -115,6 +116,9 @@ class CacheSession:
     the new tokens before ``append``, ``evict`` lowers it.  Nothing here reads
     a length on the host, so a whole step can be captured into a CUDA graph.
 
+    ``q_norm`` and ``k_norm`` have ``append`` normalise the query and key head rows first:
+    the weights (fp32 ``[columns]`` or ``[heads][columns]``), or True for none.
+
     With ``track`` the session keeps the accumulated weight and the position of
     every cached key, which ``weigh`` and ``evict`` need.  A session's calls
     share its workspaces: one stream (or replayed graph) at a time.  It is made
@@ -123,13 +127,15 @@ class CacheSession:
     """
 
     def __init__(self, desc, k_pages, v_pages, block_table, seq_lens, *, scale, rope=None, kv_scale=1.0,
-                 k_scale=None, v_scale=None, num_splits=16, track=False):
+                 k_scale=None, v_scale=None, num_splits=16, track=False, q_norm=None, k_norm=None,
+                 norm_eps=1e-6):
         dev = k_pages.device
         self.desc, self.rope = desc, rope
         self.k_pages, self.v_pages = k_pages, v_pages
         self.block_table, self.seq_lens = block_table, seq_lens
         self.scale, self.kv_scale = float(scale), float(kv_scale)
         self.k_scale, self.v_scale = k_scale, v_scale
+        self.q_norm, self.k_norm, self.norm_eps = q_norm, k_norm, float(norm_eps)
         self.num_splits = num_splits
         try:
             self.plan = splitkv_plan_fixed(desc, num_splits)
@@ -149,15 +155,23 @@ class CacheSession:
         torch.cuda.current_stream(dev).synchronize()  # (the calls may come on any stream)
 
     def append(self, positions, q, k, v, cu_tokens=None, q_out=None, stream=None):
-        """Rotates the new tokens' queries (returned) and keys and stores their
-        keys and values (``splitkv_append``); ``q`` may be None."""
+        """Rotates the new tokens' queries (returned) and keys, normalised before if the session says
+        so, and stores their keys and values (``splitkv_append``, ``splitkv_append_norm``); ``q`` may
+        be None."""
         if q is not None and q_out is None:
             with _on(stream):
                 q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        splitkv_append(self.desc, self.rope, positions, q, k, v, self.block_table, self.seq_lens, q_out,
-                       self.k_pages, self.v_pages, cu_tokens=cu_tokens, kv_scale=self.kv_scale,
-                       k_scale=self.k_scale, v_scale=self.v_scale, key_weights=self.key_weights,
-                       key_positions=self.key_positions, status=self.status, stream=stream)
+        args = (self.desc, self.rope, positions, q, k, v, self.block_table, self.seq_lens, q_out,
+                self.k_pages, self.v_pages)
+        more = dict(cu_tokens=cu_tokens, kv_scale=self.kv_scale, k_scale=self.k_scale, v_scale=self.v_scale,
+                    key_weights=self.key_weights, key_positions=self.key_positions, status=self.status,
+                    stream=stream)
+        if self.q_norm is None and self.k_norm is None:
+            splitkv_append(*args, **more)
+        else:
+            splitkv_append_norm(*args, norm_q=self.q_norm is not None, norm_k=self.k_norm is not None,
+                                q_weight=None if self.q_norm is True else self.q_norm,
+                                k_weight=None if self.k_norm is True else self.k_norm, eps=self.norm_eps, **more)
         return q_out
 
     def decode(self, q, out=None, lse=None, stream=None):
@@ -203,6 +217,29 @@ class CacheSession:
                              self.scale, out, lse, workspace, status=self.status, stream=stream)
         return out, lse
 
+    def tree_attend(self, q, tree_mask, cu_tokens=None, stream=None):
+        """Attention of a tree of drafted tokens ``q`` [n][Hq][Dk], whose keys are appended and counted by
+        the lengths: over the keys before them, and those that ``tree_mask`` int32 [n][words] names (bit i:
+        token i of the sequence)."""
+        n, d = q.shape[0], self.desc
+        size = splitkv_tree_workspace_size(d, n)
+        with _on(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+            out = torch.empty((n, d.num_q_heads, d.v_dim), dtype=torch.bfloat16, device=q.device)
+            lse = torch.empty((n, d.num_q_heads), dtype=torch.float32, device=q.device)
+        splitkv_tree_attend(d, cu_tokens, tree_mask, q, self.k_pages, self.v_pages, self.block_table, self.seq_lens,
+                            self.scale, out, lse, workspace, kv_scale=self.kv_scale, k_scale=self.k_scale,
+                            v_scale=self.v_scale, status=self.status, stream=stream)
+        return out, lse
+
+    def commit(self, path, path_lens, cu_tokens=None, stream=None):
+        """Keeps the accepted tokens of the drafted trees (``path`` int32 [B][max_path], of which the first
+        ``path_lens`` [B] count): their keys, values and state move up behind the keys before the tree, and the
+        lengths end with them."""
+        splitkv_tree_commit(self.desc, path, path_lens, self.k_pages, self.v_pages, self.block_table, self.seq_lens,
+                            self.seq_lens, cu_tokens=cu_tokens, key_weights=self.key_weights,
+                            key_positions=self.key_positions, status=self.status, stream=stream)
+
     def read_status(self):
-        """Device status bits of append, weigh, evict and cross_attend so far (synchronises)."""
+        """Device status bits of this session's calls but decode so far (synchronises)."""
         return int(self.status.item())

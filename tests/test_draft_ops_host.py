@@ -106,3 +106,96 @@ def test_commit_refuses_other_caches_and_arguments():
                 torch.zeros((2, 4), dtype=torch.int32)):  # the type, too few, rows of another length, the device
         with pytest.raises(ValueError):
             call_commit(desc(), path=bad)
+
+
+# ------------------------------------------------------------------ tree attention
+
+def call_tree(d, **kw):
+    a = dict(desc=d, cu_tokens=None, tree_mask=A, mask_words=1, q=A, k_pages=A, v_pages=None if d.v_shares_k else A, block_table=A,
+             seq_lens=A, scale=0.1, out=1 << 40, lse=A, workspace=A, workspace_bytes=1 << 40, n_tokens=d.batch * d.q_tokens, stream=0)
+    a.update(kw)
+    return skv.splitkv_tree_attend(**a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(tree_mask=None), dict(k_pages=None), dict(v_pages=None), dict(block_table=None), dict(seq_lens=None),
+    dict(out=None), dict(q=A + 8), dict(out=A), dict(out=A + 256), dict(lse=A + 2), dict(cu_tokens=A + 2), dict(tree_mask=A + 2),
+    dict(scale=0.0), dict(scale=math.nan), dict(mask_words=0), dict(mask_words=33), dict(mask_words=-1), dict(n_tokens=-1),
+    dict(n_tokens=5), dict(n_tokens=1 << 28, cu_tokens=A), dict(k_scale=A, v_scale=A), dict(status=A + 1), dict(v_pages=A + 8),
+    dict(workspace=A + 8)])
+def test_tree_refusals(kw):
+    refused(EINVAL, call_tree, desc(), **kw)
+
+
+def test_tree_scales():
+    refused(EINVAL, call_tree, desc(fp8=True), kv_scale=0.0)
+    refused(EINVAL, call_tree, desc(fp8=True), kv_scale=math.inf)
+    refused(EINVAL, call_tree, desc(fp8=True), k_scale=A)
+    refused(EINVAL, call_tree, desc(fp8=True), k_scale=A + 2, v_scale=A)
+    refused(EUNSUPPORTED, call_tree, latent(fp8=True), k_scale=A, v_scale=A)
+
+
+def test_tree_over_latent_rows():
+    refused(EINVAL, call_tree, latent(T=4), cu_tokens=A)
+    refused(EINVAL, call_tree, latent(T=4), n_tokens=7)
+    refused(EINVAL, call_tree, latent(T=4), v_pages=A)
+    for kw in (dict(T=17), dict(Hq=64), dict(P=48), dict(fp8=True, shares=0)):
+        refused(EUNSUPPORTED, call_tree, latent(**kw))
+        assert skv.splitkv_tree_workspace_size(latent(**kw), latent(**kw).batch * latent(**kw).q_tokens) == 0
+    d = latent(T=4, maxp=64, P=64)
+    need = skv.splitkv_tree_workspace_size(d, 8)
+    assert need > 2 * 4 * 128 * 512 * 4  # more than a split: partial results of every row
+    refused(EWORKSPACE, call_tree, d, workspace=None, workspace_bytes=0)
+    refused(EWORKSPACE, call_tree, d, workspace_bytes=need - 1)
+    lib = skv._lib.splitkv_tree_attend
+    for stride in (128 * 576 + 8, 128 * 576 - 8):
+        assert lib(ctypes.byref(d), 8, None, A, 1, A, stride, A, None, A, A, 0.1, 1.0, None, None, 1 << 40, None, A, 1 << 40, None,
+                   0) == EINVAL
+
+
+def test_tree_workspaces():
+    d = desc(B=1, Hkv=1, maxp=512)
+    need = skv.splitkv_tree_workspace_size(d, 1)
+    assert need == skv.splitkv_cross_workspace_size(d, 1) > 0
+    refused(EWORKSPACE, call_tree, d, workspace=None, workspace_bytes=0)
+    refused(EWORKSPACE, call_tree, d, workspace_bytes=need - 1)
+    assert skv.splitkv_tree_workspace_size(desc(fp8=True), 2) > 0
+    assert skv.splitkv_tree_workspace_size(d, 0) == skv.splitkv_tree_workspace_size(d, -1) == 0
+    call_tree(d, cu_tokens=A, n_tokens=0)  # nothing to do, nothing launched
+    for stride in (1016, 1025, 1 << 31, 1 << 62, -1024):
+        assert skv._lib.splitkv_tree_attend(ctypes.byref(d), 1, None, A, 1, A, stride, A, A, A, A, 0.1, 1.0, None, None, 1 << 40, None,
+                                            A, 1 << 40, None, 0) == EINVAL
+
+
+def test_tree_tensor_arguments():
+    d = desc()
+    for bad in (torch.zeros((2, 1)), torch.zeros((1, 1), dtype=torch.int32), torch.zeros((1, 2), dtype=torch.int32),
+                torch.zeros((3, 1), dtype=torch.int64), torch.zeros((2, 1), dtype=torch.int32)):
+        with pytest.raises(ValueError):  # the type, too few, rows of another length, the type, the device
+            call_tree(d, tree_mask=bad, mask_words=None)
+    with pytest.raises(ValueError):  # rows of two words
+        call_tree(d, tree_mask=torch.zeros((2, 2), dtype=torch.int32), mask_words=1)
+    with pytest.raises(TypeError):
+        call_tree(d, mask_words=None)
+    with pytest.raises(TypeError):
+        call_tree(d, n_tokens=None)
+    with pytest.raises(ValueError):
+        call_tree(d, out=torch.zeros((2, 8, 64), dtype=torch.bfloat16))
+
+
+def test_the_norm_struct_is_the_headers():
+    assert ctypes.sizeof(skv.splitkv_norm_t) == 40 and skv.splitkv_norm_t.eps.offset == 16
+    assert skv.splitkv_norm_t.k_per_head.offset == 32
+
+
+@pytest.mark.parametrize("name", ["cross_kernel.cuh", "tree_attend.cu", "tree_commit.cu"])
+def test_no_read_only_loads_beside_a_running_writer(name):
+    """As in the older kernels: what the kernel before may still write is read with plain loads."""
+    import os
+    import re
+
+    import split_kv_paged_splitkv_gb300._build as build
+    with open(os.path.join(build.CSRC, name)) as f:
+        text = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+    assert "wait_prerequisites" in text or "cross_kernel.cuh" in text
+    assert not re.search(r"__ldg\s*\(|ld\.global\.nc|__restrict__", text)

@@ -222,6 +222,56 @@ def test_long_calls_and_many_heads(dtype):
     run(c, [2], per_head="q")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,kv_heads,per_head,tokens", [(8, 4, "", 4300), (32, 4, "qk", 1800), (64, 8, "qk", 900),
+                                                            (6, 2, "k", 7500)])
+def test_calls_of_a_ring(dtype, heads, kv_heads, per_head, tokens):
+    """More than 2^16 rows: stages of four tokens or two, weights in shared memory or (64 heads of their own) not; an odd
+    number of tokens, sequences that end within a stage, padding behind them."""
+    counts = [tokens // 2 + 1, 0, 1, 2, tokens // 2 - 8]
+    c = Cache([n + 5 for n in counts], kv_heads=kv_heads, heads=heads, dtype=dtype, layout="NHD", device="cuda", seed=16)
+    run(c, counts, per_head=per_head, pad=3, sections=(24, 20, 20), kv_scale=0.25)
+    run(c, counts, per_head=per_head, rot=64, offset=32, pairing=1, kv_scale=0.3, which="qk", weights="k", in_place=True)
+
+
+def test_a_ring_of_keys_alone_and_many_sequences():
+    rng = np.random.default_rng(17)
+    counts = [int(x) for x in rng.integers(0, 30, 600)]
+    lens = [n + int(x) for n, x in zip(counts, rng.integers(0, 20, 600))]
+    c = Cache(lens, kv_heads=4, heads=4, device="cuda", seed=17)
+    run(c, counts, queries=False, weights="")
+
+
+def test_a_ring_reports_slots_and_pages_and_writes_the_state():
+    n = 8300
+    c = Cache([n, 40], kv_heads=4, heads=4, page=64, device="cuda", seed=18)
+    x = torch.randn((n + 40, 12, 128), device="cuda").to(torch.bfloat16)
+    w = torch.full((2, 4, c.cap), 5.0, device="cuda")
+    p = torch.full((2, 4, c.cap), -9, dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.lens[1] = 37         # the first three tokens of the second sequence have no slot
+    c.table[0, 100] = c.N  # nor a page those of keys 6400 to 6463
+    k0 = c.k.clone()
+    pos = torch.arange(n + 40, dtype=torch.int32, device="cuda").view(1, -1)
+    out = torch.zeros((n + 40, 4, 128), dtype=torch.bfloat16, device="cuda")
+    skv.splitkv_append_norm(c.desc, None, pos, x[:, :4], x[:, 4:8], x[:, 8:], c.table, c.lens, out, c.k, c.v,
+                            cu_tokens=torch.tensor([0, n, n + 40], dtype=torch.int32, device="cuda"), key_weights=w, key_positions=p,
+                            status=st)
+    torch.cuda.synchronize()
+    assert int(st) == skv.SPLITKV_DEVERR_SEQLEN | skv.SPLITKV_DEVERR_PAGE
+    want = torch.zeros((2, c.cap), dtype=torch.bool, device="cuda")
+    want[0, :n], want[1, :37] = True, True
+    want[0, 6400:6464] = False
+    assert torch.equal(w == 0, want[:, None].expand(2, 4, -1))
+    at = torch.where(want[0], torch.arange(c.cap, device="cuda"), -9)
+    assert torch.equal(p[0], at.int()[None].expand(4, -1)) and torch.equal(p[1, 0, :37], torch.arange(n + 3, n + 40, device="cuda").int())
+    pages = torch.zeros(c.N, dtype=torch.bool, device="cuda")
+    pages[c.table[0].long()[torch.arange(c.width, device="cuda") != 100][:130 - 1]] = True
+    changed = (c.k != k0).flatten(1).any(1)
+    assert not changed[[i for i in range(c.N) if not pages[i] and i != int(c.table[1, 0])]].any()
+    assert (out != 0).any(-1).all()  # the queries come whole
+
+
 def test_per_head_scales():
     c = Cache([10, 31], dtype="e4m3", device="cuda", seed=12)
     run(c, [10, 4], scales=([0.25, 0.001], [0.001, 3.0]))
