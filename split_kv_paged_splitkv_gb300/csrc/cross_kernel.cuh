@@ -873,24 +873,30 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     // V of key block j of a piece has landed; key slots past the last key may
     // hold anything (even NaN): their V rows are zeroed, so that 0 * V stays 0.
     // So are those of drafted keys that no token of the tile sees.
-    int drafts = 0;  // tokens of the piece's sequence
+    int drafts = 0;   // tokens of the piece's sequence
+    int seen_j = -1;  // the block that `vis` is of: those of its keys that some token of the tile sees
+    uint32_t vis[4];
+    auto look = [&](const Piece& pc, int j) {
+      const int valid = pc.L - (pc.j0 + j) * C::BK, d = valid - drafts;
+      uint32_t seen[5] = {0u, 0u, 0u, 0u, 0u};
+      const int t0 = pc.row0 / a.G, t1 = (pc.row0 + min(pc.n_rows, C::ROWS) - 1) / a.G;
+#pragma unroll 2
+      for (int tok = t0 + lane; tok <= t1; tok += 32) {
+        uint32_t m[5];
+        mask_words(a.mask + (int64_t(pc.first) + tok) * a.words, a.words, d, m);
+#pragma unroll
+        for (int i = 0; i < 5; ++i) seen[i] |= m[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 5; ++i) seen[i] = __reduce_or_sync(kFull, seen[i]);
+      visible(seen, d, valid, vis);
+      seen_j = j;
+    };
     auto v_ready = [&](const Piece& pc, int j, int iv) {
       const int valid = pc.L - (pc.j0 + j) * C::BK;
       if constexpr (TREE) {
-        const int d = valid - drafts;  // keys of the block before the drafted ones
-        if (d >= C::BK) return wait(B_READY + iv % C::NST, iv / C::NST);
-        uint32_t vis[4], seen[5] = {0u, 0u, 0u, 0u, 0u};
-        const int t0 = pc.row0 / a.G, t1 = (pc.row0 + min(pc.n_rows, C::ROWS) - 1) / a.G;
-#pragma unroll 2
-        for (int tok = t0 + lane; tok <= t1; tok += 32) {
-          uint32_t m[5];
-          mask_words(a.mask + (int64_t(pc.first) + tok) * a.words, a.words, d, m);
-#pragma unroll
-          for (int i = 0; i < 5; ++i) seen[i] |= m[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 5; ++i) seen[i] = __reduce_or_sync(kFull, seen[i]);
-        visible(seen, d, valid, vis);
+        if (valid - drafts >= C::BK) return wait(B_READY + iv % C::NST, iv / C::NST);
+        if (seen_j != j) look(pc, j);
         if (!wait(B_READY + iv % C::NST, iv / C::NST)) return false;
         uint8_t* v = sm + C::OFF_RING + (iv % C::NST) * C::TILE;
 #pragma unroll 1
@@ -923,7 +929,13 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     while (ok && (taken = take()) != nullptr) {
       const Piece pc = *taken;
       if (pc.nblk == 0) continue;
-      if (TREE) drafts = (pc.row0 + pc.n_rows) / a.G;
+      if (TREE) {
+        drafts = (pc.row0 + pc.n_rows) / a.G;
+        // (the first block with drafted keys, while queries and keys are on their way)
+        const int before = pc.L - drafts - pc.j0 * C::BK, j = before > 0 ? before / C::BK : 0;
+        seen_j = -1;
+        if (j < pc.nblk) look(pc, j);
+      }
       if (pc.n_rows <= 128) {
         // narrow: A takes the even key blocks, B the odd ones, of the same rows
         const bool q_in = wait(B_Q, n_q);
@@ -1115,16 +1127,14 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       if (next->nblk == 0 || (t == 1 && next->n_rows <= 128)) return true;
       if (a.row_boxes) {
         // (rows of other sequences' tokens behind the last come along, and are not used)
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          mbar_arrive_expect_tx(bar(B_Q + t), 2 * kRowBox * 128);
-          const int token = next->first + (next->row0 + t * 128 + (warp & 3) * kRowBox) / a.G;
-          for (int half = 0; half < 2; ++half)
-            tma_load_4d(smem_u32(sm + t * C::TILE + half * C::HALF + (warp & 3) * kRowBox * 128), &tq, bar(B_Q + t), 0, half,
-                        next->h * a.G, token);
-        }
+        const int token = next->first + (next->row0 + t * 128 + (warp & 3) * kRowBox) / a.G;
+        const uint32_t dst = smem_u32(sm + t * C::TILE + (warp & 3) * kRowBox * 128);
+        mbar_arrive_expect_tx_warp(bar(B_Q + t), 2 * kRowBox * 128);
+        tma_load_4d_warp(dst, &tq, bar(B_Q + t), 0, 0, next->h * a.G, token);
+        tma_load_4d_warp(dst + C::HALF, &tq, bar(B_Q + t), 0, 1, next->h * a.G, token);
         ++n_q_boxes;
       } else {
         each_row(*next, [&](int rr, bool in, int64_t token, int head) {
@@ -1187,7 +1197,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
             uint32_t vis[4];
             visible(m, d, valid, vis);
 #pragma unroll
-            for (int k = 0; k < 128; ++k) s[k] = vis[k >> 5] >> (k & 31) & 1 ? s[k] : -INFINITY;
+            for (int k = 0; k < 128; ++k) s[k] = vis[k >> 5] & (1u << (k & 31)) ? s[k] : -INFINITY;
           } else if (valid < C::BK) {
 #pragma unroll
             for (int k = 0; k < 128; ++k) s[k] = k < valid ? s[k] : -INFINITY;
