@@ -28,9 +28,11 @@
 // their root mean square and multiplied by a weight for each column:
 //     x_i <- x_i * rsqrt(mean(x^2) + eps) * w_i,
 // all in fp32, so that norm, rotation and store round once.  The mean of a row of
-// 128 is a sum over the eight lanes that hold its units; a latent row's 36 units
+// 128 is a sum over the eight lanes that hold it (append_rows_kernel and, for long
+// calls, append_stream_kernel); a latent row's 36 units
 // lie across warps, so a warp adds up its 512 columns by itself while the token's
-// place is looked up (1 KB read again, beside the 147 KB of the token's queries).
+// place is looked up (1 KB read again, beside the 147 KB of the token's queries; 1.8k
+// tokens of 129 rows into e4m3: 97 us, 5.5 TB/s, without norms 91, floor 79).
 //
 // One thread handles 32-byte units (two 16-byte chunks of a head row, the
 // two halves of the same eight pairs where pairs are half a row apart), so

@@ -24,7 +24,8 @@
 //
 // Where a power of two of at most 32 query heads share a KV head, 32 rows of it are a
 // box of the queries' and the results' tensors: a warp's Q comes, and its whole results
-// go, by TMA.  (Others by 16 bytes a lane, row by row: MEASURED.)
+// go, by TMA.  (Others go by 16 bytes a lane, row by row.  Trees of 64 young requests: 50
+// us, by lanes 71; the prompts below 715 and 735.)
 //
 // K and V blocks pass in that order through one ring of five 32 KB slots that
 // two producer warps fill by TMA, each a 64-column half of every slot, one box
@@ -33,8 +34,8 @@
 //
 // Many items: a CTA per item (prompts), or a line of all items' key blocks that the
 // CTAs share (batches of few rows a sequence; cross_deal has the rule).  The bound
-// of prompts is 4 * 128 * rows * L operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 740 to
-// 775 us, 1,380 to 1,445 TFLOP/s (floor 552 at 1,938), near the GPU's limit of
+// of prompts is 4 * 128 * rows * L operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 700 to
+// 735 us, 1,455 to 1,525 TFLOP/s (floor 561 at 1,906), near the GPU's limit of
 // 1,400 W and with the tensor pipe waiting for the softmax's turn of the row
 // blocks.
 //
@@ -47,7 +48,7 @@
 // a nanosecond into each SM once the copies flow, behind a start of 5 us (2.3
 // the plan, 2.6 the first blocks), an end of 3 (the last softmax, P . V, the
 // result) and the merge's 1.5 (one token of 8 requests over 1.2k keys of 16
-// heads: 27.7 us, floor 11.6), or the longest piece's chain of products and the
+// heads: 27.2 us, floor 11.6), or the longest piece's chain of products and the
 // 32-bit partial results (prompts of 37 to 900 tokens over 1 to 4.1k keys:
 // 21.6 us, floor 2.9).
 //
@@ -64,7 +65,12 @@
 // that their mask names.  Only the key blocks that reach past L - T_b are masked: a
 // thread shifts its row's mask words to the block's keys, and takes -inf for the
 // scores whose bit is off.  The V rows that no token of the tile sees are zeroed,
-// as those behind the length are (0 * NaN would be NaN).
+// as those behind the length are (0 * NaN would be NaN).  The trees' line (plan_line)
+// takes any lengths, as an item counts there for what it costs beside its blocks.
+// Measured, bf16: 8 tokens over 5.9k keys 16 us (floor 0.9: the chain of plan, first
+// blocks, one softmax, result and merge), 400 tokens of 32 requests over 256 to 131k keys
+// 621 us (floor 529), trees of 64 requests over 1 to 300 keys 50 us (floor 9: an item's
+// chain is 9 us, a CTA to an SM).
 //
 // FP8 (e4m3 caches, with TREE): the tile's codes land in the second half of its slot,
 // [128 keys][128], just where the rows of the second 64 columns will lie, and four
@@ -74,7 +80,11 @@
 // [2^14, 2^15) (exact, but for components below 2^-29 of it, lost among 2^-25 steps), P
 // is f16 too, and the caches' scales join the scores' and the results'.  16 warps: the
 // softmax's registers come from the others' (2 * 168 + 2 * 88 = 4 * 128; the split holds
-// only in code without calls, so that what cross attention calls is inlined here).
+// only in code without calls, so that what cross attention calls is inlined here; with
+// 128 for all, and S read twice, 173 us where it takes 159: 64 tokens of 19 requests, 8k
+// keys).  Bound by the chain of copy, conversion, product and softmax of two blocks in
+// turn: 16 tokens of 19 requests over 8k keys 109 us (floor 47), as long as in bf16 (108,
+// floor 94); trees of 16 to 61 tokens of 8 requests over 32k keys 182 us (floor 54).
 #pragma once
 
 #include <cuda.h>
@@ -173,7 +183,9 @@ static_assert(kMaxPieces * kSmCount * 32 <= kManyPieces && int64_t(kManyPieces) 
 constexpr int kPieceCost = 2, kCutCost = 2;  // in key blocks: of each piece, and of cutting anything
 constexpr int kLineCost = 8;  // and of a line of all key blocks
 // What an item takes of a line beside its key blocks: with it the parts of a tree's
-// line cost the same whatever the items' lengths are.
+// line cost the same whatever the items' lengths are.  (400 tokens of 32 requests over 256
+// to 131k keys: 629 us, with 3 blocks instead of 10 709, with 14 634; as equal pieces
+// 1,304.  64 tokens each, so that items have 256 rows: 714, as equal pieces 1,481.)
 template <bool TREE>
 constexpr int kWalkCost = TREE ? 10 : 0;
 
@@ -405,7 +417,8 @@ __device__ __forceinline__ bool next_piece(const CrossArgs& a, Tail<WARPS>& tail
 // Lane i weighs t = ceil(longest nb / (i + 1)): the blocks of the CTA with most,
 // kPieceCost for each of its pieces, and kCutCost if anything is cut.  Where few
 // rows keep the partial results small and the items, of like lengths, do not fill
-// the last round of CTAs, a line may cost less still.  (What that
+// the last round of CTAs, a line may cost less still; that of trees does for any rows
+// and lengths, as it counts what an item costs.  (What that
 // chooses for 16 heads: two key blocks stay whole, 12.5 us with one token and
 // 12.7 cut; four are cut, 13.1 and 14.8 whole, and with 256 tokens 17.3 and 20.2.)
 template <bool TREE, int WARPS>
