@@ -1398,6 +1398,15 @@ cudaError_t launch_cross_kernel(const CrossArgs& a, const CrossMaps& maps, void*
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(cross_attend_kernel<TREE, FP8>), C::SMEM, allowed);
   if (e != cudaSuccess) return e;
+  if constexpr (FP8) {
+    // The registers that the softmax takes are what the others give back of those the
+    // block is launched with: with fewer it would wait for them forever.
+    static const int launched = [] {
+      cudaFuncAttributes f{};
+      return cudaFuncGetAttributes(&f, cross_attend_kernel<TREE, FP8>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (launched * C::WARPS < 8 * (168 + 88)) return cudaErrorLaunchOutOfResources;
+  }
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;

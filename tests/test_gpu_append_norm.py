@@ -224,9 +224,9 @@ def test_long_calls_and_many_heads(dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,kv_heads,per_head,tokens", [(8, 4, "", 4300), (32, 4, "qk", 1800), (64, 8, "qk", 900),
-                                                            (6, 2, "k", 7500)])
+                                                            (6, 2, "k", 7500), (128, 8, "", 470)])
 def test_calls_of_a_ring(dtype, heads, kv_heads, per_head, tokens):
-    """More than 2^16 rows: stages of four tokens or two, weights in shared memory or (64 heads of their own) not; an odd
+    """More than 2^16 rows: stages of four tokens, two or one, weights in shared memory or (64 heads of their own) not; an odd
     number of tokens, sequences that end within a stage, padding behind them."""
     counts = [tokens // 2 + 1, 0, 1, 2, tokens // 2 - 8]
     c = Cache([n + 5 for n in counts], kv_heads=kv_heads, heads=heads, dtype=dtype, layout="NHD", device="cuda", seed=16)
