@@ -112,7 +112,7 @@ splitkv_status make_u8_map(TmaDesc* out, const void* base, int dim, int64_t rows
 
 }  // namespace
 
-splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys) {
+splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys, bool swizzled) {
   auto fn = encode_fn();
   if (!fn) return fail(SPLITKV_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const bool fp8 = d.kv_dtype == SPLITKV_FP8_E4M3;
@@ -125,7 +125,7 @@ splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_
   cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
   CUresult r = fn(&m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base),
                   gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SPLITKV_ECUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
   std::memcpy(out, &m, sizeof(m));
@@ -151,8 +151,8 @@ static splitkv_status make_rows_map(TmaDesc* out, const void* base, int64_t toke
 
 splitkv_status make_cross_maps(CrossMaps* maps, const CrossArgs& a, const void* k_pages, const void* v_pages,
                                const splitkv_desc_t& d) {
-  splitkv_status st = make_half_map(&maps->k, k_pages, d, a.box_rows);
-  if (st == SPLITKV_OK) st = make_half_map(&maps->v, v_pages, d, a.box_rows);
+  splitkv_status st = make_half_map(&maps->k, k_pages, d, a.box_rows, true);
+  if (st == SPLITKV_OK) st = make_half_map(&maps->v, v_pages, d, a.box_rows, d.kv_dtype == SPLITKV_BF16);
   if (st == SPLITKV_OK && a.row_boxes) st = make_rows_map(&maps->q, a.q, a.n_tokens, a.Hq, a.q_stride, a.G);
   if (st == SPLITKV_OK && a.row_boxes) st = make_rows_map(&maps->out, a.out, a.n_tokens, a.Hq, int64_t(a.Hq) * 128, a.G);
   return st;

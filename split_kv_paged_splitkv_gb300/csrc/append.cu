@@ -55,13 +55,6 @@ struct Token {
   int32_t b, slot, page, in_page;  // b < 0: padding; page < 0: no key is stored
 };
 
-__device__ __forceinline__ uint32_t pack_e4m3x4(const float* x) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
-  return uint32_t(lo) | (uint32_t(hi) << 16);
-}
-
 __device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll

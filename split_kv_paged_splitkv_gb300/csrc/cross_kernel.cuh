@@ -69,22 +69,30 @@
 // takes any lengths, as an item counts there for what it costs beside its blocks.
 // Measured, bf16: 8 tokens over 5.9k keys 16 us (floor 0.9: the chain of plan, first
 // blocks, one softmax, result and merge), 400 tokens of 32 requests over 256 to 131k keys
-// 621 us (floor 529), trees of 64 requests over 1 to 300 keys 50 us (floor 9: an item's
+// 570 us (floor 529), trees of 64 requests over 1 to 300 keys 48 us (floor 9: an item's
 // chain is 9 us, a CTA to an SM).
 //
-// FP8 (e4m3 caches, with TREE): the tile's codes land in the second half of its slot,
-// [128 keys][128], just where the rows of the second 64 columns will lie, and four
-// converter warps turn each row in place into the two swizzled halves, as f16 (exact,
-// one instruction for a pair of codes; bf16 would take four).  The queries are f16
-// then, each row times the power of two that brings its largest component into
-// [2^14, 2^15) (exact, but for components below 2^-29 of it, lost among 2^-25 steps), P
-// is f16 too, and the caches' scales join the scores' and the results'.  16 warps: the
-// softmax's registers come from the others' (2 * 168 + 2 * 88 = 4 * 128; the split holds
-// only in code without calls, so that what cross attention calls is inlined here; with
-// 128 for all, and S read twice, 173 us where it takes 159: 64 tokens of 19 requests, 8k
-// keys).  Bound by the chain of copy, conversion, product and softmax of two blocks in
-// turn: 16 tokens of 19 requests over 8k keys 109 us (floor 47), as long as in bf16 (108,
-// floor 94); trees of 16 to 61 tokens of 8 requests over 32k keys 182 us (floor 54).
+// Trees' softmax holds 64 columns of S at a time and reads half of S twice, in loops of
+// half the length: the code that all warps go round in has to stay in the SM's instruction
+// cache, also while a neighbour's is at another kind of piece.  (Trees of 33 tokens of 8
+// requests over 31k keys in e4m3, pieces of 256 and of 8 rows: 222 us, all of S in
+// registers 286, with three times the misses there; 64 tokens of 19 requests over 8k keys
+// 131 both.  Parts of 32: 205 and 138.  Cross attention's long prompts, all at the same
+// code, take 750 us in halves and 707 so.)
+//
+// FP8 (e4m3 caches, with TREE): K is multiplied as it is stored.  A query row, times the
+// power of two that brings its largest component into [2^7, 2^8), is a sum of two e4m3
+// codes a column, four of its eight bits each (exact, but for components below 2^-9 of the
+// largest, which keep steps of 2^-10, 2^-17 of it or less), and S is the sum of two products
+// of twice the rate.  V's codes land in the second half of their slot, [128 keys][128], just
+// where the rows of the second 64 columns will lie, and four converter warps turn each row
+// in place into the two swizzled halves, as f16 (exact, one instruction for a pair of codes;
+// bf16 would take four); P is f16 too.  The caches' scales join the scores' and the
+// results'.  K's ring has four slots of 16 KB, V's three of 32 KB, a producer each.
+// Measured: 16 tokens of 19 requests over 8k keys 85 us (floor 47; in bf16 107 of 94), 64
+// tokens 141 (in bf16 131), trees of 16 to 61 tokens of 8 requests over 32k keys 150 (floor
+// 54).  With K converted as well, both in one ring of five slots, and the softmax's
+// registers taken from the other warps' (S in one part) the three took 109, 155 and 182.
 #pragma once
 
 #include <cuda.h>
@@ -112,13 +120,17 @@ struct Cross {
   static constexpr uint32_t TMEM_COLS = 512, S_COL = 0, O_COL = 256;  // + 128 per row block
   static constexpr float RESCALE_LOG2 = 8.f;
 };
-template <bool FP8>
+template <bool TREE, bool FP8>
 struct CrossCta : Cross {
+  static constexpr int PART = TREE ? 64 : 128;  // columns of S that a softmax thread holds
   static constexpr int CONVERTER = SOFTMAX_WARPS + 4;  // first of four (warp 11 fills its warpgroup)
   static constexpr int WARPS = SOFTMAX_WARPS + (FP8 ? 8 : 3);
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TAIL = FP8 ? 2048 : 1536; // barriers, plan
   static constexpr int SMEM = 1024 + OFF_BAR + TAIL;
+  // e4m3: a ring for K's codes, one for V's and what becomes of them
+  static constexpr int K_SLOTS = 4, V_SLOTS = 3, SLOTS = K_SLOTS + V_SLOTS;
+  static_assert(K_SLOTS * HALF + V_SLOTS * TILE == NST * TILE, "in the place of the one ring");
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
@@ -133,8 +145,12 @@ enum {
   B_JOINED,                      //   A has read them and B's O (128 threads)
   B_DONE,
   B_COUNT,
-  B_CONV = B_COUNT,              // [NST] e4m3: the slot holds f16 (a lane of each converter warp)
-  B_COUNT_FP8 = B_CONV + Cross::NST
+  // e4m3: instead of B_FULL and B_EMPTY those of K's ring and, K_SLOTS further, of V's;
+  // B_CONV [V_SLOTS]: the slot holds f16 (a lane of each converter warp)
+  B_FULL_FP8 = B_COUNT,
+  B_EMPTY_FP8 = B_FULL_FP8 + CrossCta<true, true>::SLOTS,
+  B_CONV = B_EMPTY_FP8 + CrossCta<true, true>::SLOTS,
+  B_COUNT_FP8 = B_CONV + CrossCta<true, true>::V_SLOTS
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -182,15 +198,19 @@ constexpr int kManyPieces = 32767;
 static_assert(kMaxPieces * kSmCount * 32 <= kManyPieces && int64_t(kManyPieces) * 65535 < (int64_t(1) << 31), "no call's count");
 constexpr int kPieceCost = 2, kCutCost = 2;  // in key blocks: of each piece, and of cutting anything
 constexpr int kLineCost = 8;  // and of a line of all key blocks
-// What an item takes of a line beside its key blocks: with it the parts of a tree's
-// line cost the same whatever the items' lengths are.  (400 tokens of 32 requests over 256
-// to 131k keys: 629 us, with 3 blocks instead of 10 709, with 14 634; as equal pieces
-// 1,304.  64 tokens each, so that items have 256 rows: 714, as equal pieces 1,481.)
-template <bool TREE>
-constexpr int kWalkCost = TREE ? 10 : 0;
+// What counts in a line: a key block of an item of up to 128 rows and of one of more, and
+// an item beside them (trees'; with that the parts of a line cost the same whatever the
+// items' lengths are: 400 tokens of 32 requests over 256 to 131k keys took 629 us, with 3
+// blocks instead of 10 709, with 14 634; as equal pieces 1,304.  Wide and narrow blocks
+// counted alike: 8 to 130 tokens of those 1,006 us, so 968; 400 in e4m3 520 and 483.)
+template <bool TREE, bool FP8>
+struct Line {
+  static constexpr int WIDE = TREE ? 6 : 1, NARROW = TREE ? (FP8 ? 4 : 5) : 1, ITEM = TREE ? 50 : 0;
+  static __device__ __forceinline__ int block(int rows) { return rows <= 128 ? NARROW : WIDE; }
+};
 
-// Where a warp is in a line: the next key block (or what an item takes beside them), and
-// the item that holds it (of sequence b, from block `off` on) with its sequence's numbers.
+// Where a warp is in a line: the next key block, and the item that holds it (of sequence b,
+// from block `off` on) with its sequence's numbers.
 struct Walk {
   int64_t x;
   int b, item, off, first, rows, L, tiles, nb;
@@ -201,13 +221,14 @@ template <int WARPS>
 struct Tail {
   uint32_t tmem;   // written by the allocation
   int32_t pieces;  // in `piece`; -1: the line's blocks [lo, hi), `share` to a CTA
-  int64_t lo, hi, share;
+  int64_t lo, hi, share;  // (those that begin in it)
   Piece piece[kMaxPieces];
   Walk walk[WARPS];
   Piece now[WARPS];
+  uint8_t down[128];  // e4m3: of a narrow piece's rows, the exponent of what undoes their power of two
 };
-static_assert(B_COUNT * 8 + sizeof(Tail<CrossCta<false>::WARPS>) <= CrossCta<false>::TAIL, "barriers, then the tail");
-static_assert(B_COUNT_FP8 * 8 + sizeof(Tail<CrossCta<true>::WARPS>) <= CrossCta<true>::TAIL, "barriers, then the tail");
+static_assert(B_COUNT * 8 + sizeof(Tail<CrossCta<false, false>::WARPS>) <= CrossCta<false, false>::TAIL, "barriers, then the tail");
+static_assert(B_COUNT_FP8 * 8 + sizeof(Tail<CrossCta<true, true>::WARPS>) <= CrossCta<true, true>::TAIL, "barriers, then the tail");
 
 // Pieces of about t key blocks that an item of nb is cut into.  (In floating
 // point, for speed: any count in 1 .. nb is right, as long as all agree on it.)
@@ -233,6 +254,14 @@ __device__ __forceinline__ Lane lane_of(const CrossArgs& a, int b) {
   return x;
 }
 
+// What a sequence's items take of a line.
+template <class U>
+__device__ __forceinline__ int64_t units_of(const CrossArgs& a, const Lane& s) {
+  if (s.tiles == 0) return 0;
+  const int last = U::block(s.rows - (s.tiles - 1) * Cross::ROWS);
+  return a.Hkv * (int64_t(s.tiles - 1) * (s.nb * U::WIDE + U::ITEM) + s.nb * last + U::ITEM);
+}
+
 // Sum over the lanes before this one.
 template <class T>
 __device__ __forceinline__ T lanes_before(T n, int lane, T* total) {
@@ -256,14 +285,16 @@ __device__ __forceinline__ T lanes_before(T n, int lane, T* total) {
 // us, in whole items 49.7; over 4k keys 79 and 111.  kLineCost is what leaves 8
 // requests, 27.7 us and as a line 30.2, and 16, 51.8 and 55.3, as they are.
 template <bool TREE, int WARPS>
-__device__ __forceinline__ void plan_line_here(const CrossArgs& a, int lane, int64_t all, Tail<WARPS>& tail) {
-  const int64_t share = (all + a.parts - 1) / a.parts;
+__device__ __noinline__ void plan_line(const CrossArgs& a, int lane, int64_t all, Tail<WARPS>& tail) {
+  using U = Line<TREE, WARPS == CrossCta<true, true>::WARPS>;
+  // (no CTA between an item's first and its last is without a block of it)
+  const int64_t share = max(int64_t(U::WIDE), (all + a.parts - 1) / a.parts);
   const int64_t lo = min(all, int64_t(blockIdx.x) * share), hi = min(all, lo + share);
   Walk w = {lo, 0, 0, 0, 0, 0, 0, 0, 1};
   int64_t passed = 0, total;
   for (int b0 = 0; lo < hi && b0 < a.batch; b0 += 32) {
     const Lane s = lane_of<TREE>(a, b0 + lane);
-    const int64_t n = int64_t(s.tiles) * a.Hkv * (s.nb + kWalkCost<TREE>);
+    const int64_t n = units_of<U>(a, s);
     const int64_t at = passed + lanes_before(n, lane, &total);
     const unsigned m = __ballot_sync(kFull, lo >= at && lo < at + n);
     passed += total;
@@ -275,10 +306,16 @@ __device__ __forceinline__ void plan_line_here(const CrossArgs& a, int lane, int
       w.L = __shfl_sync(kFull, s.L, f);
       w.tiles = __shfl_sync(kFull, s.tiles, f);
       w.nb = __shfl_sync(kFull, s.nb, f);
-      const int64_t in = lo - __shfl_sync(kFull, at, f);
-      const int each = w.nb + kWalkCost<TREE>;
-      w.item = int(in / each);
-      w.off = int(in - int64_t(w.item) * each);
+      int64_t in = lo - __shfl_sync(kFull, at, f);
+      const int whole = w.nb * U::WIDE + U::ITEM, last = U::block(w.rows - (w.tiles - 1) * Cross::ROWS);
+      const int64_t head = int64_t(w.tiles - 1) * whole + w.nb * last + U::ITEM;
+      const int h = int(in / head);
+      in -= h * head;
+      const int tile = min(w.tiles - 1, int(in / whole)), each = tile < w.tiles - 1 ? U::WIDE : last;
+      in -= int64_t(tile) * whole;
+      w.item = h * w.tiles + tile;
+      w.off = min(w.nb, (int(in) + each - 1) / each);
+      w.x = lo - in + int64_t(w.off) * each;
       break;
     }
   }
@@ -291,18 +328,6 @@ __device__ __forceinline__ void plan_line_here(const CrossArgs& a, int lane, int
     a.split[blockIdx.x].cuts = 0;
     if (blockIdx.x == 0) *a.n_split = a.parts;
   }
-}
-
-template <bool TREE, int WARPS>
-__device__ __noinline__ void plan_line_there(const CrossArgs& a, int lane, int64_t all, Tail<WARPS>& tail) {
-  plan_line_here<TREE>(a, lane, all, tail);
-}
-template <bool TREE, int WARPS>
-__device__ __forceinline__ void plan_line(const CrossArgs& a, int lane, int64_t all, Tail<WARPS>& tail) {
-  if constexpr (WARPS == CrossCta<true>::WARPS)
-    plan_line_here<TREE>(a, lane, all, tail);
-  else
-    plan_line_there<TREE>(a, lane, all, tail);
 }
 
 // A CTA per item: head blockIdx.y, and a row tile that is found by a search, 32
@@ -346,12 +371,19 @@ __device__ __forceinline__ void plan_one(const CrossArgs& a, int lane, Tail<WARP
 
 // By warp `me`, in a line: its next piece, into tail.now[me]; false behind the last.
 template <bool TREE, int WARPS>
-__device__ __forceinline__ bool next_piece_here(const CrossArgs& a, Tail<WARPS>& tail, int me, int lane) {
+__device__ __noinline__ bool next_piece(const CrossArgs& a, Tail<WARPS>& tail, int me, int lane) {
   Walk& walk = tail.walk[me];
   __syncwarp();  // (the piece before has been read)
   Walk w = walk;
-  auto item_done = [&]() {  // (off: behind its last block)
-    w.x += w.nb + kWalkCost<TREE> - w.off;
+  using U = Line<TREE, WARPS == CrossCta<true, true>::WARPS>;
+  int tile, each;
+  auto weigh = [&]() {
+    tile = w.tiles > 1 ? w.item % w.tiles : 0;
+    each = U::block(w.rows - tile * Cross::ROWS);
+  };
+  weigh();
+  auto item_done = [&]() {
+    w.x += (w.nb - w.off) * each + U::ITEM;
     if (w.x >= tail.hi) return;
     w.off = 0;
     if (++w.item == w.tiles * a.Hkv) {  // the next sequence with tokens
@@ -364,26 +396,27 @@ __device__ __forceinline__ bool next_piece_here(const CrossArgs& a, Tail<WARPS>&
       w.tiles = s.tiles;
       w.nb = s.nb;
     }
+    weigh();
   };
   if (TREE && w.x < tail.hi && w.off >= w.nb) item_done();  // (the line's part begins behind an item's blocks)
   if (w.x >= tail.hi) return false;
-  const int len = int(min(int64_t(w.nb - w.off), tail.hi - w.x));  // blocks
+  const int len = int(min(int64_t(w.nb - w.off), (tail.hi - w.x + each - 1) / each));  // blocks
   Piece q;
   q.b = w.b;
   q.h = w.tiles > 1 ? w.item / w.tiles : w.item;
   q.first = w.first;
-  q.row0 = (w.item - q.h * w.tiles) * Cross::ROWS;
+  q.row0 = tile * Cross::ROWS;
   q.n_rows = w.rows - q.row0;
   q.L = w.L;
   q.j0 = w.off;
   q.nblk = w.L > 0 ? len : 0;
-  q.slot = len < w.nb ? 2 * int(blockIdx.x) + (w.x > tail.lo) : -1;
+  q.slot = len < w.nb ? 2 * int(blockIdx.x) + (w.off == 0) : -1;
   if (me == Cross::ISSUER && lane == 0 && len < w.nb && w.off == 0) {  // (the CTA's last piece: an item's first)
-    const int last = int((w.x + w.nb - 1) / tail.share);               // CTA of the item's last block
+    const int last = int((w.x + (w.nb - 1) * each) / tail.share);  // CTA of the item's last block
     const CrossSplit r = {last - int(blockIdx.x) + 1, q.slot, 2, q.first, q.h, q.row0, min(q.n_rows, Cross::ROWS)};
     a.split[blockIdx.x] = r;
   }
-  w.x += len;
+  w.x += len * each;
   w.off += len;
   if (w.off == w.nb && w.x < tail.hi) item_done();
   __syncwarp();
@@ -393,18 +426,6 @@ __device__ __forceinline__ bool next_piece_here(const CrossArgs& a, Tail<WARPS>&
   }
   __syncwarp();
   return true;
-}
-
-template <bool TREE, int WARPS>
-__device__ __noinline__ bool next_piece_there(const CrossArgs& a, Tail<WARPS>& tail, int me, int lane) {
-  return next_piece_here<TREE>(a, tail, me, lane);
-}
-template <bool TREE, int WARPS>
-__device__ __forceinline__ bool next_piece(const CrossArgs& a, Tail<WARPS>& tail, int me, int lane) {
-  if constexpr (WARPS == CrossCta<true>::WARPS)
-    return next_piece_here<TREE>(a, tail, me, lane);
-  else
-    return next_piece_there<TREE>(a, tail, me, lane);
 }
 
 // By a warp: which pieces this CTA computes.
@@ -430,17 +451,18 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail<W
   Lane mine;
   auto read = [&](int b0) { mine = lane_of<TREE>(a, b0 + lane); };
   int items = 0, longest = 1, shortest = INT32_MAX, widest = 0;
-  int64_t all = 0;  // key blocks
+  using U = Line<TREE, WARPS == CrossCta<true, true>::WARPS>;
+  int64_t all = 0;  // units of a line
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     read(b0);
-    const int64_t blocks = int64_t(mine.tiles) * a.Hkv * (mine.nb + kWalkCost<TREE>);
+    const int64_t units = units_of<U>(a, mine);
     if (a.line) {
       int64_t sum;
-      lanes_before(blocks, lane, &sum);
+      lanes_before(units, lane, &sum);
       all += sum;
       continue;
     }
-    all += __reduce_add_sync(kFull, int(min(int64_t(1) << 25, blocks)));  // (items are few: more need not be exact)
+    all += __reduce_add_sync(kFull, int(min(int64_t(1) << 25, units)));  // (items are few: more need not be exact)
     items += __reduce_add_sync(kFull, mine.tiles);
     longest = max(longest, __reduce_max_sync(kFull, mine.tiles > 0 ? mine.nb : 1));
     shortest = min(shortest, __reduce_min_sync(kFull, mine.tiles > 0 ? mine.nb : INT32_MAX));
@@ -465,8 +487,8 @@ __device__ __forceinline__ void plan_pieces(const CrossArgs& a, int lane, Tail<W
   const int best = __reduce_min_sync(kFull, fits ? cost * 32 + lane : ~0u) & 31;
   const float T = __shfl_sync(kFull, t, best);
   const int P = __shfl_sync(kFull, n, best);
-  const int64_t share = (all + a.parts - 1) / a.parts;
-  if ((TREE || widest <= 128) && all >= a.parts && all < (1 << 25) && (TREE || share <= 2 * int64_t(shortest)) &&
+  const int64_t share = (all + a.parts - 1) / a.parts / U::block(widest);  // key blocks
+  if ((TREE || widest <= 128) && all >= a.parts * U::WIDE && all < (1 << 25) && (TREE || share <= 2 * int64_t(shortest)) &&
       share + kLineCost < __shfl_sync(kFull, cost, best)) {
     plan_line<TREE>(a, lane, all, tail);
     return;
@@ -625,40 +647,77 @@ __device__ __forceinline__ void fma2(float& x, float& y, float s, float b) {
 // Eight MMAs of one K = 128 product, issued by a converged warp: one lane,
 // elected once, issues all of them (between two MMAs nothing but the next
 // descriptors' additions, in units of 16 bytes).
-// S = Q . K^T: both operands are two 64-column halves, 32 bytes per step.
+// S = Q . K^T: both operands are two 64-column halves, 32 bytes per step; or (e4m3) Q is
+// a sum of two tiles of 128 columns, each multiplied by the one of K.
+template <bool FP8>
 __device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
-  asm volatile(
-      "{\n\t"
-      ".reg .pred e, q, y;\n\t"
-      ".reg .b64 a, b;\n\t"
-      "setp.ne.b32 q, %4, 0;\n\t"
-      "setp.eq.b32 y, 0, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
-      "add.s64 a, %1, 2;\n\t"
-      "add.s64 b, %2, 2;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
-      "add.s64 a, %1, 4;\n\t"
-      "add.s64 b, %2, 4;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
-      "add.s64 a, %1, 6;\n\t"
-      "add.s64 b, %2, 6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
-      "add.s64 a, %1, 1024;\n\t"
-      "add.s64 b, %2, 1024;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
-      "add.s64 a, %1, 1026;\n\t"
-      "add.s64 b, %2, 1026;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
-      "add.s64 a, %1, 1028;\n\t"
-      "add.s64 b, %2, 1028;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
-      "add.s64 a, %1, 1030;\n\t"
-      "add.s64 b, %2, 1030;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
-      "}" ::"r"(d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(0)
-      : "memory");
+  if constexpr (FP8) {
+    asm volatile(
+        "{\n\t"
+        ".reg .pred e, q, y;\n\t"
+        ".reg .b64 a, b;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "setp.eq.b32 y, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, q;\n\t"
+        "add.s64 a, %1, 2;\n\t"
+        "add.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 4;\n\t"
+        "add.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 6;\n\t"
+        "add.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 1024;\n\t"
+        "add.s64 b, %2, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 1026;\n\t"
+        "add.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 1028;\n\t"
+        "add.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 1030;\n\t"
+        "add.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(0)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t"
+        ".reg .pred e, q, y;\n\t"
+        ".reg .b64 a, b;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "setp.eq.b32 y, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
+        "add.s64 a, %1, 2;\n\t"
+        "add.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 4;\n\t"
+        "add.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 6;\n\t"
+        "add.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 1024;\n\t"
+        "add.s64 b, %2, 1024;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 1026;\n\t"
+        "add.s64 b, %2, 1026;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 1028;\n\t"
+        "add.s64 b, %2, 1028;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "add.s64 a, %1, 1030;\n\t"
+        "add.s64 b, %2, 1030;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(0)
+        : "memory");
+  }
 }
 // O (+)= P . V: P in TMEM, 8 columns per step; V 16 keys of 128 bytes per step.
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t more) {
@@ -719,7 +778,7 @@ __device__ __forceinline__ void visible(const uint32_t (&m)[5], int d, int valid
 // Eight lanes to a row, all of which have read before any writes.
 __device__ __forceinline__ void convert_rows(uint8_t* raw, int rows, int lane) {
   const int seg = lane & 7, col = 2 * (seg & 3), second = seg >> 2;
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 2;  // (4: no faster, and more code)
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += 4 * kBatch) {
     uint4 x[kBatch];
@@ -741,26 +800,37 @@ __device__ __forceinline__ void convert_rows(uint8_t* raw, int rows, int lane) {
 }
 
 template <bool TREE, bool FP8>
-__global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
+__global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
     cross_attend_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq,
                         const __grid_constant__ CUtensorMap to) {
   static_assert(TREE || !FP8, "e4m3 caches are served with TREE");
-  using C = CrossCta<FP8>;
+  using C = CrossCta<TREE, FP8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   auto& tail = *reinterpret_cast<Tail<C::WARPS>*>(bars + (FP8 ? B_COUNT_FP8 : B_COUNT));
-  constexpr int B_READY = FP8 ? B_CONV : B_FULL;  // a slot's 16-bit rows
   auto bar = [&](int i) { return smem_u32(bars + i); };
+  // The slot of the n-th key block's K (v = 0) or V (v = 1), counted over all pieces: its
+  // barriers, its turn's phase and its place.
+  auto slot_of = [&](int v, int n) {
+    return !FP8 ? (2 * n + v) % C::NST : v ? C::K_SLOTS + n % C::V_SLOTS : n % C::K_SLOTS;
+  };
+  auto turn_of = [&](int v, int n) { return !FP8 ? (2 * n + v) / C::NST : n / (v ? C::V_SLOTS : C::K_SLOTS); };
+  auto full = [&](int v, int n) { return bar((FP8 ? B_FULL_FP8 : B_FULL) + slot_of(v, n)); };
+  auto empty = [&](int v, int n) { return bar((FP8 ? B_EMPTY_FP8 : B_EMPTY) + slot_of(v, n)); };
+  auto slot_at = [&](int v, int n) {
+    return C::OFF_RING + (!FP8 ? slot_of(v, n) * C::TILE : v ? C::K_SLOTS * C::HALF + n % C::V_SLOTS * C::TILE
+                                                             : slot_of(0, n) * C::HALF);
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::NST; ++s) {
-      mbar_init(bar(B_FULL + s), 2);  // (a half by each producer)
-      mbar_init(bar(B_EMPTY + s), 1);
-      if (FP8) mbar_init(bar(B_CONV + s), 4);
+    for (int s = 0; s < (FP8 ? C::SLOTS : C::NST); ++s) {
+      mbar_init(bar((FP8 ? B_FULL_FP8 : B_FULL) + s), FP8 ? 1 : 2);  // (e4m3: one producer's; else a half by each)
+      mbar_init(bar((FP8 ? B_EMPTY_FP8 : B_EMPTY) + s), 1);
     }
+    for (int s = 0; FP8 && s < C::V_SLOTS; ++s) mbar_init(bar(B_CONV + s), 4);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(B_Q + t), !FP8 && a.row_boxes ? 4 : 128);
       mbar_init(bar(B_S + t), 1);
@@ -802,7 +872,6 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     return next_piece<TREE>(a, tail, warp, lane) ? &tail.now[warp] : nullptr;
   };
 
-  if (FP8 && warp >= C::SOFTMAX_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == C::PRODUCER || warp == C::PRODUCER + 1) {
     // ------------------------------------------------------------- producers
     // Of all pieces, key block j's K is ring item 2 j, its V item 2 j + 1; item
@@ -813,49 +882,56 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     // last key are not read.
     const int half = warp - C::PRODUCER;
     const int br = a.box_rows;
+    // (e4m3: one warp copies the whole rows of K, the other those of V, into the second
+    // half of the slot.)
     bool ok = true;
-    int item = 0;
+    int n = 0;       // key blocks so far
+    int issued = 0;  // what this warp asked for: K, V, K, ..., or (e4m3) the blocks of one of them
     const Piece* taken;
     while (ok && (taken = take()) != nullptr) {
       const Piece pc = *taken;
       const int32_t* trow = a.block_table + size_t(pc.b) * a.max_pages;
-      for (int j = 0; j < pc.nblk && ok; ++j) {
-        const int key0 = (pc.j0 + j) * C::BK;
-        const int np = (min(C::BK, pc.L - key0) + br - 1) / br;
-        int ph = 0, in = 0;
-        if (lane < np) {
-          const int key = key0 + lane * br, lp = key / a.P;
-          in = key - lp * a.P;
-          ph = trow[lp];
-          if (ph < 0 || ph >= a.num_pages) {
-            if (a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
-            ph = 0;
-          }
+      int next_ph = 0, next_in = 0;  // of the block after this one, asked for a block ahead
+      auto look_up = [&](int j) {
+        const int key = (pc.j0 + j) * C::BK + lane * br, lp = key / a.P;
+        next_in = key - lp * a.P;
+        next_ph = lane < C::BK / br && key < pc.L ? trow[lp] : 0;
+      };
+      if (pc.nblk > 0) look_up(0);
+      for (int j = 0; j < pc.nblk && ok; ++j, ++n) {
+        const int np = (min(C::BK, pc.L - (pc.j0 + j) * C::BK) + br - 1) / br;
+        int ph = next_ph;
+        const int in = next_in;
+        if (ph < 0 || ph >= a.num_pages) {
+          if (a.status) atomicOr(a.status, SPLITKV_DEVERR_PAGE);
+          ph = 0;
         }
+        if (j + 1 < pc.nblk) look_up(j + 1);
 #pragma unroll 1
-        for (int v = 0; v < 2; ++v, ++item) {
-          const int st = item % C::NST;
-          if (item >= C::NST) ok = __all_sync(kFull, mbar_wait(bar(B_EMPTY + st), (item / C::NST - 1) & 1));
+        for (int v = FP8 ? half : 0; v < (FP8 ? half + 1 : 2); ++v) {
+          if (turn_of(v, n) > 0) ok = __all_sync(kFull, mbar_wait(empty(v, n), (turn_of(v, n) - 1) & 1));
           if (!ok) break;
-          // (e4m3: whole rows into the second half, every other group by each warp)
-          mbar_arrive_expect_tx_warp(bar(B_FULL + st), uint32_t((FP8 ? (np + 1 - half) / 2 : np) * br * 128));
-          const uint32_t dst = smem_u32(sm + C::OFF_RING + st * C::TILE) + (FP8 ? 1 : half) * C::HALF;
+          mbar_arrive_expect_tx_warp(full(v, n), uint32_t(np * br * 128));
+          const uint32_t dst = smem_u32(sm + slot_at(v, n)) + (FP8 ? v : half) * C::HALF;
           const CUtensorMap* tm = v ? &tv : &tk;
-          for (int g = FP8 ? half : 0; g < np; g += FP8 ? 2 : 1) {
+          for (int g = 0; g < np; ++g) {
             const int pg = __shfl_sync(kFull, ph, g), kp = __shfl_sync(kFull, in, g);
-            tma_load_5d_warp(dst + g * br * 128, tm, bar(B_FULL + st), 0, kp, FP8 ? 0 : half, pc.h, pg);
+            tma_load_5d_warp(dst + g * br * 128, tm, full(v, n), 0, kp, FP8 ? 0 : half, pc.h, pg);
           }
+          ++issued;
         }
       }
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
-    // Stay until every copy has landed: the last item of each slot.
+    // Stay until every copy has landed: the last of each slot.
     if (lane == 0)
-      for (int i = item - 1; i >= 0 && i >= item - C::NST; --i)  // (item: the first that was not issued)
-        mbar_wait(bar(B_FULL + i % C::NST), (i / C::NST) & 1);
+      for (int i = issued - 1; i >= 0 && i >= issued - (!FP8 ? C::NST : half ? C::V_SLOTS : C::K_SLOTS); --i) {
+        const int v = FP8 ? half : i & 1;
+        mbar_wait(full(v, FP8 ? i : i >> 1), turn_of(v, FP8 ? i : i >> 1) & 1);
+      }
   } else if (warp == C::ISSUER) {
     // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idesc_qk = FP8 ? umma_idesc_f16(128, 128, 0, 0) : umma_idesc_bf16(128, 128, 0, 0),
+    constexpr uint32_t idesc_qk = FP8 ? umma_idesc_e4m3(128, 128) : umma_idesc_bf16(128, 128, 0, 0),
                        idesc_pv = FP8 ? umma_idesc_f16(128, 128, 0, 1) : umma_idesc_bf16(128, 128, 0, 1);
     // one CTA reports lengths that the cache cannot hold
     if (a.status && blockIdx.x == 0 && blockIdx.y == 0)
@@ -864,25 +940,28 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
         if (a.seq_lens[i] != keys_of<TREE>(a, i, TREE ? tokens_of(a, i, &first) : 0)) atomicOr(a.status, SPLITKV_DEVERR_SEQLEN);
       }
     bool ok = true;
-    int item = 0;                      // ring items consumed
+    int n = 0;                  // key blocks of the pieces before
     uint32_t n_q = 0, n_p = 0;  // phases of B_Q and B_P so far, a bit per row block
     auto wait = [&](int i, int phase) {
       ok = ok && __all_sync(kFull, mbar_wait(bar(i), phase & 1));
       return ok;
     };
-    auto slot = [&](int i) { return smem_u32(sm + C::OFF_RING + (i % C::NST) * C::TILE); };
+    auto landed = [&](int v, int n) {
+      ok = ok && __all_sync(kFull, mbar_wait(full(v, n), turn_of(v, n) & 1));
+      return ok;
+    };
+    auto v_in_smem = [&](int n) { return FP8 ? wait(B_CONV + n % C::V_SLOTS, turn_of(1, n)) : landed(1, n); };
     static_assert(C::HALF >> 4 == 1024, "descriptor steps of mma_qk");
-    auto qk = [&](int t, int q, int i) {  // S_t = Q_q . K^T, K in ring item i
-      mma_qk(tmem + C::S_COL + 128 * t, umma_desc(smem_u32(sm + q * C::TILE), 16, 1024, 2), umma_desc(slot(i), 16, 1024, 2),
-             idesc_qk);
+    auto qk = [&](int t, int q, int n) {  // S_t = Q_q . K^T
+      mma_qk<FP8>(tmem + C::S_COL + 128 * t, umma_desc(smem_u32(sm + q * C::TILE), 16, 1024, 2),
+                  umma_desc(smem_u32(sm + slot_at(0, n)), 16, 1024, 2), idesc_qk);
       umma_commit_warp(bar(B_S + t));
     };
-    auto pv = [&](int t, int i, bool more) {  // O_t (+)= P_t . V, V in ring item i
-      mma_pv(tmem + C::O_COL + 128 * t, tmem + C::S_COL + 128 * t, umma_desc(slot(i), C::HALF, 1024, 2), idesc_pv, more);
+    auto pv = [&](int t, int n, bool more) {  // O_t (+)= P_t . V
+      mma_pv(tmem + C::O_COL + 128 * t, tmem + C::S_COL + 128 * t, umma_desc(smem_u32(sm + slot_at(1, n)), C::HALF, 1024, 2),
+             idesc_pv, more);
     };
-    auto release = [&](int i) {
-      umma_commit_warp(bar(B_EMPTY + i % C::NST));
-    };
+    auto release = [&](int v, int n) { umma_commit_warp(empty(v, n)); };
     // V of key block j of a piece has landed; key slots past the last key may
     // hold anything (even NaN): their V rows are zeroed, so that 0 * V stays 0.
     // So are those of drafted keys that no token of the tile sees.
@@ -905,13 +984,13 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       visible(seen, d, valid, vis);
       seen_j = j;
     };
-    auto v_ready = [&](const Piece& pc, int j, int iv) {
+    auto v_ready = [&](const Piece& pc, int j, int n) {
       const int valid = pc.L - (pc.j0 + j) * C::BK;
       if constexpr (TREE) {
-        if (valid - drafts >= C::BK) return wait(B_READY + iv % C::NST, iv / C::NST);
+        if (valid - drafts >= C::BK) return v_in_smem(n);
         if (seen_j != j) look(pc, j);
-        if (!wait(B_READY + iv % C::NST, iv / C::NST)) return false;
-        uint8_t* v = sm + C::OFF_RING + (iv % C::NST) * C::TILE;
+        if (!v_in_smem(n)) return false;
+        uint8_t* v = sm + slot_at(1, n);
 #pragma unroll 1
         for (int w = 0; w < 4; ++w) {
           const uint32_t x = w < 2 ? (w ? vis[1] : vis[0]) : (w == 2 ? vis[2] : vis[3]);
@@ -927,9 +1006,9 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
         }
         return true;
       }
-      if (!wait(B_READY + iv % C::NST, iv / C::NST)) return false;
+      if (!v_in_smem(n)) return false;
       if (valid < C::BK) {
-        uint8_t* v = sm + C::OFF_RING + (iv % C::NST) * C::TILE;
+        uint8_t* v = sm + slot_at(1, n);
         for (int x = lane; x < (C::BK - valid) * 16; x += 32)
           *reinterpret_cast<uint4*>(v + (x & 1) * C::HALF + (valid + (x >> 4)) * 128 + ((x >> 1) & 7) * 16) =
               make_uint4(0, 0, 0, 0);
@@ -954,71 +1033,71 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
         const bool q_in = wait(B_Q, n_q);
         n_q ^= 1u;
         for (int j = 0; j < min(2, pc.nblk) && q_in; ++j) {
-          if (!wait(B_READY + (item + 2 * j) % C::NST, (item + 2 * j) / C::NST)) break;
+          if (!landed(0, n + j)) break;
           tc_fence_after();
-          qk(j, 0, item + 2 * j);
-          release(item + 2 * j);
+          qk(j, 0, n + j);
+          release(0, n + j);
         }
         for (int j = 0; j < pc.nblk && ok; ++j) {
-          const int t = j & 1, iv = item + 2 * j + 1, ik = item + 2 * j + 4;  // V of this block, K of the next but one
-          if (!v_ready(pc, j, iv) || !wait(B_P + t, n_p >> t)) break;
+          const int t = j & 1;
+          if (!v_ready(pc, j, n + j) || !wait(B_P + t, n_p >> t)) break;
           n_p ^= 1u << t;
           tc_fence_after();
-          pv(t, iv, j > 1);
+          pv(t, n + j, j > 1);
           if (j + 2 < pc.nblk) {
-            release(iv);  // (K of the next block but one is waited for in the slot that V before this one left)
-            if (!wait(B_READY + ik % C::NST, ik / C::NST)) break;
+            release(1, n + j);  // (K of the next block but one is waited for in the slot that V before this one left)
+            if (!landed(0, n + j + 2)) break;
             tc_fence_after();
-            qk(t, 0, ik);
-            release(ik);
+            qk(t, 0, n + j + 2);
+            release(0, n + j + 2);
           } else {
             umma_commit_warp(bar(B_O + t));
-            release(iv);
+            release(1, n + j);
           }
         }
-        item += 2 * pc.nblk;
+        n += pc.nblk;
         continue;
       }
       for (int t = 0; t < 2 && ok; ++t) {
         const bool q_in = wait(B_Q + t, n_q >> t);
         n_q ^= 1u << t;
-        if (!q_in || (t == 0 && !wait(B_READY + item % C::NST, item / C::NST))) break;
+        if (!q_in || (t == 0 && !landed(0, n))) break;
         tc_fence_after();
-        qk(t, t, item);
-        if (t == 1) release(item);
+        qk(t, t, n);
+        if (t == 1) release(0, n);
       }
       for (int j = 0; j < pc.nblk && ok; ++j) {
-        const int iv = item + 2 * j + 1, ik = iv + 1;  // V of this block, K of the next
+        const int next = n + j + 1;
         bool k_in = true;
         for (int t = 0; t < 2 && ok; ++t) {
           if (t == 0) {
             // (off the way from P to the next product, if K has landed by now)
             if (j + 1 < pc.nblk)
-              k_in = __all_sync(kFull, mbar_test(bar(B_READY + ik % C::NST), (ik / C::NST) & 1));
-            if (!v_ready(pc, j, iv)) break;
+              k_in = __all_sync(kFull, mbar_test(full(0, next), turn_of(0, next) & 1));
+            if (!v_ready(pc, j, n + j)) break;
           }
           if (!wait(B_P + t, n_p >> t)) break;
           n_p ^= 1u << t;
           tc_fence_after();
-          pv(t, iv, j > 0);
+          pv(t, n + j, j > 0);
           if (j + 1 < pc.nblk) {
             if (!k_in) {
-              if (!wait(B_READY + ik % C::NST, ik / C::NST)) break;
+              if (!landed(0, next)) break;
               tc_fence_after();
               k_in = true;
             }
-            qk(t, t, ik);
+            qk(t, t, next);
           } else {
             umma_commit_warp(bar(B_O + t));
           }
           // (behind the products, which are not to wait for it)
           if (t == 1) {
-            release(iv);
-            if (j + 1 < pc.nblk) release(ik);
+            release(1, n + j);
+            if (j + 1 < pc.nblk) release(0, next);
           }
         }
       }
-      item += 2 * pc.nblk;
+      n += pc.nblk;
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
     // every MMA issued above completes before TMEM is released
@@ -1027,35 +1106,32 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     mbar_wait(bar(B_DONE), 0);
   } else if (FP8 && warp >= C::SOFTMAX_WARPS) {
     // ------------------------------------------------------------ converters
-    // A warp turns 32 rows of every item (those that hold keys).
+    // A warp turns 32 rows of every V (those that hold keys).
     bool ok = true;
-    int item = 0;
+    int n = 0;
     const Piece* taken;
     while (warp >= C::CONVERTER && ok && (taken = take()) != nullptr) {
       const int nblk = taken->nblk, row0 = 32 * (warp - C::CONVERTER);
       int left = taken->L - taken->j0 * C::BK - row0;
-      for (int j = 0; j < nblk && ok; ++j, left -= C::BK)
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v, ++item) {
-          const int st = item % C::NST;
-          ok = __all_sync(kFull, mbar_wait(bar(B_FULL + st), (item / C::NST) & 1));
-          if (!ok) break;
-          convert_rows(sm + C::OFF_RING + st * C::TILE + C::HALF + row0 * 128, min(32, left), lane);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_CONV + st));
-        }
+      for (int j = 0; j < nblk; ++j, ++n, left -= C::BK) {
+        ok = __all_sync(kFull, mbar_wait(full(1, n), turn_of(1, n) & 1));
+        if (!ok) break;
+        convert_rows(sm + slot_at(1, n) + C::HALF + row0 * 128, min(32, left), lane);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_CONV + n % C::V_SLOTS));
+      }
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
   } else {
     // --------------------------------------------------------- softmax warps
-    if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int t = warp >> 2;                       // row block
     const int r = (warp & 3) * 32 + lane;          // TMEM lane
     // this warp's lanes and the columns of S and, + 256 - 128 t, of O
     const uint32_t scol = tmem + (uint32_t((warp & 3) * 32) << 16) + C::S_COL + 128 * t;
     const uint32_t ocol = scol + (C::O_COL - C::S_COL);
-    float sl2 = a.qk_scale_log2, next_sl2 = sl2;  // scores to log2 units, of this piece's row and the next one's
+    float sl2 = a.qk_scale_log2;  // scores to log2 units, of this piece's row
+    uint32_t n_q = 0;             // e4m3, B: pieces so far whose Q is A's or both row blocks'
     uint32_t n_s = 0, n_o = 0;  // phases of B_S and B_O so far
     bool ok = true;
     // 16-byte chunk `ch` of row `rr` of the row block's Q in shared memory.
@@ -1075,53 +1151,53 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
         for (g += 2; g >= a.G; g -= a.G) ++tok;
       }
     };
-    // e4m3: the query rows of this warp's lanes in f16, each times its power of two,
-    // whose inverse goes into the lane's row's next_sl2.  (Of a narrow piece both
-    // row blocks' warps look at the same rows, and A's store them.)
-    auto query_rows = [&](const Piece& q) {
-      const bool narrow = q.n_rows <= 128;
-      const int row0 = narrow ? 0 : t * 128;
-      int rr = (warp & 3) * 32 + (lane >> 4);
-      const int first = q.row0 + row0 + rr;
-      int tok = first / a.G, g = first - tok * a.G;
-      float inverse = 1.f;
-      constexpr int kBatch = 8;
+    // e4m3: 16-byte chunk `ch` of a row before it is a code.  A row's chunks 2 i and 2 i + 1
+    // lie where its codes' chunk i of both tiles will.
+    auto raw_at = [&](int rr, int ch) -> uint8_t* {
+      return sm + t * C::TILE + (ch & 1) * C::HALF + rr * 128 + (((ch >> 1) ^ (rr & 7)) << 4);
+    };
+    // The row of this lane, in place, as the sum of two codes a column, times the power of
+    // two that brings its largest into [2^7, 2^8).  Returns that power's inverse.  (Rolled: as
+    // straight code for eight rows at once, 16 lanes to a row, it waited 11 us for itself.)
+    auto encode_row = [&]() {
+      uint32_t top = 0;
 #pragma unroll 1
-      for (int i0 = 0; i0 < 16; i0 += kBatch) {
-        uint4 x[kBatch];
+      for (int i = 0; i < 16; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(raw_at(r, i));
+        top = max_u16x2(max_u16x2(top, max_u16x2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)),
+                        max_u16x2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+      }
+      top = max(top & 0xffffu, top >> 16);
+      int k = 0;
+      if (top > 0) k = min(126, max(-120, 7 - (int(top >> 7) - 127)));
+      // (an infinity is no code: its row is NaN, as its softmax would be)
+      const float up = top >= 0x7f80u ? NAN : __uint_as_float(uint32_t(127 + k) << 23);
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        uint4* at[2] = {reinterpret_cast<uint4*>(raw_at(r, 2 * i)), reinterpret_cast<uint4*>(raw_at(r, 2 * i + 1))};
+        uint32_t code[2][4];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (row0 + rr + 2 * i < q.n_rows)
-            x[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (int64_t(q.first) + tok) * a.q_stride +
-                                                  (q.h * a.G + g) * 128)[lane & 15];
-          for (g += 2; g >= a.G; g -= a.G) ++tok;
-        }
+        for (int c = 0; c < 2; ++c) {
+          const uint4 x = *at[c];
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          float amax = 0.f;
+          for (int e = 0; e < 2; ++e) {
+            float z[4] = {__uint_as_float(w[2 * e] << 16) * up, __uint_as_float(w[2 * e] & 0xffff0000u) * up,
+                          __uint_as_float(w[2 * e + 1] << 16) * up, __uint_as_float(w[2 * e + 1] & 0xffff0000u) * up};
+            float y[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-#pragma unroll
-          for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-          int k = 0;
-          if (amax > 0.f) k = min(126, max(-113, 14 - (int((__float_as_uint(amax) >> 23) & 0xff) - 127)));
-          const float up = __uint_as_float(uint32_t(127 + k) << 23);
-          const float down = __shfl_sync(kFull, __uint_as_float(uint32_t(127 - k) << 23), (lane & 1) * 16);
-          if (lane >> 1 == i0 + i) inverse = down;
-          if (t == 0 || !narrow) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = pack_f16(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
-            *reinterpret_cast<uint4*>(chunk_at(rr + 2 * i, lane & 15)) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int f = 0; f < 4; ++f) {
+              y[f] = __uint_as_float(__float_as_uint(z[f]) & 0xfff00000u);  // (four of its eight bits)
+              z[f] -= y[f];
+            }
+            code[0][2 * c + e] = pack_e4m3x4(y);
+            code[1][2 * c + e] = pack_e4m3x4(z);
           }
         }
-        rr += 2 * kBatch;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) *at[c] = make_uint4(code[c][0], code[c][1], code[c][2], code[c][3]);
       }
-      next_sl2 = a.qk_scale_log2 * (a.k_scale ? a.k_scale[q.h] : 1.f) * inverse;
+      return uint32_t(127 - k);
     };
     // The next piece with rows of this row block: its query rows, swizzled, on
     // their way into shared memory (rows behind the last are zero).  Not before
@@ -1129,16 +1205,19 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     const Piece* next = nullptr;
     int n_q_boxes = 0;  // pieces whose Q came by boxes
     auto take_piece = [&]() {
+      bool skip;
       do {
         next = take();
         if (next == nullptr) return false;
-      } while (t == 1 && next->n_rows <= 128 && next->nblk < 2);
-      if constexpr (FP8) {
-        if (next->nblk > 0) query_rows(*next);
-        return true;
-      }
+        skip = t == 1 && next->n_rows <= 128 && next->nblk < 2;
+        if (FP8 && t == 1 && next->nblk > 0) {
+          // (B looks at A's Q only in narrow pieces, but no turn of it may pass unseen)
+          if (skip) ok = ok && __all_sync(kFull, mbar_wait(bar(B_Q), n_q & 1));
+          ++n_q;
+        }
+      } while (skip);
       if (next->nblk == 0 || (t == 1 && next->n_rows <= 128)) return true;
-      if (a.row_boxes) {
+      if (!FP8 && a.row_boxes) {
         // (rows of other sequences' tokens behind the last come along, and are not used)
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1152,7 +1231,7 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       } else {
         each_row(*next, [&](int rr, bool in, int64_t token, int head) {
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (in ? token * a.q_stride + head * 128 : 0);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(chunk_at(rr, lane & 15))),
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(FP8 ? raw_at(rr, lane & 15) : chunk_at(rr, lane & 15))),
                        "l"(src + 8 * (lane & 15)), "r"(in ? 16 : 0)
                        : "memory");
         });
@@ -1164,7 +1243,6 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
     bool more = take_piece();
     while (ok && more) {
       const Piece pc = *next;
-      sl2 = next_sl2;
       // A narrow piece (up to 128 rows) has its key blocks dealt to A and B in
       // turn, as if they were two row blocks, and A joins the two results: a
       // single row block's chain of products and softmaxes would be longer
@@ -1180,9 +1258,20 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
       // registers, with the next piece's Q already on its way.
       const bool staged = whole && !narrow;
       if (pc.nblk > 0 && (t == 0 || !narrow) && (FP8 || !a.row_boxes)) {
-        if (!FP8) asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (FP8) {
+          __syncwarp();
+          const uint32_t down = any ? encode_row() : 127;
+          if (narrow) tail.down[r] = uint8_t(down);
+          sl2 = a.qk_scale_log2 * (a.k_scale ? a.k_scale[pc.h] : 1.f) * __uint_as_float(down << 23);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(bar(B_Q + t));
+      }
+      if (FP8 && t == 1 && narrow && pc.nblk > 0) {
+        ok = __all_sync(kFull, mbar_wait(bar(B_Q), (n_q - 1) & 1));
+        if (!ok) break;
+        sl2 = a.qk_scale_log2 * (a.k_scale ? a.k_scale[pc.h] : 1.f) * __uint_as_float(uint32_t(tail.down[r]) << 23);
       }
       float m_ref = -INFINITY, l = 0.f;
       const int step = narrow ? 2 : 1;
@@ -1192,8 +1281,36 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
           TREE ? a.mask + (int64_t(pc.first) + (pc.row0 + (live ? row : 0)) / a.G) * a.words : nullptr;
       for (int j = narrow ? t : 0; j < pc.nblk; j += step, valid -= step * C::BK) {
         const int d = valid - drafts;  // keys of the block before the drafted ones
-        uint32_t m[5];
-        if (TREE && d < C::BK) mask_words(mask, a.words, d, m);  // (under way while S is waited for)
+        uint32_t vis[4];
+        const bool masked = TREE ? d < C::BK : valid < C::BK;
+        if (TREE && masked) {  // (while S is waited for)
+          uint32_t m[5];
+          mask_words(mask, a.words, d, m);
+          visible(m, d, valid, vis);
+        }
+        // Part i of S, C::PART columns of it.
+        auto read_part = [&](float (&s)[C::PART], int i) {
+          if constexpr (C::PART == 128) {
+            tmem_ld64(scol, s);
+            tmem_ld64(scol + 64, s + 64);
+          } else if constexpr (C::PART == 64) {
+            tmem_ld64(scol + 64 * i, s);
+          } else {
+            tmem_ld32(scol + 32 * i, s);
+          }
+          if (!masked) return;
+          if constexpr (TREE) {
+            uint32_t w[C::PART / 32];
+#pragma unroll
+            for (int k = 0; k < C::PART / 32; ++k)
+              w[k] = C::PART == 128 ? vis[k] : C::PART == 64 ? (i ? vis[2 + k % 2] : vis[k % 2]) : i < 2 ? (i ? vis[1] : vis[0]) : (i == 2 ? vis[2] : vis[3]);
+#pragma unroll
+            for (int k = 0; k < C::PART; ++k) s[k] = w[k >> 5] & (1u << (k & 31)) ? s[k] : -INFINITY;
+          } else {
+#pragma unroll
+            for (int k = 0; k < C::PART; ++k) s[k] = C::PART * i + k < valid ? s[k] : -INFINITY;
+          }
+        };
         ok = __all_sync(kFull, mbar_wait(bar(B_S + t), n_s++ & 1));
         if (!ok) break;
         tc_fence_after();
@@ -1203,27 +1320,23 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
           if (!ok) break;
         }
         if (any) {
-          float s[128];
-          tmem_ld64(scol, s);
-          tmem_ld64(scol + 64, s + 64);
-          if (TREE && d < C::BK) {
-            uint32_t vis[4];
-            visible(m, d, valid, vis);
+          // S in parts, the first last, which stays: the others are read once more below, when
+          // P is written over those before
+          float s[C::PART];
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int h = 128 / C::PART - 1; h >= 0; --h) {
+            read_part(s, h);
+            float m4[4];
 #pragma unroll
-            for (int k = 0; k < 128; ++k) s[k] = vis[k >> 5] & (1u << (k & 31)) ? s[k] : -INFINITY;
-          } else if (valid < C::BK) {
+            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(s[i], s[4 + i]);
 #pragma unroll
-            for (int k = 0; k < 128; ++k) s[k] = k < valid ? s[k] : -INFINITY;
+            for (int k = 8; k < C::PART; k += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[k + i], s[k + 4 + i]);
+            mx = max3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           }
-          // row maximum on the raw scores (the scale is positive)
-          float m4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(s[i], s[4 + i]);
-#pragma unroll
-          for (int k = 8; k < 128; k += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], s[k + i], s[k + 4 + i]);
-          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * sl2;
+          mx *= sl2;  // (the scale is positive)
           float alpha = 1.f;
           bool rescale = false;
           if (mx > m_ref + C::RESCALE_LOG2 || (m_ref == -INFINITY && mx != -INFINITY)) {
@@ -1245,19 +1358,23 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
           }
           const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int h = 0; h < 128 / C::PART; ++h) {
+            if (h > 0) read_part(s, h);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint32_t pk[8];
+            for (int q = 0; q < C::PART / 16; ++q) {
+              uint32_t pk[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float x = s[16 * q + 2 * i], y = s[16 * q + 2 * i + 1];
-              fma2(x, y, sl2, nm);
-              x = ex2(x);
-              y = ex2(y);
-              add2(l4[(2 * i) & 3], l4[(2 * i + 1) & 3], x, y);
-              pk[i] = FP8 ? pack_f16(x, y) : pack_bf16(x, y);
+              for (int i = 0; i < 8; ++i) {
+                float x = s[16 * q + 2 * i], y = s[16 * q + 2 * i + 1];
+                fma2(x, y, sl2, nm);
+                x = ex2(x);
+                y = ex2(y);
+                add2(l4[(2 * i) & 3], l4[(2 * i + 1) & 3], x, y);
+                pk[i] = FP8 ? pack_f16(x, y) : pack_bf16(x, y);
+              }
+              tmem_st8(scol + C::PART / 2 * h + 8 * q, pk);
             }
-            tmem_st8(scol + 8 * q, pk);
           }
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
           tmem_wait_st();
@@ -1394,19 +1511,10 @@ __global__ void __launch_bounds__(CrossCta<FP8>::THREADS, 1)
 
 template <bool TREE, bool FP8>
 cudaError_t launch_cross_kernel(const CrossArgs& a, const CrossMaps& maps, void* stream) {
-  using C = CrossCta<FP8>;
+  using C = CrossCta<TREE, FP8>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(cross_attend_kernel<TREE, FP8>), C::SMEM, allowed);
   if (e != cudaSuccess) return e;
-  if constexpr (FP8) {
-    // The registers that the softmax takes are what the others give back of those the
-    // block is launched with: with fewer it would wait for them forever.
-    static const int launched = [] {
-      cudaFuncAttributes f{};
-      return cudaFuncGetAttributes(&f, cross_attend_kernel<TREE, FP8>) == cudaSuccess ? f.numRegs : 0;
-    }();
-    if (launched * C::WARPS < 8 * (168 + 88)) return cudaErrorLaunchOutOfResources;
-  }
   cudaLaunchAttribute la[1];
   la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[0].val.programmaticStreamSerializationAllowed = 1;

@@ -313,9 +313,9 @@ cudaError_t launch_cross_merge(const CrossArgs& a, int64_t row_tiles, void* stre
 cudaError_t launch_tree(const CrossArgs& a, int64_t row_tiles, const CrossMaps& maps, bool fp8, void* stream);
 // Tensor map over a pool of 128-wide rows, coordinates (columns, key in page,
 // column half, KV head, page) in either layout: boxes of `keys` keys and one
-// column half, 128-byte swizzle, of bf16; of `keys` keys and whole rows, as they lie,
-// of e4m3 (one "half") (api.cu).
-splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys);
+// column half of bf16; of `keys` keys and whole rows of e4m3 (one "half"); with a 128-byte
+// swizzle or as they lie (api.cu).
+splitkv_status make_half_map(TmaDesc* out, const void* base, const splitkv_desc_t& d, int keys, bool swizzled);
 // The maps of a call of cross attention's kernel (api.cu).
 splitkv_status make_cross_maps(CrossMaps* maps, const CrossArgs& a, const void* k_pages, const void* v_pages,
                                const splitkv_desc_t& d);
