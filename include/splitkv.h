@@ -693,6 +693,8 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
  * in a key that a token does not see leaves it as it is; in the value of a drafted key
  * it may reach every token whose rows share a tile of 256 with a token that sees it
  * (latent rows: it does not).
+ * Over e4m3 caches with rows of 128 a query component below 2^-9 of its row's largest is
+ * off by up to 2^-16 of that largest; a row with an infinity is NaN throughout.
  * A length outside [0, max_pages_per_seq * P], or below T_b and not 0, sets
  * SPLITKV_DEVERR_SEQLEN and counts as 0; a page id out of range sets
  * SPLITKV_DEVERR_PAGE (page 0 is read in its place).  One kernel or two.

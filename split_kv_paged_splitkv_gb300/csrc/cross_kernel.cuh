@@ -83,8 +83,9 @@
 // FP8 (e4m3 caches, with TREE): K is multiplied as it is stored.  A query row, times the
 // power of two that brings its largest component into [2^7, 2^8), is a sum of two e4m3
 // codes a column, four of its eight bits each (exact, but for components below 2^-9 of the
-// largest, which keep steps of 2^-10, 2^-17 of it or less), and S is the sum of two products
-// of twice the rate.  V's codes land in the second half of their slot, [128 keys][128], just
+// largest: codes below 2^-6 go in steps of 2^-9, so that their two roundings are off by 2^-9
+// together, 2^-16 of the largest, at most), and S is the sum of two products of twice the
+// rate.  V's codes land in the second half of their slot, [128 keys][128], just
 // where the rows of the second 64 columns will lie, and four converter warps turn each row
 // in place into the two swizzled halves, as f16 (exact, one instruction for a pair of codes;
 // bf16 would take four); P is f16 too.  The caches' scales join the scores' and the

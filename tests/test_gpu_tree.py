@@ -1,8 +1,10 @@
 """GPU tests of tree attention against a plain 64-bit implementation.
 
-Tolerances.  A score is a sum of fp32 additions of exact products (the e4m3 caches' codes and, times a power of two, the
-queries are f16 values), off by at most e = D * 2^-23 * sum |q_d K_d| * scale for rows of D (the tensor cores may
-truncate), and its exponent's argument rounds a few times more at its size; a weight is off by that factor, and by 2^-8
+Tolerances.  A score is a sum of fp32 additions of exact products, off by at most e = D * 2^-23 * sum |q_d K_d| * scale for
+rows of D (the tensor cores may truncate).  Over e4m3 caches a query component times a power of two, the row's largest in
+[2^7, 2^8), is the sum of two e4m3 codes: its four leading bits, and the rest, of four bits too.  Both are exact from 2^-2
+on, as codes have steps of 2^-9 and less; below, each is off by half such a step, so that components below 2^-9 of the
+row's largest are off by 2^-16 of it, and e has 2^-16 * max |q| * sum |K_d| over those d besides.  A score's exponent's argument rounds a few times more at its size; a weight is off by that factor, and by 2^-8
 where it is rounded to bf16 for the product with V (f16: 2^-11, and 2^-25 of a piece's largest weight below 2^-14).  With
 A = sum_j p_j |V_j| the output is off by at most (2^-8 + 2 e) A, in f16 by n_keys * 2^-25 * max |V| too, and by half a step of
 bf16, 2^-8 |out|, where it is rounded itself.  The log-sum-exp is off by e and a few roundings of fp32 at its size.
@@ -109,6 +111,9 @@ def run(c, counts, masks=None, n_words=None, pad=0, before=0, cu=True, stride=0,
                 top = np.where(seen, x, 0)
                 e = (c.dim * 2.0 ** -23 * (np.abs(qs) @ np.abs(kh).T * scale).max(initial=0) +
                      4 * 2.0 ** -24 * np.abs(top).max(initial=0))
+                if fp8 and c.dim == 128:
+                    most = np.abs(qs).max(1, initial=0)[:, None]
+                    e += 2.0 ** -16 * scale * (most * ((np.abs(qs) < 2.0 ** -9 * most) @ np.abs(kh).T)).max(initial=0)
                 peak = x.max(1, initial=-np.inf)
                 empty = peak == -np.inf
                 z = np.where(empty, -np.inf, np.where(empty, 0, peak) + np.log(np.exp(x - np.where(empty, 0, peak)[:, None]).sum(1)))
