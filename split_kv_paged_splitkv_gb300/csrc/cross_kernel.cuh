@@ -124,7 +124,10 @@ struct Cross {
 template <bool TREE, bool FP8>
 struct CrossCta : Cross {
   static constexpr int PART = TREE ? 64 : 128;  // columns of S that a softmax thread holds
-  static constexpr int CONVERTER = SOFTMAX_WARPS + 4;  // first of four (warp 11 fills its warpgroup)
+  // e4m3: four converters, none on the issuer's scheduler (every fourth warp; trees of 8
+  // requests over 32k keys 147 us, with one there 149)
+  static constexpr int CONVERTER = SOFTMAX_WARPS + 3, IDLE = SOFTMAX_WARPS + 6;
+  static_assert((IDLE - ISSUER) % 4 == 0, "beside the issuer: no converter");
   static constexpr int WARPS = SOFTMAX_WARPS + (FP8 ? 8 : 3);
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TAIL = FP8 ? 2048 : 1536; // barriers, plan
@@ -1110,9 +1113,10 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
     // A warp turns 32 rows of every V (those that hold keys).
     bool ok = true;
     int n = 0;
+    const int row0 = 32 * (warp - C::CONVERTER - (warp > C::IDLE));
     const Piece* taken;
-    while (warp >= C::CONVERTER && ok && (taken = take()) != nullptr) {
-      const int nblk = taken->nblk, row0 = 32 * (warp - C::CONVERTER);
+    while (warp != C::IDLE && ok && (taken = take()) != nullptr) {
+      const int nblk = taken->nblk;
       int left = taken->L - taken->j0 * C::BK - row0;
       for (int j = 0; j < nblk; ++j, ++n, left -= C::BK) {
         ok = __all_sync(kFull, mbar_wait(full(1, n), turn_of(1, n) & 1));
