@@ -25,7 +25,7 @@
 // Where a power of two of at most 32 query heads share a KV head, 32 rows of it are a
 // box of the queries' and the results' tensors: a warp's Q comes, and its whole results
 // go, by TMA.  (Others go by 16 bytes a lane, row by row.  Trees of 64 young requests: 50
-// us, by lanes 71; the prompts below 715 and 735.)
+// us, by lanes 71; the prompts below 715 and 735; in larger code.)
 //
 // K and V blocks pass in that order through one ring of five 32 KB slots that
 // two producer warps fill by TMA, each a 64-column half of every slot, one box
@@ -34,8 +34,8 @@
 //
 // Many items: a CTA per item (prompts), or a line of all items' key blocks that the
 // CTAs share (batches of few rows a sequence; cross_deal has the rule).  The bound
-// of prompts is 4 * 128 * rows * L operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 700 to
-// 735 us, 1,455 to 1,525 TFLOP/s (floor 561 at 1,906), near the GPU's limit of
+// of prompts is 4 * 128 * rows * L operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 675 to
+// 700 us, 1,530 to 1,585 TFLOP/s (floor 561 at 1,906), near the GPU's limit of
 // 1,400 W and with the tensor pipe waiting for the softmax's turn of the row
 // blocks.
 //
@@ -48,14 +48,19 @@
 // a nanosecond into each SM once the copies flow, behind a start of 5 us (2.3
 // the plan, 2.6 the first blocks), an end of 3 (the last softmax, P . V, the
 // result) and the merge's 1.5 (one token of 8 requests over 1.2k keys of 16
-// heads: 27.2 us, floor 11.6), or the longest piece's chain of products and the
+// heads: 25 us, floor 11.6), or the longest piece's chain of products and the
 // 32-bit partial results (prompts of 37 to 900 tokens over 1 to 4.1k keys:
-// 21.6 us, floor 2.9).
+// 21.4 us, floor 2.9).
 //
-// The code that runs once in a piece is kept small: it waits for its own
-// instructions, and the softmax's loop runs slower beside more of them (the
-// epilogue's columns unrolled by two: 754 us for the prompts above, rolled
-// 800; the rescaling of O unrolled as well: 810).
+// The code is kept small: what runs once in a piece waits for its own instructions, and
+// the loops of all warps together have to stay in the SM's instruction cache.  So waits
+// and what is rare are rolled or functions of their own, the next piece is taken in two
+// places, and the MMAs stand in a branch that one elected lane takes, not under its
+// predicate, where each is some 30 instructions.  With all that (200 KB of code before,
+// 146 after) the prompts above 707 -> 690 us, one token of 8 requests 27.2 -> 25, of 512
+// requests over 512 keys 236 -> 218, trees of 8 tokens over 5.9k keys 16.7 -> 15.  (Too small: the
+// producers' boxes in a rolled loop, trees of 32 requests over up to 131k keys 587 us
+// for 567; the rescaling of O and the loop over the row blocks stay as they are.)
 //
 // P is rounded to bf16 for the second product (half a step, 2^-8 of a weight,
 // as in the decode kernels); sums, maxima and O are fp32.
@@ -67,14 +72,14 @@
 // scores whose bit is off.  The V rows that no token of the tile sees are zeroed,
 // as those behind the length are (0 * NaN would be NaN).  The trees' line (plan_line)
 // takes any lengths, as an item counts there for what it costs beside its blocks.
-// Measured, bf16: 8 tokens over 5.9k keys 16 us (floor 0.9: the chain of plan, first
+// Measured, bf16: 8 tokens over 5.9k keys 14 us (floor 0.9: the chain of plan, first
 // blocks, one softmax, result and merge), 400 tokens of 32 requests over 256 to 131k keys
-// 570 us (floor 529), trees of 64 requests over 1 to 300 keys 48 us (floor 9: an item's
+// 564 us (floor 529), trees of 64 requests over 1 to 300 keys 44 us (floor 9: an item's
 // chain is 9 us, a CTA to an SM).
 //
 // Trees' softmax holds 64 columns of S at a time and reads half of S twice, in loops of
-// half the length: the code that all warps go round in has to stay in the SM's instruction
-// cache, also while a neighbour's is at another kind of piece.  (Trees of 33 tokens of 8
+// half the length, for the instruction cache again, in which a neighbour at another kind
+// of piece takes its share.  (Before the code was made smaller: trees of 33 tokens of 8
 // requests over 31k keys in e4m3, pieces of 256 and of 8 rows: 222 us, all of S in
 // registers 286, with three times the misses there; 64 tokens of 19 requests over 8k keys
 // 131 both.  Parts of 32: 205 and 138.  Cross attention's long prompts, all at the same
@@ -90,9 +95,9 @@
 // in place into the two swizzled halves, as f16 (exact, one instruction for a pair of codes;
 // bf16 would take four); P is f16 too.  The caches' scales join the scores' and the
 // results'.  K's ring has four slots of 16 KB, V's three of 32 KB, a producer each.
-// Measured: 16 tokens of 19 requests over 8k keys 85 us (floor 47; in bf16 107 of 94), 64
-// tokens 141 (in bf16 131), trees of 16 to 61 tokens of 8 requests over 32k keys 150 (floor
-// 54).  With K converted as well, both in one ring of five slots, and the softmax's
+// Measured: 16 tokens of 19 requests over 8k keys 76 us (floor 47; in bf16 105 of 94), 64
+// tokens 132 (in bf16 121), trees of 16 to 61 tokens of 8 requests over 32k keys 133 (floor
+// 54).  In larger code 85, 141 and 148; with K converted as well, both in one ring of five slots, and the softmax's
 // registers taken from the other warps' (S in one part) the three took 109, 155 and 182.
 #pragma once
 
@@ -649,7 +654,7 @@ __device__ __forceinline__ void fma2(float& x, float& y, float s, float b) {
 }
 
 // Eight MMAs of one K = 128 product, issued by a converged warp: one lane,
-// elected once, issues all of them (between two MMAs nothing but the next
+// elected once, takes the branch that issues all of them (between two MMAs nothing but the next
 // descriptors' additions, in units of 16 bytes).
 // S = Q . K^T: both operands are two 64-column halves, 32 bytes per step; or (e4m3) Q is
 // a sum of two tiles of 128 columns, each multiplied by the one of K.
@@ -663,29 +668,31 @@ __device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a_desc, uint64_t b_d
         "setp.ne.b32 q, %4, 0;\n\t"
         "setp.eq.b32 y, 0, 0;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, q;\n\t"
+      "@!e bra DONE%=;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, q;\n\t"
         "add.s64 a, %1, 2;\n\t"
         "add.s64 b, %2, 2;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 4;\n\t"
         "add.s64 b, %2, 4;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 6;\n\t"
         "add.s64 b, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 1024;\n\t"
         "add.s64 b, %2, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 1026;\n\t"
         "add.s64 b, %2, 2;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 1028;\n\t"
         "add.s64 b, %2, 4;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 1030;\n\t"
         "add.s64 b, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
-        "}" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, y;\n\t"
+        "DONE%=:\n\t"
+      "}" ::"r"(d),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(0)
         : "memory");
   } else {
@@ -696,29 +703,31 @@ __device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a_desc, uint64_t b_d
         "setp.ne.b32 q, %4, 0;\n\t"
         "setp.eq.b32 y, 0, 0;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
+      "@!e bra DONE%=;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
         "add.s64 a, %1, 2;\n\t"
         "add.s64 b, %2, 2;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 4;\n\t"
         "add.s64 b, %2, 4;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 6;\n\t"
         "add.s64 b, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 1024;\n\t"
         "add.s64 b, %2, 1024;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 1026;\n\t"
         "add.s64 b, %2, 1026;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 1028;\n\t"
         "add.s64 b, %2, 1028;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
         "add.s64 a, %1, 1030;\n\t"
         "add.s64 b, %2, 1030;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
-        "}" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, y;\n\t"
+        "DONE%=:\n\t"
+      "}" ::"r"(d),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(0)
         : "memory");
   }
@@ -733,28 +742,30 @@ __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a_tmem, uint64_t b_d
       "setp.ne.b32 q, %4, 0;\n\t"
       "setp.eq.b32 y, 0, 0;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+      "@!e bra DONE%=;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
       "add.s32 a, %1, 8;\n\t"
       "add.s64 b, %2, 128;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
       "add.s32 a, %1, 16;\n\t"
       "add.s64 b, %2, 256;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
       "add.s32 a, %1, 24;\n\t"
       "add.s64 b, %2, 384;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
       "add.s32 a, %1, 32;\n\t"
       "add.s64 b, %2, 512;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
       "add.s32 a, %1, 40;\n\t"
       "add.s64 b, %2, 640;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
       "add.s32 a, %1, 48;\n\t"
       "add.s64 b, %2, 768;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
       "add.s32 a, %1, 56;\n\t"
       "add.s64 b, %2, 896;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, y;\n\t"
+      "DONE%=:\n\t"
       "}" ::"r"(d),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(more)
       : "memory");
@@ -774,6 +785,48 @@ __device__ __forceinline__ void visible(const uint32_t (&m)[5], int d, int valid
   for (int w = 0; w < 4; ++w) {
     const int left = valid - 32 * w;
     vis[w] = __funnelshift_r(m[w], m[w + 1], (-d) & 31) & (left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1);
+  }
+}
+
+// mbar_wait in less code.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  for (int i = 1; !mbar_try_wait(bar, parity); ++i)
+    if (i % 16 == 0 && clock64() - t0 > kWaitTimeoutCycles) return false;
+  return true;
+}
+
+// Which of a block's keys some token of tokens t0 .. t1 sees (see mask_words), by a warp.
+__device__ __noinline__ uint4 seen_by(const uint32_t* mask, int words, int t0, int t1, int d, int valid, int lane) {
+  uint32_t seen[5] = {0u, 0u, 0u, 0u, 0u}, vis[4];
+#pragma unroll 1
+  for (int tok = t0 + lane; tok <= t1; tok += 32) {
+    uint32_t m[5];
+    mask_words(mask + int64_t(tok) * words, words, d, m);
+#pragma unroll
+    for (int i = 0; i < 5; ++i) seen[i] |= m[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 5; ++i) seen[i] = __reduce_or_sync(kFull, seen[i]);
+  visible(seen, d, valid, vis);
+  return make_uint4(vis[0], vis[1], vis[2], vis[3]);
+}
+// Zeros over the 16-bit rows of a V block's other keys, by a warp.
+__device__ __noinline__ void zero_unseen(uint8_t* rows, uint4 vis, int lane) {
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t x = w < 2 ? (w ? vis.y : vis.x) : (w == 2 ? vis.z : vis.w);
+    if (~x >> lane & 1)
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i)  // (in eight orders, so that the lanes write to all banks)
+        *reinterpret_cast<uint4*>(rows + (i & 1) * Cross::HALF + (32 * w + lane) * 128 + (((i >> 1) + lane) & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+  }
+  if ((vis.x & vis.y & vis.z & vis.w) != ~0u) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
   }
 }
 
@@ -913,7 +966,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         if (j + 1 < pc.nblk) look_up(j + 1);
 #pragma unroll 1
         for (int v = FP8 ? half : 0; v < (FP8 ? half + 1 : 2); ++v) {
-          if (turn_of(v, n) > 0) ok = __all_sync(kFull, mbar_wait(empty(v, n), (turn_of(v, n) - 1) & 1));
+          if (turn_of(v, n) > 0) ok = __all_sync(kFull, wait_for(empty(v, n), (turn_of(v, n) - 1) & 1));
           if (!ok) break;
           mbar_arrive_expect_tx_warp(full(v, n), uint32_t(np * br * 128));
           const uint32_t dst = smem_u32(sm + slot_at(v, n)) + (FP8 ? v : half) * C::HALF;
@@ -931,7 +984,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
     if (lane == 0)
       for (int i = issued - 1; i >= 0 && i >= issued - (!FP8 ? C::NST : half ? C::V_SLOTS : C::K_SLOTS); --i) {
         const int v = FP8 ? half : i & 1;
-        mbar_wait(full(v, FP8 ? i : i >> 1), turn_of(v, FP8 ? i : i >> 1) & 1);
+        wait_for(full(v, FP8 ? i : i >> 1), turn_of(v, FP8 ? i : i >> 1) & 1);
       }
   } else if (warp == C::ISSUER) {
     // ------------------------------------------------------------ MMA issuer
@@ -947,11 +1000,11 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
     int n = 0;                  // key blocks of the pieces before
     uint32_t n_q = 0, n_p = 0;  // phases of B_Q and B_P so far, a bit per row block
     auto wait = [&](int i, int phase) {
-      ok = ok && __all_sync(kFull, mbar_wait(bar(i), phase & 1));
+      ok = ok && __all_sync(kFull, wait_for(bar(i), phase & 1));
       return ok;
     };
     auto landed = [&](int v, int n) {
-      ok = ok && __all_sync(kFull, mbar_wait(full(v, n), turn_of(v, n) & 1));
+      ok = ok && __all_sync(kFull, wait_for(full(v, n), turn_of(v, n) & 1));
       return ok;
     };
     auto v_in_smem = [&](int n) { return FP8 ? wait(B_CONV + n % C::V_SLOTS, turn_of(1, n)) : landed(1, n); };
@@ -971,43 +1024,20 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
     // So are those of drafted keys that no token of the tile sees.
     int drafts = 0;   // tokens of the piece's sequence
     int seen_j = -1;  // the block that `vis` is of: those of its keys that some token of the tile sees
-    uint32_t vis[4];
+    uint4 vis;
     auto look = [&](const Piece& pc, int j) {
-      const int valid = pc.L - (pc.j0 + j) * C::BK, d = valid - drafts;
-      uint32_t seen[5] = {0u, 0u, 0u, 0u, 0u};
-      const int t0 = pc.row0 / a.G, t1 = (pc.row0 + min(pc.n_rows, C::ROWS) - 1) / a.G;
-#pragma unroll 2
-      for (int tok = t0 + lane; tok <= t1; tok += 32) {
-        uint32_t m[5];
-        mask_words(a.mask + (int64_t(pc.first) + tok) * a.words, a.words, d, m);
-#pragma unroll
-        for (int i = 0; i < 5; ++i) seen[i] |= m[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 5; ++i) seen[i] = __reduce_or_sync(kFull, seen[i]);
-      visible(seen, d, valid, vis);
+      const int valid = pc.L - (pc.j0 + j) * C::BK;
+      vis = seen_by(a.mask + int64_t(pc.first) * a.words, a.words, pc.row0 / a.G,
+                    (pc.row0 + min(pc.n_rows, C::ROWS) - 1) / a.G, valid - drafts, valid, lane);
       seen_j = j;
     };
     auto v_ready = [&](const Piece& pc, int j, int n) {
       const int valid = pc.L - (pc.j0 + j) * C::BK;
       if constexpr (TREE) {
-        if (valid - drafts >= C::BK) return v_in_smem(n);
-        if (seen_j != j) look(pc, j);
+        const bool masked = valid - drafts < C::BK;
+        if (masked && seen_j != j) look(pc, j);
         if (!v_in_smem(n)) return false;
-        uint8_t* v = sm + slot_at(1, n);
-#pragma unroll 1
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t x = w < 2 ? (w ? vis[1] : vis[0]) : (w == 2 ? vis[2] : vis[3]);
-          if (~x >> lane & 1)
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i)  // (in eight orders, so that the lanes write to all banks)
-              *reinterpret_cast<uint4*>(v + (i & 1) * C::HALF + (32 * w + lane) * 128 + (((i >> 1) + lane) & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-        }
-        if ((vis[0] & vis[1] & vis[2] & vis[3]) != ~0u) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
+        if (masked) zero_unseen(sm + slot_at(1, n), vis, lane);
         return true;
       }
       if (!v_in_smem(n)) return false;
@@ -1036,6 +1066,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         // narrow: A takes the even key blocks, B the odd ones, of the same rows
         const bool q_in = wait(B_Q, n_q);
         n_q ^= 1u;
+#pragma unroll 1
         for (int j = 0; j < min(2, pc.nblk) && q_in; ++j) {
           if (!landed(0, n + j)) break;
           tc_fence_after();
@@ -1062,6 +1093,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         n += pc.nblk;
         continue;
       }
+#pragma unroll 1
       for (int t = 0; t < 2 && ok; ++t) {
         const bool q_in = wait(B_Q + t, n_q >> t);
         n_q ^= 1u << t;
@@ -1107,7 +1139,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
     // every MMA issued above completes before TMEM is released
     umma_commit_warp(bar(B_DONE));
     __syncwarp();
-    mbar_wait(bar(B_DONE), 0);
+    wait_for(bar(B_DONE), 0);
   } else if (FP8 && warp >= C::SOFTMAX_WARPS) {
     // ------------------------------------------------------------ converters
     // A warp turns 32 rows of every V (those that hold keys).
@@ -1119,7 +1151,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
       const int nblk = taken->nblk;
       int left = taken->L - taken->j0 * C::BK - row0;
       for (int j = 0; j < nblk; ++j, ++n, left -= C::BK) {
-        ok = __all_sync(kFull, mbar_wait(full(1, n), turn_of(1, n) & 1));
+        ok = __all_sync(kFull, wait_for(full(1, n), turn_of(1, n) & 1));
         if (!ok) break;
         convert_rows(sm + slot_at(1, n) + C::HALF + row0 * 128, min(32, left), lane);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1150,7 +1182,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
       int rr = (warp & 3) * 32 + (lane >> 4);
       const int first = q.row0 + t * 128 + rr;  // (not called for B's share of a narrow piece)
       int tok = first / a.G, g = first - tok * a.G;
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < 16; ++i, rr += 2) {
         body(rr, t * 128 + rr < q.n_rows, int64_t(q.first) + tok, q.h * a.G + g);
         for (g += 2; g >= a.G; g -= a.G) ++tok;
@@ -1217,7 +1249,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         skip = t == 1 && next->n_rows <= 128 && next->nblk < 2;
         if (FP8 && t == 1 && next->nblk > 0) {
           // (B looks at A's Q only in narrow pieces, but no turn of it may pass unseen)
-          if (skip) ok = ok && __all_sync(kFull, mbar_wait(bar(B_Q), n_q & 1));
+          if (skip) ok = ok && __all_sync(kFull, wait_for(bar(B_Q), n_q & 1));
           ++n_q;
         }
       } while (skip);
@@ -1245,8 +1277,11 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
     };
     uint32_t n_ml = 0, n_ob = 0;  // phases of B_ML and, seen by A, of B's B_O
     bool joining = false;         // B: A has still to read its last narrow piece's O
-    bool more = take_piece();
-    while (ok && more) {
+    bool taken = false;  // (the next piece is)
+    while (ok) {
+      if (!taken && !take_piece()) break;
+      taken = false;
+      if (!ok) break;
       const Piece pc = *next;
       // A narrow piece (up to 128 rows) has its key blocks dealt to A and B in
       // turn, as if they were two row blocks, and A joins the two results: a
@@ -1274,7 +1309,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         mbar_arrive(bar(B_Q + t));
       }
       if (FP8 && t == 1 && narrow && pc.nblk > 0) {
-        ok = __all_sync(kFull, mbar_wait(bar(B_Q), (n_q - 1) & 1));
+        ok = __all_sync(kFull, wait_for(bar(B_Q), (n_q - 1) & 1));
         if (!ok) break;
         sl2 = a.qk_scale_log2 * (a.k_scale ? a.k_scale[pc.h] : 1.f) * __uint_as_float(uint32_t(tail.down[r]) << 23);
       }
@@ -1316,12 +1351,12 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
             for (int k = 0; k < C::PART; ++k) s[k] = C::PART * i + k < valid ? s[k] : -INFINITY;
           }
         };
-        ok = __all_sync(kFull, mbar_wait(bar(B_S + t), n_s++ & 1));
+        ok = __all_sync(kFull, wait_for(bar(B_S + t), n_s++ & 1));
         if (!ok) break;
         tc_fence_after();
         if (joining) {  // (B's O is written over by what its next P starts)
           joining = false;
-          ok = __all_sync(kFull, mbar_wait(bar(B_JOINED), (n_ml - 1) & 1));
+          ok = __all_sync(kFull, wait_for(bar(B_JOINED), (n_ml - 1) & 1));
           if (!ok) break;
         }
         if (any) {
@@ -1400,20 +1435,20 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         ++n_ml;
         ++n_o;
         joining = true;
-        more = take_piece();
         continue;
       }
       float2 other = make_float2(0.f, 0.f);
       if (two) {
-        ok = __all_sync(kFull, mbar_wait(bar(B_ML), n_ml++ & 1));
+        ok = __all_sync(kFull, wait_for(bar(B_ML), n_ml++ & 1));
         tc_fence_after();
         if (ok) tmem_ld2(scol + 128 + 126, other.x, other.y);  // (before the next queries, with which S_B is written)
         tc_fence_before();
-        if (ok) ok = __all_sync(kFull, mbar_wait(bar(B_O + 1), n_ob & 1));
+        if (ok) ok = __all_sync(kFull, wait_for(bar(B_O + 1), n_ob & 1));
       }
       n_ob += two || (!narrow && pc.nblk > 0);
-      if (ok && !staged) more = take_piece();
-      if (ok && pc.nblk > 0) ok = __all_sync(kFull, mbar_wait(bar(B_O + t), n_o++ & 1));
+      bool more = true;
+      if (ok && !staged) taken = more = take_piece();
+      if (ok && pc.nblk > 0) ok = __all_sync(kFull, wait_for(bar(B_O + t), n_o++ & 1));
       if (!ok) break;
       tc_fence_after();
       // weights of A's own result and of B's
@@ -1434,7 +1469,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         const size_t slot = pc.slot;
         const int tok = (pc.row0 + row) / a.G, g = (pc.row0 + row) - tok * a.G;
         const size_t out_row = (size_t(pc.first) + tok) * a.Hq + size_t(pc.h) * a.G + g;
-#pragma unroll 2
+#pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
           float o[32];
           if (pc.nblk > 0) {
@@ -1495,11 +1530,11 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         tc_fence_before();
         mbar_arrive(bar(B_JOINED));
       }
-      if (staged) more = take_piece();
+      if (!more) break;
     }
     if (!FP8) {
       asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out)
-      if (!ok && n_q_boxes > 0) mbar_wait(bar(B_Q + t), (n_q_boxes - 1) & 1);
+      if (!ok && n_q_boxes > 0) wait_for(bar(B_Q + t), (n_q_boxes - 1) & 1);
       if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, SPLITKV_DEVERR_TIMEOUT);
