@@ -120,11 +120,11 @@ int64_t cross_row_tiles(const splitkv_desc_t& d, int64_t n_tokens) {
 
 // How the items are dealt.  Few: pieces of a cost.  Many of few rows (half a tile
 // a sequence, on average): a line, so that a CTA's K and V keep coming while it goes
-// from one item to the next (one token of 512 requests, 8 heads, 512 keys: 280 us,
-// a CTA per item 405).  Many of more rows: a CTA per item, for its results pass
+// from one item to the next (one token of 512 requests, 8 heads, 512 keys: 218 us,
+// a CTA per item 309).  Many of more rows: a CTA per item, for its results pass
 // through the shared memory that the next item's queries need (80 prompts of 40
-// to 80 tokens, 32 heads on 8, 512 keys: 99 us, as a line 116; prompts of 4k
-// tokens the same either way).
+// to 80 tokens, 32 heads on 8, 512 keys: 84 us, as a line 99; trees of 64 young
+// requests 44 and 51; prompts of 4k tokens the same either way).
 CrossDeal cross_deal(const splitkv_desc_t& d, int64_t n_tokens) {
   if (cross_row_tiles(d, n_tokens) * d.num_kv_heads <= kMaxPieces * kSmCount) return CrossDeal::kPieces;
   const int64_t rows = n_tokens * (d.num_q_heads / d.num_kv_heads);
