@@ -32,7 +32,7 @@
 // calls, append_stream_kernel); a latent row's 36 units
 // lie across warps, so a warp adds up its 512 columns by itself while the token's
 // place is looked up (1 KB read again, beside the 147 KB of the token's queries; 1.8k
-// tokens of 129 rows into e4m3: 97 us, 5.5 TB/s, without norms 91, floor 79).
+// tokens of 129 rows into e4m3: 95 us, 5.6 TB/s, without norms 91, floor 79).
 //
 // One thread handles 32-byte units (two 16-byte chunks of a head row, the
 // two halves of the same eight pairs where pairs are half a row apart), so
@@ -213,12 +213,29 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       c1 += c1 >= rot0 ? rotc : 0;
     }
   };
+  // A token's latent queries: the units that are not rotated first, rows one behind the
+  // other (with 64 rotated columns a warp's units are a row's 512 others), which are copied as
+  // they are, then those that are.  (29k tokens of 17 rows into e4m3: 180 us, with every row's
+  // units together and unpacked 189.)
+  const int turning = rotc / 2, plain = UK - turning;
   // Unit i of the CTA: kind 0 q, 1 k, 2 v; token, head row, chunks.
   auto unit = [&](int i, int& kind, int& t, int& row, int& c0, int& c1) {
     t = int(__umulhi(unsigned(i), a.per_tok_magic));  // i / per_tok
     int u = i - t * per_tok;
     kind = u < qu ? 0 : u < qu + ku ? 1 : 2;
-    if (kind < 2) {
+    if (DK != DV && kind == 0) {
+      if (u < a.Hq * plain) {
+        row = plain == 32 ? u >> 5 : u / plain;
+        c0 = 2 * (u - row * plain);
+        c0 += c0 >= rot0 ? rotc : 0;
+        c1 = c0 + 1;
+      } else {
+        u -= a.Hq * plain;
+        row = u / turning;
+        c0 = rot0 + (u - row * turning) * (halves ? 1 : 2);
+        c1 = c0 + (halves ? turning : 1);
+      }
+    } else if (kind < 2) {
       u -= kind ? qu : 0;
       row = u / UK;
       chunks(u - row * UK, c0, c1);
@@ -286,6 +303,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       const int t = tag[r] & 31, kind = tag[r] >> 5 & 3, c0 = tag[r] >> 7 & 127, c1 = tag[r] >> 14 & 127, row = rows[r];
       const Token tk = tok[t];
       if (tk.b < 0 || (kind > 0 && tk.page < 0)) continue;
+      if (DK != DV && kind == 0 && (c0 < rot0 || c0 >= rot0 + rotc)) {
+        uint4* dst = reinterpret_cast<uint4*>(q_out + int64_t(t) * int(a.q_out_stride) + row * DK);
+        dst[c0] = x0[r];
+        dst[c1] = x1[r];
+        continue;
+      }
       float f0[8], f1[8];
       unpack8(x0[r], f0);
       unpack8(x1[r], f1);
@@ -796,7 +819,7 @@ dim3 append_grid(AppendArgs& a, int per_tok, int pass, bool longer, int* tok_per
   // its units (which share the lookup of the places and the sines: 26k tokens of
   // 40 rows, 99 us, with one pass 106), that leaves at most a twelfth of the
   // threads idle in the last, or else the best within kPasses (29k tokens of 17
-  // latent rows, e4m3: four tokens 172 us, one 230).  A token of more units than
+  // latent rows, e4m3: four tokens 172 us, one 230, before plain units went by themselves).  A token of more units than
   // that goes to several CTAs.
   const int most = (longer ? kPasses : 1) * pass;
   const int64_t slices = (int64_t(per_tok) + most - 1) / most;
