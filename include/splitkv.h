@@ -263,6 +263,9 @@ splitkv_status splitkv_plan_upload(const splitkv_plan_t* plan, void* workspace,
  *   lse          fp32 [B][T][Hq], natural-log LSE of the scaled scores; may be
  *                NULL
  *   workspace    uploaded with splitkv_plan_upload for this plan
+ * Weights are rounded for the product with V, to bf16, or over e4m3 caches to f16:
+ * there those below 2^-25 of a split's largest at the time are lost from the product, though not
+ * from the log-sum-exp (out is off by at most L * 2^-25 * max |V| for that).
  * Attended keys and queries hold no NaN: a row that meets one in a key is NaN in
  * `out`, but not in `lse`, which is that of the splits without it (-inf if there
  * is none); a row with a NaN query may come out as one without keys.
@@ -694,7 +697,10 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
  * it may reach every token whose rows share a tile of 256 with a token that sees it
  * (latent rows: it does not).
  * Over e4m3 caches with rows of 128 a query component below 2^-9 of its row's largest is
- * off by up to 2^-16 of that largest; a row with an infinity is NaN throughout.
+ * off by up to 2^-16 of that largest; a row with an infinity is NaN throughout.  Weights
+ * are rounded for the product with V, to bf16 (2^-8 of each) over bf16 caches and to f16
+ * (2^-11) over e4m3 ones, where those below 2^-21 of the row's largest are off by
+ * up to 2^-32 of it instead: out by at most L * 2^-32 * max |V| for that.
  * A length outside [0, max_pages_per_seq * P], or below T_b and not 0, sets
  * SPLITKV_DEVERR_SEQLEN and counts as 0; a page id out of range sets
  * SPLITKV_DEVERR_PAGE (page 0 is read in its place).  One kernel or two.

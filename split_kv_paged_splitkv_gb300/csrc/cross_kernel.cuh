@@ -93,8 +93,11 @@
 // rate.  V's codes land in the second half of their slot, [128 keys][128], just
 // where the rows of the second 64 columns will lie, and four converter warps turn each row
 // in place into the two swizzled halves, as f16 (exact, one instruction for a pair of codes;
-// bf16 would take four); P is f16 too.  The caches' scales join the scores' and the
-// results'.  K's ring has four slots of 16 KB, V's three of 32 KB, a producer each.
+// bf16 would take four).  P is f16 too, times 2^P_UP: a weight is at most 2^8 of the reference
+// maximum's, so that at most 2^15 is stored, and the steps of 2^-24 that f16 has below 2^-14 are
+// 2^-31 of that maximum's weight (2^-24 without, of which long tails of small weights beside
+// one large one lost all that was below a half).  Sums are of the weights times 2^P_UP as well,
+// which cancels but in the log-sum-exp.  The caches' scales join the scores' and the results'.  K's ring has four slots of 16 KB, V's three of 32 KB, a producer each.
 // Measured: 16 tokens of 19 requests over 8k keys 76 us (floor 47; in bf16 105 of 94), 64
 // tokens 132 (in bf16 121), trees of 16 to 61 tokens of 8 requests over 32k keys 133 (floor
 // 54).  In larger code 85, 141 and 148; with K converted as well, both in one ring of five slots, and the softmax's
@@ -129,6 +132,8 @@ struct Cross {
 template <bool TREE, bool FP8>
 struct CrossCta : Cross {
   static constexpr int PART = TREE ? 64 : 128;  // columns of S that a softmax thread holds
+  static constexpr float P_UP = FP8 ? 7.f : 0.f;  // log2 of what P is multiplied with
+  static constexpr float P_DOWN = FP8 ? 0x1p-7f : 1.f;
   // e4m3: four converters, none on the issuer's scheduler (every fourth warp; trees of 8
   // requests over 32k keys 147 us, with one there 149)
   static constexpr int CONVERTER = SOFTMAX_WARPS + 3, IDLE = SOFTMAX_WARPS + 6;
@@ -1396,7 +1401,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
               tmem_st16(ocol + c0, o);
             }
           }
-          const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+          const float nm = m_ref == -INFINITY ? 0.f : FP8 ? C::P_UP - m_ref : -m_ref;
           float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
           for (int h = 0; h < 128 / C::PART; ++h) {
@@ -1463,7 +1468,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
       if (any) {
         // (a row without keys has l = 0; a NaN or a score of +inf makes l NaN, and the row)
         const float inv = l == 0.f ? 0.f : (FP8 ? a.v_scale ? a.v_scale[pc.h] : a.o_scale : 1.f) / l;
-        const float lse = l == 0.f ? -INFINITY : (m_ref + lg2(l)) * kLn2;
+        const float lse = l == 0.f ? -INFINITY : (m_ref + lg2(l * C::P_DOWN)) * kLn2;
         wa *= inv;
         wb *= inv;
         const size_t slot = pc.slot;

@@ -62,7 +62,8 @@
 // sees the keys before the last T and those of the last T that bit i of its mask
 // names.  A CTA has the rows of one token, so a block that reaches past L - T has one
 // 64-bit word of visible keys for all of them: the softmax warps take -inf for the
-// others' scores, and the issuer zeroes their V rows.  12 tokens over 64k rows: 272 us
+// others' scores, and the issuer zeroes their V rows.  Over e4m3 rows P, in f16, is a
+// tree's weights times 2^7 (as in cross_kernel.cuh; the decode's are as they are).  12 tokens over 64k rows: 272 us
 // with the merge (floor 115), as the chain of as many tokens takes.
 #include <cuda_runtime.h>
 
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
         m_ref = mx;
         l *= alpha;
       }
-      const float nms = m_ref == -INFINITY ? 0.f : -m_ref;
+      const float nms = m_ref == -INFINITY ? 0.f : TREE && FP8 ? 7.f - m_ref : -m_ref;
       uint32_t pk[32];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -773,7 +774,7 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
     // ---- epilogue: O / l for this CTA's 256 V columns
     const int row_n = t * C::ROWS + r;  // row of the item's partial block
     float lse_n = -INFINITY;
-    if (l > 0.f) lse_n = (m_ref + lg2(l)) * kLn2m;
+    if (l > 0.f) lse_n = (m_ref + lg2(TREE && FP8 ? l * 0x1p-7f : l)) * kLn2m;
     const float inv = l > 0.f ? a.o_scale / l : 0.f;  // o_scale: the FP8 cache scale, else 1
     bool have_o = ok && nblk > 0;
     // PV(nblk - 1) complete (its commit covers every earlier MMA, PV(nblk - 2) too)
