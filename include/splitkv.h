@@ -689,7 +689,8 @@ splitkv_status splitkv_cross_attend(const splitkv_desc_t* desc, int32_t n_tokens
  *                k_scale and v_scale (fp32 [Hkv], device) are given (rows of 128)
  *   out          bf16 [n_tokens][Hq][Dv]; must not overlap q
  *   lse          fp32 [n_tokens][Hq] natural-log LSE of the scaled scores, or
- *                NULL.  A token that sees no key gets out = 0 and lse = -inf
+ *                NULL.  A token that sees no key gets out = 0 and lse = -inf,
+ *                a row with a NaN or +inf among its scores NaN in both.
  *   workspace    splitkv_tree_workspace_size bytes (0: may be NULL), 16-byte
  *                aligned, used by this call alone until it has finished
  * Keys that no token sees (padding of a tree) may hold anything.  A NaN or infinity

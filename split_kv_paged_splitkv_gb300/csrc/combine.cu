@@ -4,7 +4,9 @@
 // For a row with partials (O_s, lse_s), s < S:  M = max_s lse_s,
 // lse = M + ln sum_s exp(lse_s - M),  out = sum_s exp(lse_s - lse) O_s.
 // Partials with lse_s = -inf weigh nothing; a row whose partials are all
-// -inf gets out = 0 and lse = -inf.  This is the merge step of "vLLM 0.30.0
+// -inf gets out = 0 and lse = -inf.  A NaN lse_s (trees over latent rows, which merge
+// by the lengths) makes its row NaN in both; in the other forms in out alone.
+// This is the merge step of "vLLM 0.30.0
 // FA4 SplitKV Bug: H100 Decode Can Be 48% Slower", section "Why the result
 // is still correct" (empty splits contribute zero weight).
 #include <cuda_runtime.h>
@@ -136,7 +138,7 @@ __device__ __forceinline__ void combine_body(
     }
     float m_new = m_run;
 #pragma unroll
-    for (int u = 0; u < PER_WAY; ++u) m_new = fmaxf(m_new, lv[u]);
+    for (int u = 0; u < PER_WAY; ++u) m_new = CAP ? max_nan(m_new, lv[u]) : fmaxf(m_new, lv[u]);
     if (m_new == -INFINITY) continue;  // every split so far is empty
     const float rs = ex2((m_run - m_new) * kLog2e);  // 0 when m_run is -inf
     acc.x *= rs; acc.y *= rs; acc.z *= rs; acc.w *= rs;
@@ -168,7 +170,7 @@ __device__ __forceinline__ void combine_body(
     __syncthreads();
     M = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < WAYS; ++k) M = fmaxf(M, red_m[dl + DL * k]);
+    for (int k = 0; k < WAYS; ++k) M = CAP ? max_nan(M, red_m[dl + DL * k]) : fmaxf(M, red_m[dl + DL * k]);
     const float sc = m_run == -INFINITY ? 0.f : ex2((m_run - M) * kLog2e);
     float4 v = make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc);
     float w = wsum * sc;
@@ -194,7 +196,7 @@ __device__ __forceinline__ void combine_body(
     }
   }
   float lse_n = -INFINITY;
-  if (wtot > 0.f) {
+  if (CAP ? !(wtot == 0.f) : wtot > 0.f) {
     const float inv = __frcp_rn(wtot);
     tot.x *= inv; tot.y *= inv; tot.z *= inv; tot.w *= inv;
     lse_n = M + lg2(wtot) * kLn2;

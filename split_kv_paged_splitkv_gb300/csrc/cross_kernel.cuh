@@ -635,13 +635,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return m;
 }
 
-// NaN if either is.
-__device__ __forceinline__ float max_nan(float x, float y) {
-  float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
-  return m;
-}
-
 // Two sums at once.
 __device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
   asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"

@@ -774,8 +774,11 @@ __global__ void __launch_bounds__(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS
     // ---- epilogue: O / l for this CTA's 256 V columns
     const int row_n = t * C::ROWS + r;  // row of the item's partial block
     float lse_n = -INFINITY;
-    if (l > 0.f) lse_n = (m_ref + lg2(TREE && FP8 ? l * 0x1p-7f : l)) * kLn2m;
-    const float inv = l > 0.f ? a.o_scale / l : 0.f;  // o_scale: the FP8 cache scale, else 1
+    // (a tree's row that sees a NaN is NaN here and in the merge: l, which is 0 only without
+    // keys; the decode's counts as one without keys, but for its results)
+    const bool some = TREE ? !(l == 0.f) : l > 0.f;
+    if (some) lse_n = (m_ref + lg2(TREE && FP8 ? l * 0x1p-7f : l)) * kLn2m;
+    const float inv = some ? a.o_scale / l : 0.f;  // o_scale: the FP8 cache scale, else 1
     bool have_o = ok && nblk > 0;
     // PV(nblk - 1) complete (its commit covers every earlier MMA, PV(nblk - 2) too)
     if (have_o && !__all_sync(kFull, mbar_wait(bar(B_PFREE + ((nblk - 1) & 1)),

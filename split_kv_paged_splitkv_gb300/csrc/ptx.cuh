@@ -295,6 +295,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+// The larger, NaN if either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+  return m;
+}
+
 // The larger of each two 16-bit numbers.
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
   uint32_t r;
