@@ -160,11 +160,15 @@ enum {
   B_DONE,
   B_COUNT,
   // e4m3: instead of B_FULL and B_EMPTY those of K's ring and, K_SLOTS further, of V's;
-  // B_CONV [V_SLOTS]: the slot holds f16 (a lane of each converter warp)
+  // B_CONV [V_SLOTS]: the slot holds f16 (a lane of each converter warp); B_DOWN: the rows' exponents
+  // of a narrow piece of two blocks or more (128 threads of A).  (B_Q is for the issuer alone: A fills
+  // Q for pieces that B has no part in, without waiting for it, and a turn that B does not
+  // see in time it would wait for in vain.  B has a part in all pieces that B_DOWN tells of.)
   B_FULL_FP8 = B_COUNT,
   B_EMPTY_FP8 = B_FULL_FP8 + CrossCta<true, true>::SLOTS,
   B_CONV = B_EMPTY_FP8 + CrossCta<true, true>::SLOTS,
-  B_COUNT_FP8 = B_CONV + CrossCta<true, true>::V_SLOTS
+  B_DOWN = B_CONV + CrossCta<true, true>::V_SLOTS,
+  B_COUNT_FP8
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -886,6 +890,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
       mbar_init(bar((FP8 ? B_EMPTY_FP8 : B_EMPTY) + s), 1);
     }
     for (int s = 0; FP8 && s < C::V_SLOTS; ++s) mbar_init(bar(B_CONV + s), 4);
+    if (FP8) mbar_init(bar(B_DOWN), 128);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(B_Q + t), !FP8 && a.row_boxes ? 4 : 128);
       mbar_init(bar(B_S + t), 1);
@@ -1166,7 +1171,7 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
     const uint32_t scol = tmem + (uint32_t((warp & 3) * 32) << 16) + C::S_COL + 128 * t;
     const uint32_t ocol = scol + (C::O_COL - C::S_COL);
     float sl2 = a.qk_scale_log2;  // scores to log2 units, of this piece's row
-    uint32_t n_q = 0;             // e4m3, B: pieces so far whose Q is A's or both row blocks'
+    uint32_t n_down = 0;          // e4m3, B: phases of B_DOWN so far
     uint32_t n_s = 0, n_o = 0;  // phases of B_S and B_O so far
     bool ok = true;
     // 16-byte chunk `ch` of row `rr` of the row block's Q in shared memory.
@@ -1245,11 +1250,6 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         next = take();
         if (next == nullptr) return false;
         skip = t == 1 && next->n_rows <= 128 && next->nblk < 2;
-        if (FP8 && t == 1 && next->nblk > 0) {
-          // (B looks at A's Q only in narrow pieces, but no turn of it may pass unseen)
-          if (skip) ok = ok && __all_sync(kFull, wait_for(bar(B_Q), n_q & 1));
-          ++n_q;
-        }
       } while (skip);
       if (next->nblk == 0 || (t == 1 && next->n_rows <= 128)) return true;
       if (!FP8 && a.row_boxes) {
@@ -1300,14 +1300,15 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         if constexpr (FP8) {
           __syncwarp();
           const uint32_t down = any ? encode_row() : 127;
-          if (narrow) tail.down[r] = uint8_t(down);
+          if (two) tail.down[r] = uint8_t(down);  // (B has read those before: A has had its maxima since)
           sl2 = a.qk_scale_log2 * (a.k_scale ? a.k_scale[pc.h] : 1.f) * __uint_as_float(down << 23);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(bar(B_Q + t));
+        if (FP8 && two) mbar_arrive(bar(B_DOWN));
       }
-      if (FP8 && t == 1 && narrow && pc.nblk > 0) {
-        ok = __all_sync(kFull, wait_for(bar(B_Q), (n_q - 1) & 1));
+      if (FP8 && t == 1 && two) {
+        ok = __all_sync(kFull, wait_for(bar(B_DOWN), n_down++ & 1));
         if (!ok) break;
         sl2 = a.qk_scale_log2 * (a.k_scale ? a.k_scale[pc.h] : 1.f) * __uint_as_float(uint32_t(tail.down[r]) << 23);
       }
