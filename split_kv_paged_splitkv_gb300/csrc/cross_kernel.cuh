@@ -1251,10 +1251,15 @@ __global__ void __launch_bounds__(CrossCta<TREE, FP8>::THREADS, 1)
         if (next == nullptr) return false;
         skip = t == 1 && next->n_rows <= 128 && next->nblk < 2;
       } while (skip);
-      if (next->nblk == 0 || (t == 1 && next->n_rows <= 128)) return true;
+      if (t == 1 && next->n_rows <= 128) return true;
+      if (!FP8 && a.row_boxes && lane == 0)  // (queries, or zeros of an item without keys, go where whole results came from)
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      if (next->nblk == 0) {
+        __syncwarp();
+        return true;
+      }
       if (!FP8 && a.row_boxes) {
         // (rows of other sequences' tokens behind the last come along, and are not used)
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         const int token = next->first + (next->row0 + t * 128 + (warp & 3) * kRowBox) / a.G;
