@@ -176,15 +176,11 @@ LatentTree latent_tree(const splitkv_desc_t& d) {
 
 }  // namespace
 
-cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+cudaError_t set_attribute(const void* kernel, cudaFuncAttribute attribute, int value, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
+  return once_per_device(done, dev, cudaSuccess, [&] { return cudaFuncSetAttribute(kernel, attribute, value); });
 }
 
 }  // namespace splitkv

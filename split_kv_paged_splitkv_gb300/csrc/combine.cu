@@ -258,15 +258,13 @@ bool warp_per_row(int max_splits, long groups, int rows, int dv) {
 
 // Shared-memory carveout: the kernel's 3 KB of shared memory would otherwise
 // cap the resident CTAs below what the registers allow.  Set once per
-// instantiation.
+// instantiation and device.
 template <int WAYS, int PER_WAY, bool CAP>
 cudaError_t combine_attrs() {
-  static cudaError_t e =
-      CAP ? cudaFuncSetAttribute(combine_cap_kernel<WAYS, PER_WAY>,
-                                 cudaFuncAttributePreferredSharedMemoryCarveout, 50)
-          : cudaFuncSetAttribute(combine_kernel<WAYS, PER_WAY>,
-                                 cudaFuncAttributePreferredSharedMemoryCarveout, 50);
-  return e;
+  static std::atomic<uint64_t> done{0};
+  const void* kernel = CAP ? reinterpret_cast<const void*>(combine_cap_kernel<WAYS, PER_WAY>)
+                           : reinterpret_cast<const void*>(combine_kernel<WAYS, PER_WAY>);
+  return set_attribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 50, done);
 }
 
 template <int WAYS, int PER_WAY, bool CAP>

@@ -870,7 +870,7 @@ __global__ void __launch_bounds__(128) gather_debug_kernel(const __grid_constant
 
 namespace {
 
-// One-time shared-memory opt-in of an instantiation, then a launch with
+// One-time shared-memory opt-in of an instantiation on a device, then a launch with
 // programmatic dependent launch: the kernel's prologue may overlap the tail
 // of the previous kernel on the stream; it waits (griddepcontrol.wait)
 // before touching anything that kernel could have written.
@@ -878,10 +878,9 @@ template <bool FP8, int HPI, int NRG = 1, int NST = 2>
 cudaError_t launch_gqa_t(const DecodeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                          cudaStream_t s) {
   using C = Gqa<FP8, HPI, NRG, NST>;
-  // The shared-memory opt-in is a per-process attribute: set it on first use only.
-  static cudaError_t attr = cudaFuncSetAttribute(
-      gqa_splitkv_kernel<FP8, HPI, NRG, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(gqa_splitkv_kernel<FP8, HPI, NRG, NST>), C::SMEM, allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_items, 1, 1);
   cfg.blockDim = dim3(C::THREADS, 1, 1);

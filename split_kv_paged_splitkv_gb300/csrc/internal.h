@@ -8,6 +8,7 @@
 
 #include <cuda_runtime_api.h>
 
+#include "once_per_device.h"
 #include "splitkv.h"
 
 namespace splitkv {
@@ -288,9 +289,12 @@ struct CrossArgs {
   int32_t words;
 };
 
-// Once per device and kernel: opts in to `bytes` of dynamic shared memory on the
-// current device.  `done` is the kernel's own, a bit per device.
-cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>& done);
+// Once per device and kernel (once_per_device.h): sets an attribute on the current device, or
+// opts in to `bytes` of dynamic shared memory there.  `done` is the kernel's own.
+cudaError_t set_attribute(const void* kernel, cudaFuncAttribute attribute, int value, std::atomic<uint64_t>& done);
+inline cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  return set_attribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
+}
 
 cudaError_t launch_append(const AppendArgs& a, int qk_dim, int v_dim, bool fp8, void* stream);
 cudaError_t launch_key_weights(const WeightArgs& a, bool fp8, void* stream);

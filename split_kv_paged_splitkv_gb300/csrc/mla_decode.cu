@@ -910,9 +910,9 @@ namespace {
 template <bool SEPV, bool SMALLP, bool FP8, bool TREE>
 cudaError_t launch_mla_t(const DecodeArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                          cudaStream_t s) {
-  static cudaError_t attr = cudaFuncSetAttribute(
-      mla_splitkv_kernel<SEPV, SMALLP, FP8, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Mla::SMEM);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(mla_splitkv_kernel<SEPV, SMALLP, FP8, TREE>), Mla::SMEM, allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_items * a.T * 2, 1, 1);
   cfg.blockDim = dim3(SEPV ? Mla::THREADS + 32 : (FP8 ? Mla::THREADS + 128 : Mla::THREADS), 1, 1);
