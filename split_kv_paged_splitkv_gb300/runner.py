@@ -117,7 +117,8 @@ class CacheSession:
     a length on the host, so a whole step can be captured into a CUDA graph.
 
     ``q_norm`` and ``k_norm`` have ``append`` normalise the query and key head rows first:
-    the weights (fp32 ``[columns]`` or ``[heads][columns]``), or True for none.
+    the weights (fp32 ``[columns]`` or ``[heads][columns]``), or True for none; None and False
+    leave them as they are.
 
     With ``track`` the session keeps the accumulated weight and the position of
     every cached key, which ``weigh`` and ``evict`` need.  A session's calls
@@ -166,12 +167,13 @@ class CacheSession:
         more = dict(cu_tokens=cu_tokens, kv_scale=self.kv_scale, k_scale=self.k_scale, v_scale=self.v_scale,
                     key_weights=self.key_weights, key_positions=self.key_positions, status=self.status,
                     stream=stream)
-        if self.q_norm is None and self.k_norm is None:
+        norm_q, norm_k = (x is not None and x is not False for x in (self.q_norm, self.k_norm))
+        if not norm_q and not norm_k:
             splitkv_append(*args, **more)
         else:
-            splitkv_append_norm(*args, norm_q=self.q_norm is not None, norm_k=self.k_norm is not None,
-                                q_weight=None if self.q_norm is True else self.q_norm,
-                                k_weight=None if self.k_norm is True else self.k_norm, eps=self.norm_eps, **more)
+            q_weight, k_weight = (None if isinstance(x, bool) else x for x in (self.q_norm, self.k_norm))
+            splitkv_append_norm(*args, norm_q=norm_q, norm_k=norm_k, q_weight=q_weight, k_weight=k_weight,
+                                eps=self.norm_eps, **more)
         return q_out
 
     def decode(self, q, out=None, lse=None, stream=None):
