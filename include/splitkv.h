@@ -736,7 +736,8 @@ splitkv_status splitkv_tree_attend(const splitkv_desc_t* desc, int32_t n_tokens,
  * P], or below T_b, sets SPLITKV_DEVERR_SEQLEN, a path that does not rise within
  * [0, T_b) or is longer than max_path SPLITKV_DEVERR_PATH: the sequence and its
  * length stay as they are.  A page id out of range sets SPLITKV_DEVERR_PAGE and the
- * row that it would hold, or that it should come from, is not moved.  One kernel.
+ * row that it would hold, or that it should come from, is not moved (its state is).  One
+ * kernel.
  */
 splitkv_status splitkv_tree_commit(const splitkv_desc_t* desc, int32_t max_path, const int32_t* path,
                                    const int32_t* path_lens, const int32_t* cu_tokens, void* k_pages,

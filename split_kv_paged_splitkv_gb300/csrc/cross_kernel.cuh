@@ -35,7 +35,7 @@
 // Many items: a CTA per item (prompts), or a line of all items' key blocks that the
 // CTAs share (batches of few rows a sequence; cross_deal has the rule).  The bound
 // of prompts is 4 * 128 * rows * L operations.  Two sequences of 4k tokens, 32 heads on 4, over 8k keys: 675 to
-// 700 us, 1,530 to 1,585 TFLOP/s (floor 561 at 1,906), near the GPU's limit of
+// 715 us, 1,490 to 1,585 TFLOP/s (floor 561 at 1,906), near the GPU's limit of
 // 1,400 W and with the tensor pipe waiting for the softmax's turn of the row
 // blocks.
 //
@@ -74,7 +74,7 @@
 // takes any lengths, as an item counts there for what it costs beside its blocks.
 // Measured, bf16: 8 tokens over 5.9k keys 14 us (floor 0.9: the chain of plan, first
 // blocks, one softmax, result and merge), 400 tokens of 32 requests over 256 to 131k keys
-// 564 us (floor 529), trees of 64 requests over 1 to 300 keys 44 us (floor 9: an item's
+// 563 us (floor 529), trees of 64 requests over 1 to 300 keys 43 us (floor 9: an item's
 // chain is 9 us, a CTA to an SM).
 //
 // Trees' softmax holds 64 columns of S at a time and reads half of S twice, in loops of
@@ -98,8 +98,8 @@
 // 2^-31 of that maximum's weight (2^-24 without, of which long tails of small weights beside
 // one large one lost all that was below a half).  Sums are of the weights times 2^P_UP as well,
 // which cancels but in the log-sum-exp.  The caches' scales join the scores' and the results'.  K's ring has four slots of 16 KB, V's three of 32 KB, a producer each.
-// Measured: 16 tokens of 19 requests over 8k keys 76 us (floor 47; in bf16 105 of 94), 64
-// tokens 132 (in bf16 121), trees of 16 to 61 tokens of 8 requests over 32k keys 133 (floor
+// Measured: 16 tokens of 19 requests over 8k keys 78 us (floor 47; in bf16 105 of 94), 64
+// tokens 130 (in bf16 115), trees of 16 to 61 tokens of 8 requests over 32k keys 133 (floor
 // 54).  In larger code 85, 141 and 148; with K converted as well, both in one ring of five slots, and the softmax's
 // registers taken from the other warps' (S in one part) the three took 109, 155 and 182.
 #pragma once

@@ -16,8 +16,8 @@
 // One CTA for each sequence: its barrier separates all reads of the length from the
 // write of the new one (which may be the same word).  Bound by the chain of
 // dependent loads (length and path, page ids, rows), not by bytes: a path's rows are
-// a few KB per head.  One request 3.2 us, 64 in e4m3 with state 4.2, 256 over latent rows
-// 3.6, of which a launch is most.
+// a few KB per head.  One request 2.3 us, 64 in e4m3 with state 3.5, 256 over latent rows
+// 3.0, of which a launch is most.
 #include <cuda_runtime.h>
 
 #include "internal.h"

@@ -222,7 +222,8 @@ class CacheSession:
     def tree_attend(self, q, tree_mask, cu_tokens=None, stream=None):
         """Attention of a tree of drafted tokens ``q`` [n][Hq][Dk], whose keys are appended and counted by
         the lengths: over the keys before them, and those that ``tree_mask`` int32 [n][words] names (bit i:
-        token i of the sequence)."""
+        token i of the sequence).  Over latent rows every sequence has the description's ``q_tokens`` of
+        them, and ``cu_tokens`` is None."""
         n, d = q.shape[0], self.desc
         size = splitkv_tree_workspace_size(d, n)
         with _on(stream):
